@@ -351,6 +351,149 @@ gdp_status gdp_chunk_fwd_noalloc(const void* q, const void* k, const void* v, co
  */
 gdp_status gdp_debug_wait_fault(int arm, double budget_seconds);
 
+/*
+ * Linear attention with a decay for each head (no delta rule): per (sequence,
+ * value head) the fp32 state S [K, V] takes
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t,
+ * value head hv with key/query head hv / (HV / H).
+ *
+ * Arguments shared by the four calls:
+ *   q, k [B, T, H, K], v [B, T, HV, V] in dtype `dt`, the last dimension
+ *           contiguous; `strides` is a HOST array of nine element strides
+ *           (batch, token, head) of q, of k and of v, so views of a fused
+ *           projection go in as they are.
+ *   g       natural-log decay, fp32: g_per_token != 0: [B, T, HV] contiguous;
+ *           0: [HV], one per value head; NULL: no decay. -inf is a reset (the
+ *           state before the token is dropped).
+ *   o       [B, T, HV, V] contiguous, dtype `dt`; sums and states are fp32.
+ *   K <= 256, V <= 1024, HV % H == 0, T and B T below 2^31; state bases 16-byte
+ *   aligned.
+ *
+ * Paged states. state_pool [n_pages, HV, K, V] fp32; block_tables [n,
+ * max_blocks] int32 names the page of each block of block_size tokens of a
+ * request; context_lens [n] counts its tokens before the call. The page of block
+ * b holds the state after the block's last token, or after the request's last
+ * token so far. A call reads the page of token context - 1 (zeros when
+ * the context is 0) and writes the page of every block that it ends and of the
+ * last token: whole blocks keep their states, so another request can share them
+ * as a prefix. Pages that one call writes must not be read or written by another
+ * request of the same call.
+ * Errors (all four): GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED (dtype, sizes),
+ * GDP_ERR_CUDA; the chunked calls also GDP_ERR_WORKSPACE.
+ */
+
+/* Workspace of the chunked calls in bytes; 0 for sizes they refuse. */
+size_t gdp_linear_chunk_fwd_workspace_size(int B, int T, int N_seq, int H, int HV, int K, int V,
+                                           gdp_dtype dt);
+
+/*
+ * gdp_linear_chunk_fwd - the chunked form, for prompts. cu_seqlens (nullable)
+ * int32 [N_seq + 1] on the device packs N_seq sequences along T (B == 1);
+ * without it N_seq == B. initial_state [N_seq, HV, K, V] (nullable: zeros),
+ * final_state likewise (nullable). Tokens outside every sequence are left
+ * untouched in o. cu_seqlens is checked on the device: a bad list sets the
+ * status word of the workspace (gdp_read_status), leaves o untouched and gives
+ * every sequence its initial state.
+ */
+gdp_status gdp_linear_chunk_fwd(const void* q, const void* k, const void* v, const int64_t* strides,
+                                const float* g, int g_per_token, const float* initial_state,
+                                const int32_t* cu_seqlens, int N_seq, int B, int T, int H, int HV,
+                                int K, int V, float scale, gdp_dtype dt, void* o,
+                                float* final_state, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * gdp_linear_chunk_fwd_paged - the chunked form over packed prompts (B == 1)
+ * with paged states; block_size a multiple of 64. A sequence with a negative
+ * context or with a block whose table entry lies outside the pool is skipped
+ * (its o rows and pages untouched) and sets the status word.
+ */
+gdp_status gdp_linear_chunk_fwd_paged(const void* q, const void* k, const void* v,
+                                      const int64_t* strides, const float* g, int g_per_token,
+                                      const int32_t* cu_seqlens, int N_seq, int T, int H, int HV,
+                                      int K, int V, float scale, gdp_dtype dt, float* state_pool,
+                                      int n_pages, const int32_t* block_tables, int max_blocks,
+                                      const int32_t* context_lens, int block_size, void* o,
+                                      void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/*
+ * gdp_linear_recurrent_update - the recurrent form, for decoding: S (1..16)
+ * tokens for each of n requests (B = n, T = S); state [n, HV, K, V] is updated
+ * in place.
+ */
+gdp_status gdp_linear_recurrent_update(const void* q, const void* k, const void* v,
+                                       const int64_t* strides, const float* g, int g_per_token,
+                                       float* state, int n, int S, int H, int HV, int K, int V,
+                                       float scale, gdp_dtype dt, void* o, cudaStream_t stream);
+
+/*
+ * gdp_linear_recurrent_update_paged - the same with paged states (any
+ * block_size). A request whose last token's table entry is -1 is padding: its o
+ * rows are zero and no state is touched. A request with a negative context, with
+ * a page outside the pool, or that writes a page which another request of the
+ * call reads or writes is treated as padding and sets *status (nullable
+ * int32 on the device) to 1; *status is not cleared.
+ */
+gdp_status gdp_linear_recurrent_update_paged(const void* q, const void* k, const void* v,
+                                             const int64_t* strides, const float* g,
+                                             int g_per_token, float* state_pool, int n_pages,
+                                             const int32_t* block_tables, int max_blocks,
+                                             const int32_t* context_lens, int block_size, int n,
+                                             int S, int H, int HV, int K, int V, float scale,
+                                             gdp_dtype dt, void* o, int32_t* status,
+                                             cudaStream_t stream);
+
+/*
+ * gdp_block_plan - what a serving step needs to know of its requests, built on
+ * the device from their lengths in one launch.
+ *   context_lens, query_lens [n] int32: tokens before the step, tokens in it (0: the
+ *           request sits the step out).
+ *   block_tables [n, max_blocks] int32, in and out: on entry the pages of
+ *           the blocks that the context reaches; the entries of the step's new
+ *           blocks are written, all others left as they are.
+ *   free_pages [n_free] int32, free_used [1] int32: a list of free pages and how many
+ *           of it are taken; new blocks take the next ones in request order.
+ * Outputs: cu_seqlens [n + 1] int32; token_req, token_pos [max_tokens] int32 and
+ * slot_map [max_tokens] int64: a token's request, its position and its slot
+ * page * block_size + position % block_size in a per-token cache (-1 where the
+ * table names no page), all -1 past the last token; free_used_out [1] int32
+ * (may not alias free_used); status (nullable int32): 0, or the sum of 1 (a request
+ * with a negative length, or longer than its table: it is planned as empty; or a
+ * negative free_used) and 2 (pages or tokens ran out: requests are planned in
+ * order while they fit, and the first that does not and all after it are planned
+ * as empty).
+ * n <= 16384, max_blocks * block_size below 2^31.
+ * Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED, GDP_ERR_CUDA.
+ */
+gdp_status gdp_block_plan(const int32_t* context_lens, const int32_t* query_lens, int n,
+                          int32_t* block_tables, int max_blocks, const int32_t* free_pages,
+                          int n_free, const int32_t* free_used, int block_size, int max_tokens,
+                          int32_t* cu_seqlens, int32_t* token_req, int32_t* token_pos,
+                          int64_t* slot_map, int32_t* free_used_out, int32_t* status,
+                          cudaStream_t stream);
+
+typedef enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1 } gdp_activation;
+
+/*
+ * gdp_group_norm - group norm with an activation, channels last. x [N, L, C] in
+ * dtype `dt`, element strides x_sn (sample) and x_sl (position), channels
+ * contiguous; G groups of C / G channels, statistics over (L, C / G):
+ *     z = (x - mean) / sqrt(var + eps) * weight + bias
+ * (weight, bias [C] fp32, nullable), y = act(z), or with a gate (same shape,
+ * strides gate_sn, gate_sl, dtype dt_out) y = z * act(gate). L = 1 normalises
+ * each token's heads. y [N, L, C] contiguous in dtype dt_out, which is dt, or
+ * bf16 or fp16 for an fp32 x. Statistics are fp32, the variance the two-pass one.
+ * y may be x where their layouts agree and L == 1.
+ * Errors: GDP_ERR_INVALID_ARG (sizes, C % G != 0, strides shorter than a row, a
+ * negative eps), GDP_ERR_UNSUPPORTED (dtype, activation), GDP_ERR_CUDA.
+ */
+gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate,
+                          int64_t gate_sn, int64_t gate_sl, const float* weight,
+                          const float* bias, int64_t N, int64_t L, int C, int G, float eps,
+                          gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
+                          cudaStream_t stream);
+
 /* Number of stage-boundary events gdp_set_stage_events takes. */
 #define GDP_STAGE_EVENTS 5
 

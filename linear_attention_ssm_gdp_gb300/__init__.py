@@ -22,6 +22,9 @@ __all__ = [
     "gdp_read_status", "gdp_version", "gdp_set_stage_events", "gdp_chunk_fwd_noalloc",
     "gdp_recurrent_update_slots", "gdp_debug_wait_fault", "gdp_prefill_conv_prepare",
     "gdp_decode_conv_prepare",
+    "gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged", "gdp_linear_chunk_fwd_workspace_size",
+    "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged", "gdp_block_plan",
+    "gdp_group_norm",
     "LIB_PATH",
 ]
 
@@ -66,6 +69,23 @@ def load() -> ctypes.CDLL:
             lib.gdp_recurrent_update_slots.argtypes = ([P] * 7 + [I] * 7 + [F, I, I, P, P, P])
             lib.gdp_chunk_fwd_noalloc.argtypes = [P] * 7 + [I] * 9 + [F, I, I] + [P, P, P]
             lib.gdp_chunk_fwd_noalloc.restype = I
+            lin = [P] * 5 + [I]  # q, k, v, strides, g, g_per_token
+            pages = [P, I, P, I, P, I]  # pool, n_pages, tables, max_blocks, contexts, block_size
+            lib.gdp_linear_chunk_fwd_workspace_size.argtypes = [I] * 8
+            lib.gdp_linear_chunk_fwd_workspace_size.restype = SZ
+            lib.gdp_linear_chunk_fwd.argtypes = lin + [P, P] + [I] * 7 + [F, I, P, P, P, SZ, P]
+            lib.gdp_linear_chunk_fwd_paged.argtypes = (lin + [P] + [I] * 6 + [F, I] + pages
+                                                       + [P, P, SZ, P])
+            lib.gdp_linear_recurrent_update.argtypes = lin + [P] + [I] * 6 + [F, I, P, P]
+            lib.gdp_linear_recurrent_update_paged.argtypes = (lin + pages + [I] * 6
+                                                              + [F, I, P, P, P])
+            lib.gdp_block_plan.argtypes = [P, P, I, P, I, P, I, P, I, I] + [P] * 7
+            lib.gdp_group_norm.argtypes = ([P, I64, I64, P, I64, I64, P, P, I64, I64, I, I, F, I,
+                                            I, I, P, P])
+            for f in ("gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged",
+                      "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged",
+                      "gdp_block_plan", "gdp_group_norm"):
+                getattr(lib, f).restype = I
             lib.gdp_read_status.argtypes = [P, P]
             lib.gdp_debug_wait_fault.argtypes = [I, ctypes.c_double]
             lib.gdp_debug_wait_fault.restype = I
@@ -101,6 +121,26 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("libgdp works on CUDA tensors only")
+
+
+def _a(t):
+    """Address of an optional tensor."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(t):
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _out_ok(t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() \
+            or not t.is_cuda:
+        raise ValueError(f"an output must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+
+
+def _status_ok(t):
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1 or not t.is_cuda):
+        raise ValueError("status must be an int32 device tensor")
 
 
 def gdp_version() -> int:
@@ -439,3 +479,262 @@ def gdp_decode_conv_prepare(xp, conv_w, conv_b, ba, A_log, dt_bias, num_househol
         _p(g), _p(status), _stream(dev))
     _check("gdp_decode_conv_prepare", st)
     return q, k, v, beta, g
+
+
+# ----------------------------------------------------------------------------------
+# linear attention with a decay for each head
+# ----------------------------------------------------------------------------------
+
+def _linear_args(q, k, v, g):
+    """Checks shared by the linear-attention calls: (B, T, H, HV, K, V, strides, g per token)."""
+    _need_cuda(q, k, v, g)
+    if q.dim() != 4 or v.dim() != 4 or k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+        raise ValueError("q, k must be [B, T, H, K] and v [B, T, HV, V]")
+    B, T, H, K = q.shape
+    HV, V = v.shape[2], v.shape[3]
+    dt = q.dtype
+    if dt != k.dtype or dt != v.dtype or dt not in _DTYPE:
+        raise ValueError("q, k, v must share a dtype in {bf16, fp16, fp32}")
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    if (sq[3] != 1 and K > 1) or (sk[3] != 1 and K > 1) or (sv[3] != 1 and V > 1):
+        raise ValueError("the last dimension of q, k, v must be contiguous")
+    per_token = 0
+    if g is not None:
+        if g.dtype != torch.float32 or not g.is_contiguous():
+            raise ValueError("g must be fp32 and contiguous")
+        if g.shape == (B, T, HV):
+            per_token = 1
+        elif g.shape != (HV,):
+            raise ValueError("g must be [B, T, HV] or [HV]")
+    return B, T, H, HV, K, V, _Strides(*sq[:3], *sk[:3], *sv[:3]), per_token
+
+
+_Strides = ctypes.c_int64 * 9
+
+
+def _state_ok(name, t, shape):
+    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous fp32 {list(shape)}")
+
+
+def _tables_ok(n, HV, K, V, state_pool, block_tables, context_lens):
+    _need_cuda(state_pool, block_tables, context_lens)
+    if (state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (HV, K, V)
+            or state_pool.dtype != torch.float32 or not state_pool.is_contiguous()):
+        raise ValueError("state_pool must be contiguous fp32 [n_pages, HV, K, V]")
+    if (block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.shape != (n,)
+            or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or not block_tables.is_contiguous() or not context_lens.is_contiguous()):
+        raise ValueError("block_tables must be int32 [n, max_blocks] and context_lens int32 [n]")
+
+
+def gdp_linear_chunk_fwd_workspace_size(B, T, N_seq, H, HV, K, V, dtype) -> int:
+    return int(load().gdp_linear_chunk_fwd_workspace_size(B, T, N_seq, H, HV, K, V,
+                                                          _DTYPE[dtype]))
+
+
+def _linear_workspace(workspace, B, T, N, H, HV, K, V, q):
+    if workspace is None:
+        need = load().gdp_linear_chunk_fwd_workspace_size(B, T, N, H, HV, K, V, _DTYPE[q.dtype])
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _need_cuda(workspace)
+    return workspace
+
+
+def _packed(cu_seqlens, B):
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+            or cu_seqlens.numel() < 1 or B != 1:
+        raise ValueError("cu_seqlens must be int32 [N + 1], with B == 1")
+    return cu_seqlens.numel() - 1
+
+
+def gdp_linear_chunk_fwd(q, k, v, g=None, cu_seqlens=None, scale: float | None = None,
+                         initial_state=None, output_final_state: bool = True, workspace=None,
+                         out=None):
+    """Chunked linear attention with a decay for each head:
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k [B,T,H,K], v [B,T,HV,V] (bf16/fp16/fp32; any strides with a contiguous last
+    dimension), g fp32 natural-log decay [B,T,HV] per token, [HV] per head or None,
+    cu_seqlens [N+1] int32 on the device (B must be 1), initial_state [N,HV,K,V] fp32.
+    ``scale`` defaults to K**-0.5. Returns (o [B,T,HV,V] in q's dtype, final_state
+    [N,HV,K,V] fp32 or None)."""
+    B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
+    _need_cuda(cu_seqlens, initial_state)
+    N = B if cu_seqlens is None else _packed(cu_seqlens, B)
+    _state_ok("initial_state", initial_state, (N, HV, K, V))
+    ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
+    if out is None:
+        o = torch.empty((B, T, HV, V), dtype=q.dtype, device=q.device)
+        fs = (torch.empty((N, HV, K, V), dtype=torch.float32, device=q.device)
+              if output_final_state else None)
+    else:
+        o, fs = out
+        _state_ok("final_state", fs, (N, HV, K, V))
+        _out_ok(o, (B, T, HV, V), q.dtype)
+    st = load().gdp_linear_chunk_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token, _a(initial_state),
+        _a(cu_seqlens), N, B, T, H, HV, K, V, K ** -0.5 if scale is None else scale,
+        _DTYPE[q.dtype], o.data_ptr(), _a(fs), ws.data_ptr(), ws.numel(), _raw_stream(q))
+    if st:
+        _check("gdp_linear_chunk_fwd", st)
+    return o, fs
+
+
+def gdp_linear_chunk_fwd_paged(q, k, v, g, cu_seqlens, state_pool, block_tables, context_lens,
+                               block_size: int, scale: float | None = None, workspace=None,
+                               out=None):
+    """Chunked linear attention over packed prompts whose states live in pages:
+    request r starts from the page of its token context_lens[r] - 1 (zeros for a new
+    request) and writes ``state_pool`` [n_pages,HV,K,V] fp32 at every block of
+    block_size tokens (a multiple of 64) that it ends and at its last token;
+    block_tables [n, max_blocks] names the pages. q, k [1,T,H,K], v [1,T,HV,V].
+    Returns o."""
+    B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
+    _need_cuda(cu_seqlens)
+    N = _packed(cu_seqlens, B)
+    _tables_ok(N, HV, K, V, state_pool, block_tables, context_lens)
+    ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
+    o = out
+    if o is None:
+        o = torch.empty((B, T, HV, V), dtype=q.dtype, device=q.device)
+    _out_ok(o, (B, T, HV, V), q.dtype)
+    st = load().gdp_linear_chunk_fwd_paged(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token,
+        cu_seqlens.data_ptr(), N, T, H, HV, K, V, K ** -0.5 if scale is None else scale,
+        _DTYPE[q.dtype], state_pool.data_ptr(), state_pool.shape[0], block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), block_size, o.data_ptr(),
+        ws.data_ptr(), ws.numel(), _raw_stream(q))
+    if st:
+        _check("gdp_linear_chunk_fwd_paged", st)
+    return o
+
+
+def gdp_linear_recurrent_update(q, k, v, g, state, scale: float | None = None, out=None):
+    """One decode step of linear attention with a decay for each head: S (1..16) tokens
+    for each of n requests; ``state`` [n,HV,K,V] fp32 is updated in place. q, k
+    [n,S,H,K], v [n,S,HV,V], g [n,S,HV], [HV] or None. Returns o [n,S,HV,V] in q's
+    dtype."""
+    n, S, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
+    _need_cuda(state)
+    _state_ok("state", state, (n, HV, K, V))
+    o = out
+    if o is None:
+        o = torch.empty((n, S, HV, V), dtype=q.dtype, device=q.device)
+    _out_ok(o, (n, S, HV, V), q.dtype)
+    st = load().gdp_linear_recurrent_update(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token, state.data_ptr(), n,
+        S, H, HV, K, V, K ** -0.5 if scale is None else scale, _DTYPE[q.dtype], o.data_ptr(),
+        _raw_stream(q))
+    if st:
+        _check("gdp_linear_recurrent_update", st)
+    return o
+
+
+def gdp_linear_recurrent_update_paged(q, k, v, g, state_pool, block_tables, context_lens,
+                                      block_size: int, scale: float | None = None, status=None,
+                                      out=None):
+    """gdp_linear_recurrent_update with the states in pages, addressed as in
+    gdp_linear_chunk_fwd_paged (any block_size). A request whose last token has no
+    page (-1) is padding: zero o rows, no state touched. ``status`` (optional int32
+    device tensor) is set to 1 when a request's pages lie outside the pool or clash
+    with another's; those requests are skipped like padding. Returns o."""
+    n, S, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
+    _tables_ok(n, HV, K, V, state_pool, block_tables, context_lens)
+    _status_ok(status)
+    o = out
+    if o is None:
+        o = torch.empty((n, S, HV, V), dtype=q.dtype, device=q.device)
+    _out_ok(o, (n, S, HV, V), q.dtype)
+    st = load().gdp_linear_recurrent_update_paged(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token,
+        state_pool.data_ptr(), state_pool.shape[0], block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), block_size, n, S, H, HV, K, V,
+        K ** -0.5 if scale is None else scale, _DTYPE[q.dtype], o.data_ptr(), _a(status),
+        _raw_stream(q))
+    if st:
+        _check("gdp_linear_recurrent_update_paged", st)
+    return o
+
+
+# ----------------------------------------------------------------------------------
+# block plan, group norm
+# ----------------------------------------------------------------------------------
+
+def gdp_block_plan(context_lens, query_lens, block_tables, free_pages, free_used, block_size: int,
+                   max_tokens: int, status=None, out=None):
+    """Plan of a serving step from request lengths, on the device: writes the new
+    entries of ``block_tables`` [n, max_blocks] in place from ``free_pages`` (its first
+    free_used[0] entries are taken) and returns (cu_seqlens [n+1], token_req
+    [max_tokens], token_pos [max_tokens], slot_map [max_tokens] int64, free_used_out
+    [1]); see include/gdp.h for ``status`` and for requests that do not fit."""
+    _need_cuda(context_lens, query_lens, block_tables, free_pages, free_used)
+    for t in (context_lens, query_lens, block_tables, free_pages, free_used):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("lengths, tables and free pages must be contiguous int32")
+    n = context_lens.numel()
+    if (context_lens.shape != (n,) or query_lens.shape != (n,) or block_tables.dim() != 2
+            or block_tables.shape[0] != n or free_used.numel() != 1):
+        raise ValueError("lengths must be [n], block_tables [n, max_blocks], free_used [1]")
+    _status_ok(status)
+    dev = context_lens.device
+    if out is None:
+        ints = torch.empty(n + 2 + 2 * max_tokens, dtype=torch.int32, device=dev)
+        cu, used, req, pos = ints.split([n + 1, 1, max_tokens, max_tokens])
+        out = (cu, req, pos, torch.empty(max_tokens, dtype=torch.int64, device=dev), used)
+    else:
+        for t, m, dt in zip(out, (n + 1, max_tokens, max_tokens, max_tokens, 1),
+                            (torch.int32,) * 3 + (torch.int64, torch.int32)):
+            _out_ok(t, (m,), dt)
+    cu, req, pos, slot, used = out
+    st = load().gdp_block_plan(
+        context_lens.data_ptr(), query_lens.data_ptr(), n, block_tables.data_ptr(),
+        block_tables.shape[1], free_pages.data_ptr(), free_pages.numel(), free_used.data_ptr(),
+        block_size, max_tokens, cu.data_ptr(), req.data_ptr(), pos.data_ptr(), slot.data_ptr(),
+        used.data_ptr(), _a(status), _raw_stream(context_lens))
+    if st:
+        _check("gdp_block_plan", st)
+    return out
+
+
+_ACTIVATION = {"none": 0, "silu": 1}
+
+
+def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: float = 1e-5,
+                   activation: str = "silu", out_dtype=None, out=None):
+    """Group norm with an activation, channels last: x [N, L, C] (or [N, C]: one
+    position per sample, such as a token's heads), statistics over the positions and
+    the C / num_groups channels of a group, z = (x - mean) / sqrt(var + eps) * weight
+    + bias; returns act(z), or z * act(gate) with a gate. weight, bias [C] fp32;
+    out_dtype is x's dtype, or bf16/fp16 for an fp32 x; the gate has it too. Rows of
+    x and gate may be strided (contiguous channels)."""
+    _need_cuda(x, weight, bias, gate)
+    if x.dim() not in (2, 3) or x.stride(-1) != 1:
+        raise ValueError("x must be [N, L, C] or [N, C] with contiguous channels")
+    dt_out = x.dtype if out_dtype is None else out_dtype
+    if x.dtype not in _DTYPE or dt_out not in _DTYPE:
+        raise ValueError("x and out_dtype must be bf16, fp16 or fp32")
+    if activation not in _ACTIVATION:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATION)}")
+    shape = x.shape
+    N, L, C = (shape[0], 1, shape[1]) if x.dim() == 2 else shape
+    x_sn, x_sl = (x.stride(0), 0) if x.dim() == 2 else x.stride()[:2]
+    g_sn = g_sl = 0
+    if gate is not None:
+        if gate.shape != shape or gate.dtype != dt_out or gate.stride(-1) != 1:
+            raise ValueError("gate must have x's shape, the output's dtype, contiguous channels")
+        g_sn, g_sl = (gate.stride(0), 0) if x.dim() == 2 else gate.stride()[:2]
+    for t in (weight, bias):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (C,)
+                              or not t.is_contiguous()):
+            raise ValueError("weight and bias must be contiguous fp32 [C]")
+    if out is None:
+        out = torch.empty(shape, dtype=dt_out, device=x.device)
+    _out_ok(out, tuple(shape), dt_out)
+    st = load().gdp_group_norm(x.data_ptr(), x_sn, x_sl, _a(gate), g_sn, g_sl, _a(weight),
+                               _a(bias), N, L, C, num_groups, eps, _ACTIVATION[activation],
+                               _DTYPE[x.dtype], _DTYPE[dt_out], out.data_ptr(), _raw_stream(x))
+    if st:
+        _check("gdp_group_norm", st)
+    return out

@@ -31,6 +31,10 @@ UNITS = {
     "chunk_tc.cu": [],
     "recurrent.cu": [],
     "noalloc.cu": [],
+    "linear_api.cu": [],
+    "linear_token.cu": [],
+    "block_plan.cu": [],
+    "group_norm.cu": [],
 }
 
 

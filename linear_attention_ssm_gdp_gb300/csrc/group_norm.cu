@@ -1,0 +1,371 @@
+// Group norm with an activation, channels last: x [N, L, C], G groups of C / G
+// neighbouring channels, statistics over (L, C / G) of each sample and group,
+//     z = (x - mean) / sqrt(var + eps) * weight + bias,
+//     y = act(z),  or with a gate  y = z * act(gate).
+// L = 1 is the norm of a token's heads (the output norm and gate of a linear
+// attention layer).
+//
+// The bound is HBM: x (and the gate) read once, y written once. Both kernels hold
+// what they have read (in registers, or in shared memory) while they form the mean
+// and then the squared distances from it, so the variance is the two-pass one, in
+// fp32, and no element is read twice. Sums run in a fixed order.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gdp_internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gdp {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+
+// n neighbouring elements as one or two vector accesses (p aligned to min(16, n sizeof(T))).
+template <typename T, int n>
+struct alignas(n * sizeof(T) < 16 ? n * sizeof(T) : 16) Pack {
+  T e[n];
+};
+
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + expf(-a)); }
+
+struct NormArgs {
+  const void *x, *gate;
+  int64_t x_sn, x_sl, g_sn, g_sl;
+  const float *w, *b;
+  void* y;
+  int64_t N, L;
+  int C, G, Cg;
+  float eps;
+  int silu;
+  int GS, sets;   // groups per CTA, CTAs along the groups
+  int rows;       // positions per CTA
+  int resident;   // the CTA's elements stay in shared memory
+};
+
+template <bool GATE>
+__device__ __forceinline__ float finish(const NormArgs& a, float z, float gt) {
+  const float u = GATE ? gt : z;
+  const float act = a.silu ? silu(u) : u;
+  return GATE ? z * act : act;
+}
+
+// ---------------------------------------------------------------- one position per sample
+// TG lanes hold one (sample, group): NV 16-byte vectors each; U of them per lane group are
+// in flight at once.
+template <typename TX, typename TO, int TG, int NV, int U, bool GATE>
+__global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ NormArgs a) {
+  pdl_wait();
+  constexpr int VEC = 16 / sizeof(TX);
+  using PX = Pack<TX, VEC>;
+  using PO = Pack<TO, VEC>;
+  const int sub = threadIdx.x % TG;
+  const int64_t item0 = (int64_t)blockIdx.x * (256 / TG * U) + threadIdx.x / TG;
+  const int64_t items = a.N * a.G;
+  const int nvec = a.Cg / VEC;
+  PX x[U][NV];
+  PO gt[GATE ? U : 1][GATE ? NV : 1];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t it = item0 + u * (256 / TG), n = it / a.G;
+    const int c = (int)(it - n * a.G) * a.Cg;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int vi = sub + j * TG;
+      if (it < items && vi < nvec) {
+        x[u][j] = *reinterpret_cast<const PX*>(static_cast<const TX*>(a.x) + n * a.x_sn + c + vi * VEC);
+        if (GATE)
+          gt[u][j] = *reinterpret_cast<const PO*>(static_cast<const TO*>(a.gate) + n * a.g_sn + c + vi * VEC);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) put(&x[u][j].e[e], 0.f);
+      }
+    }
+  }
+  const float inv = 1.f / (float)a.Cg;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t it = item0 + u * (256 / TG), n = it / a.G;
+    const int c = (int)(it - n * a.G) * a.Cg;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += to_f(x[u][j].e[e]);
+#pragma unroll
+    for (int o = TG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float mean = s * inv;
+    float m2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (sub + j * TG < nvec)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = to_f(x[u][j].e[e]) - mean;
+          m2 = fmaf(d, d, m2);
+        }
+#pragma unroll
+    for (int o = TG / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+    const float rstd = rsqrtf(m2 * inv + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int vi = sub + j * TG;
+      if (it >= items || vi >= nvec) continue;
+      const int cc = c + vi * VEC;
+      PO out;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float z = (to_f(x[u][j].e[e]) - mean) * rstd;
+        if (a.w) z *= a.w[cc + e];
+        if (a.b) z += a.b[cc + e];
+        put(&out.e[e], finish<GATE>(a, z, GATE ? to_f(gt[GATE ? u : 0][GATE ? j : 0].e[e]) : 0.f));
+      }
+      *reinterpret_cast<PO*>(static_cast<TO*>(a.y) + n * a.C + cc) = out;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many positions per sample
+// A cluster of CTAs takes one sample and a set of GS neighbouring groups (enough that its row
+// segments fill whole sectors), each CTA a run of positions; the group sums meet through
+// distributed shared memory. A thread keeps one vector column, so that its channels' groups
+// are fixed, and walks down the positions.
+constexpr int kMapThreads = 256;
+constexpr int kMaxGS = 128;
+
+template <typename TX, typename TO, int VEC, bool GATE>
+__global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_constant__ NormArgs a) {
+  pdl_wait();
+  extern __shared__ __align__(16) uint8_t raw[];
+  using PX = Pack<TX, VEC>;
+  using PO = Pack<TO, VEC>;
+  __shared__ float part[kMapThreads * VEC];
+  __shared__ float gsum[2][kMaxGS];  // this CTA's group sums: elements, squared distances
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks();
+  const int64_t unit = blockIdx.x / CL;
+  const int64_t n = unit / a.sets;
+  const int set = (int)(unit - n * a.sets);
+  const int g0 = set * a.GS, gs = min(a.GS, a.G - g0);
+  const int c0 = g0 * a.Cg, W = gs * a.Cg, cols = W / VEC;
+  const int64_t l0 = (int64_t)rank * a.rows, l1 = min(l0 + a.rows, a.L);
+  const int nrow = (int)max((int64_t)0, l1 - l0);
+  // thread -> (first vector column, column step, row, row step)
+  const int tc = min(cols, kMapThreads), ty = threadIdx.x / tc, tx = threadIdx.x % tc;
+  const int nty = kMapThreads / tc;
+  const bool on = ty < nty;
+  PX* keep = reinterpret_cast<PX*>(raw);
+  const TX* xb = static_cast<const TX*>(a.x) + n * a.x_sn + l0 * a.x_sl + c0;
+  const float inv = 1.f / ((float)a.L * (float)a.Cg);
+
+  float mean_of[VEC];  // per channel of the thread's column (one group: all the same)
+  float acc[VEC];
+  auto reduce = [&](int which) {
+    // this CTA's sums by group, then the cluster's
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[threadIdx.x * VEC + e] = on ? acc[e] : 0.f;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = warp; g < gs; g += kMapThreads / 32) {
+      float s = 0.f;
+      if (gs == 1) {
+        for (int i = lane; i < kMapThreads * VEC; i += 32) s += part[i];
+      } else {  // channels [g Cg, (g + 1) Cg) of every row group
+        for (int i = lane; i < nty * a.Cg; i += 32) {
+          const int y = i / a.Cg, c = g * a.Cg + i - y * a.Cg;
+          s += part[(y * tc + c / VEC) * VEC + c % VEC];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) gsum[which][g] = s;
+    }
+    cl.sync();
+    // `part` takes the cluster's sums
+    for (int g = threadIdx.x; g < gs; g += kMapThreads) {
+      float s = 0.f;
+      for (int r = 0; r < CL; ++r) s += cl.map_shared_rank(&gsum[which][0], r)[g];
+      part[g] = s;
+    }
+    __syncthreads();
+  };
+  auto group_of = [&](int col, int e) { return gs == 1 ? 0 : (col * VEC + e) / a.Cg; };
+
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  if (on)
+    for (int r = ty; r < nrow; r += nty)
+      for (int c = tx; c < cols; c += tc) {
+        const PX x = *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
+        if (a.resident) keep[(int64_t)r * cols + c] = x;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
+      }
+  reduce(0);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    mean_of[e] = part[group_of(tx, e)] * inv;
+    acc[e] = 0.f;
+  }
+  __syncthreads();
+  if (on)
+    for (int r = ty; r < nrow; r += nty)
+      for (int c = tx; c < cols; c += tc) {
+        const PX x = a.resident ? keep[(int64_t)r * cols + c]
+                                : *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = to_f(x.e[e]) - mean_of[e];
+          acc[e] = fmaf(d, d, acc[e]);
+        }
+      }
+  reduce(1);
+  float rstd[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(part[group_of(tx, e)] * inv + a.eps);
+  const TO* gb = static_cast<const TO*>(a.gate);
+  if (GATE) gb += n * a.g_sn + l0 * a.g_sl + c0;
+  TO* yb = static_cast<TO*>(a.y) + (n * a.L + l0) * a.C + c0;
+  if (on)
+    for (int c = tx; c < cols; c += tc) {
+      float ww[VEC], bb[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        ww[e] = a.w ? a.w[c0 + c * VEC + e] : 1.f;
+        bb[e] = a.b ? a.b[c0 + c * VEC + e] : 0.f;
+      }
+      for (int r = ty; r < nrow; r += nty) {
+        const PX x = a.resident ? keep[(int64_t)r * cols + c]
+                                : *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
+        PO gt, out;
+        if (GATE) gt = *reinterpret_cast<const PO*>(gb + r * a.g_sl + c * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          put(&out.e[e], finish<GATE>(a, fmaf((to_f(x.e[e]) - mean_of[e]) * rstd[e], ww[e], bb[e]),
+                                      GATE ? to_f(gt.e[e]) : 0.f));
+        *reinterpret_cast<PO*>(yb + (int64_t)r * a.C + c * VEC) = out;
+      }
+    }
+  cl.sync();  // no CTA leaves while another may still read its sums
+}
+
+template <typename TX, typename TO, int TG, int NV, int U>
+cudaError_t go_rows(const NormArgs& a, cudaStream_t s) {
+  const int64_t grid = cdiv(a.N * a.G, 256 / TG * U);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return a.gate ? launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, true>, dim3((unsigned)grid), dim3(256), 0, s, a)
+                : launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, false>, dim3((unsigned)grid), dim3(256), 0, s, a);
+}
+
+template <typename TX, typename TO, int VEC, bool GATE>
+cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
+  auto kern = norm_map_kernel<TX, TO, VEC, GATE>;
+  if (smem > 32 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t grid = a.N * a.sets * CL;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CL;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <typename TX, typename TO, int VEC>
+cudaError_t go_map(NormArgs a, cudaStream_t s) {
+  // whole sectors per row: at least 128 bytes of neighbouring groups, a multiple of a vector
+  a.GS = 1;
+  while (a.GS < a.G && a.GS < kMaxGS &&
+         ((int64_t)a.GS * a.Cg * sizeof(TX) < 128 || (a.GS * a.Cg) % VEC != 0))
+    ++a.GS;
+  // a thread's channels must keep their groups, so a set of several groups is one pass of columns
+  a.sets = (int)cdiv(a.G, a.GS);
+  const int64_t units = a.N * a.sets;
+  const int64_t seg = (int64_t)a.GS * a.Cg * sizeof(TX);
+  // CTAs per cluster: until the machine is filled twice, or 64 rows of work are left each
+  int CL = 1;
+  while (CL < 8 && units * CL < 2 * sm_count() && a.L * seg > (int64_t)CL * 8192) CL *= 2;
+  while (CL < 8 && cdiv(a.L, CL) * seg > 96 * 1024) CL *= 2;
+  a.rows = (int)cdiv(a.L, CL);
+  const int64_t bytes = (int64_t)a.rows * seg;
+  a.resident = bytes <= 200 * 1024;
+  const size_t smem = a.resident ? (size_t)bytes : 0;
+  return a.gate ? go_map2<TX, TO, VEC, true>(a, CL, smem, s) : go_map2<TX, TO, VEC, false>(a, CL, smem, s);
+}
+
+bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <typename TX, typename TO>
+cudaError_t run(NormArgs a, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(TX);
+  // vectors: 16 bytes of x, as many elements of the gate and of y
+  constexpr int GA = std::min<int>(16, VEC * sizeof(TO));
+  const bool rows_ok = a.x_sn % VEC == 0 && a.x_sl % VEC == 0 && aligned(a.x, 16) &&
+                       aligned(a.y, GA) && a.C % VEC == 0 &&
+                       (!a.gate || (a.g_sn % VEC == 0 && a.g_sl % VEC == 0 && aligned(a.gate, GA)));
+  if (a.L == 1 && rows_ok && a.Cg % VEC == 0) {
+    const int nvec = a.Cg / VEC;
+    if (nvec <= 1) return go_rows<TX, TO, 1, 1, 2>(a, s);
+    if (nvec <= 2) return go_rows<TX, TO, 2, 1, 2>(a, s);
+    if (nvec <= 4) return go_rows<TX, TO, 4, 1, 2>(a, s);
+    if (nvec <= 8) return go_rows<TX, TO, 8, 1, 2>(a, s);
+    if (nvec <= 16) return go_rows<TX, TO, 16, 1, 2>(a, s);
+    if (nvec <= 32) return go_rows<TX, TO, 32, 1, 2>(a, s);
+    if (nvec <= 64) return go_rows<TX, TO, 32, 2, 1>(a, s);
+    if (nvec <= 128) return go_rows<TX, TO, 32, 4, 1>(a, s);
+  }
+  // several groups share a vector only where the set of groups ends on one
+  if (rows_ok && (a.Cg % VEC == 0 || a.Cg * sizeof(TX) < 128)) return go_map<TX, TO, VEC>(a, s);
+  return go_map<TX, TO, 1>(a, s);
+}
+
+}  // namespace
+}  // namespace gdp
+
+using namespace gdp;
+
+extern "C" gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate,
+                                     int64_t gate_sn, int64_t gate_sl, const float* weight,
+                                     const float* bias, int64_t N, int64_t L, int C, int G,
+                                     float eps, gdp_activation activation, gdp_dtype dt,
+                                     gdp_dtype dt_out, void* y, cudaStream_t stream) {
+  if (N < 0 || L < 0 || C <= 0 || G <= 0 || C % G != 0 || !(eps >= 0.f)) return GDP_ERR_INVALID_ARG;
+  if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU) return GDP_ERR_UNSUPPORTED;
+  if (N == 0 || L == 0) return GDP_OK;
+  if (!x || !y) return GDP_ERR_INVALID_ARG;
+  if ((L > 1 && (x_sl < C || (gate && gate_sl < C))) ||
+      (N > 1 && (x_sn < C || (gate && gate_sn < C))))
+    return GDP_ERR_INVALID_ARG;
+  if (L > INT32_MAX) return GDP_ERR_UNSUPPORTED;
+  if (L == 1) x_sl = gate_sl = 0;  // the stride of a single position or sample means nothing
+  if (N == 1) x_sn = gate_sn = 0;
+  NormArgs a{x, gate, x_sn, x_sl, gate_sn, gate_sl, weight, bias, y, N, L, C, G, C / G, eps,
+             activation == GDP_ACT_SILU, 0, 0, 0, 0};
+  cudaError_t e;
+  if (dt == GDP_BF16 && dt_out == GDP_BF16) e = run<__nv_bfloat16, __nv_bfloat16>(a, stream);
+  else if (dt == GDP_F16 && dt_out == GDP_F16) e = run<__half, __half>(a, stream);
+  else if (dt == GDP_F32 && dt_out == GDP_F32) e = run<float, float>(a, stream);
+  else if (dt == GDP_F32 && dt_out == GDP_BF16) e = run<float, __nv_bfloat16>(a, stream);
+  else if (dt == GDP_F32 && dt_out == GDP_F16) e = run<float, __half>(a, stream);
+  else return GDP_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
+}

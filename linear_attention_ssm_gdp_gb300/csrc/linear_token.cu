@@ -1,0 +1,297 @@
+// Linear attention with a decay for each head, recurrent form (single tokens and
+// short runs of draft tokens):
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+// with the fp32 state S [K, V] of each (request, value head) read once and
+// written once per call; value head hv reads key/query head hv / (HV / H).
+//
+// The work is the state's read and write (8 bytes per element and call, against
+// 5 operations), so the kernel is an HBM stream: a CTA of 256 threads takes one
+// (request, value head, slice of up to 128 columns) and holds it in registers,
+// four columns (16 bytes) by R rows per thread, all loads in flight at once.
+// The sum over K of a read-out is in-thread over R rows, then shuffles across
+// the lanes of equal columns, then the eight warps through shared memory in a
+// fixed order. Sums and states are fp32; o alone is rounded, to the inputs' type.
+// The decay factor is a pair of floats (hi + lo from a 64-bit exponential, one per
+// step): a decay that stays the same from token to token, rounded to 24 bits, would
+// drift from e^{n g} by n roundings in one direction.
+#include <algorithm>
+
+#include "linear_internal.cuh"
+
+namespace gdp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStep = 16;  // steps staged in shared memory at a time
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+
+struct WalkArgs {
+  LinearProblem p;
+  const int4* recs;
+  int VS;      // value columns per CTA
+  int slices;  // CTAs along V
+};
+
+// Page of block b of request r, or -1 when it has none in the pool.
+__device__ __forceinline__ int page_of(const LinearProblem& p, int r, int64_t b) {
+  if (b < 0 || b >= p.width) return -1;
+  const int pg = p.tables[(int64_t)r * p.width + b];
+  return pg >= 0 && pg < p.n_pages ? pg : -1;
+}
+
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_constant__ WalkArgs a) {
+  pdl_wait();
+  extern __shared__ __align__(16) float sm[];
+  const LinearProblem& p = a.p;
+  const int K = p.K, V = p.V, VS = a.VS, tid = threadIdx.x;
+  float* sq = sm;                    // [kStep][K]
+  float* sk = sq + kStep * K;        // [kStep][K]
+  float* sv = sk + kStep * K;        // [kStep][VS]
+  float* sw = sv + kStep * VS;       // [2][kStep] decay factors, hi and lo
+  float* red = sw + 2 * kStep;       // [2][8][VS]
+  const int slice = blockIdx.x % a.slices, rest = blockIdx.x / a.slices;
+  const int hv = rest % p.HV, seq = rest / p.HV;
+  const int v0 = slice * VS, h = hv / (p.HV / p.H);
+  const int CG = VS / VEC, RG = kThreads / CG;   // column groups, row groups
+  const int cg = tid % CG, rg = tid / CG, c0 = v0 + cg * VEC;
+  const bool col_ok = c0 < V;                    // VEC divides V
+
+  int b = seq, t0 = 0, len = p.T, ctx = 0;
+  if (a.recs) {
+    const int4 rec = a.recs[seq];
+    b = 0; t0 = rec.x; len = rec.y; ctx = rec.w;
+  } else if (p.ctx) {
+    ctx = p.ctx[seq];
+  }
+  const float* src = p.s0 ? p.s0 + ((int64_t)seq * p.HV + hv) * K * V : nullptr;
+  bool live = true;
+  if (p.pool && !a.recs) {
+    // a padding request names no page for its last token; one whose pages lie
+    // outside the pool, or that writes a page which another request reads or
+    // writes, would make the update ill-defined and is treated the same
+    const int64_t b0 = ctx > 0 ? (ctx - 1) / p.block : 0;
+    const int64_t w0 = ctx >= 0 ? ctx / p.block : 0, w1 = ((int64_t)ctx + len - 1) / p.block;
+    const int last = ctx >= 0 && w1 < p.width ? p.tables[(int64_t)seq * p.width + w1] : -2;
+    live = last != -1;
+    bool bad = false;
+    if (live) {
+      for (int64_t j = b0; j <= w1; ++j) bad |= page_of(p, seq, j) < 0;
+      bad |= ctx < 0;
+      for (int r = tid; r < p.N_seq && !bad; r += kThreads) {
+        const int rc = p.ctx[r];
+        if (r == seq || rc < 0) continue;
+        const int64_t r1 = ((int64_t)rc + len - 1) / p.block;
+        if (page_of(p, r, r1) < 0) continue;
+        for (int64_t i = rc > 0 ? (rc - 1) / p.block : 0; i <= r1; ++i) {
+          const int pg = page_of(p, r, i);
+          for (int64_t j = w0; j <= w1; ++j) bad |= pg >= 0 && pg == page_of(p, seq, j);
+        }
+      }
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0 && p.status) atomicExch(p.status, 1);
+      live = false;
+    }
+  }
+  T* o = static_cast<T*>(p.o) + ((int64_t)b * p.T + t0) * p.HV * V + (int64_t)hv * V;
+  const int64_t orow = (int64_t)p.HV * V;
+  if (!live) {
+    for (int i = tid; i < len * VS; i += kThreads) {
+      const int c = v0 + i % VS;
+      if (c < V) put(o + (i / VS) * orow + c, 0.f);
+    }
+    return;
+  }
+  if (p.pool && ctx > 0 && len > 0)
+    src = p.pool + ((int64_t)page_of(p, seq, (ctx - 1) / p.block) * p.HV + hv) * K * V;
+
+  float s[R][VEC];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = rg + RG * i;
+    if (src && col_ok && row < K) {
+      if (VEC == 4) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)row * V + c0));
+        s[i][0] = x.x; s[i][1 % VEC] = x.y; s[i][2 % VEC] = x.z; s[i][3 % VEC] = x.w;
+      } else {
+        s[i][0] = src[(int64_t)row * V + c0];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) s[i][c] = 0.f;
+    }
+  }
+  auto store = [&](float* dst) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int row = rg + RG * i;
+      if (col_ok && row < K) {
+        if (VEC == 4)
+          __stcs(reinterpret_cast<float4*>(dst + (int64_t)row * V + c0),
+                 make_float4(s[i][0], s[i][1 % VEC], s[i][2 % VEC], s[i][3 % VEC]));
+        else
+          dst[(int64_t)row * V + c0] = s[i][0];
+      }
+    }
+  };
+
+  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + t0 * p.qs[1] + h * p.qs[2];
+  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + t0 * p.ks[1] + h * p.ks[2];
+  const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + t0 * p.vs[1] + hv * p.vs[2];
+  const float* g = !p.g ? nullptr : p.g_token ? p.g + ((int64_t)b * p.T + t0) * p.HV + hv : p.g + hv;
+  for (int base = 0; base < len; base += kStep) {
+    const int m = min(kStep, len - base);
+    __syncthreads();
+    for (int i = tid; i < m * K; i += kThreads) {
+      const int t = i / K, c = i - t * K;
+      sq[i] = to_f(q[(int64_t)(base + t) * p.qs[1] + c]);
+      sk[i] = to_f(k[(int64_t)(base + t) * p.ks[1] + c]);
+    }
+    for (int i = tid; i < m * VS; i += kThreads) {
+      const int t = i / VS, c = i - t * VS;
+      sv[i] = v0 + c < V ? to_f(v[(int64_t)(base + t) * p.vs[1] + v0 + c]) : 0.f;
+    }
+    if (tid < m) {
+      const double w = !g ? 1.0 : exp((double)(p.g_token ? g[(int64_t)(base + tid) * p.HV] : *g));
+      sw[tid] = (float)w;
+      sw[kStep + tid] = isinf(sw[tid]) ? 0.f : (float)(w - (double)sw[tid]);
+    }
+    __syncthreads();
+    for (int t = 0; t < m; ++t) {
+      const float w = sw[t], wl = sw[kStep + t];
+      float vv[VEC], acc[VEC];
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        vv[c] = sv[t * VS + cg * VEC + c];
+        acc[c] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int row = rg + RG * i;
+        if (row < K) {
+          const float kk = sk[t * K + row], qq = sq[t * K + row];
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            s[i][c] = fmaf(w, s[i][c], fmaf(wl, s[i][c], kk * vv[c]));
+            acc[c] = fmaf(qq, s[i][c], acc[c]);
+          }
+        }
+      }
+      // lanes of equal columns are CG apart inside a warp
+      for (int off = CG; off < 32; off <<= 1)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], off);
+      float* rb = red + (t & 1) * 8 * VS;
+      if ((tid & 31) < CG)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) rb[(tid >> 5) * VS + cg * VEC + c] = acc[c];
+      __syncthreads();
+      if (tid < VS && v0 + tid < V) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += rb[i * VS + tid];
+        put(o + (int64_t)(base + t) * orow + v0 + tid, x * p.scale);
+      }
+      if (p.pool) {
+        const int64_t end = (int64_t)ctx + base + t + 1;
+        if (end % p.block == 0 || base + t + 1 == len) {
+          const int pg = page_of(p, seq, (end - 1) / p.block);
+          if (pg >= 0) store(p.pool + ((int64_t)pg * p.HV + hv) * K * V);
+        }
+      }
+    }
+  }
+  if (p.sT) store(p.sT + ((int64_t)seq * p.HV + hv) * K * V);
+}
+
+// Packed batches: one record per sequence from cu_seqlens, checked on the device
+// (offsets ascending inside [0, T]; for paged states also that every page that
+// a sequence reads or writes lies in the pool). A bad offset list empties every
+// sequence, a bad table row its own; both set the status word.
+__global__ void __launch_bounds__(512) linear_records_kernel(const __grid_constant__ LinearProblem p,
+                                                             int4* recs) {
+  pdl_wait();
+  const int tid = threadIdx.x;
+  bool bad = false;
+  for (int i = tid; i < p.N_seq; i += 512) {
+    const int x = p.cu[i], y = p.cu[i + 1];
+    bad |= x < 0 || y < x || y > p.T;
+  }
+  bad = __syncthreads_or(bad);
+  bool any = bad;
+  for (int i = tid; i < p.N_seq; i += 512) {
+    int4 r = make_int4(0, 0, i, 0);
+    if (!bad) {
+      r.x = p.cu[i];
+      r.y = p.cu[i + 1] - r.x;
+      if (p.pool && r.y > 0) {
+        r.w = p.ctx[i];
+        bool off = r.w < 0;
+        if (!off)
+          for (int64_t j = r.w > 0 ? (r.w - 1) / p.block : 0; j <= ((int64_t)r.w + r.y - 1) / p.block; ++j)
+            off |= page_of(p, i, j) < 0;
+        if (off) r.y = 0;
+        any |= off;
+      }
+    }
+    recs[i] = r;
+  }
+  any = __syncthreads_or(any);
+  if (tid == 0 && p.status) *p.status = any ? kDevBadSeqlens : kDevOk;
+}
+
+template <typename T, int VEC, int R>
+cudaError_t go(const WalkArgs& a, int smem) {
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(linear_walk_kernel<T, VEC, R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t grid = (int64_t)a.p.N_seq * a.p.HV * a.slices;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(linear_walk_kernel<T, VEC, R>, dim3((unsigned)grid), dim3(kThreads), smem,
+                    a.p.stream, a);
+}
+
+template <typename T>
+cudaError_t pick(const LinearProblem& p, const int4* recs) {
+  WalkArgs a{p, recs, 0, 0};
+  const bool vec = p.V % 4 == 0;  // 16-byte state columns (the API checks the base's alignment)
+  int VS = vec ? 128 : 32;
+  while (vec && VS > 32 && (VS / 2 >= p.V ||
+         (int64_t)p.N_seq * p.HV * cdiv(p.V, VS) < 2 * sm_count()))
+    VS /= 2;
+  a.VS = VS;
+  a.slices = (int)cdiv(p.V, VS);
+  const int RG = kThreads / (vec ? VS / 4 : VS), rows = (int)cdiv(p.K, RG);
+  const int smem = (2 * kStep * p.K + kStep * VS + 2 * kStep + 16 * VS) * 4;
+  if (!vec) return rows <= 16 ? go<T, 1, 16>(a, smem) : go<T, 1, 32>(a, smem);
+  if (rows <= 4) return go<T, 4, 4>(a, smem);
+  if (rows <= 8) return go<T, 4, 8>(a, smem);
+  if (rows <= 16) return go<T, 4, 16>(a, smem);
+  return go<T, 4, 32>(a, smem);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_records(const LinearProblem& p, int4* recs) {
+  return launch_pdl(linear_records_kernel, dim3(1), dim3(512), 0, p.stream, p, recs);
+}
+
+cudaError_t launch_linear_walk(const LinearProblem& p, const int4* recs) {
+  if (p.N_seq == 0) return cudaSuccess;
+  switch (p.dt) {
+    case GDP_BF16: return pick<__nv_bfloat16>(p, recs);
+    case GDP_F16: return pick<__half>(p, recs);
+    default: return pick<float>(p, recs);
+  }
+}
+
+}  // namespace gdp
