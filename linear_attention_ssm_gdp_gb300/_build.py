@@ -32,6 +32,7 @@ UNITS = {
     "recurrent.cu": [],
     "noalloc.cu": [],
     "linear_api.cu": [],
+    "linear_chunk.cu": [],
     "linear_token.cu": [],
     "block_plan.cu": [],
     "group_norm.cu": [],

@@ -1,6 +1,8 @@
 // C ABI entry points of the linear-attention operators: argument validation and
 // dispatch. Every validation runs before anything is launched; nothing here
 // allocates device memory or synchronises.
+#include <algorithm>
+
 #include "linear_internal.cuh"
 
 using namespace gdp;
@@ -14,10 +16,11 @@ struct LinearWs {
   size_t status = 0, recs = 0, total = 0;
 };
 
-LinearWs linear_ws(int N_seq) {
+LinearWs linear_ws(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
   LinearWs w;
   w.recs = kAlign;
   w.total = align_up(w.recs + (size_t)N_seq * sizeof(int4));
+  if (linear_tc_shape(K, V, dt)) w.total = std::max(w.total, linear_tc_workspace(N_seq, B, T, HV, K, V));
   return w;
 }
 
@@ -57,12 +60,14 @@ gdp_status chunk(LinearProblem& p, const int64_t* strides, void* workspace, size
   const gdp_status st = check(p, strides);
   if (st != GDP_OK) return st;
   if (p.cu ? p.B != 1 : p.N_seq != p.B) return GDP_ERR_INVALID_ARG;
-  const LinearWs w = linear_ws(p.N_seq);
+  const LinearWs w = linear_ws(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || bytes < w.total)
     return GDP_ERR_WORKSPACE;
   set_strides(p, strides);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int32_t*>(ws + w.status);
+  if ((int64_t)p.B * p.T > 0 && linear_tc_ok(p))
+    return launch_linear_tc(p, ws) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
   int4* recs = nullptr;
   if (p.cu) {
     recs = reinterpret_cast<int4*>(ws + w.recs);
@@ -80,7 +85,7 @@ extern "C" {
 size_t gdp_linear_chunk_fwd_workspace_size(int B, int T, int N_seq, int H, int HV, int K, int V,
                                            gdp_dtype dt) {
   if (!sizes_ok(N_seq, B, T, H, HV, K, V) || K > 256 || V > 1024 || !dtype_ok(dt)) return 0;
-  return linear_ws(N_seq).total;
+  return linear_ws(N_seq, B, T, HV, K, V, dt).total;
 }
 
 gdp_status gdp_linear_chunk_fwd(const void* q, const void* k, const void* v, const int64_t* strides,

@@ -44,4 +44,11 @@ cudaError_t launch_linear_records(const LinearProblem& p, int4* recs);
 // recs: null for dense batches.
 cudaError_t launch_linear_walk(const LinearProblem& p, const int4* recs);
 
+// The chunked form on the tensor cores: whether sizes and type fit it, whether the
+// tensors' addresses and strides do too (16-byte steps, for TMA), its workspace.
+bool linear_tc_shape(int K, int V, gdp_dtype dt);
+bool linear_tc_ok(const LinearProblem& p);
+size_t linear_tc_workspace(int N_seq, int B, int T, int HV, int K, int V);
+cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws);
+
 }  // namespace gdp

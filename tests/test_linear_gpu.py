@@ -97,6 +97,23 @@ def test_chunk(gdp, B, T, H, HV, K, V, dtype, decay, packed):
     assert err(fs, after[-1]) <= TOL_S
 
 
+@pytest.mark.parametrize("B,T,H,HV,K,V", [(10, 1100, 8, 16, 128, 128), (170, 700, 1, 1, 64, 64), (1, 9000, 1, 2, 128, 128)])
+def test_chunk_long(gdp, B, T, H, HV, K, V):
+    """Many chunks per sequence, more sequences than SMs, several items per CTA: the last
+    tokens and the final states against the walk over the last stretch from the state that
+    the call itself gives there, and the first tokens against the walk."""
+    q, k, v, g, s0 = inputs(B, T, H, HV, K, V, BF, "token", seed=1)
+    o, fs = gdp.gdp_linear_chunk_fwd(q, k, v, g, initial_state=s0)
+    cut = T - 40  # inside a chunk
+    o1, mid = gdp.gdp_linear_chunk_fwd(q[:, :cut], k[:, :cut], v[:, :cut], g[:, :cut].contiguous(), initial_state=s0)
+    few = [0, B // 2, B - 1]
+    ro, _ = walk(*(x[few, :70] for x in (q, k, v, g)), s0[few], K ** -0.5)
+    assert o_ok(o[few, :70], ro) and o_ok(o1[few, :70], ro)
+    ro, after = walk(*(x[few, cut:] for x in (q, k, v, g)), mid[few], K ** -0.5)
+    assert o_ok(o[few, cut:], ro) and err(fs[few], after[-1]) <= TOL_S
+    assert torch.equal(o[:, :cut - cut % 64], o1[:, :cut - cut % 64]) or o_ok(o1, o[:, :cut])
+
+
 @pytest.mark.parametrize("K,V,dtype", [(128, 128, BF), (64, 64, BF), (32, 48, F32), (64, 64, FP16)])
 def test_chunk_packed_sequences(gdp, K, V, dtype):
     """Empty, one-token and ragged sequences; tokens outside every sequence stay
