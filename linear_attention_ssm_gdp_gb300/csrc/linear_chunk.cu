@@ -19,16 +19,19 @@
 // for the same reason. Decay exponents are differences of compensated prefix sums, so
 // a strong decay earlier in the chunk costs no digits.
 //
-// What bounds it: q, k, v, o are 1 KB per token and head against 0.33 MFLOP of
-// tensor work as laid out above, so HBM, if the steps of a chunk overlap. Nothing
-// in the state's chain depends on the state but one multiply-add per element
-// (U does not), so a CTA is split into groups that meet at mbarriers and work on
-// neighbouring chunks at the same time:
-//     warps 0-7   state: v' for the next U, the state update, S as bf16
-//     warps 8-11  output: o = e^{Gam_t} INTER + INTRA, stores
+// What bounds it: q, k, v, o are 64 KB per chunk and head, 1.5 us of an SM's share of HBM.
+// A product with both operands in shared memory runs at that memory's 128 bytes a clock
+// ((A + B) / 128 cycles, measured), more than the tensor pipe needs, so the operands that
+// are made on chip (S, v') live in tensor memory, where they cost none of it: about 2300
+// cycles of shared memory a chunk with both there, 3200 without. Nothing in the state's
+// chain depends on the state but one multiply-add per element (U does not), so a CTA is
+// split into groups that meet at mbarriers and work on neighbouring chunks at once:
+//     warps 0-7   the state update, S as bf16; o = e^{Gam_t} INTER + INTRA, stores
+//     warps 8-11  v' of the next chunk
 //     warps 12,13 scores: P
-//     warp 14     TMA loads, decays of the chunk, rows outside the sequence zeroed
-//     warp 15     one thread issues each product as soon as its operands are there
+//     warp 14     decays of the chunk, rows outside the sequence zeroed
+//     warp 15     one thread issues each product as soon as its operands are there, and the
+//                 TMA loads as stages come free
 //
 // Sequences are cut into segments when there are too few (sequence, head) pairs to
 // fill the GPU: a first launch of the same kernel without its output half (OUT =
@@ -156,7 +159,8 @@ struct Item {
 };
 
 // Item `it` of the launch, value slices of a head and heads of a sequence side by side.
-__device__ __forceinline__ bool get_item(const ChunkArgs& a, int it, Item& x) {
+// (Not inlined: the roles' loops together have to fit the instruction cache.)
+__device__ __noinline__ bool get_item(const ChunkArgs& a, int it, Item& x) {
   const int slice = it % a.slices, rest = it / a.slices;
   x.hv = rest % a.p.HV;
   x.h = x.hv / (a.p.HV / a.p.H);
@@ -204,11 +208,13 @@ struct Sync {
   volatile int* dead;  // a wait of this CTA ran out: everybody leaves
   int* status;
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_test(bar, parity)) {
+    uint64_t t0 = 0;
+    for (int i = 0; !mbar_test(bar, parity); ++i) {
+      if ((i & 15) != 15) continue;
       if (*dead) return false;
-      if (globaltimer_ns() - t0 > kWaitBudgetNs) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitBudgetNs) {
         if (status) atomicExch(status, kDevTimeout);
         *dead = 1;
         return false;
@@ -222,10 +228,10 @@ struct Sync {
   }
 };
 
-// Barrier over the 128 output threads that combines a flag.
-__device__ __forceinline__ bool output_and(bool pred) {
+// Barrier over the 256 state threads that combines a flag.
+__device__ __forceinline__ bool state_and(bool pred) {
   uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, 128, p;\n"
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, 256, p;\n"
                " selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r) : "r"((uint32_t)pred) : "memory");
   return r != 0;
 }
@@ -233,24 +239,24 @@ __device__ __forceinline__ bool output_and(bool pred) {
 // ------------------------------------------------------------------ shared memory
 template <int KD, bool OUT>
 struct Lay {
-  static constexpr int NST = OUT ? 2 : 3;               // stages of q, k, v
+  static constexpr int NST = 3;                         // stages of q, k, v
   static constexpr int KH = KD / 64;                    // 64-column halves of q and k
   static constexpr int QK = KH * 16384;                 // [q | k] by half, 64 rows of 128 bytes each
   static constexpr int STG = QK + 16384;                // then v, two halves
-  static constexpr int VP = NST * STG;                  // v': three parts
-  static constexpr int S = VP + 3 * 16384;              // state as bf16, [v][k] by half
-  static constexpr int P = S + (OUT ? KH * 16384 : 0);  // scores, two buffers
+  static constexpr int P = NST * STG;                   // scores, two buffers
   static constexpr int O = P + (OUT ? 2 * 8192 : 0);    // output tile, two halves
   static constexpr int G = O + (OUT ? 16384 : 0);       // decays, four slots
   static constexpr int GS = 272 * 4;                    // hi2, lo2, wend, ein [64] each, e^Gam hi, lo
   static constexpr int BAR = G + 4 * GS;
   static constexpr int BYTES = BAR + 256 + 1024;
 };
-// full, ready, free by stage; scores, P, O, O read by parity; S, v' and U
-enum { B_FULL = 0, B_READY = 3, B_FREE = 6, B_QK = 9, B_P = 11, B_O = 13, B_OREAD = 15, B_S = 17, B_V = 18, B_U = 19, B_N = 20 };
+// full, ready, free by stage; P and INTRA by parity; the rest single
+enum {
+  B_FULL = 0, B_READY = 3, B_FREE = 6, B_P = 9, B_A = 11, B_QK = 13, B_SREAD, B_I, B_OREAD, B_S, B_V, B_U, B_UREAD, B_N
+};
 
-// TMEM columns: scores [2][64], INTER and INTRA [2][64] each, U [KD]
-constexpr uint32_t T_QK = 0, T_INTER = 128, T_INTRA = 256, T_U = 384;
+// TMEM columns: scores [64], INTER and INTRA [64] each, U [KD], S [KD / 2], v' [3][32]
+constexpr uint32_t T_QK = 0, T_INTER = 64, T_INTRA = 128, T_U = 192, T_S = 320, T_V = 384;
 
 template <int KD, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + B_N);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_total = reinterpret_cast<int*>(s_tmem + 2);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const LinearProblem& p = a.p;
 
   if (warp == 0) {
@@ -274,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   if (tid == 32) {
     for (int i = 0; i < B_N; ++i) {
       int n = 1;
-      if (i >= B_P && i < B_O) n = 2;      // score warps
-      if (i >= B_OREAD && i < B_S) n = 4;  // output warps
-      if (i == B_S || i == B_V) n = 8;     // state warps
+      if ((i >= B_P && i < B_A) || i == B_SREAD) n = 2;              // score warps
+      if (i == B_OREAD || i == B_S || i == B_UREAD) n = 8;           // state warps
+      if (i == B_V) n = 4;                                           // v' warps
       mbar_init(&bars[i], n);
     }
     fence_mbar_init();
@@ -316,23 +322,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   const int K = p.K, V = p.V;
 
   if (warp < 8) {
-    // ---------------------------------------------------------------- state
+    // ---------------------------------------------------------------- state, output
     constexpr int NC = KD / 2;  // state columns (k) per thread
-    const int quarter = warp & 3, cb = (warp >> 2) * NC;
+    const int quarter = warp & 3, half = warp >> 2, cb = half * NC;
     const int row = quarter * 32 + lane;  // value column of the slice
-    const uint32_t t_u = tmem + ((uint32_t)(quarter * 32) << 16) + T_U + cb;
+    const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16);
+    // the thread's 16-bit column of the output tile: row t's 16-byte chunks are permuted by t % 8
+    uint8_t* ot = sm + L::O + (row >> 6) * 8192 + half * 4096 + (row & 7) * 2;
+    const uint32_t oc = (row & 63) >> 3;
     float s[NC];
     int n = 0;
     bool ok = true;
-    for (int kk = 0; ok; ++kk) {
+    for (int kk = 0; ok && (int64_t)kk * gridDim.x < a.items; ++kk) {
       const int it = nth_item(kk);
-      if ((int64_t)kk * gridDim.x >= a.items) break;
-      Item x;
-      if (it >= a.items || !get_item(a, it, x) || skip<OUT>(x)) continue;
+      Item got;
+      if (it >= a.items || !get_item(a, it, got) || skip<OUT>(got)) continue;
+      const Item x = got;
       const bool von = x.v0 + row < V;
       const int64_t page_sz = (int64_t)K * V, at = (int64_t)x.hv * page_sz + x.v0 + row;
-      auto page = [&](int64_t end) {  // page of the state after token end - 1
-        return p.pool + (int64_t)p.tables[(int64_t)x.r.seq * p.width + (end - 1) / p.block] * p.HV * page_sz;
+      auto page = [&](uint32_t end) {  // page of the state after token end - 1
+        return p.pool + (int64_t)p.tables[(int64_t)x.r.seq * p.width + (end - 1) / (uint32_t)p.block] * p.HV * page_sz;
       };
       const float* src = nullptr;
       if (OUT) {
@@ -342,81 +351,44 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         else if (p.pool) src = x.r.pos0 > 0 && x.r.n > 0 ? page(x.r.pos0) : nullptr;
         else if (p.s0) src = p.s0 + (int64_t)x.r.seq * p.HV * page_sz;
       }
+      {
+        const float* q = src ? src + at + (int64_t)cb * V : nullptr;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        s[c] = src && von && cb + c < K ? __ldcg(src + at + (int64_t)(cb + c) * V) : 0.f;
-      auto store = [&](float* dst) {
-        if (von)
+        for (int c = 0; c < NC; ++c, q += V) s[c] = src && von && cb + c < K ? __ldcg(q) : 0.f;
+      }
+      auto publish = [&] {  // the state as the A operand of INTER (whose last product is done)
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (cb + c < K) dst[at + (int64_t)(cb + c) * V] = s[c];
-      };
-      auto publish = [&] {  // the state as the A operand of INTER
+        for (int q = 0; q < NC / 32; ++q) {
+          uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < NC / 8; ++j) {
-          const int k8 = cb + 8 * j;
-          uint4 w;
-          w.x = cvt2(s[8 * j], s[8 * j + 1]);
-          w.y = cvt2(s[8 * j + 2], s[8 * j + 3]);
-          w.z = cvt2(s[8 * j + 4], s[8 * j + 5]);
-          w.w = cvt2(s[8 * j + 6], s[8 * j + 7]);
-          *reinterpret_cast<uint4*>(sm + L::S + (k8 >> 6) * 16384 + sw128_offset(row, (k8 & 63) * 2)) = w;
+          for (int e = 0; e < 16; ++e) w[e] = cvt2(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]);
+          GDP_TMEM_ST16(lb + T_S + cb / 2 + 16 * q, w);
         }
-        fence_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_S]);
       };
       if (OUT && x.chunks > 0) publish();
       float2 wseg = make_float2(1.f, 0.f);
       for (int c = 0; c < x.chunks; ++c, ++n) {
-        const int st = n % L::NST;
-        if (!(ok = tiles(n))) break;
-        const float* g = gates(n);
-        {  // v' = wend v in three bf16 parts: eight lanes to a row of 128 bytes
-          const uint8_t* vt = sm + st * L::STG + L::QK;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int i = (tid >> 3) + 32 * (m >> 1);
-            const uint32_t o = (m & 1) * 8192 + sw128_offset(i, (tid & 7) * 16);
-            const uint4 u = *reinterpret_cast<const uint4*>(vt + o);
-            const f2 w = pk2(g[128 + i], g[128 + i]);
-            const uint32_t e[4] = {u.x, u.y, u.z, u.w};
-            uint32_t h[4], md[4], l[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              f2 y = mul2(wide(e[q]), w);
-              float2 f = upk2(y);
-              h[q] = cvt2(f.x, f.y);
-              y = sub2(y, wide(h[q]));
-              f = upk2(y);
-              md[q] = cvt2(f.x, f.y);
-              f = upk2(sub2(y, wide(md[q])));
-              l[q] = cvt2(f.x, f.y);
-            }
-            *reinterpret_cast<uint4*>(sm + L::VP + o) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(sm + L::VP + 16384 + o) = make_uint4(md[0], md[1], md[2], md[3]);
-            *reinterpret_cast<uint4*>(sm + L::VP + 32768 + o) = make_uint4(l[0], l[1], l[2], l[3]);
-          }
-        }
-        const float wh = g[256], wl = g[257];
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_V]);
-        if (!OUT) {  // the segment's whole decay, pair by pair
-          const float ph = wseg.x * wh;
-          const float pl = fmaf(wseg.x, wh, -ph) + (wseg.x * wl + wseg.y * wh);
-          wseg.x = ph + pl;
-          wseg.y = pl - (wseg.x - ph);
-        }
-        if (!(ok = sy.wait_warp(&bars[B_U], n & 1))) break;
+        // a failed wait leaves through the barrier below, with the whole group
+        ok = sy.wait_warp(&bars[B_U], n & 1);
+        if (!OUT && !ok) break;
         tc_fence_after();
+        const float* g = gates(n);
+        const float wh = g[256], wl = g[257];
         const f2 wh2 = pk2(wh, wh), wl2 = pk2(wl, wl);
 #pragma unroll
         for (int q = 0; q < NC / 32; ++q) {
           uint32_t r[32];
-          GDP_TMEM_LD32(t_u + 32 * q, r);
+          GDP_TMEM_LD32(lb + T_U + cb + 32 * q, r);
           tmem_wait_ld();
+          if (q == NC / 32 - 1) {  // the next U may overwrite this one
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_UREAD]);
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float* d = s + 32 * q + e;
@@ -427,96 +399,141 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           }
         }
         const bool more = c + 1 < x.chunks;
-        if (OUT && more) publish();
-        if (OUT && p.pool) {
-          const int64_t end = (int64_t)x.r.pos0 - x.off + (int64_t)(c + 1) * C;
-          if (!more ? x.r.last || end % p.block == 0 : end % p.block == 0)
-            store(page(min(end, (int64_t)x.r.pos0 + x.r.n)));
+        float* dst = nullptr;  // where the state after this chunk is kept
+        if (!OUT) {            // the segment's whole decay, pair by pair
+          const float ph = wseg.x * wh;
+          const float pl = fmaf(wseg.x, wh, -ph) + (wseg.x * wl + wseg.y * wh);
+          wseg.x = ph + pl;
+          wseg.y = pl - (wseg.x - ph);
+          if (!more) {
+            dst = a.segS + (int64_t)x.r.id * p.HV * page_sz;
+            if (row == 0 && cb == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
+          }
+        } else if (p.pool) {
+          const uint32_t end = (uint32_t)(x.r.pos0 - x.off) + (uint32_t)(c + 1) * C;
+          if ((!more && x.r.last) || end % (uint32_t)p.block == 0) dst = page(min(end, (uint32_t)x.r.pos0 + (uint32_t)x.r.n));
+        } else if (!more && x.r.last && p.sT) {
+          dst = p.sT + (int64_t)x.r.seq * p.HV * page_sz;
+        }
+        if (OUT) {
+        ok = sy.wait_warp(&bars[B_I], n & 1) && ok;
+        if (more && ok) publish();
+        ok = sy.wait_warp(&bars[B_A + (n & 1)], (n >> 1) & 1) && ok;
+        const float* ein = g + 192 + 32 * half;
+        uint32_t out[16];
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t r[16], w[16];
+            GDP_TMEM_LD16(lb + T_INTER + 32 * half + 16 * q, r);
+            GDP_TMEM_LD16(lb + T_INTRA + 32 * half + 16 * q, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 g4 = *reinterpret_cast<const float4*>(ein + 16 * q + e);
+              const float2 f = upk2(fma2(pk2(g4.x, g4.y), pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                         pk2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]))));
+              const float2 h = upk2(fma2(pk2(g4.z, g4.w), pk2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])),
+                                         pk2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]))));
+              out[8 * q + e / 2] = cvt2(f.x, f.y);
+              out[8 * q + e / 2 + 1] = cvt2(h.x, h.y);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_OREAD]);
+        }
+        // the previous chunk's stores have read the tile
+        if (tid == 0) tma_store_wait_read();
+        if (!(ok = state_and(ok))) break;
+#pragma unroll
+        for (int t = 0; t < 32; t += 2) {
+          const uint32_t o2 = out[t >> 1];
+          *reinterpret_cast<uint16_t*>(ot + t * 128 + ((oc ^ (t & 7)) << 4)) = (uint16_t)o2;
+          *reinterpret_cast<uint16_t*>(ot + (t + 1) * 128 + ((oc ^ ((t + 1) & 7)) << 4)) = (uint16_t)(o2 >> 16);
+        }
+        // rows of the tile inside the sequence
+        const int base = x.r.t0 - x.off + c * C;
+        const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
+        const bool whole = lo == 0 && (hi == C || (!a.recs && x.r.last));
+        if (whole) {  // rows past a dense batch's end are clipped by the map
+          fence_async_smem();
+          state_and(true);
+          if (tid == 0) {
+            tma_store_4d(&map_o, sm + L::O, x.v0, x.hv, base, x.b);
+            if (x.v0 + 64 < V) tma_store_4d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b);
+            tma_store_commit();
+          }
+        } else {
+          state_and(true);
+          bf16* og = static_cast<bf16*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
+          const int j = tid & 15, c8 = 8 * j;  // 16-byte piece of the row (V is a multiple of 8)
+          if (x.v0 + c8 < V)
+            for (int t = lo + (tid >> 4); t < hi; t += 16)
+              *reinterpret_cast<uint4*>(og + (int64_t)t * p.HV * V + c8) =
+                  *reinterpret_cast<const uint4*>(sm + L::O + (j >> 3) * 8192 + t * 128 + (((j & 7) ^ (t & 7)) << 4));
+          // the next chunk's barrier orders these reads before its writes
+        }
+        }
+        if (dst && von) {
+          dst += at + (int64_t)cb * V;
+#pragma unroll
+          for (int c2 = 0; c2 < NC; ++c2, dst += V)
+            if (cb + c2 < K) *dst = s[c2];
         }
       }
       if (!ok) break;
-      if (!OUT) {
-        store(a.segS + (int64_t)x.r.id * p.HV * page_sz);
-        if (row == 0 && cb == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
-      } else if (!p.pool && p.sT && x.r.last) {
-        store(p.sT + (int64_t)x.r.seq * p.HV * page_sz);
+      if (OUT && x.chunks == 0 && p.sT && von && x.r.last) {  // an empty sequence keeps its state
+        float* dst = p.sT + (int64_t)x.r.seq * p.HV * page_sz + at;
+        src += src ? at : 0;
+#pragma unroll 1
+        for (int k = cb; k < min(cb + NC, K); ++k) dst[(int64_t)k * V] = src ? __ldcg(src + (int64_t)k * V) : 0.f;
       }
     }
+    if (OUT && tid == 0) tma_store_wait_all();
   } else if (warp < 12) {
-    // ---------------------------------------------------------------- output
-    if (OUT) {
-      const int quarter = warp & 3, v = quarter * 32 + lane;
-      const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16);
-      uint8_t* ot = sm + L::O + (v >> 6) * 8192;
-      const uint32_t vb = (v & 63) * 2, vchunk = vb >> 4, vin = vb & 15;
-      int n = 0;
-      bool ok = true;
-      for (int kk = 0; ok && (int64_t)kk * gridDim.x < a.items; ++kk) {
-        const int it = nth_item(kk);
-        Item x;
-        if (it >= a.items || !get_item(a, it, x)) continue;
-        for (int c = 0; c < x.chunks; ++c, ++n) {
-          const int b = n & 1;
-          ok = sy.wait_warp(&bars[B_O + b], (n >> 1) & 1);
-          const float* ein = gates(n) + 192;
-          uint32_t out[32];
-          if (ok) {
-            tc_fence_after();
+    // ---------------------------------------------------------------- v'
+    const int v = (warp & 3) * 32 + lane;
+    const uint32_t lb = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t vc = (v & 63) >> 3, vo = L::QK + (v >> 6) * 8192 + (v & 7) * 2;
+    for (int n = 0; n < total; ++n) {
+      if (!tiles(n)) break;
+      const uint8_t* vt = sm + (n % L::NST) * L::STG + vo;
+      const float* g = gates(n) + 128;
+      uint32_t h[32], m[32], l[32];  // two positions to a word
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t r[32], w[32];
-              GDP_TMEM_LD32(lb + T_INTER + 64 * b + 32 * q, r);
-              GDP_TMEM_LD32(lb + T_INTRA + 64 * b + 32 * q, w);
-              tmem_wait_ld();
+      for (int i = 0; i < C; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(g + i);
+        uint32_t e[4];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(ein + 32 * q + e);
-                const float2 f = upk2(fma2(pk2(g4.x, g4.y), pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                           pk2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]))));
-                const float2 h = upk2(fma2(pk2(g4.z, g4.w), pk2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])),
-                                           pk2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]))));
-                out[16 * q + e / 2] = cvt2(f.x, f.y);
-                out[16 * q + e / 2 + 1] = cvt2(h.x, h.y);
-              }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_OREAD + b]);
-          }
-          // the previous chunk's stores have read the tile
-          if (warp == 8 && lane == 0) tma_store_wait_read();
-          if (!(ok = output_and(ok))) break;
+        for (int j = 0; j < 4; ++j)
+          e[j] = (uint32_t)*reinterpret_cast<const uint16_t*>(vt + (i + j) * 128 + ((vc ^ ((i + j) & 7)) << 4)) << 16;
 #pragma unroll
-          for (int t = 0; t < 64; t += 2) {
-            const uint32_t o2 = out[t >> 1];
-            *reinterpret_cast<uint16_t*>(ot + t * 128 + ((vchunk ^ (t & 7)) << 4) + vin) = (uint16_t)o2;
-            *reinterpret_cast<uint16_t*>(ot + (t + 1) * 128 + ((vchunk ^ ((t + 1) & 7)) << 4) + vin) = (uint16_t)(o2 >> 16);
-          }
-          // rows of the tile inside the sequence
-          const int base = x.r.t0 - x.off + c * C;
-          const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
-          const bool whole = lo == 0 && (hi == C || (!a.recs && x.r.last));
-          if (whole) {  // rows past a dense batch's end are clipped by the map
-            fence_async_smem();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (warp == 8 && lane == 0) {
-              tma_store_4d(&map_o, sm + L::O, x.v0, x.hv, base, x.b);
-              if (x.v0 + 64 < V) tma_store_4d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b);
-              tma_store_commit();
-            }
-          } else {
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            bf16* og = static_cast<bf16*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
-            const int j = tid & 15, c8 = 8 * j;  // 16-byte piece of the row (V is a multiple of 8)
-            if (x.v0 + c8 < V)
-              for (int t = lo + ((tid - 256) >> 4); t < hi; t += 8)
-                *reinterpret_cast<uint4*>(og + (int64_t)t * p.HV * V + c8) =
-                    *reinterpret_cast<const uint4*>(sm + L::O + (j >> 3) * 8192 + t * 128 + (((j & 7) ^ (t & 7)) << 4));
-            // the next chunk's barrier orders these reads before its writes
-          }
+        for (int j = 0; j < 2; ++j) {
+          f2 y = mul2(pk2(__uint_as_float(e[2 * j]), __uint_as_float(e[2 * j + 1])),
+                      j ? pk2(w.z, w.w) : pk2(w.x, w.y));
+          float2 f = upk2(y);
+          h[i / 2 + j] = cvt2(f.x, f.y);
+          y = sub2(y, wide(h[i / 2 + j]));
+          f = upk2(y);
+          m[i / 2 + j] = cvt2(f.x, f.y);
+          f = upk2(sub2(y, wide(m[i / 2 + j])));
+          l[i / 2 + j] = cvt2(f.x, f.y);
         }
       }
-      if (warp == 8 && lane == 0) tma_store_wait_all();
+      if (n > 0 && !sy.wait_warp(&bars[B_U], (n - 1) & 1)) break;  // U(n - 1) has read its v'
+      tc_fence_after();
+      GDP_TMEM_ST16(lb + T_V, h);
+      GDP_TMEM_ST16(lb + T_V + 16, (h + 16));
+      GDP_TMEM_ST16(lb + T_V + 32, m);
+      GDP_TMEM_ST16(lb + T_V + 48, (m + 16));
+      GDP_TMEM_ST16(lb + T_V + 64, l);
+      GDP_TMEM_ST16(lb + T_V + 80, (l + 16));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_V]);
     }
   } else if (warp < 14) {
     // ---------------------------------------------------------------- scores
@@ -526,13 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       const f2 sc2 = pk2(p.scale, p.scale);
       for (int n = 0; n < total; ++n) {
         const int b = n & 1;
-        if (!sy.wait_warp(&bars[B_QK + b], (n >> 1) & 1)) break;
-        if (n >= 2 && !sy.wait_warp(&bars[B_O + b], ((n >> 1) - 1) & 1)) break;  // INTRA has read the buffer
+        if (!sy.wait_warp(&bars[B_QK], n & 1)) break;
         tc_fence_after();
+        if (n >= 2 && !sy.wait_warp(&bars[B_A + b], ((n >> 1) - 1) & 1)) break;  // INTRA has read the buffer
         const float* g = gates(n);
         const f2 hi = pk2(g[t], g[t]), lo = pk2(g[64 + t], g[64 + t]);
         uint8_t* pt = sm + L::P + b * 8192;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t pk[16];
           if (q == 1 && warp == 12) {  // columns past every row of this warp
@@ -540,21 +557,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
             for (int e = 0; e < 16; ++e) pk[e] = 0;
           } else {
             uint32_t r[32];
-            GDP_TMEM_LD32(lb + T_QK + 64 * b + 32 * q, r);
+            GDP_TMEM_LD32(lb + T_QK + 32 * q, r);
             tmem_wait_ld();
+            if (q == warp - 12) {  // this warp's last scores are read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_SREAD]);
+            }
+            const int ti = t - 32 * q;  // columns i <= ti are this row's
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const int i = 32 * q + e;
-              const float4 h4 = *reinterpret_cast<const float4*>(g + i);
-              const float4 l4 = *reinterpret_cast<const float4*>(g + 64 + i);
+              const float4 h4 = *reinterpret_cast<const float4*>(g + 32 * q + e);
+              const float4 l4 = *reinterpret_cast<const float4*>(g + 64 + 32 * q + e);
               const float2 x0 = upk2(add2(sub2(hi, pk2(h4.x, h4.y)), sub2(lo, pk2(l4.x, l4.y))));
               const float2 x1 = upk2(add2(sub2(hi, pk2(h4.z, h4.w)), sub2(lo, pk2(l4.z, l4.w))));
               const float2 y0 = upk2(mul2(mul2(pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2),
                                           pk2(ex2_approx(x0.x), ex2_approx(x0.y))));
               const float2 y1 = upk2(mul2(mul2(pk2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2),
                                           pk2(ex2_approx(x1.x), ex2_approx(x1.y))));
-              pk[e / 2] = cvt2(i <= t ? y0.x : 0.f, i + 1 <= t ? y0.y : 0.f);
-              pk[e / 2 + 1] = cvt2(i + 2 <= t ? y1.x : 0.f, i + 3 <= t ? y1.y : 0.f);
+              pk[e / 2] = cvt2(e <= ti ? y0.x : 0.f, e + 1 <= ti ? y0.y : 0.f);
+              pk[e / 2 + 1] = cvt2(e + 2 <= ti ? y1.x : 0.f, e + 3 <= ti ? y1.y : 0.f);
             }
           }
 #pragma unroll
@@ -563,50 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
                 make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
         }
         fence_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_P + b]);
       }
     }
   } else if (warp == 14) {
-    // ---------------------------------------------------------------- loads, decays
-    int n = 0, issued = 0;
+    // ---------------------------------------------------------------- decays
+    int n = 0;
     bool ok = true;
-    // walk of the loads, up to a stage ahead of the decays
-    int lk = -1, lc = 0;
-    Item lx;
-    lx.chunks = 0;
-    auto load_next = [&] {  // lane 0: the tiles of chunk `issued`
-      while (lc >= lx.chunks) {
-        ++lk;
-        lc = 0;
-        lx.chunks = 0;
-        const int it = nth_item(lk);
-        if (it >= a.items || !get_item(a, it, lx) || skip<OUT>(lx)) lx.chunks = 0;
-      }
-      const int st = issued % L::NST, t = lx.r.t0 - lx.off + lc * C;
-      if (issued >= L::NST && !sy.wait(&bars[B_FREE + st], (issued / L::NST - 1) & 1)) return false;
-      const bool two = lx.v0 + 64 < V;
-      uint8_t* tile = sm + st * L::STG;
-      uint64_t* bar = &bars[B_FULL + st];
-      mbar_expect_tx(bar, 8192 * ((OUT ? 2 : 1) * L::KH + (two ? 2 : 1)));
-#pragma unroll
-      for (int hh = 0; hh < L::KH; ++hh) {
-        if (OUT) tma_load_4d(tile + hh * 16384, &map_q, 64 * hh, lx.h, t, lx.b, bar);
-        tma_load_4d(tile + hh * 16384 + 8192, &map_k, 64 * hh, lx.h, t, lx.b, bar);
-      }
-      tma_load_4d(tile + L::QK, &map_v, lx.v0, lx.hv, t, lx.b, bar);
-      if (two) tma_load_4d(tile + L::QK + 8192, &map_v, lx.v0 + 64, lx.hv, t, lx.b, bar);
-      ++lc;
-      ++issued;
-      return true;
-    };
-    if (lane == 0)
-      while (issued < min(L::NST, total)) load_next();
     for (int kk = 0; ok && (int64_t)kk * gridDim.x < a.items; ++kk) {
       const int it = nth_item(kk);
-      Item x;
-      if (it >= a.items || !get_item(a, it, x) || skip<OUT>(x)) continue;
+      Item got;
+      if (it >= a.items || !get_item(a, it, got) || skip<OUT>(got)) continue;
+      const Item x = got;
       const float* gb = !p.g ? nullptr : p.g_token ? p.g + (int64_t)x.b * p.T * p.HV + x.hv : p.g + x.hv;
       auto load = [&](int c, int u) {  // g at position 2 lane + u of chunk c
         const int r = x.r.t0 - x.off + c * C + 2 * lane + u;
@@ -642,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           nx0 = load(c + 1, 0);
           nx1 = load(c + 1, 1);
         }
-        const float2 w = exp_pair(hl, ll);
+        const float2 w = exp_pair(hl, ll), bl = log2e_pair(hl, ll);
         const int base = x.r.t0 - x.off + c * C;
         const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
         float2 b2[2];
@@ -651,8 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         for (int u = 0; u < 2; ++u) {
           const int i = 2 * lane + u;
           b2[u] = log2e_pair(h[u], l[u]);
-          we[u] = i >= lo && i < hi ? expf((hl - h[u]) + (ll - l[u])) : 0.f;
-          ei[u] = p.scale * expf(h[u] + l[u]);
+          // 2^x is good to 2^-22; a rounded exponent matters less the smaller the factor
+          we[u] = i >= lo && i < hi ? ex2_approx((bl.x - b2[u].x) + (bl.y - b2[u].y)) : 0.f;
+          ei[u] = p.scale * ex2_approx(b2[u].x + b2[u].y);
         }
         if (!(ok = sy.wait_warp(&bars[B_FULL + st], (n / L::NST) & 1))) break;
         float* g = gates(n);
@@ -678,73 +670,88 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_READY + st]);
-        // the stage that the chunk before last leaves takes the next tiles
-        int go = 1;
-        if (lane == 0 && n >= 1 && issued < total) go = load_next();
-        if (!(ok = __shfl_sync(0xffffffffu, go, 0))) break;
       }
     }
-    // nothing may still write shared memory when the CTA leaves
-    if (lane == 0)
-      for (int m = max(0, issued - L::NST); m < issued; ++m) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
-      }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ---------------------------------------------------------------- products
     const uint32_t id_qk = idesc_bf16(128, 64, false, false), id_a = idesc_bf16(128, 64, true, false);
-    const uint32_t id_u = idesc_bf16(128, KD, true, true);
-    int nq = OUT ? 0 : total, ni = OUT ? 0 : total, na = OUT ? 0 : total, nu = 0;  // next chunk of each product
+    const uint32_t id_u = idesc_bf16(128, KD, false, true);
+    // next chunk of each product, next stage to give back
+    int nq = OUT ? 0 : total, ni = nq, na = nq, nu = 0, nf = 0;
+    int nl = 0, lk = -1, lc = 0;  // next load: chunk lc of this CTA's item lk
+    Item lx;
+    lx.chunks = 0;
     auto poll_tiles = [&](int n) {
       const uint32_t ph = (n / L::NST) & 1;
       return mbar_poll(&bars[B_READY + n % L::NST], ph) && mbar_poll(&bars[B_FULL + n % L::NST], ph);
     };
-    auto o_read = [&](int n) { return n < 2 || mbar_poll(&bars[B_OREAD + (n & 1)], ((n >> 1) - 1) & 1); };
+    auto before = [&](int bar, int n) { return n == 0 || mbar_poll(&bars[bar], (n - 1) & 1); };
     uint64_t t0 = 0;
     int idle = 0;
-    while (nu < total || na < total) {
+    while (nf < total) {
       bool did = false;
-      if (OUT && ni < total && mbar_poll(&bars[B_S], ni & 1) && poll_tiles(ni) && o_read(ni)) {
-        tc_fence_after();
-        mma_run<KD / 16, false, 16384, 32, 16384, 32>(tmem + T_INTER + 64 * (ni & 1), sdesc_sw128(smb + L::S, 16, 1024),
-                                                      sdesc_sw128(smb + (ni % L::NST) * L::STG, 16, 1024), id_qk);
-        ++ni;
-        if (na >= ni) mma_commit(&bars[B_O + ((ni - 1) & 1)]);
+      if (nl < total && (nl < L::NST || mbar_poll(&bars[B_FREE + nl % L::NST], (nl / L::NST - 1) & 1))) {
+        while (lc >= lx.chunks) {
+          ++lk;
+          lc = 0;
+          const int it = nth_item(lk);
+          if (it >= a.items || !get_item(a, it, lx) || skip<OUT>(lx)) lx.chunks = 0;
+        }
+        const int st = nl % L::NST, t = lx.r.t0 - lx.off + lc * C;
+        const bool two = lx.v0 + 64 < V;
+        uint8_t* tile = sm + st * L::STG;
+        uint64_t* bar = &bars[B_FULL + st];
+        mbar_expect_tx(bar, 8192 * ((OUT ? 2 : 1) * L::KH + (two ? 2 : 1)));
+#pragma unroll
+        for (int hh = 0; hh < L::KH; ++hh) {
+          if (OUT) tma_load_4d(tile + hh * 16384, &map_q, 64 * hh, lx.h, t, lx.b, bar);
+          tma_load_4d(tile + hh * 16384 + 8192, &map_k, 64 * hh, lx.h, t, lx.b, bar);
+        }
+        tma_load_4d(tile + L::QK, &map_v, lx.v0, lx.hv, t, lx.b, bar);
+        if (two) tma_load_4d(tile + L::QK + 8192, &map_v, lx.v0 + 64, lx.hv, t, lx.b, bar);
+        ++lc;
+        ++nl;
         did = true;
       }
-      // U(n) after INTER(n): its commit is also what lets the state warps rewrite S
-      if (nu < ni && nu < total && mbar_poll(&bars[B_V], nu & 1) && poll_tiles(nu)) {
+      if (nu < total && mbar_poll(&bars[B_V], nu & 1) && before(B_UREAD, nu) && poll_tiles(nu)) {
         tc_fence_after();
         const uint64_t kd = sdesc_sw128(smb + (nu % L::NST) * L::STG + 8192, 16384, 1024);
-        mma_run<4, false, 0, 2048, 0, 2048>(tmem + T_U, sdesc_sw128(smb + L::VP + 32768, 8192, 1024), kd, id_u);
-        mma_run<4, true, 0, 2048, 0, 2048>(tmem + T_U, sdesc_sw128(smb + L::VP + 16384, 8192, 1024), kd, id_u);
-        mma_run<4, true, 0, 2048, 0, 2048>(tmem + T_U, sdesc_sw128(smb + L::VP, 8192, 1024), kd, id_u);
+        mma_run_ts<4, false, 0, 2048>(tmem + T_U, tmem + T_V + 64, kd, id_u);
+        mma_run_ts<4, true, 0, 2048>(tmem + T_U, tmem + T_V + 32, kd, id_u);
+        mma_run_ts<4, true, 0, 2048>(tmem + T_U, tmem + T_V, kd, id_u);
         mma_commit(&bars[B_U]);
         ++nu;
-        if (na >= nu) mma_commit(&bars[B_FREE + (nu - 1) % L::NST]);
         did = true;
       }
-      if (OUT && nq < total && nq < na + 2 && poll_tiles(nq)) {  // scores n - 2 have been read: INTRA(n - 2) was issued
+      if (OUT && ni < total && mbar_poll(&bars[B_S], ni & 1) && before(B_OREAD, ni) && poll_tiles(ni)) {
+        tc_fence_after();
+        mma_run_ts<KD / 16, false, 16384, 32>(tmem + T_INTER, tmem + T_S,
+                                              sdesc_sw128(smb + (ni % L::NST) * L::STG, 16, 1024), id_qk);
+        mma_commit(&bars[B_I]);
+        ++ni;
+        did = true;
+      }
+      if (OUT && na < nq && mbar_poll(&bars[B_P + (na & 1)], (na >> 1) & 1) && before(B_OREAD, na)) {
+        tc_fence_after();
+        mma_run<4, false, 0, 2048, 0, 32>(tmem + T_INTRA, sdesc_sw128(smb + (na % L::NST) * L::STG + L::QK, 8192, 1024),
+                                          sdesc_sw128(smb + L::P + (na & 1) * 8192, 16, 1024), id_a);
+        mma_commit(&bars[B_A + (na & 1)]);
+        ++na;
+        did = true;
+      }
+      if (OUT && nq < total && before(B_SREAD, nq) && poll_tiles(nq)) {
         tc_fence_after();
         const uint32_t t = smb + (nq % L::NST) * L::STG;
-        mma_run<KD / 16, false, 16384, 32, 16384, 32>(tmem + T_QK + 64 * (nq & 1), sdesc_sw128(t, 16, 1024),
+        mma_run<KD / 16, false, 16384, 32, 16384, 32>(tmem + T_QK, sdesc_sw128(t, 16, 1024),
                                                       sdesc_sw128(t + 8192, 16, 1024), id_qk);
-        mma_commit(&bars[B_QK + (nq & 1)]);
+        mma_commit(&bars[B_QK]);
         ++nq;
         did = true;
       }
-      if (OUT && na < nq && mbar_poll(&bars[B_P + (na & 1)], (na >> 1) & 1) && o_read(na)) {
-        tc_fence_after();
-        mma_run<4, false, 0, 2048, 0, 32>(tmem + T_INTRA + 64 * (na & 1),
-                                          sdesc_sw128(smb + (na % L::NST) * L::STG + L::QK, 8192, 1024),
-                                          sdesc_sw128(smb + L::P + (na & 1) * 8192, 16, 1024), id_a);
-        ++na;
-        if (ni >= na) mma_commit(&bars[B_O + ((na - 1) & 1)]);
-        if (nu >= na) mma_commit(&bars[B_FREE + (na - 1) % L::NST]);
-        did = true;
-      }
+      for (; nf < min(nu, min(ni, na)); ++nf) mma_commit(&bars[B_FREE + nf % L::NST]);
       if (did) {
         idle = 0;
+        t0 = 0;
       } else if (++idle == 64) {  // every so often the clock
         idle = 0;
         if (*s_dead) break;
@@ -756,7 +763,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           break;
         }
       }
-      if (did) t0 = 0;
+    }
+    // nothing may still write shared memory when the CTA leaves
+    for (int m = max(0, nl - L::NST); m < nl; ++m) {
+      const uint64_t w0 = globaltimer_ns();
+      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - w0 < kWaitBudgetNs) {}
     }
   }
   __syncwarp();

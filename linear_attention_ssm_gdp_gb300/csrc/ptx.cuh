@@ -212,6 +212,41 @@ __device__ __forceinline__ void mma_run(uint32_t d_tmem, uint64_t a0, uint64_t b
                      b0 + (uint64_t)((((kk >> 2) * B_HI) + (kk & 3) * B_LO) >> 4), idesc);
 }
 
+// One elected thread of a converged warp (code under it is known to be one thread's, which
+// lets the compiler issue tcgen05 instructions back to back).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: row r of A in TMEM lane r, K elements packed two to a
+// 32-bit column.
+template <bool ACC>
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// NK of them along K (16 elements, 8 columns of A, a step); B's steps as in mma_run.
+template <int NK, bool ACC0, int B_HI, int B_LO>
+__device__ __forceinline__ void mma_run_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b0,
+                                           uint32_t idesc) {
+  mma_bf16_ts<ACC0>(d_tmem, a_tmem, b0, idesc);
+#pragma unroll
+  for (int kk = 1; kk < NK; ++kk)
+    mma_bf16_ts<true>(d_tmem, a_tmem + 8 * kk,
+                      b0 + (uint64_t)((((kk >> 2) * B_HI) + (kk & 3) * B_LO) >> 4), idesc);
+}
+
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
@@ -281,6 +316,19 @@ __device__ __forceinline__ uint32_t sw64_chunk(uint32_t r, uint32_t j) {
         "=r"(r[30]), "=r"(r[31])                                                           \
       : "r"(taddr))
 
+// Registers -> TMEM, the same lane and column mapping.
+#define GDP_TMEM_ST16(taddr, r)                                                            \
+  asm volatile(                                                                           \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "                                     \
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),           \
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),        \
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),    \
+      "r"(r[14]), "r"(r[15])                                                              \
+      : "memory")
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
