@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -47,6 +48,8 @@ class GDPError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libgdp.so once; raises if it is missing (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -128,8 +131,15 @@ def _a(t):
     return None if t is None else t.data_ptr()
 
 
+# The handle of a device's current stream without a Stream object in between: a call of the
+# small operators below takes about 10 us of host time, 2 of them that object's.
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream_of(t.device.index)
 
 
 def _out_ok(t, shape, dtype):
@@ -485,18 +495,23 @@ def gdp_decode_conv_prepare(xp, conv_w, conv_b, ba, A_log, dt_bias, num_househol
 # linear attention with a decay for each head
 # ----------------------------------------------------------------------------------
 
+_pack_strides = struct.Struct("9q").pack
+
+
 def _linear_args(q, k, v, g):
     """Checks shared by the linear-attention calls: (B, T, H, HV, K, V, strides, g per token)."""
-    _need_cuda(q, k, v, g)
-    if q.dim() != 4 or v.dim() != 4 or k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and (g is None or g.is_cuda)):
+        raise ValueError("libgdp works on CUDA tensors only")
+    shape, vshape, dt = q.shape, v.shape, q.dtype
+    if (len(shape) != 4 or len(vshape) != 4 or k.shape != shape or vshape[0] != shape[0]
+            or vshape[1] != shape[1]):
         raise ValueError("q, k must be [B, T, H, K] and v [B, T, HV, V]")
-    B, T, H, K = q.shape
-    HV, V = v.shape[2], v.shape[3]
-    dt = q.dtype
+    B, T, H, K = shape
+    HV, V = vshape[2], vshape[3]
     if dt != k.dtype or dt != v.dtype or dt not in _DTYPE:
         raise ValueError("q, k, v must share a dtype in {bf16, fp16, fp32}")
-    sq, sk, sv = q.stride(), k.stride(), v.stride()
-    if (sq[3] != 1 and K > 1) or (sk[3] != 1 and K > 1) or (sv[3] != 1 and V > 1):
+    (a0, a1, a2, a3), (b0, b1, b2, b3), (c0, c1, c2, c3) = q.stride(), k.stride(), v.stride()
+    if ((a3 != 1 or b3 != 1) and K > 1) or (c3 != 1 and V > 1):
         raise ValueError("the last dimension of q, k, v must be contiguous")
     per_token = 0
     if g is not None:
@@ -506,16 +521,13 @@ def _linear_args(q, k, v, g):
             per_token = 1
         elif g.shape != (HV,):
             raise ValueError("g must be [B, T, HV] or [HV]")
-    return B, T, H, HV, K, V, _Strides(*sq[:3], *sk[:3], *sv[:3]), per_token
-
-
-_Strides = ctypes.c_int64 * 9
+    return B, T, H, HV, K, V, _pack_strides(a0, a1, a2, b0, b1, b2, c0, c1, c2), per_token
 
 
 def _state_ok(name, t, shape):
-    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32
-                          or not t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous fp32 {list(shape)}")
+    if t is not None and (t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous()
+                          or not t.is_cuda):
+        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)}")
 
 
 def _tables_ok(n, HV, K, V, state_pool, block_tables, context_lens):
@@ -542,7 +554,16 @@ def _linear_workspace(workspace, B, T, N, H, HV, K, V, q):
     return workspace
 
 
+def _linear_out(v, out):
+    """The output: v's shape and dtype, contiguous."""
+    if out is None:
+        return torch.empty_like(v, memory_format=torch.contiguous_format)
+    _out_ok(out, v.shape, v.dtype)
+    return out
+
+
 def _packed(cu_seqlens, B):
+    _need_cuda(cu_seqlens)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
             or cu_seqlens.numel() < 1 or B != 1:
         raise ValueError("cu_seqlens must be int32 [N + 1], with B == 1")
@@ -561,18 +582,17 @@ def gdp_linear_chunk_fwd(q, k, v, g=None, cu_seqlens=None, scale: float | None =
     ``scale`` defaults to K**-0.5. Returns (o [B,T,HV,V] in q's dtype, final_state
     [N,HV,K,V] fp32 or None)."""
     B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
-    _need_cuda(cu_seqlens, initial_state)
     N = B if cu_seqlens is None else _packed(cu_seqlens, B)
     _state_ok("initial_state", initial_state, (N, HV, K, V))
     ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
     if out is None:
-        o = torch.empty((B, T, HV, V), dtype=q.dtype, device=q.device)
+        o = _linear_out(v, None)
         fs = (torch.empty((N, HV, K, V), dtype=torch.float32, device=q.device)
               if output_final_state else None)
     else:
         o, fs = out
         _state_ok("final_state", fs, (N, HV, K, V))
-        _out_ok(o, (B, T, HV, V), q.dtype)
+        _linear_out(v, o)
     st = load().gdp_linear_chunk_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token, _a(initial_state),
         _a(cu_seqlens), N, B, T, H, HV, K, V, K ** -0.5 if scale is None else scale,
@@ -592,14 +612,10 @@ def gdp_linear_chunk_fwd_paged(q, k, v, g, cu_seqlens, state_pool, block_tables,
     block_tables [n, max_blocks] names the pages. q, k [1,T,H,K], v [1,T,HV,V].
     Returns o."""
     B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
-    _need_cuda(cu_seqlens)
     N = _packed(cu_seqlens, B)
     _tables_ok(N, HV, K, V, state_pool, block_tables, context_lens)
     ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
-    o = out
-    if o is None:
-        o = torch.empty((B, T, HV, V), dtype=q.dtype, device=q.device)
-    _out_ok(o, (B, T, HV, V), q.dtype)
+    o = _linear_out(v, out)
     st = load().gdp_linear_chunk_fwd_paged(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token,
         cu_seqlens.data_ptr(), N, T, H, HV, K, V, K ** -0.5 if scale is None else scale,
@@ -617,12 +633,8 @@ def gdp_linear_recurrent_update(q, k, v, g, state, scale: float | None = None, o
     [n,S,H,K], v [n,S,HV,V], g [n,S,HV], [HV] or None. Returns o [n,S,HV,V] in q's
     dtype."""
     n, S, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
-    _need_cuda(state)
     _state_ok("state", state, (n, HV, K, V))
-    o = out
-    if o is None:
-        o = torch.empty((n, S, HV, V), dtype=q.dtype, device=q.device)
-    _out_ok(o, (n, S, HV, V), q.dtype)
+    o = _linear_out(v, out)
     st = load().gdp_linear_recurrent_update(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token, state.data_ptr(), n,
         S, H, HV, K, V, K ** -0.5 if scale is None else scale, _DTYPE[q.dtype], o.data_ptr(),
@@ -643,10 +655,7 @@ def gdp_linear_recurrent_update_paged(q, k, v, g, state_pool, block_tables, cont
     n, S, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
     _tables_ok(n, HV, K, V, state_pool, block_tables, context_lens)
     _status_ok(status)
-    o = out
-    if o is None:
-        o = torch.empty((n, S, HV, V), dtype=q.dtype, device=q.device)
-    _out_ok(o, (n, S, HV, V), q.dtype)
+    o = _linear_out(v, out)
     st = load().gdp_linear_recurrent_update_paged(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _a(g), per_token,
         state_pool.data_ptr(), state_pool.shape[0], block_tables.data_ptr(),
@@ -681,7 +690,7 @@ def gdp_block_plan(context_lens, query_lens, block_tables, free_pages, free_used
     dev = context_lens.device
     if out is None:
         ints = torch.empty(n + 2 + 2 * max_tokens, dtype=torch.int32, device=dev)
-        cu, used, req, pos = ints.split([n + 1, 1, max_tokens, max_tokens])
+        cu, used, req, pos = ints.split_with_sizes((n + 1, 1, max_tokens, max_tokens))
         out = (cu, req, pos, torch.empty(max_tokens, dtype=torch.int64, device=dev), used)
     else:
         for t, m, dt in zip(out, (n + 1, max_tokens, max_tokens, max_tokens, 1),
@@ -731,7 +740,8 @@ def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: f
             raise ValueError("weight and bias must be contiguous fp32 [C]")
     if out is None:
         out = torch.empty(shape, dtype=dt_out, device=x.device)
-    _out_ok(out, tuple(shape), dt_out)
+    else:
+        _out_ok(out, shape, dt_out)
     st = load().gdp_group_norm(x.data_ptr(), x_sn, x_sl, _a(gate), g_sn, g_sl, _a(weight),
                                _a(bias), N, L, C, num_groups, eps, _ACTIVATION[activation],
                                _DTYPE[x.dtype], _DTYPE[dt_out], out.data_ptr(), _raw_stream(x))

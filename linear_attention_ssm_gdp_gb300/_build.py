@@ -33,6 +33,8 @@ UNITS = {
     "noalloc.cu": [],
     "linear_api.cu": [],
     "linear_chunk.cu": [],
+    "linear_mma.cu": [],
+    "linear_segments.cu": [],
     "linear_token.cu": [],
     "block_plan.cu": [],
     "group_norm.cu": [],

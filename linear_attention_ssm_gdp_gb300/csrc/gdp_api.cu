@@ -25,6 +25,17 @@ int sm_count() {
   return cache[dev];
 }
 
+cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Profiling hook (gdp_set_stage_events): caller-created events recorded at the
 // stage boundaries of every gdp_chunk_fwd call.
 static cudaEvent_t g_stage_events[GDP_STAGE_EVENTS];

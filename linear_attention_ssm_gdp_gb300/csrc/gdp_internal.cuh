@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "gdp.h"
@@ -110,6 +111,15 @@ cudaError_t launch_recurrent(const void* q, const void* k, const void* v, const 
                              cudaStream_t stream);
 
 int sm_count();  // multiprocessors on the current device (cached per device)
+
+// Raises a kernel's limit of dynamic shared memory, once per kernel and device (the call takes
+// a microsecond of host time). `done` is the kernel's own mask of devices.
+cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>* done);
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  return allow_smem(reinterpret_cast<const void*>(Kern), bytes, &done);
+}
 
 // Programmatic dependent launch. A kernel launched with launch_pdl is launched
 // as soon as the kernel before it in the stream completes, while that kernel's

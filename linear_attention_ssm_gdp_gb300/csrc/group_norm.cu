@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
 // are fixed, and walks down the positions.
 constexpr int kMapThreads = 256;
 constexpr int kMaxGS = 128;
+constexpr int kMapSmem = 200 * 1024;  // most that a CTA keeps
 
 template <typename TX, typename TO, int VEC, bool GATE>
 __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_constant__ NormArgs a) {
@@ -269,7 +270,7 @@ template <typename TX, typename TO, int VEC, bool GATE>
 cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
   auto kern = norm_map_kernel<TX, TO, VEC, GATE>;
   if (smem > 32 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem<norm_map_kernel<TX, TO, VEC, GATE>>(kMapSmem);
     if (e != cudaSuccess) return e;
   }
   const int64_t grid = a.N * a.sets * CL;
@@ -307,7 +308,7 @@ cudaError_t go_map(NormArgs a, cudaStream_t s) {
   while (CL < 8 && cdiv(a.L, CL) * seg > 96 * 1024) CL *= 2;
   a.rows = (int)cdiv(a.L, CL);
   const int64_t bytes = (int64_t)a.rows * seg;
-  a.resident = bytes <= 200 * 1024;
+  a.resident = bytes <= kMapSmem;
   const size_t smem = a.resident ? (size_t)bytes : 0;
   return a.gate ? go_map2<TX, TO, VEC, true>(a, CL, smem, s) : go_map2<TX, TO, VEC, false>(a, CL, smem, s);
 }

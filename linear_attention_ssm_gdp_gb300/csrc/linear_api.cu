@@ -11,17 +11,11 @@ namespace {
 
 bool dtype_ok(gdp_dtype dt) { return dt == GDP_BF16 || dt == GDP_F16 || dt == GDP_F32; }
 
-// Workspace: status word, then one record per sequence.
-struct LinearWs {
-  size_t status = 0, recs = 0, total = 0;
-};
-
-LinearWs linear_ws(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
-  LinearWs w;
-  w.recs = kAlign;
-  w.total = align_up(w.recs + (size_t)N_seq * sizeof(int4));
-  if (linear_tc_shape(K, V, dt)) w.total = std::max(w.total, linear_tc_workspace(N_seq, B, T, HV, K, V));
-  return w;
+// Workspace: status word, then what the kernel that takes the problem lays out. The size does
+// not depend on the strides, so it is the larger of the two kernels' where both may.
+size_t linear_ws(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
+  const size_t m = linear_mma_workspace(N_seq, B, T, HV, K, V);
+  return linear_tc_shape(K, V, dt) ? std::max(m, linear_tc_workspace(N_seq, B, T, HV, K, V)) : m;
 }
 
 bool sizes_ok(int N_seq, int B, int T, int H, int HV, int K, int V) {
@@ -60,22 +54,14 @@ gdp_status chunk(LinearProblem& p, const int64_t* strides, void* workspace, size
   const gdp_status st = check(p, strides);
   if (st != GDP_OK) return st;
   if (p.cu ? p.B != 1 : p.N_seq != p.B) return GDP_ERR_INVALID_ARG;
-  const LinearWs w = linear_ws(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt);
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || bytes < w.total)
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 ||
+      bytes < linear_ws(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt))
     return GDP_ERR_WORKSPACE;
   set_strides(p, strides);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.status = reinterpret_cast<int32_t*>(ws + w.status);
-  if ((int64_t)p.B * p.T > 0 && linear_tc_ok(p))
-    return launch_linear_tc(p, ws) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
-  int4* recs = nullptr;
-  if (p.cu) {
-    recs = reinterpret_cast<int4*>(ws + w.recs);
-    if (launch_linear_records(p, recs) != cudaSuccess) return GDP_ERR_CUDA;
-  } else if (cudaMemsetAsync(p.status, 0, 4, p.stream) != cudaSuccess) {
-    return GDP_ERR_CUDA;
-  }
-  return launch_linear_walk(p, recs) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  const cudaError_t e = (int64_t)p.B * p.T > 0 && linear_tc_ok(p) ? launch_linear_tc(p, ws) : launch_linear_mma(p, ws);
+  return e == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
 }
 
 }  // namespace
@@ -85,7 +71,7 @@ extern "C" {
 size_t gdp_linear_chunk_fwd_workspace_size(int B, int T, int N_seq, int H, int HV, int K, int V,
                                            gdp_dtype dt) {
   if (!sizes_ok(N_seq, B, T, H, HV, K, V) || K > 256 || V > 1024 || !dtype_ok(dt)) return 0;
-  return linear_ws(N_seq, B, T, HV, K, V, dt).total;
+  return linear_ws(N_seq, B, T, HV, K, V, dt);
 }
 
 gdp_status gdp_linear_chunk_fwd(const void* q, const void* k, const void* v, const int64_t* strides,
@@ -132,7 +118,7 @@ gdp_status gdp_linear_recurrent_update(const void* q, const void* k, const void*
   const gdp_status st = check(p, strides);
   if (st != GDP_OK || n == 0) return st;
   set_strides(p, strides);
-  return launch_linear_walk(p, nullptr) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
+  return launch_linear_walk(p) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
 }
 
 gdp_status gdp_linear_recurrent_update_paged(const void* q, const void* k, const void* v,
@@ -152,7 +138,7 @@ gdp_status gdp_linear_recurrent_update_paged(const void* q, const void* k, const
   const gdp_status st = check(p, strides);
   if (st != GDP_OK || n == 0) return st;
   set_strides(p, strides);
-  return launch_linear_walk(p, nullptr) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
+  return launch_linear_walk(p) == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
 }
 
 }  // extern "C"

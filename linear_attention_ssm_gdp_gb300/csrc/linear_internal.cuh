@@ -36,13 +36,12 @@ struct LinearProblem {
   cudaStream_t stream;
 };
 
-// Record of one sequence (packed batches): x = first row, y = tokens, z = sequence,
-// w = context length (paged states).
-cudaError_t launch_linear_records(const LinearProblem& p, int4* recs);
+// The recurrent form: one walk over a few tokens with the state in registers.
+cudaError_t launch_linear_walk(const LinearProblem& p);
 
-// One walk over the tokens with the state in registers: the recurrent form.
-// recs: null for dense batches.
-cudaError_t launch_linear_walk(const LinearProblem& p, const int4* recs);
+// The chunked form for any type, size and stride.
+size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V);
+cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws);
 
 // The chunked form on the tensor cores: whether sizes and type fit it, whether the
 // tensors' addresses and strides do too (16-byte steps, for TMA), its workspace.

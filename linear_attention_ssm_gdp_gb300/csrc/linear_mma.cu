@@ -1,0 +1,379 @@
+// Linear attention with a decay for each head, chunked form for every type, size and stride
+// that the tensor-memory kernel does not take: fp32 and fp16 inputs, K up to 256, odd sizes.
+//
+// The same algebra on chunks of 64 tokens (see linear_chunk.cu), one CTA of eight warps per
+// (segment, value head, slice of value columns), the products with mma.sync in tf32: an
+// operand that has more than tf32's 11 bits goes in as two parts (x = hi + lo to 2^-22)
+// and a product of two such operands takes three instructions, so that sums are fp32 to a few
+// 2^-22 whatever the input type. 16-bit inputs are exact in one part. The state stays in
+// registers as the accumulator fragments of U, in fp32, with a copy in shared memory that the
+// read-out q S takes its operands from.
+//
+// What bounds it: the latency of its phases (a chunk is loaded, scored, read out and
+// added up by the same eight warps); tiles of the next chunk stream in by cp.async
+// meanwhile where two fit in shared memory.
+#include <algorithm>
+
+#include "linear_chunk.cuh"
+#include "ptx.cuh"
+
+namespace gdp {
+namespace {
+
+using namespace linear;
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void zero(float* p) { *p = 0.f; }
+__device__ __forceinline__ void zero(__nv_bfloat16* p) { *p = __float2bfloat16_rn(0.f); }
+__device__ __forceinline__ void zero(__half* p) { *p = __float2half_rn(0.f); }
+
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// D += A B, one m16n8k8 step.
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// An operand fragment of N registers: hi, and lo unless EXACT.
+template <int N, bool EXACT>
+struct Frag {
+  uint32_t hi[N], lo[EXACT ? 1 : N];
+  __device__ __forceinline__ void set(int i, float x) {
+    if (EXACT) {
+      hi[i] = __float_as_uint(x);
+    } else {
+      hi[i] = tf32(x);
+      lo[EXACT ? 0 : i] = tf32(x - __uint_as_float(hi[i]));
+    }
+  }
+};
+template <bool EA, bool EB>
+__device__ __forceinline__ void mma_parts(float* d, const Frag<4, EA>& a, const Frag<2, EB>& b) {
+  if (!EA) mma(d, a.lo, b.hi);
+  if (!EB) mma(d, a.hi, b.lo);
+  mma(d, a.hi, b.hi);
+}
+
+template <typename T, int KD>
+struct MmaLay {
+  static constexpr int VS = KD <= 128 ? 64 : 32;  // value columns per CTA
+  static constexpr int LK = KD + 16 / sizeof(T);  // row lengths in elements: rows spread over the banks
+  static constexpr int LV = VS + 8;
+  static constexpr int Q = 0, Kt = Q + C * LK * (int)sizeof(T), Vt = Kt + C * LK * (int)sizeof(T);
+  static constexpr int TILE = Vt + C * LV * (int)sizeof(T);
+  static constexpr int REST = KD * LV * 4 + C * (C + 4) * 4 + 2 * 272 * 4;  // S, P, decays
+  static constexpr int STAGES = 2 * TILE + REST <= 227 * 1024 ? 2 : 1;
+  static constexpr int S = STAGES * TILE, P = S + KD * LV * 4, G = P + C * (C + 4) * 4;
+  static constexpr int BYTES = G + 2 * 272 * 4;
+  static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+template <typename T, int KD, bool OUT>
+__global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ ChunkArgs a, int vec) {
+  pdl_wait();
+  using L = MmaLay<T, KD>;
+  constexpr bool EX = sizeof(T) == 2;  // inputs are exact in tf32
+  constexpr int VS = L::VS, LK = L::LK, LV = L::LV, LP = C + 4;
+  extern __shared__ __align__(16) uint8_t sm[];
+  const LinearProblem& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+  if (!a.recs && blockIdx.x == 0 && tid == 0 && p.status) *p.status = kDevOk;
+  Item x;
+  if (!get_item(a, blockIdx.x, x) || skip<OUT>(x)) return;
+  float* sS = reinterpret_cast<float*>(sm + L::S);
+  float* sP = reinterpret_cast<float*>(sm + L::P);
+  const int K = p.K, V = p.V;
+  const T* gq = static_cast<const T*>(p.q) + x.b * p.qs[0] + x.h * p.qs[2];
+  const T* gk = static_cast<const T*>(p.k) + x.b * p.ks[0] + x.h * p.ks[2];
+  const T* gv = static_cast<const T*>(p.v) + x.b * p.vs[0] + x.hv * p.vs[2] + x.v0;
+  const int nv = min(VS, V - x.v0);
+
+  // tile rows of `cols` elements (the rest of the tile's width and rows outside the sequence zero)
+  auto tile = [&](int off, int ld, int width, const T* src, int64_t step, int cols, int base) {
+    T* dst = reinterpret_cast<T*>(sm + off);
+    constexpr int VEC = 16 / sizeof(T);
+    if (vec) {
+      const int per = width / VEC;
+      for (int i = tid; i < C * per; i += kThreads) {
+        const int r = i / per, c = (i - r * per) * VEC, row = base + r;
+        T* d = dst + r * ld + c;
+        const bool in = row >= x.r.t0 && row < x.r.t0 + x.r.n && c < cols;
+        // a short copy is zero-filled: cols is a multiple of VEC here
+        const int bytes = in ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(d)),
+                     "l"(in ? src + row * step + c : src), "r"(bytes)
+                     : "memory");
+      }
+    } else {
+      for (int i = tid; i < C * width; i += kThreads) {
+        const int r = i / width, c = i - r * width, row = base + r;
+        if (row >= x.r.t0 && row < x.r.t0 + x.r.n && c < cols) dst[r * ld + c] = src[row * step + c];
+        else zero(dst + r * ld + c);
+      }
+    }
+  };
+  auto load = [&](int c) {
+    const int base = x.r.t0 - x.off + c * C, o = (c % L::STAGES) * L::TILE;
+    if (OUT) tile(o + L::Q, LK, KD, gq, p.qs[1], K, base);
+    tile(o + L::Kt, LK, KD, gk, p.ks[1], K, base);
+    tile(o + L::Vt, LV, VS, gv, p.vs[1], nv, base);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  // state fragments: U's accumulators. KD = 64: warps 4 x 2 over (k, v); otherwise over k
+  constexpr int MT = KD / 64 <= 2 ? 1 : KD / 128;  // 16-row tiles of k per warp
+  constexpr int NT = KD == 64 ? VS / 16 : VS / 8;  // 8-column tiles of v per warp
+  const int m0 = KD == 64 ? 16 * (warp & 3) : 16 * MT * warp, n0 = KD == 64 ? (VS / 2) * (warp >> 2) : 0;
+  float s[MT][NT][4];
+  const int64_t at = (int64_t)x.hv * K * V + x.v0;
+  auto each_state = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = m0 + 16 * i + gr + 8 * (e >> 1), v = n0 + 8 * j + 2 * tq + (e & 1);
+          f(s[i][j][e], k, v, k < K && v < nv);
+        }
+  };
+  {
+    const float* src = state_src<OUT>(a, x);
+    each_state([&](float& y, int k, int v, bool in) { y = src && in ? __ldcg(src + at + (int64_t)k * V + v) : 0.f; });
+  }
+  float2 wseg = make_float2(1.f, 0.f);
+  float g0 = 0.f, g1 = 0.f;
+  if (warp == 0) {
+    g0 = load_g(p, x, x.r.t0 - x.off, 2 * lane);
+    g1 = load_g(p, x, x.r.t0 - x.off, 2 * lane + 1);
+  }
+  if (x.chunks > 0) load(0);
+  for (int c = 0; c < x.chunks; ++c) {
+    const int base = x.r.t0 - x.off + c * C;
+    const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
+    float* g = reinterpret_cast<float*>(sm + L::G) + (c & 1) * 272;
+    if (L::STAGES == 1 && c > 0) {
+      __syncthreads();  // the last chunk's readers are done with the tiles
+      load(c);
+    }
+    if (OUT)  // the state before the chunk, for the read-out
+      each_state([&](float& y, int k, int v, bool) { sS[k * LV + v] = y; });
+    if (warp == 0) {
+      chunk_decays(g0, g1, p.scale, lo, hi, lane, g);
+      if (c + 1 < x.chunks) {
+        g0 = load_g(p, x, base + C, 2 * lane);
+        g1 = load_g(p, x, base + C, 2 * lane + 1);
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (L::STAGES == 2 && c + 1 < x.chunks) load(c + 1);  // its stage was last read before this barrier
+    const uint8_t* st = sm + (c % L::STAGES) * L::TILE;
+    const T* tQ = reinterpret_cast<const T*>(st + L::Q);
+    const T* tK = reinterpret_cast<const T*>(st + L::Kt);
+    const T* tV = reinterpret_cast<const T*>(st + L::Vt);
+    const int kk = (K + 7) / 8;  // steps over K
+    if (OUT) {
+      // scores: rows 16 (warp % 4), columns 32 (warp / 4), only tiles that reach the diagonal
+      const int r0 = 16 * (warp & 3), c0 = 32 * (warp >> 2);
+      float d[4][4] = {};
+      if (c0 <= r0 + 15) {
+        for (int k0 = 0; k0 < 8 * kk; k0 += 8) {
+          Frag<4, EX> fa;
+          const T* qa = tQ + (r0 + gr) * LK + k0 + tq;
+          fa.set(0, to_f(qa[0]));
+          fa.set(1, to_f(qa[8 * LK]));
+          fa.set(2, to_f(qa[4]));
+          fa.set(3, to_f(qa[8 * LK + 4]));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            Frag<2, EX> fb;
+            const T* kb = tK + (c0 + 8 * j + gr) * LK + k0 + tq;
+            fb.set(0, to_f(kb[0]));
+            fb.set(1, to_f(kb[4]));
+            mma_parts<EX, EX>(d[j], fa, fb);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = r0 + gr + 8 * (e >> 1), i = c0 + 8 * j + 2 * tq + (e & 1);
+          const float f = ex2_approx((g[t] - g[i]) + (g[64 + t] - g[64 + i]));
+          sP[t * LP + i] = i <= t ? d[j][e] * (p.scale * f) : 0.f;
+        }
+      __syncthreads();
+      // o: rows r0, value columns of this warp's half
+      constexpr int NO = VS / 16;
+      const int v0 = (VS / 2) * (warp >> 2);
+      float o[NO][4] = {};
+      for (int k0 = 0; k0 < 8 * kk; k0 += 8) {
+        Frag<4, EX> fa;
+        const T* qa = tQ + (r0 + gr) * LK + k0 + tq;
+        fa.set(0, to_f(qa[0]));
+        fa.set(1, to_f(qa[8 * LK]));
+        fa.set(2, to_f(qa[4]));
+        fa.set(3, to_f(qa[8 * LK + 4]));
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          Frag<2, false> fb;
+          const float* sb = sS + (k0 + tq) * LV + v0 + 8 * j + gr;
+          fb.set(0, sb[0]);
+          fb.set(1, sb[4 * LV]);
+          mma_parts<EX, false>(o[j], fa, fb);
+        }
+      }
+      const float e0 = g[192 + r0 + gr], e1 = g[192 + r0 + gr + 8];
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        o[j][0] *= e0;
+        o[j][1] *= e0;
+        o[j][2] *= e1;
+        o[j][3] *= e1;
+      }
+      for (int i0 = 0; i0 < r0 + 16; i0 += 8) {
+        Frag<4, false> fa;
+        const float* pa = sP + (r0 + gr) * LP + i0 + tq;
+        fa.set(0, pa[0]);
+        fa.set(1, pa[8 * LP]);
+        fa.set(2, pa[4]);
+        fa.set(3, pa[8 * LP + 4]);
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          Frag<2, EX> fb;
+          const T* vb = tV + (i0 + tq) * LV + v0 + 8 * j + gr;
+          fb.set(0, to_f(vb[0]));
+          fb.set(1, to_f(vb[4 * LV]));
+          mma_parts<false, EX>(o[j], fa, fb);
+        }
+      }
+      T* og = static_cast<T*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = r0 + gr + 8 * (e >> 1), v = v0 + 8 * j + 2 * tq + (e & 1);
+          if (t >= lo && t < hi && v < nv) put(og + (int64_t)t * p.HV * V + v, o[j][e]);
+        }
+    }
+    // U = k^T (w v), then S = e^Gam S + U
+    const float wh = g[256], wl = g[257];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float u[NT][4] = {};
+      for (int t0 = 0; t0 < C; t0 += 8) {
+        Frag<4, EX> fa;
+        const T* ka = tK + (t0 + tq) * LK + m0 + 16 * i + gr;
+        fa.set(0, to_f(ka[0]));
+        fa.set(1, to_f(ka[8]));
+        fa.set(2, to_f(ka[4 * LK]));
+        fa.set(3, to_f(ka[4 * LK + 8]));
+        const float w0 = g[128 + t0 + tq], w1 = g[128 + t0 + tq + 4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          Frag<2, false> fb;
+          const T* vb = tV + (t0 + tq) * LV + n0 + 8 * j + gr;
+          fb.set(0, w0 * to_f(vb[0]));
+          fb.set(1, w1 * to_f(vb[4 * LV]));
+          mma_parts<EX, false>(u[j], fa, fb);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][j][e] = fmaf(wh, s[i][j][e], fmaf(wl, s[i][j][e], u[j][e]));
+    }
+    if (!OUT) wseg = mul_pair(wseg, make_float2(wh, wl));
+    if (float* dst = state_dst<OUT>(a, x, c))
+      each_state([&](float& y, int k, int v, bool in) {
+        if (in) dst[at + (int64_t)k * V + v] = y;
+      });
+    if (OUT) __syncthreads();  // S and P are rewritten next
+  }
+  if (!OUT && tid == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
+  if (OUT && x.chunks == 0 && x.r.last && !p.pool && p.sT)  // an empty sequence keeps its state
+    each_state([&](float& y, int k, int v, bool in) {
+      if (in) p.sT[x.r.seq * (int64_t)p.HV * K * V + at + (int64_t)k * V + v] = y;
+    });
+}
+
+template <typename T, int KD, bool OUT>
+cudaError_t go(const ChunkArgs& a, int vec) {
+  constexpr int smem = MmaLay<T, KD>::BYTES;
+  cudaError_t e = allow_smem<linear_mma_kernel<T, KD, OUT>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(linear_mma_kernel<T, KD, OUT>, dim3((unsigned)a.items), dim3(kThreads), smem, a.p.stream, a, vec);
+}
+template <typename T, bool OUT>
+cudaError_t go_k(const ChunkArgs& a, int vec) {
+  return a.p.K <= 64 ? go<T, 64, OUT>(a, vec) : a.p.K <= 128 ? go<T, 128, OUT>(a, vec) : go<T, 256, OUT>(a, vec);
+}
+template <bool OUT>
+cudaError_t go_t(const ChunkArgs& a, int vec) {
+  switch (a.p.dt) {
+    case GDP_BF16: return go_k<__nv_bfloat16, OUT>(a, vec);
+    case GDP_F16: return go_k<__half, OUT>(a, vec);
+    default: return go_k<float, OUT>(a, vec);
+  }
+}
+
+constexpr double kStateCost = 0.5;  // the state pass leaves out scores and read-out
+int slice_of(int K) { return K <= 128 ? 64 : 32; }
+
+}  // namespace
+
+size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V) {
+  // the query does not say whether the batch is packed
+  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, slice_of(K), kStateCost).total : 0;
+  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, slice_of(K), kStateCost).total : 0);
+}
+
+cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
+  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, slice_of(p.K), kStateCost);
+  ChunkArgs a{};
+  a.p = p;
+  a.nseg = x.nseg;
+  a.Lseg = x.Lseg;
+  a.slices = x.slices;
+  a.vt = slice_of(p.K);
+  if ((int64_t)x.bound * p.HV * x.slices > INT32_MAX) return cudaErrorInvalidValue;
+  a.items = x.bound * p.HV * x.slices;
+  if (a.items == 0) return cudaSuccess;
+  int2* seqs = nullptr;
+  if (p.cu) {
+    SegRec* recs = reinterpret_cast<SegRec*>(ws + x.recs);
+    seqs = reinterpret_cast<int2*>(ws + x.seqs);
+    a.recs = recs;
+    const cudaError_t e = launch_segments(p, x, recs, seqs);
+    if (e != cudaSuccess) return e;
+  }
+  // 16-byte copies: rows and bases on 16-byte steps, whole vectors in a row
+  const int n = p.dt == GDP_F32 ? 4 : 8;
+  const auto fits = [n](const void* b, const int64_t* s) {
+    return reinterpret_cast<uintptr_t>(b) % 16 == 0 && s[0] % n == 0 && s[1] % n == 0 && s[2] % n == 0;
+  };
+  const int vec = p.K % n == 0 && p.V % n == 0 && fits(p.q, p.qs) && fits(p.k, p.ks) && fits(p.v, p.vs);
+  if (x.segS) {
+    a.segS = reinterpret_cast<float*>(ws + x.segS);
+    a.segW = reinterpret_cast<float2*>(ws + x.segW);
+    cudaError_t e = go_t<false>(a, vec);
+    if (e == cudaSuccess) e = launch_combine(a, seqs);
+    if (e != cudaSuccess) return e;
+  }
+  return go_t<true>(a, vec);
+}
+
+}  // namespace gdp

@@ -1,0 +1,233 @@
+// Linear attention, chunked forms: how sequences are cut into segments, the segment records of
+// packed batches, and the states at the segment starts.
+//
+// A segment is a work item of its own when there are too few (sequence, head) pairs to fill the
+// GPU: the state pass of a chunked kernel forms each segment's own U from a zero state, the
+// combine kernel here turns those into the states at the segment starts, and the whole pass then
+// runs over all segments at once. Reading k and v twice costs less than idle SMs.
+#include <algorithm>
+
+#include "linear_chunk.cuh"
+
+namespace gdp {
+namespace linear {
+namespace {
+
+// Segment records of a packed batch (one CTA): offsets and block tables checked as in
+// linear_records_kernel, each sequence cut at multiples of Lseg positions, records sorted by
+// length, longest first.
+constexpr int kRecThreads = 512;
+constexpr int kSortMax = 4096;
+
+__device__ __forceinline__ int table_page(const LinearProblem& p, int r, int64_t b) {
+  if (b < 0 || b >= p.width) return -1;
+  const int pg = p.tables[(int64_t)r * p.width + b];
+  return pg >= 0 && pg < p.n_pages ? pg : -1;
+}
+
+__global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __grid_constant__ LinearProblem p,
+                                                                      int Lseg, int bound, SegRec* recs, int2* seqs) {
+  pdl_wait();
+  __shared__ int lens[kSortMax];
+  __shared__ int wsum[kRecThreads / 32 + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  for (int i = tid; i < p.N_seq; i += kRecThreads) {
+    const int x = p.cu[i], y = p.cu[i + 1];
+    bad |= x < 0 || y < x || y > p.T;
+  }
+  bad = __syncthreads_or(bad);
+  bool any = bad;
+  int base = 0;  // segments before this round of sequences
+  for (int i0 = 0; i0 < p.N_seq; i0 += kRecThreads) {
+    const int i = i0 + tid;
+    int t0 = 0, n = 0, pos = 0, cnt = 0;
+    if (i < p.N_seq) {
+      if (!bad) {
+        t0 = p.cu[i];
+        n = p.cu[i + 1] - t0;
+      }
+      if (p.pool && n > 0) {
+        pos = p.ctx[i];
+        bool off = pos < 0;
+        if (!off)
+          for (int64_t j = pos > 0 ? (pos - 1) / p.block : 0; j <= ((int64_t)pos + n - 1) / p.block; ++j)
+            off |= table_page(p, i, j) < 0;
+        if (off) n = pos = 0;
+        any |= off;
+      }
+      cnt = n > 0 ? (int)(((int64_t)pos % C + n + Lseg - 1) / Lseg) : 1;
+    }
+    int s = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    if (tid == 0) {
+      int run = 0;
+      for (int w = 0; w < kRecThreads / 32; ++w) {
+        const int y = wsum[w];
+        wsum[w] = run;
+        run += y;
+      }
+      wsum[kRecThreads / 32] = run;
+    }
+    __syncthreads();
+    const int first = base + wsum[warp] + s - cnt;
+    base += wsum[kRecThreads / 32];
+    if (i < p.N_seq) {
+      if (seqs) seqs[i] = make_int2(first, cnt);
+      const int off = pos % C;
+      for (int j = 0; j < cnt; ++j) {
+        const int lo = j == 0 ? 0 : j * Lseg - off, hi = min(n, (j + 1) * Lseg - off);
+        SegRec r{t0 + lo, hi - lo, i, p.pool ? pos + lo : lo, j == 0, j == cnt - 1, first + j, 0};
+        recs[first + j] = r;
+        if (first + j < kSortMax) lens[first + j] = r.n;
+      }
+    }
+    __syncthreads();
+  }
+  any = __syncthreads_or(any);
+  if (tid == 0 && p.status) *p.status = any ? kDevBadSeqlens : kDevOk;
+  const int count = base;
+  if (count <= kSortMax && count > 1) {  // in place: every thread reads its records first
+    SegRec mine[kSortMax / kRecThreads];
+    int rank[kSortMax / kRecThreads];
+#pragma unroll
+    for (int q = 0; q < kSortMax / kRecThreads; ++q) {
+      const int i = tid + q * kRecThreads;
+      if (i < count) {
+        mine[q] = recs[i];
+        int r = 0;
+        const int len = lens[i];
+        for (int j = 0; j < count; ++j) r += lens[j] > len || (lens[j] == len && j < i);
+        rank[q] = r;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSortMax / kRecThreads; ++q)
+      if (tid + q * kRecThreads < count) recs[rank[q]] = mine[q];
+  }
+  for (int i = count + tid; i < bound; i += kRecThreads) recs[i] = SegRec{0, 0, -1, 0, 0, 0, 0, 0};
+}
+
+// States at the segment starts: S_0 = the sequence's initial state, S_{j+1} = w_j S_j + U_j,
+// in place of the U's. A thread per VEC state elements.
+template <int VEC>
+__global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
+  pdl_wait();
+  const LinearProblem& p = a.p;
+  const int64_t sz = (int64_t)p.K * p.V;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
+  const int hv = blockIdx.y, seq = blockIdx.z;
+  int first, cnt;
+  if (a.recs) {
+    const int2 x = seqs[seq];
+    first = x.x;
+    cnt = x.y;
+  } else {
+    first = seq * a.nseg;
+    cnt = a.nseg;
+  }
+  if (cnt < 2 || e >= sz) return;
+  const float* src = nullptr;
+  if (p.pool) {
+    const int c = p.ctx[seq];
+    if (c > 0) src = p.pool + (int64_t)p.tables[(int64_t)seq * p.width + (c - 1) / p.block] * p.HV * sz;
+  } else if (p.s0) {
+    src = p.s0 + (int64_t)seq * p.HV * sz;
+  }
+  float s[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+  auto load = [](float* d, const float* q) {
+    if (VEC == 4) *reinterpret_cast<float4*>(d) = __ldcg(reinterpret_cast<const float4*>(q));
+    else *d = __ldcg(q);
+  };
+  if (src) load(s, src + hv * sz + e);
+  float* seg = a.segS + ((int64_t)first * p.HV + hv) * sz + e;
+  const int64_t step = (int64_t)p.HV * sz;
+  const float2* w = a.segW + (int64_t)first * p.HV + hv;
+  for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight segments' loads in flight
+    const int m = min(8, cnt - 1 - j0);
+    alignas(16) float u[8][VEC];
+    float2 f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < m) {
+        load(u[j], seg + (j0 + j) * step);
+        f[j] = __ldcg(w + (int64_t)(j0 + j) * p.HV);
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < cnt) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) seg[(j0 + j) * step + i] = s[i];
+        if (j < m)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[i] = fmaf(f[j].x, s[i], fmaf(f[j].y, s[i], u[j][i]));
+      }
+  }
+}
+
+}  // namespace
+
+Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, double state_cost) {
+  Plan x{};
+  const int G = sm_count();
+  x.slices = (int)cdiv(V, vt);
+  const int chunks = (int)cdiv(T, C);
+  const int64_t heads = (int64_t)HV * x.slices;
+  x.nseg = 1;
+  x.Lseg = std::max(1, chunks) * C;
+  if (!packed) {
+    // time in units of a chunk of the second pass: rounds of items over the SMs, the state pass
+    // at state_cost of that and its two extra launches at about eight chunks
+    const int64_t units = heads * B;
+    double best = (double)cdiv(units, G) * chunks;
+    for (int n = 2; n <= chunks && n <= 64; ++n) {
+      const int64_t per = cdiv(chunks, n);
+      if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
+      const double t = (double)cdiv(units * n, G) * per + state_cost * cdiv(units * (n - 1), G) * per + 8.0;
+      if (t < 0.95 * best) {
+        best = t;
+        x.nseg = n;
+        x.Lseg = (int)per * C;
+      }
+    }
+    x.bound = B * x.nseg;
+  } else {
+    // packed: no more than an SM's share of the whole batch in one item
+    const int64_t share = cdiv(cdiv((int64_t)T * heads, G), C) * C;
+    x.Lseg = (int)std::min<int64_t>(x.Lseg + C, std::max<int64_t>(share, 512));
+    x.bound = (int)(((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq);
+  }
+  const bool split = packed ? x.Lseg < T : x.nseg > 1;
+  x.recs = kAlign;
+  x.seqs = align_up(x.recs + (packed ? (size_t)x.bound * sizeof(SegRec) : 0));
+  x.segW = align_up(x.seqs + (packed ? (size_t)N_seq * sizeof(int2) : 0));
+  x.segS = align_up(x.segW + (split ? (size_t)x.bound * HV * sizeof(float2) : 0));
+  x.total = align_up(x.segS + (split ? (size_t)x.bound * HV * K * V * 4 : 0));
+  if (!split) x.segS = 0;
+  return x;
+}
+
+
+cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs) {
+  return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs);
+}
+
+cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs) {
+  const int64_t sz = (int64_t)a.p.K * a.p.V;
+  const bool vec = sz % 4 == 0;
+  const dim3 grid((unsigned)cdiv(sz, vec ? 1024 : 256), a.p.HV, a.p.N_seq);
+  return vec ? launch_pdl(linear_combine_kernel<4>, grid, dim3(256), 0, a.p.stream, a, seqs)
+             : launch_pdl(linear_combine_kernel<1>, grid, dim3(256), 0, a.p.stream, a, seqs);
+}
+
+}  // namespace linear
+}  // namespace gdp

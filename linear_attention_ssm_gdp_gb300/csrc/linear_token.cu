@@ -33,7 +33,6 @@ __device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x
 
 struct WalkArgs {
   LinearProblem p;
-  const int4* recs;
   int VS;      // value columns per CTA
   int slices;  // CTAs along V
 };
@@ -63,16 +62,10 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
   const int cg = tid % CG, rg = tid / CG, c0 = v0 + cg * VEC;
   const bool col_ok = c0 < V;                    // VEC divides V
 
-  int b = seq, t0 = 0, len = p.T, ctx = 0;
-  if (a.recs) {
-    const int4 rec = a.recs[seq];
-    b = 0; t0 = rec.x; len = rec.y; ctx = rec.w;
-  } else if (p.ctx) {
-    ctx = p.ctx[seq];
-  }
+  const int len = p.T, ctx = p.ctx ? p.ctx[seq] : 0;
   const float* src = p.s0 ? p.s0 + ((int64_t)seq * p.HV + hv) * K * V : nullptr;
   bool live = true;
-  if (p.pool && !a.recs) {
+  if (p.pool) {
     // a padding request names no page for its last token; one whose pages lie
     // outside the pool, or that writes a page which another request reads or
     // writes, would make the update ill-defined and is treated the same
@@ -100,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
       live = false;
     }
   }
-  T* o = static_cast<T*>(p.o) + ((int64_t)b * p.T + t0) * p.HV * V + (int64_t)hv * V;
+  T* o = static_cast<T*>(p.o) + (int64_t)seq * len * p.HV * V + (int64_t)hv * V;
   const int64_t orow = (int64_t)p.HV * V;
   if (!live) {
     for (int i = tid; i < len * VS; i += kThreads) {
@@ -109,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
     }
     return;
   }
-  if (p.pool && ctx > 0 && len > 0)
+  if (p.pool && ctx > 0)
     src = p.pool + ((int64_t)page_of(p, seq, (ctx - 1) / p.block) * p.HV + hv) * K * V;
 
   float s[R][VEC];
@@ -142,10 +135,10 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
     }
   };
 
-  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + t0 * p.qs[1] + h * p.qs[2];
-  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + t0 * p.ks[1] + h * p.ks[2];
-  const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + t0 * p.vs[1] + hv * p.vs[2];
-  const float* g = !p.g ? nullptr : p.g_token ? p.g + ((int64_t)b * p.T + t0) * p.HV + hv : p.g + hv;
+  const T* q = static_cast<const T*>(p.q) + seq * p.qs[0] + h * p.qs[2];
+  const T* k = static_cast<const T*>(p.k) + seq * p.ks[0] + h * p.ks[2];
+  const T* v = static_cast<const T*>(p.v) + seq * p.vs[0] + hv * p.vs[2];
+  const float* g = !p.g ? nullptr : p.g_token ? p.g + (int64_t)seq * len * p.HV + hv : p.g + hv;
   for (int base = 0; base < len; base += kStep) {
     const int m = min(kStep, len - base);
     __syncthreads();
@@ -211,49 +204,10 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
   if (p.sT) store(p.sT + ((int64_t)seq * p.HV + hv) * K * V);
 }
 
-// Packed batches: one record per sequence from cu_seqlens, checked on the device
-// (offsets ascending inside [0, T]; for paged states also that every page that
-// a sequence reads or writes lies in the pool). A bad offset list empties every
-// sequence, a bad table row its own; both set the status word.
-__global__ void __launch_bounds__(512) linear_records_kernel(const __grid_constant__ LinearProblem p,
-                                                             int4* recs) {
-  pdl_wait();
-  const int tid = threadIdx.x;
-  bool bad = false;
-  for (int i = tid; i < p.N_seq; i += 512) {
-    const int x = p.cu[i], y = p.cu[i + 1];
-    bad |= x < 0 || y < x || y > p.T;
-  }
-  bad = __syncthreads_or(bad);
-  bool any = bad;
-  for (int i = tid; i < p.N_seq; i += 512) {
-    int4 r = make_int4(0, 0, i, 0);
-    if (!bad) {
-      r.x = p.cu[i];
-      r.y = p.cu[i + 1] - r.x;
-      if (p.pool && r.y > 0) {
-        r.w = p.ctx[i];
-        bool off = r.w < 0;
-        if (!off)
-          for (int64_t j = r.w > 0 ? (r.w - 1) / p.block : 0; j <= ((int64_t)r.w + r.y - 1) / p.block; ++j)
-            off |= page_of(p, i, j) < 0;
-        if (off) r.y = 0;
-        any |= off;
-      }
-    }
-    recs[i] = r;
-  }
-  any = __syncthreads_or(any);
-  if (tid == 0 && p.status) *p.status = any ? kDevBadSeqlens : kDevOk;
-}
-
 template <typename T, int VEC, int R>
 cudaError_t go(const WalkArgs& a, int smem) {
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(linear_walk_kernel<T, VEC, R>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_smem<linear_walk_kernel<T, VEC, R>>(52 * 1024);  // K = 256: 49 KB
+  if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)a.p.N_seq * a.p.HV * a.slices;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(linear_walk_kernel<T, VEC, R>, dim3((unsigned)grid), dim3(kThreads), smem,
@@ -261,8 +215,8 @@ cudaError_t go(const WalkArgs& a, int smem) {
 }
 
 template <typename T>
-cudaError_t pick(const LinearProblem& p, const int4* recs) {
-  WalkArgs a{p, recs, 0, 0};
+cudaError_t pick(const LinearProblem& p) {
+  WalkArgs a{p, 0, 0};
   const bool vec = p.V % 4 == 0;  // 16-byte state columns (the API checks the base's alignment)
   int VS = vec ? 128 : 32;
   while (vec && VS > 32 && (VS / 2 >= p.V ||
@@ -281,16 +235,12 @@ cudaError_t pick(const LinearProblem& p, const int4* recs) {
 
 }  // namespace
 
-cudaError_t launch_linear_records(const LinearProblem& p, int4* recs) {
-  return launch_pdl(linear_records_kernel, dim3(1), dim3(512), 0, p.stream, p, recs);
-}
-
-cudaError_t launch_linear_walk(const LinearProblem& p, const int4* recs) {
+cudaError_t launch_linear_walk(const LinearProblem& p) {
   if (p.N_seq == 0) return cudaSuccess;
   switch (p.dt) {
-    case GDP_BF16: return pick<__nv_bfloat16>(p, recs);
-    case GDP_F16: return pick<__half>(p, recs);
-    default: return pick<float>(p, recs);
+    case GDP_BF16: return pick<__nv_bfloat16>(p);
+    case GDP_F16: return pick<__half>(p);
+    default: return pick<float>(p);
   }
 }
 
