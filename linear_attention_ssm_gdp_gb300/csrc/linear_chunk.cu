@@ -7,7 +7,7 @@
 //     S  <- e^{Gam} S + sum_i k_i (e^{Gam - Gam_i} v_i)^T.
 // Four products per chunk of 64 tokens, with the value columns on the 128 rows of
 // the tensor core's accumulator wherever the product has them:
-//     QK     [t | i]  = q k^T            (rows 64.. of the A tile are k's: unused)
+//     QK     [t | i]  = q k^T            (rows 64.. of the A tile are other data: unused)
 //     INTER  [v | t]  = S^T q^T          S as bf16
 //     INTRA  [v | t]  = v^T P^T          P = masked, decayed scores as bf16
 //     U      [v | k]  = v'^T k           v' = e^{Gam - Gam_i} v_i as three bf16 parts
@@ -139,23 +139,27 @@ __device__ __forceinline__ int chunks_of(const ChunkArgs& a, int it) {
 }
 
 // ------------------------------------------------------------------ waits
+// (The loop is not inlined: it would be a third of the kernel's code.)
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, int* status) {
+  uint64_t t0 = 0;
+  for (int i = 0; !mbar_test(bar, parity); ++i) {
+    if ((i & 15) != 15) continue;
+    if (*dead) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitBudgetNs) {
+      if (status) atomicExch(status, kDevTimeout);
+      *dead = 1;
+      return false;
+    }
+  }
+  return true;
+}
 struct Sync {
   volatile int* dead;  // a wait of this CTA ran out: everybody leaves
   int* status;
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    uint64_t t0 = 0;
-    for (int i = 0; !mbar_test(bar, parity); ++i) {
-      if ((i & 15) != 15) continue;
-      if (*dead) return false;
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitBudgetNs) {
-        if (status) atomicExch(status, kDevTimeout);
-        *dead = 1;
-        return false;
-      }
-    }
-    return true;
+    return mbar_test(bar, parity) || wait_slow(bar, parity, dead, status);
   }
   // by a whole warp, with one answer for all its lanes
   __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
@@ -172,14 +176,18 @@ __device__ __forceinline__ bool state_and(bool pred) {
 }
 
 // ------------------------------------------------------------------ shared memory
+struct TcArgs : ChunkArgs {
+  int k_halves, v_halves;  // 64-column halves in the boxes of q and k, and of v and o
+};
+
 template <int KD, bool OUT>
 struct Lay {
-  static constexpr int NST = 4;                         // stages of q, k, v
+  static constexpr int NST = 3;                         // stages of q, k, v
   static constexpr int KH = KD / 64;                    // 64-column halves of q and k
-  static constexpr int QK = KH * 16384;                 // [q | k] by half, 64 rows of 128 bytes each
-  static constexpr int STG = QK + 16384;                // then v, two halves
-  static constexpr int P = NST * STG;                   // scores
-  static constexpr int O = P + (OUT ? 8192 : 0);        // output tile, two halves
+  // q, k and v by halves of 64 columns: 64 rows of 128 bytes each
+  static constexpr int KT = KH * 8192, VT = 2 * KT, STG = VT + 16384;
+  static constexpr int P = NST * STG;                   // scores, two buffers
+  static constexpr int O = P + (OUT ? 16384 : 0);       // output tile, two halves
   // decays: more slots than stages, since the output still reads them when the stage is free
   static constexpr int G = O + (OUT ? 16384 : 0);
   static constexpr int GS = 272 * 4;                    // hi2, lo2, wend, ein [64] each, e^Gam hi, lo
@@ -188,9 +196,10 @@ struct Lay {
   static constexpr int BYTES = ITEM + (kSW + 2) * 64 + 1024;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-// full, ready, free by stage; v' ready and free by step; the rest single (B_O: INTER and INTRA)
+// full, ready, free by stage; v' ready and free by step; INTER and INTRA done by parity; the rest
+// single
 enum {
-  B_FULL = 0, B_READY = 4, B_FREE = 8, B_V = 12, B_VFREE = 16, B_QK = 20, B_O, B_OREAD, B_S, B_U, B_UREAD, B_N
+  B_FULL = 0, B_READY = 3, B_FREE = 6, B_V = 9, B_VFREE = 13, B_O = 17, B_QK = 19, B_OREAD, B_S, B_U, B_UREAD, B_N
 };
 
 // TMEM columns: scores [64], INTER and INTRA [64] each, U [KD], S [KD / 2], v' [3][32]
@@ -200,7 +209,7 @@ template <int KD, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
-    const __grid_constant__ ChunkArgs a) {
+    const __grid_constant__ TcArgs a) {
   using L = Lay<KD, OUT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   if (tid == 32) {
     for (int i = 0; i < B_N; ++i) {
       int n = 1;
-      if (i >= B_FREE && i < B_V) n = OUT ? 2 : 1;                   // both issuing threads
+      if (i >= B_FREE && i < B_V) n = OUT ? 2 : 1;                   // both issuing warps
       if (i == B_OREAD || i == B_S || i == B_UREAD) n = kSW;         // state warps
       if (i >= B_V && i < B_VFREE) n = 4;                            // v' warps
       mbar_init(&bars[i], n);
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           dst = p.sT + (int64_t)x.r.seq * p.HV * page_sz;
         }
         if (OUT) {
-        ok = sy.wait_warp(&bars[B_O], n & 1) && ok;
+        ok = sy.wait_warp(&bars[B_O + (n & 1)], (n >> 1) & 1) && ok;
         tc_fence_after();
         if (more && ok) publish();
         // o of 16 value columns at a time, as fragments: pairs of rows t in a register
@@ -404,8 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           fence_async_smem();
           state_and(true);
           if (tid == 0) {
-            tma_store_4d(&map_o, sm + L::O, x.v0, x.hv, base, x.b);
-            if (x.v0 + 64 < V) tma_store_4d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b);
+            if (a.v_halves == 1) {
+              tma_store_5d(&map_o, sm + L::O, x.v0, x.hv, base, x.b, 0);
+              if (x.v0 + 64 < V) tma_store_5d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b, 0);
+            } else {
+              tma_store_5d(&map_o, sm + L::O, 0, x.hv, base, x.b, x.v0 >> 6);
+            }
             tma_store_commit();
           }
         } else {
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16) + T_V;
     // transposing loads: lanes 8 m .. 8 m + 7 address rows i of value block m (16-byte chunk
     // 4 (quarter % 2) + m, permuted by i % 8)
-    const uint32_t vrow = L::QK + (quarter >> 1) * 8192 + (lane & 7) * 128 +
+    const uint32_t vrow = L::VT + (quarter >> 1) * 8192 + (lane & 7) * 128 +
                           (((4 * (quarter & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
     bool ok = true;
     for (int n = 0; n < total && ok; ++n) {
@@ -490,55 +503,64 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       const f2 sc2 = pk2(p.scale, p.scale);
       const uint32_t id_qk = idesc_bf16(128, 64, false, false);  // and of INTER
       const uint32_t id_a = idesc_bf16(128, 64, true, false);
+      // (loops are rolled where they can be: the roles together have to fit 32 KB of instruction
+      // cache, or every SM of a GPC waits for the same next level)
       auto qk = [&](int n) {  // the first warp
         if (elect_one()) {
           tc_fence_after();
           const uint32_t tl = smb + (n % L::NST) * L::STG;
-          mma_run<KD / 16, false, 16384, 32, 16384, 32>(tmem + T_QK, sdesc_sw128(tl, 16, 1024),
-                                                        sdesc_sw128(tl + 8192, 16, 1024), id_qk);
+          const uint64_t qd = sdesc_sw128(tl, 16, 1024), kd = sdesc_sw128(tl + L::KT, 16, 1024);
+#pragma unroll 1
+          for (int i = 0; i < KD / 16; ++i) {
+            const uint64_t o = (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2);
+            mma_bf16(tmem + T_QK, qd + o, kd + o, id_qk, i > 0);
+          }
           mma_commit(&bars[B_QK]);
         }
         __syncwarp();
       };
       bool ok = true;
-      if (warp == kScore && total > 0 && (ok = tiles(0))) qk(0);
-      for (int n = 0; n < total; ++n) {
+#pragma unroll 1
+      for (int n = -1; n < total; ++n) {  // round -1 only issues the first scores
+        if (n >= 0) {
+        // INTRA(n - 2) has read this P buffer
+        if (n >= 2) ok = sy.wait_warp(&bars[B_O + (n & 1)], ((n >> 1) - 1) & 1) && ok;
         ok = sy.wait_warp(&bars[B_QK], n & 1) && ok;
         tc_fence_after();
         const float* g = gates(n);
         const f2 hi = pk2(g[t], g[t]), lo = pk2(g[64 + t], g[64 + t]);
-        uint32_t pk[32];
-#pragma unroll
+        uint8_t* pt = sm + L::P + (n & 1) * 8192;
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
+          uint32_t pk[8];
           if (q >= 2 && warp == kScore) {  // columns past every row of this warp
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pk[8 * q + e] = 0;
+            for (int e = 0; e < 8; ++e) pk[e] = 0;
           } else {
             uint32_t r[16];
             GDP_TMEM_LD16(lb + T_QK + 16 * q, r);
             tmem_wait_ld();
+            const int ti = t - 16 * q;  // columns e <= ti are this row's
+            const float* gq = g + 16 * q;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const int i = 16 * q + e;
-              const float4 h4 = *reinterpret_cast<const float4*>(g + i);
-              const float4 l4 = *reinterpret_cast<const float4*>(g + 64 + i);
+              const float4 h4 = *reinterpret_cast<const float4*>(gq + e);
+              const float4 l4 = *reinterpret_cast<const float4*>(gq + 64 + e);
               const float2 x0 = upk2(add2(sub2(hi, pk2(h4.x, h4.y)), sub2(lo, pk2(l4.x, l4.y))));
               const float2 x1 = upk2(add2(sub2(hi, pk2(h4.z, h4.w)), sub2(lo, pk2(l4.z, l4.w))));
               const float2 y0 = upk2(mul2(mul2(pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2),
                                           pk2(ex2_approx(x0.x), ex2_approx(x0.y))));
               const float2 y1 = upk2(mul2(mul2(pk2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2),
                                           pk2(ex2_approx(x1.x), ex2_approx(x1.y))));
-              pk[i / 2] = cvt2(i <= t ? y0.x : 0.f, i + 1 <= t ? y0.y : 0.f);
-              pk[i / 2 + 1] = cvt2(i + 2 <= t ? y1.x : 0.f, i + 3 <= t ? y1.y : 0.f);
+              pk[e / 2] = cvt2(e <= ti ? y0.x : 0.f, e + 1 <= ti ? y0.y : 0.f);
+              pk[e / 2 + 1] = cvt2(e + 2 <= ti ? y1.x : 0.f, e + 3 <= ti ? y1.y : 0.f);
             }
           }
-        }
-        if (n > 0) ok = sy.wait_warp(&bars[B_O], (n - 1) & 1) && ok;  // INTRA(n - 1) has read P
-        uint8_t* pt = sm + L::P;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(pt + sw128_offset(t, 16 * j)) =
-              make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(pt + sw128_offset(t, 32 * q + 16 * j)) =
+                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        }
         fence_async_smem();
         tc_fence_before();
         // both warps have read the scores and written P
@@ -546,30 +568,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 2, 64, p;\n"
                      " selp.u32 %0, 1, 0, q;\n}\n" : "=r"(all) : "r"((uint32_t)ok) : "memory");
         if (!(ok = all != 0)) break;
+        }
         if (warp == kScore) {
           // the next scores go first if their tiles are there
           bool ahead = n + 1 == total;
-          if (!ahead && __all_sync(0xffffffffu, mbar_poll(&bars[B_READY + (n + 1) % L::NST], ((n + 1) / L::NST) & 1))) {
-            ok = tiles(n + 1);
-            qk(n + 1);
+          if (!ahead && __all_sync(0xffffffffu, mbar_poll(&bars[B_READY + (n + 1) % L::NST], ((n + 1) / L::NST) & 1)))
             ahead = true;
-          }
-          // the state before the chunk is published before the last output is read
-          if (n > 0) ok = sy.wait_warp(&bars[B_OREAD], (n - 1) & 1) && ok;
-          ok = sy.wait_warp(&bars[B_S], n & 1) && ok;
-          if (ok && elect_one()) {
-            tc_fence_after();
-            mma_run_ts<KD / 16, false, 16384, 32>(tmem + T_INTER, tmem + T_S,
-                                                  sdesc_sw128(smb + (n % L::NST) * L::STG, 16, 1024), id_qk);
-            mma_run<4, false, 0, 2048, 0, 32>(tmem + T_INTRA, sdesc_sw128(smb + (n % L::NST) * L::STG + L::QK, 8192, 1024),
-                                              sdesc_sw128(smb + L::P, 16, 1024), id_a);
-            mma_commit(&bars[B_O]);
-            mma_commit(&bars[B_FREE + n % L::NST]);
-          }
-          __syncwarp();
-          if (!ahead) {
-            ok = tiles(n + 1) && ok;
-            if (ok) qk(n + 1);
+#pragma unroll 1
+          for (int step = 0; step < 2; ++step) {
+            if (step == (ahead ? 0 : 1)) {
+              if (n + 1 < total) {
+                ok = tiles(n + 1) && ok;
+                qk(n + 1);
+              }
+              continue;
+            }
+            if (n < 0) continue;
+            // the state before the chunk is published before the last output is read
+            if (n > 0) ok = sy.wait_warp(&bars[B_OREAD], (n - 1) & 1) && ok;
+            ok = sy.wait_warp(&bars[B_S], n & 1) && ok;
+            if (ok && elect_one()) {
+              tc_fence_after();
+              const uint32_t tl = smb + (n % L::NST) * L::STG;
+              const uint64_t qd = sdesc_sw128(tl, 16, 1024);
+#pragma unroll 1
+              for (int i = 0; i < KD / 16; ++i)
+                mma_bf16_ts(tmem + T_INTER, tmem + T_S + 8 * i, qd + (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2), id_qk,
+                            i > 0);
+              const uint64_t vd = sdesc_sw128(tl + L::VT, 8192, 1024);
+              const uint64_t pd = sdesc_sw128(smb + L::P + (n & 1) * 8192, 16, 1024);
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) mma_bf16(tmem + T_INTRA, vd + i * (2048 >> 4), pd + i * 2, id_a, i > 0);
+              mma_commit(&bars[B_O + (n & 1)]);
+              mma_commit(&bars[B_FREE + n % L::NST]);
+            }
+            __syncwarp();
           }
         }
       }
@@ -601,17 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         }
         if (elect_one()) {
           const int t = lx.r.t0 - lx.off + lc * C;
-          const bool two = lx.v0 + 64 < V;
           uint8_t* tile = sm + st * L::STG;
           uint64_t* bar = &bars[B_FULL + st];
-          mbar_expect_tx(bar, 8192 * ((OUT ? 2 : 1) * L::KH + (two ? 2 : 1)));
-#pragma unroll
-          for (int hh = 0; hh < L::KH; ++hh) {
-            if (OUT) tma_load_4d(tile + hh * 16384, &map_q, 64 * hh, lx.h, t, lx.b, bar);
-            tma_load_4d(tile + hh * 16384 + 8192, &map_k, 64 * hh, lx.h, t, lx.b, bar);
+          // a tensor whose width is whole halves comes by one load, both halves in its box; of
+          // another the second half is its own load (zeros past the width), if there is one
+          const bool two = a.v_halves == 1 && lx.v0 + 64 < V, twok = KD == 128 && a.k_halves == 1;
+          mbar_expect_tx(bar, (OUT ? 2 : 1) * L::KT + 8192 * (two ? 2 : a.v_halves));
+          if (OUT) tma_load_5d(tile, &map_q, 0, lx.h, t, lx.b, 0, bar);
+          tma_load_5d(tile + L::KT, &map_k, 0, lx.h, t, lx.b, 0, bar);
+          if (a.v_halves == 1) tma_load_5d(tile + L::VT, &map_v, lx.v0, lx.hv, t, lx.b, 0, bar);
+          else tma_load_5d(tile + L::VT, &map_v, 0, lx.hv, t, lx.b, lx.v0 >> 6, bar);
+          if (twok) {
+            if (OUT) tma_load_5d(tile + 8192, &map_q, 64, lx.h, t, lx.b, 0, bar);
+            tma_load_5d(tile + L::KT + 8192, &map_k, 64, lx.h, t, lx.b, 0, bar);
           }
-          tma_load_4d(tile + L::QK, &map_v, lx.v0, lx.hv, t, lx.b, bar);
-          if (two) tma_load_4d(tile + L::QK + 8192, &map_v, lx.v0 + 64, lx.hv, t, lx.b, bar);
+          if (two) tma_load_5d(tile + L::VT + 8192, &map_v, lx.v0 + 64, lx.hv, t, lx.b, 0, bar);
         }
         __syncwarp();
         ++lc;
@@ -619,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       }
       return true;
     };
-    loads(0);
     for (int kk = 0; ok && (int64_t)kk * gridDim.x < a.items; ++kk) {
       const int it = nth_item(kk);
       Item& x = *reinterpret_cast<Item*>(sm + L::ITEM + (kSW + 1) * 64);
@@ -645,15 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
               const uint32_t o = i * 128 + (lane & 7) * 16;
 #pragma unroll
               for (int hh = 0; hh < L::KH; ++hh)
-                *reinterpret_cast<uint4*>(tile + hh * 16384 + 8192 + o) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(tile + L::QK + o) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(tile + L::QK + 8192 + o) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(tile + L::KT + hh * 8192 + o) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + L::VT + o) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + L::VT + 8192 + o) = make_uint4(0, 0, 0, 0);
             }
           fence_async_smem();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_READY + st]);
-        if (!(ok = loads(n + 1))) break;
       }
     }
     // nothing may still write shared memory when the CTA leaves
@@ -667,19 +702,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     for (int n = 0; n < total; ++n) {
       bool ok = tiles(n);
       if (n > 0) ok = sy.wait_warp(&bars[B_UREAD], (n - 1) & 1) && ok;
-      const uint64_t kd = sdesc_sw128(smb + (n % L::NST) * L::STG + 8192, 16384, 1024);
-#pragma unroll
+      const uint64_t kd = sdesc_sw128(smb + (n % L::NST) * L::STG + L::KT, 8192, 1024);
+#pragma unroll 1
       for (int ks = 0; ks < 4; ++ks) {
         ok = ok && sy.wait_warp(&bars[B_V + ks], n & 1);
         if (!ok) break;
         if (elect_one()) {
           tc_fence_after();
-          const uint64_t k = kd + ((ks * 2048) >> 4);
+          const uint64_t k = kd + (uint64_t)(ks * (2048 >> 4));
           const uint32_t av = tmem + T_V + 8 * ks;
-          if (ks == 0) mma_bf16_ts<false>(tmem + T_U, av + 64, k, id_u);
-          else mma_bf16_ts<true>(tmem + T_U, av + 64, k, id_u);
-          mma_bf16_ts<true>(tmem + T_U, av + 32, k, id_u);
-          mma_bf16_ts<true>(tmem + T_U, av, k, id_u);
+          mma_bf16_ts(tmem + T_U, av + 64, k, id_u, ks > 0);
+          mma_bf16_ts(tmem + T_U, av + 32, k, id_u, 1);
+          mma_bf16_ts(tmem + T_U, av, k, id_u, 1);
           mma_commit(&bars[B_VFREE + ks]);
           if (ks == 3) {
             mma_commit(&bars[B_U]);
@@ -722,17 +756,20 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [B][T][heads][width] with element strides s (batch, token, head); boxes of 64 x 1 x 64 x 1.
-bool map4(CUtensorMap* m, const void* base, int width, int heads, int T, int B, const int64_t* s) {
+// [B][T][heads][width] with element strides s (batch, token, head); boxes of 64 x 1 x 64 x 1,
+// `halves` of them side by side where the width is a multiple of 64 (1: any width).
+bool map5(CUtensorMap* m, const void* base, int width, int halves, int heads, int T, int B, const int64_t* s) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
+  const bool split = halves > 1;
+  const cuuint64_t dims[5] = {(cuuint64_t)(split ? 64 : width), (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B,
+                              (cuuint64_t)(split ? width / 64 : 1)};
   // the stride of a dimension of one entry is never used; the encoder wants a valid one
   const cuuint64_t some = 16;
-  const cuuint64_t st[3] = {heads > 1 ? (cuuint64_t)s[2] * 2 : some, T > 1 ? (cuuint64_t)s[1] * 2 : some,
-                            B > 1 ? (cuuint64_t)s[0] * 2 : some};
-  const cuuint32_t box[4] = {64, 1, 64, 1}, es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, es,
+  const cuuint64_t st[4] = {heads > 1 ? (cuuint64_t)s[2] * 2 : some, T > 1 ? (cuuint64_t)s[1] * 2 : some,
+                            B > 1 ? (cuuint64_t)s[0] * 2 : some, split ? (cuuint64_t)128 : some};
+  const cuuint32_t box[5] = {64, 1, 64, 1, (cuuint32_t)halves}, es[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, st, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -743,7 +780,7 @@ bool map_ok(const void* base, int heads, int T, int B, const int64_t* s) {
 }
 
 template <int KD, bool OUT>
-cudaError_t go(const ChunkArgs& a, const CUtensorMap* m) {
+cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
   constexpr int smem = Lay<KD, OUT>::BYTES;
   auto kern = linear_chunk_kernel<KD, OUT>;
   cudaError_t e = allow_smem<linear_chunk_kernel<KD, OUT>>(smem);
@@ -771,7 +808,7 @@ bool linear_tc_ok(const LinearProblem& p) {
 
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, kStateCost);
-  ChunkArgs a{};
+  TcArgs a{};
   a.p = p;
   a.nseg = x.nseg;
   a.Lseg = x.Lseg;
@@ -790,8 +827,10 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   }
   CUtensorMap m[4];
   const int64_t os[3] = {(int64_t)p.T * p.HV * p.V, (int64_t)p.HV * p.V, p.V};
-  if (!map4(&m[0], p.q, p.K, p.H, p.T, p.B, p.qs) || !map4(&m[1], p.k, p.K, p.H, p.T, p.B, p.ks) ||
-      !map4(&m[2], p.v, p.V, p.HV, p.T, p.B, p.vs) || !map4(&m[3], p.o, p.V, p.HV, p.T, p.B, os))
+  a.k_halves = p.K == 128 ? 2 : 1;
+  a.v_halves = p.V % 128 == 0 ? 2 : 1;
+  if (!map5(&m[0], p.q, p.K, a.k_halves, p.H, p.T, p.B, p.qs) || !map5(&m[1], p.k, p.K, a.k_halves, p.H, p.T, p.B, p.ks) ||
+      !map5(&m[2], p.v, p.V, a.v_halves, p.HV, p.T, p.B, p.vs) || !map5(&m[3], p.o, p.V, a.v_halves, p.HV, p.T, p.B, os))
     return cudaErrorInvalidValue;
   if (x.segS) {
     a.segS = reinterpret_cast<float*>(ws + x.segS);

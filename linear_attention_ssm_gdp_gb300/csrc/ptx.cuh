@@ -100,12 +100,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y,
-                                            int z, int w, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, int u, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(u),
+      "r"(smem_u32(bar))
       : "memory");
 }
 // Tiled bulk store shared -> global (coordinates must be >= 0; the innermost one
@@ -119,12 +120,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y,
-                                             int z, int w) {
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z, int w, int u) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
+      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::
           "l"(reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(u)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_commit() {
@@ -226,25 +227,14 @@ __device__ __forceinline__ bool elect_one() {
 
 // D[tmem] (+)= A[tmem] * B[smem]: row r of A in TMEM lane r, K elements packed two to a
 // 32-bit column.
-template <bool ACC>
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc) {
+                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// NK of them along K (16 elements, 8 columns of A, a step); B's steps as in mma_run.
-template <int NK, bool ACC0, int B_HI, int B_LO>
-__device__ __forceinline__ void mma_run_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b0,
-                                           uint32_t idesc) {
-  mma_bf16_ts<ACC0>(d_tmem, a_tmem, b0, idesc);
-#pragma unroll
-  for (int kk = 1; kk < NK; ++kk)
-    mma_bf16_ts<true>(d_tmem, a_tmem + 8 * kk,
-                      b0 + (uint64_t)((((kk >> 2) * B_HI) + (kk & 3) * B_LO) >> 4), idesc);
 }
 
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread is done.
