@@ -7,7 +7,7 @@
 //     S  <- e^{Gam} S + sum_i k_i (e^{Gam - Gam_i} v_i)^T.
 // Four products per chunk of 64 tokens, with the value columns on the 128 rows of
 // the tensor core's accumulator wherever the product has them:
-//     QK     [t | i]  = q k^T            (rows 64.. of the A tile are other data: unused)
+//     QK     [t | i]  = q k^T            (64 rows: 16 in each warp's quarter of the lanes)
 //     INTER  [v | t]  = S^T q^T          S as bf16
 //     INTRA  [v | t]  = v^T P^T          P = masked, decayed scores as bf16
 //     U      [v | k]  = v'^T k           v' = e^{Gam - Gam_i} v_i as three bf16 parts
@@ -28,9 +28,12 @@
 // split into groups that meet at mbarriers and work on neighbouring chunks at once:
 //     8 state warps   the state update, S as bf16; o = e^{Gam_t} INTER + INTRA, stores
 //     4 v' warps      v' of the next chunk
-//     2 score warps   P; the first issues QK, INTER and INTRA
+//     4 score warps   P
 //     1 warp          TMA loads, decays of the chunk, rows outside the sequence zeroed
-//     1 warp          issues U
+//     3 warps         issue U, QK, and INTER with INTRA
+// The roles' loops are rolled where they can be: together they have to fit the 32 KB
+// first-level instruction cache, or the SMs of a GPC wait for their common next level (with
+// them unrolled a third of the warps' time went there, at 80 % of that cache's bandwidth).
 //
 // Sequences are cut into segments when there are too few (sequence, head) pairs to
 // fill the GPU: a first launch of the same kernel without its output half (OUT =
@@ -50,9 +53,10 @@ using namespace linear;
 using bf16 = __nv_bfloat16;
 
 constexpr int kVT = 128;       // value columns per CTA
-constexpr int kSW = 8, kVW = 4;  // state warps, v' warps (multiples of 4)
-constexpr int kScore = kSW + kVW;  // first score warp; then loads and decays, then U
-constexpr int kThreads = (kScore + 4) * 32;
+constexpr int kSW = 8, kVW = 4;    // state warps, v' warps (multiples of 4)
+constexpr int kScore = kSW + kVW;  // first of the four score warps
+constexpr int kLoad = kScore + 4;  // loads and decays; then the issuers of U, QK, INTER and INTRA
+constexpr int kThreads = (kLoad + 4) * 32;
 
 // ------------------------------------------------------------------ arithmetic
 typedef unsigned long long f2;
@@ -196,10 +200,11 @@ struct Lay {
   static constexpr int BYTES = ITEM + (kSW + 2) * 64 + 1024;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-// full, ready, free by stage; v' ready and free by step; INTER and INTRA done by parity; the rest
-// single
+// full, ready, free by stage; v' ready and free by step; INTER and INTRA done, P done by parity;
+// the rest single
 enum {
-  B_FULL = 0, B_READY = 3, B_FREE = 6, B_V = 9, B_VFREE = 13, B_O = 17, B_QK = 19, B_OREAD, B_S, B_U, B_UREAD, B_N
+  B_FULL = 0, B_READY = 3, B_FREE = 6, B_V = 9, B_VFREE = 13, B_O = 17, B_P = 19, B_QK = 21, B_SREAD, B_OREAD, B_S, B_U,
+  B_UREAD, B_N
 };
 
 // TMEM columns: scores [64], INTER and INTRA [64] each, U [KD], S [KD / 2], v' [3][32]
@@ -229,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       int n = 1;
       if (i >= B_FREE && i < B_V) n = OUT ? 2 : 1;                   // both issuing warps
       if (i == B_OREAD || i == B_S || i == B_UREAD) n = kSW;         // state warps
-      if (i >= B_V && i < B_VFREE) n = 4;                            // v' warps
+      if ((i >= B_V && i < B_VFREE) || i == B_P || i == B_P + 1 || i == B_SREAD) n = 4;  // v' or score warps
       mbar_init(&bars[i], n);
     }
     fence_mbar_init();
     *s_dead = 0;
   }
-  if (warp == kScore + 2 && lane == 0) {
+  if (warp == kLoad && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
     if (OUT) prefetch_tmap(&map_q);
@@ -328,19 +333,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         const float wh = g[256], wl = g[257];
         const f2 wh2 = pk2(wh, wh), wl2 = pk2(wl, wl);
 #pragma unroll
-        for (int q = 0; q < NC; q += 32) {
-          constexpr int W = NC < 32 ? NC : 32;
-          uint32_t r[W];
-          if constexpr (W == 32) GDP_TMEM_LD32(lb + T_U + cb + q, r);
-          else GDP_TMEM_LD16(lb + T_U + cb + q, r);
+        for (int q = 0; q < NC; q += 16) {
+          uint32_t r[16];
+          GDP_TMEM_LD16(lb + T_U + cb + q, r);
           tmem_wait_ld();
-          if (q + W == NC) {
+          if (q + 16 == NC) {
             tc_fence_before();  // the next U may overwrite this one
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_UREAD]);
           }
 #pragma unroll
-          for (int e = 0; e < W; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             float* d = s + q + e;
             const f2 old = pk2(d[0], d[1]);
             const float2 f = upk2(fma2(wh2, old, fma2(wl2, old, pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])))));
@@ -369,42 +372,36 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         ok = sy.wait_warp(&bars[B_O + (n & 1)], (n >> 1) & 1) && ok;
         tc_fence_after();
         if (more && ok) publish();
-        // o of 16 value columns at a time, as fragments: pairs of rows t in a register
+        // the previous chunk's stores have read the tile
+        if (tid == 0) tma_store_wait_read();
+        if (!(ok = state_and(ok))) break;
+        // eight rows t at a time, as fragments: pairs of rows in a register, by value block of 8
         const float* ein = g + 192 + (64 / NP) * part + 2 * (lane & 3);
-        uint32_t out[32 / NP];  // by t block of 8, value block of 8
-#pragma unroll
-        for (int z = 0; z < 4 / NP; ++z) {  // 16 rows t at a time
-          uint32_t r[16], w[16];
+#pragma unroll 1
+        for (int z = 0; z < 8 / NP; ++z) {
+          const uint32_t col = (64 / NP) * part + 8 * z;
+          uint32_t r[8], w[8], out[4];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            GDP_TMEM_LD_16X256_X2(lb + (q << 20) + T_INTER + (64 / NP) * part + 16 * z, (r + 8 * q));
-            GDP_TMEM_LD_16X256_X2(lb + (q << 20) + T_INTRA + (64 / NP) * part + 16 * z, (w + 8 * q));
+            GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTER + col, (r + 4 * q));
+            GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTRA + col, (w + 4 * q));
           }
+          const float2 e = *reinterpret_cast<const float2*>(ein + 8 * z);
           tmem_wait_ld();
-          if (z == 4 / NP - 1) {  // the next products may overwrite these
+          if (z == 8 / NP - 1) {  // the next products may overwrite these
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_OREAD]);
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 e = *reinterpret_cast<const float2*>(ein + 16 * z + 8 * j);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int i = 8 * (u >> 1) + 4 * j + 2 * (u & 1);
-              const float2 f = upk2(fma2(pk2(e.x, e.y), pk2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                         pk2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]))));
-              out[8 * z + 4 * j + u] = cvt2(f.x, f.y);
-            }
+          for (int u = 0; u < 4; ++u) {
+            const float2 f = upk2(fma2(pk2(e.x, e.y), pk2(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])),
+                                       pk2(__uint_as_float(w[2 * u]), __uint_as_float(w[2 * u + 1]))));
+            out[u] = cvt2(f.x, f.y);
           }
+          // lanes 8 m .. address value block m
+          stmatrix_x4_trans(orow + z * 1024 + ((oc ^ (lane & 7)) << 4), out[0], out[1], out[2], out[3]);
         }
-        // the previous chunk's stores have read the tile
-        if (tid == 0) tma_store_wait_read();
-        if (!(ok = state_and(ok))) break;
-#pragma unroll
-        for (int j = 0; j < 8 / NP; ++j)  // rows 8 j .. of this part; lanes 8 m .. address value block m
-          stmatrix_x4_trans(orow + j * 1024 + ((oc ^ (lane & 7)) << 4), out[4 * j], out[4 * j + 1], out[4 * j + 2],
-                            out[4 * j + 3]);
         // rows of the tile inside the sequence
         const int base = x.r.t0 - x.off + c * C;
         const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
@@ -495,119 +492,57 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         if (lane == 0) mbar_arrive(&bars[B_V + ks]);
       }
     }
-  } else if (warp < kScore + 2) {
+  } else if (warp < kLoad) {
     // ---------------------------------------------------------------- scores
     if (OUT) {
-      const int t = (warp - kScore) * 32 + lane;
-      const uint32_t lb = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      // rows t0 + l / 4 (+ 8) of the chunk, columns 2 (l % 4) (+ 1) of a block of 8, as fragments
+      const int quarter = warp & 3, t0 = 16 * quarter + (lane >> 2), i0 = 2 * (lane & 3);
+      const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16) + T_QK;
+      // stores: lanes 8 m .. address rows 8 (m % 2) .. of the warp's 16 and 16-byte chunk m / 2
+      const int srow = 16 * quarter + 8 * ((lane >> 3) & 1) + (lane & 7);
+      const uint32_t prow = smb + L::P + srow * 128;
       const f2 sc2 = pk2(p.scale, p.scale);
-      const uint32_t id_qk = idesc_bf16(128, 64, false, false);  // and of INTER
-      const uint32_t id_a = idesc_bf16(128, 64, true, false);
-      // (loops are rolled where they can be: the roles together have to fit 32 KB of instruction
-      // cache, or every SM of a GPC waits for the same next level)
-      auto qk = [&](int n) {  // the first warp
-        if (elect_one()) {
-          tc_fence_after();
-          const uint32_t tl = smb + (n % L::NST) * L::STG;
-          const uint64_t qd = sdesc_sw128(tl, 16, 1024), kd = sdesc_sw128(tl + L::KT, 16, 1024);
-#pragma unroll 1
-          for (int i = 0; i < KD / 16; ++i) {
-            const uint64_t o = (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2);
-            mma_bf16(tmem + T_QK, qd + o, kd + o, id_qk, i > 0);
-          }
-          mma_commit(&bars[B_QK]);
-        }
-        __syncwarp();
-      };
-      bool ok = true;
-#pragma unroll 1
-      for (int n = -1; n < total; ++n) {  // round -1 only issues the first scores
-        if (n >= 0) {
+      for (int n = 0; n < total; ++n) {
         // INTRA(n - 2) has read this P buffer
-        if (n >= 2) ok = sy.wait_warp(&bars[B_O + (n & 1)], ((n >> 1) - 1) & 1) && ok;
-        ok = sy.wait_warp(&bars[B_QK], n & 1) && ok;
+        if (n >= 2 && !sy.wait_warp(&bars[B_O + (n & 1)], ((n >> 1) - 1) & 1)) break;
+        if (!sy.wait_warp(&bars[B_QK], n & 1)) break;
         tc_fence_after();
         const float* g = gates(n);
-        const f2 hi = pk2(g[t], g[t]), lo = pk2(g[64 + t], g[64 + t]);
-        uint8_t* pt = sm + L::P + (n & 1) * 8192;
+        const f2 hi0 = pk2(g[t0], g[t0]), lo0 = pk2(g[64 + t0], g[64 + t0]);
+        const f2 hi1 = pk2(g[t0 + 8], g[t0 + 8]), lo1 = pk2(g[72 + t0], g[72 + t0]);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          uint32_t pk[8];
-          if (q >= 2 && warp == kScore) {  // columns past every row of this warp
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pk[e] = 0;
-          } else {
-            uint32_t r[16];
-            GDP_TMEM_LD16(lb + T_QK + 16 * q, r);
+          uint32_t pk[4] = {0, 0, 0, 0};
+          if (q <= quarter) {  // else columns past every row of this warp
+            uint32_t r[8];
+            GDP_TMEM_LD_16X256_X2(lb + 16 * q, r);
+            const float* gq = g + 16 * q + i0;
+            const float2 h0 = *reinterpret_cast<const float2*>(gq), h1 = *reinterpret_cast<const float2*>(gq + 8);
+            const float2 l0 = *reinterpret_cast<const float2*>(gq + 64), l1 = *reinterpret_cast<const float2*>(gq + 72);
             tmem_wait_ld();
-            const int ti = t - 16 * q;  // columns e <= ti are this row's
-            const float* gq = g + 16 * q;
+            if (q == quarter) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_SREAD]);
+            }
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 h4 = *reinterpret_cast<const float4*>(gq + e);
-              const float4 l4 = *reinterpret_cast<const float4*>(gq + 64 + e);
-              const float2 x0 = upk2(add2(sub2(hi, pk2(h4.x, h4.y)), sub2(lo, pk2(l4.x, l4.y))));
-              const float2 x1 = upk2(add2(sub2(hi, pk2(h4.z, h4.w)), sub2(lo, pk2(l4.z, l4.w))));
-              const float2 y0 = upk2(mul2(mul2(pk2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2),
-                                          pk2(ex2_approx(x0.x), ex2_approx(x0.y))));
-              const float2 y1 = upk2(mul2(mul2(pk2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2),
-                                          pk2(ex2_approx(x1.x), ex2_approx(x1.y))));
-              pk[e / 2] = cvt2(e <= ti ? y0.x : 0.f, e + 1 <= ti ? y0.y : 0.f);
-              pk[e / 2 + 1] = cvt2(e + 2 <= ti ? y1.x : 0.f, e + 3 <= ti ? y1.y : 0.f);
+            for (int u = 0; u < 4; ++u) {  // block u / 2 of 8 columns, rows + 8 (u % 2)
+              const f2 h = u < 2 ? pk2(h0.x, h0.y) : pk2(h1.x, h1.y), l = u < 2 ? pk2(l0.x, l0.y) : pk2(l1.x, l1.y);
+              const float2 x = upk2(add2(sub2(u & 1 ? hi1 : hi0, h), sub2(u & 1 ? lo1 : lo0, l)));
+              const float2 y = upk2(mul2(mul2(pk2(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])), sc2),
+                                         pk2(ex2_approx(x.x), ex2_approx(x.y))));
+              const int d = t0 + 8 * (u & 1) - 16 * q - 8 * (u >> 1) - i0;  // t - i
+              pk[u] = cvt2(d >= 0 ? y.x : 0.f, d >= 1 ? y.y : 0.f);
             }
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint4*>(pt + sw128_offset(t, 32 * q + 16 * j)) =
-                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          stmatrix_x4(prow + (n & 1) * 8192 + (((2 * q + (lane >> 4)) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
         }
         fence_async_smem();
-        tc_fence_before();
-        // both warps have read the scores and written P
-        uint32_t all;
-        asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 2, 64, p;\n"
-                     " selp.u32 %0, 1, 0, q;\n}\n" : "=r"(all) : "r"((uint32_t)ok) : "memory");
-        if (!(ok = all != 0)) break;
-        }
-        if (warp == kScore) {
-          // the next scores go first if their tiles are there
-          bool ahead = n + 1 == total;
-          if (!ahead && __all_sync(0xffffffffu, mbar_poll(&bars[B_READY + (n + 1) % L::NST], ((n + 1) / L::NST) & 1)))
-            ahead = true;
-#pragma unroll 1
-          for (int step = 0; step < 2; ++step) {
-            if (step == (ahead ? 0 : 1)) {
-              if (n + 1 < total) {
-                ok = tiles(n + 1) && ok;
-                qk(n + 1);
-              }
-              continue;
-            }
-            if (n < 0) continue;
-            // the state before the chunk is published before the last output is read
-            if (n > 0) ok = sy.wait_warp(&bars[B_OREAD], (n - 1) & 1) && ok;
-            ok = sy.wait_warp(&bars[B_S], n & 1) && ok;
-            if (ok && elect_one()) {
-              tc_fence_after();
-              const uint32_t tl = smb + (n % L::NST) * L::STG;
-              const uint64_t qd = sdesc_sw128(tl, 16, 1024);
-#pragma unroll 1
-              for (int i = 0; i < KD / 16; ++i)
-                mma_bf16_ts(tmem + T_INTER, tmem + T_S + 8 * i, qd + (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2), id_qk,
-                            i > 0);
-              const uint64_t vd = sdesc_sw128(tl + L::VT, 8192, 1024);
-              const uint64_t pd = sdesc_sw128(smb + L::P + (n & 1) * 8192, 16, 1024);
-#pragma unroll 1
-              for (int i = 0; i < 4; ++i) mma_bf16(tmem + T_INTRA, vd + i * (2048 >> 4), pd + i * 2, id_a, i > 0);
-              mma_commit(&bars[B_O + (n & 1)]);
-              mma_commit(&bars[B_FREE + n % L::NST]);
-            }
-            __syncwarp();
-          }
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_P + (n & 1)]);
       }
     }
-  } else if (warp == kScore + 2) {
+  } else if (warp == kLoad) {
     // ---------------------------------------------------------------- loads, decays
     int n = 0;
     bool ok = true;
@@ -696,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
     }
-  } else {
+  } else if (warp == kLoad + 1) {
     // ---------------------------------------------------------------- U
     const uint32_t id_u = idesc_bf16(128, KD, false, true);
     for (int n = 0; n < total; ++n) {
@@ -724,10 +659,54 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       }
       if (!ok) break;
     }
+  } else if (OUT && warp == kLoad + 2) {
+    // ---------------------------------------------------------------- QK
+    const uint32_t id = idesc_bf16(64, 64, false, false);
+    for (int n = 0; n < total; ++n) {
+      if (!tiles(n)) break;
+      if (n > 0 && !sy.wait_warp(&bars[B_SREAD], (n - 1) & 1)) break;
+      if (elect_one()) {
+        tc_fence_after();
+        const uint32_t tl = smb + (n % L::NST) * L::STG;
+        const uint64_t qd = sdesc_sw128(tl, 16, 1024), kd = sdesc_sw128(tl + L::KT, 16, 1024);
+#pragma unroll 1
+        for (int i = 0; i < KD / 16; ++i) {
+          const uint64_t o = (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2);
+          mma_bf16(tmem + T_QK, qd + o, kd + o, id, i > 0);
+        }
+        mma_commit(&bars[B_QK]);
+      }
+      __syncwarp();
+    }
+  } else if (OUT) {
+    // ---------------------------------------------------------------- INTER, INTRA
+    const uint32_t id_i = idesc_bf16(128, 64, false, false), id_a = idesc_bf16(128, 64, true, false);
+    for (int n = 0; n < total; ++n) {
+      if (!tiles(n)) break;
+      // the state before the chunk, its scores, and the last output out of the way
+      if (!sy.wait_warp(&bars[B_S], n & 1)) break;
+      if (!sy.wait_warp(&bars[B_P + (n & 1)], (n >> 1) & 1)) break;
+      if (n > 0 && !sy.wait_warp(&bars[B_OREAD], (n - 1) & 1)) break;
+      if (elect_one()) {
+        tc_fence_after();
+        const uint32_t tl = smb + (n % L::NST) * L::STG;
+        const uint64_t qd = sdesc_sw128(tl, 16, 1024);
+#pragma unroll 1
+        for (int i = 0; i < KD / 16; ++i)
+          mma_bf16_ts(tmem + T_INTER, tmem + T_S + 8 * i, qd + (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2), id_i, i > 0);
+        const uint64_t vd = sdesc_sw128(tl + L::VT, 8192, 1024);
+        const uint64_t pd = sdesc_sw128(smb + L::P + (n & 1) * 8192, 16, 1024);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) mma_bf16(tmem + T_INTRA, vd + i * (2048 >> 4), pd + i * 2, id_a, i > 0);
+        mma_commit(&bars[B_O + (n & 1)]);
+        mma_commit(&bars[B_FREE + n % L::NST]);
+      }
+      __syncwarp();
+    }
   }
   __syncwarp();
   if (*s_dead) {  // products in flight end before their operands and columns go away
-    if (warp == kScore + 3 && lane == 0) {
+    if (warp == kLoad + 1 && lane == 0) {
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) {}  // a chunk's products take microseconds
     }

@@ -185,14 +185,16 @@ Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt,
   x.nseg = 1;
   x.Lseg = std::max(1, chunks) * C;
   if (!packed) {
-    // time in units of a chunk of the second pass: rounds of items over the SMs, the state pass
-    // at state_cost of that and its two extra launches at about eight chunks
+    // time in units of a chunk of the second pass: rounds of items over the SMs, each item with
+    // about three chunks' time for its states and its start, the state pass at state_cost of
+    // that and the two extra launches at about eight chunks
     const int64_t units = heads * B;
-    double best = (double)cdiv(units, G) * chunks;
+    double best = (double)cdiv(units, G) * (chunks + 3);
     for (int n = 2; n <= chunks && n <= 64; ++n) {
       const int64_t per = cdiv(chunks, n);
       if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
-      const double t = (double)cdiv(units * n, G) * per + state_cost * cdiv(units * (n - 1), G) * per + 8.0;
+      const double t =
+          ((double)cdiv(units * n, G) + state_cost * cdiv(units * (n - 1), G)) * (per + 3) + 8.0;
       if (t < 0.95 * best) {
         best = t;
         x.nseg = n;

@@ -308,9 +308,13 @@ __device__ __forceinline__ uint32_t sw64_chunk(uint32_t r, uint32_t j) {
 
 // Registers -> TMEM, the same lane and column mapping.
 // The 16-lane shapes: taddr names the first of 16 lanes (a half of the warp's quarter).
-// 16x256b.x2 (16 columns): register 4 j + 2 a + b of lane l holds TMEM lane 8 a + l / 4, column
+// 16x256b.x2 (16 columns; x1: 8): register 4 j + 2 a + b of lane l holds TMEM lane 8 a + l / 4, column
 // 8 j + 2 (l % 4) + b. 16x128b.x2 (8 columns): register 2 j + a holds lane 8 a + l / 4, column
 // 4 j + l % 4: the fragments that ldmatrix and stmatrix move, transposed or not.
+#define GDP_TMEM_LD_16X256_X1(taddr, r)                                                    \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"              \
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])                           \
+               : "r"(taddr))
 #define GDP_TMEM_LD_16X256_X2(taddr, r)                                                    \
   asm volatile(                                                                           \
       "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"           \
@@ -328,6 +332,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                            uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1,
