@@ -35,7 +35,15 @@ struct alignas(n * sizeof(T) < 16 ? n * sizeof(T) : 16) Pack {
   T e[n];
 };
 
-__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + expf(-a)); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a / (1 + e^-a): 2^x by the hardware (2^-22; the exponent's rounding adds |a| 2^-24 where e^-a
+// counts at all, |a| below ~20) and an approximate division (2 ulp; 0 for a denominator above
+// 2^126, where the quotient is below 1e-36).
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + ex2(-1.44269504f * a)); }
 
 struct NormArgs {
   const void *x, *gate;
@@ -59,28 +67,29 @@ __device__ __forceinline__ float finish(const NormArgs& a, float z, float gt) {
 }
 
 // ---------------------------------------------------------------- one position per sample
-// TG lanes hold one (sample, group): NV 16-byte vectors each; U of them per lane group are
-// in flight at once.
+// TG lanes hold one (sample, group): NV 16-byte vectors each; U samples per lane group are in
+// flight at once, far apart in N so that they share their channels' weights. 8192 x 4096 bf16
+// with a gate: see the table of measured cases; scalar weight loads and an exact exponential
+// made the kernel issue-bound (77 us).
 template <typename TX, typename TO, int TG, int NV, int U, bool GATE>
-__global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ NormArgs a, int64_t Nu) {
   pdl_wait();
   constexpr int VEC = 16 / sizeof(TX);
   using PX = Pack<TX, VEC>;
   using PO = Pack<TO, VEC>;
   const int sub = threadIdx.x % TG;
-  const int64_t item0 = (int64_t)blockIdx.x * (256 / TG * U) + threadIdx.x / TG;
-  const int64_t items = a.N * a.G;
-  const int nvec = a.Cg / VEC;
+  const int64_t item = (int64_t)blockIdx.x * (256 / TG) + threadIdx.x / TG;  // of the first Nu samples
+  const int64_t n0 = item / a.G;
+  const int c = (int)(item - n0 * a.G) * a.Cg, nvec = a.Cg / VEC;
   PX x[U][NV];
   PO gt[GATE ? U : 1][GATE ? NV : 1];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t it = item0 + u * (256 / TG), n = it / a.G;
-    const int c = (int)(it - n * a.G) * a.Cg;
+    const int64_t n = n0 + u * Nu;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int vi = sub + j * TG;
-      if (it < items && vi < nvec) {
+      if (n0 < Nu && n < a.N && vi < nvec) {
         x[u][j] = *reinterpret_cast<const PX*>(static_cast<const TX*>(a.x) + n * a.x_sn + c + vi * VEC);
         if (GATE)
           gt[u][j] = *reinterpret_cast<const PO*>(static_cast<const TO*>(a.gate) + n * a.g_sn + c + vi * VEC);
@@ -90,11 +99,23 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
       }
     }
   }
+  float w[NV][VEC], bi[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int vi = sub + j * TG, cc = c + vi * VEC;
+    const bool on = n0 < Nu && vi < nvec;
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {  // (C is a multiple of VEC; the host checks the 16-byte bases)
+      const float4 w4 = on && a.w ? __ldg(reinterpret_cast<const float4*>(a.w + cc + e)) : make_float4(1.f, 1.f, 1.f, 1.f);
+      const float4 b4 = on && a.b ? __ldg(reinterpret_cast<const float4*>(a.b + cc + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[j][e] = w4.x; w[j][e + 1] = w4.y; w[j][e + 2] = w4.z; w[j][e + 3] = w4.w;
+      bi[j][e] = b4.x; bi[j][e + 1] = b4.y; bi[j][e + 2] = b4.z; bi[j][e + 3] = b4.w;
+    }
+  }
   const float inv = 1.f / (float)a.Cg;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t it = item0 + u * (256 / TG), n = it / a.G;
-    const int c = (int)(it - n * a.G) * a.Cg;
+    const int64_t n = n0 + u * Nu;
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -118,17 +139,13 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int vi = sub + j * TG;
-      if (it >= items || vi >= nvec) continue;
-      const int cc = c + vi * VEC;
+      if (n0 >= Nu || n >= a.N || vi >= nvec) continue;
       PO out;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float z = (to_f(x[u][j].e[e]) - mean) * rstd;
-        if (a.w) z *= a.w[cc + e];
-        if (a.b) z += a.b[cc + e];
-        put(&out.e[e], finish<GATE>(a, z, GATE ? to_f(gt[GATE ? u : 0][GATE ? j : 0].e[e]) : 0.f));
-      }
-      *reinterpret_cast<PO*>(static_cast<TO*>(a.y) + n * a.C + cc) = out;
+      for (int e = 0; e < VEC; ++e)
+        put(&out.e[e], finish<GATE>(a, fmaf((to_f(x[u][j].e[e]) - mean) * rstd, w[j][e], bi[j][e]),
+                                    GATE ? to_f(gt[GATE ? u : 0][GATE ? j : 0].e[e]) : 0.f));
+      *reinterpret_cast<PO*>(static_cast<TO*>(a.y) + n * a.C + c + vi * VEC) = out;
     }
   }
 }
@@ -203,13 +220,22 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
   if (on)
-    for (int r = ty; r < nrow; r += nty)
-      for (int c = tx; c < cols; c += tc) {
-        const PX x = *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
-        if (a.resident) keep[(int64_t)r * cols + c] = x;
+    for (int c = tx; c < cols; c += tc) {
+      constexpr int D = 8;  // rows in flight
+      for (int r = ty; r < nrow; r += D * nty) {
+        PX x[D];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
+        for (int d = 0; d < D; ++d)
+          if (r + d * nty < nrow) x[d] = *reinterpret_cast<const PX*>(xb + (int64_t)(r + d * nty) * a.x_sl + c * VEC);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+          if (r + d * nty < nrow) {
+            if (a.resident) keep[(int64_t)(r + d * nty) * cols + c] = x[d];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] += to_f(x[d].e[e]);
+          }
       }
+    }
   reduce(0);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -218,10 +244,10 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   }
   __syncthreads();
   if (on)
-    for (int r = ty; r < nrow; r += nty)
-      for (int c = tx; c < cols; c += tc) {
+    for (int c = tx; c < cols; c += tc)
+      for (int r = ty; r < nrow; r += nty) {
         const PX x = a.resident ? keep[(int64_t)r * cols + c]
-                                : *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
+                                : *reinterpret_cast<const PX*>(xb + (int64_t)r * a.x_sl + c * VEC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float d = to_f(x.e[e]) - mean_of[e];
@@ -245,9 +271,9 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
       }
       for (int r = ty; r < nrow; r += nty) {
         const PX x = a.resident ? keep[(int64_t)r * cols + c]
-                                : *reinterpret_cast<const PX*>(xb + r * a.x_sl + c * VEC);
+                                : *reinterpret_cast<const PX*>(xb + (int64_t)r * a.x_sl + c * VEC);
         PO gt, out;
-        if (GATE) gt = *reinterpret_cast<const PO*>(gb + r * a.g_sl + c * VEC);
+        if (GATE) gt = *reinterpret_cast<const PO*>(gb + (int64_t)r * a.g_sl + c * VEC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           put(&out.e[e], finish<GATE>(a, fmaf((to_f(x.e[e]) - mean_of[e]) * rstd[e], ww[e], bb[e]),
@@ -260,10 +286,10 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
 
 template <typename TX, typename TO, int TG, int NV, int U>
 cudaError_t go_rows(const NormArgs& a, cudaStream_t s) {
-  const int64_t grid = cdiv(a.N * a.G, 256 / TG * U);
+  const int64_t Nu = cdiv(a.N, U), grid = cdiv(Nu * a.G, 256 / TG);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return a.gate ? launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, true>, dim3((unsigned)grid), dim3(256), 0, s, a)
-                : launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, false>, dim3((unsigned)grid), dim3(256), 0, s, a);
+  return a.gate ? launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, true>, dim3((unsigned)grid), dim3(256), 0, s, a, Nu)
+                : launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, false>, dim3((unsigned)grid), dim3(256), 0, s, a, Nu);
 }
 
 template <typename TX, typename TO, int VEC, bool GATE>
@@ -323,15 +349,15 @@ cudaError_t run(NormArgs a, cudaStream_t s) {
   const bool rows_ok = a.x_sn % VEC == 0 && a.x_sl % VEC == 0 && aligned(a.x, 16) &&
                        aligned(a.y, GA) && a.C % VEC == 0 &&
                        (!a.gate || (a.g_sn % VEC == 0 && a.g_sl % VEC == 0 && aligned(a.gate, GA)));
-  if (a.L == 1 && rows_ok && a.Cg % VEC == 0) {
+  if (a.L == 1 && rows_ok && a.Cg % VEC == 0 && aligned(a.w, 16) && aligned(a.b, 16)) {
     const int nvec = a.Cg / VEC;
-    if (nvec <= 1) return go_rows<TX, TO, 1, 1, 2>(a, s);
-    if (nvec <= 2) return go_rows<TX, TO, 2, 1, 2>(a, s);
-    if (nvec <= 4) return go_rows<TX, TO, 4, 1, 2>(a, s);
-    if (nvec <= 8) return go_rows<TX, TO, 8, 1, 2>(a, s);
-    if (nvec <= 16) return go_rows<TX, TO, 16, 1, 2>(a, s);
-    if (nvec <= 32) return go_rows<TX, TO, 32, 1, 2>(a, s);
-    if (nvec <= 64) return go_rows<TX, TO, 32, 2, 1>(a, s);
+    if (nvec <= 1) return go_rows<TX, TO, 1, 1, 4>(a, s);
+    if (nvec <= 2) return go_rows<TX, TO, 2, 1, 4>(a, s);
+    if (nvec <= 4) return go_rows<TX, TO, 4, 1, 4>(a, s);
+    if (nvec <= 8) return go_rows<TX, TO, 8, 1, 4>(a, s);
+    if (nvec <= 16) return go_rows<TX, TO, 16, 1, 4>(a, s);
+    if (nvec <= 32) return go_rows<TX, TO, 32, 1, 4>(a, s);
+    if (nvec <= 64) return go_rows<TX, TO, 32, 2, 2>(a, s);
     if (nvec <= 128) return go_rows<TX, TO, 32, 4, 1>(a, s);
   }
   // several groups share a vector only where the set of groups ends on one

@@ -146,8 +146,7 @@ __device__ __forceinline__ int chunks_of(const ChunkArgs& a, int it) {
 // (The loop is not inlined: it would be a third of the kernel's code.)
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, int* status) {
   uint64_t t0 = 0;
-  for (int i = 0; !mbar_test(bar, parity); ++i) {
-    if ((i & 15) != 15) continue;
+  while (!mbar_test_for(bar, parity, 20000)) {
     if (*dead) return false;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;

@@ -11,18 +11,17 @@
 // The sum over K of a read-out is in-thread over R rows, then shuffles across
 // the lanes of equal columns, then the eight warps through shared memory in a
 // fixed order. Sums and states are fp32; o alone is rounded, to the inputs' type.
-// The decay factor is a pair of floats (hi + lo from a 64-bit exponential, one per
-// step): a decay that stays the same from token to token, rounded to 24 bits, would
+// The decay factor is a pair of floats: a decay that stays the same from token to token, rounded to 24 bits, would
 // drift from e^{n g} by n roundings in one direction.
 #include <algorithm>
 
-#include "linear_internal.cuh"
+#include "linear_chunk.cuh"
 
 namespace gdp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStep = 16;  // steps staged in shared memory at a time
+constexpr int kStep = 16;  // most steps of a call
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -38,22 +37,22 @@ struct WalkArgs {
 };
 
 // Page of block b of request r, or -1 when it has none in the pool.
-__device__ __forceinline__ int page_of(const LinearProblem& p, int r, int64_t b) {
-  if (b < 0 || b >= p.width) return -1;
+__device__ __forceinline__ int page_of(const LinearProblem& p, int r, uint32_t b) {
+  if (b >= (uint32_t)p.width) return -1;
   const int pg = p.tables[(int64_t)r * p.width + b];
   return pg >= 0 && pg < p.n_pages ? pg : -1;
 }
 
 template <typename T, int VEC, int R>
-__global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_constant__ WalkArgs a) {
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : R <= 16 ? 2 : 1) linear_walk_kernel(const __grid_constant__ WalkArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) float sm[];
   const LinearProblem& p = a.p;
-  const int K = p.K, V = p.V, VS = a.VS, tid = threadIdx.x;
-  float* sq = sm;                    // [kStep][K]
-  float* sk = sq + kStep * K;        // [kStep][K]
-  float* sv = sk + kStep * K;        // [kStep][VS]
-  float* sw = sv + kStep * VS;       // [2][kStep] decay factors, hi and lo
+  const int K = p.K, V = p.V, VS = a.VS, tid = threadIdx.x, len = p.T;
+  float* sq = sm;                    // [len][K]
+  float* sk = sq + len * K;          // [len][K]
+  float* sv = sk + len * K;          // [len][VS]
+  float* sw = sv + len * VS;         // [2][kStep] decay factors, hi and lo
   float* red = sw + 2 * kStep;       // [2][8][VS]
   const int slice = blockIdx.x % a.slices, rest = blockIdx.x / a.slices;
   const int hv = rest % p.HV, seq = rest / p.HV;
@@ -62,54 +61,30 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
   const int cg = tid % CG, rg = tid / CG, c0 = v0 + cg * VEC;
   const bool col_ok = c0 < V;                    // VEC divides V
 
-  const int len = p.T, ctx = p.ctx ? p.ctx[seq] : 0;
+  // A padded request names no page for its last token; one with a page outside the pool or a
+  // negative context is ill-defined and treated the same (and reported).
   const float* src = p.s0 ? p.s0 + ((int64_t)seq * p.HV + hv) * K * V : nullptr;
-  bool live = true;
+  uint32_t ctx = 0, b0 = 0, w0 = 0, w1 = 0;  // blocks read and written: [b0, w1], [w0, w1]
+  bool live = true, bad = false;
   if (p.pool) {
-    // a padding request names no page for its last token; one whose pages lie
-    // outside the pool, or that writes a page which another request reads or
-    // writes, would make the update ill-defined and is treated the same
-    const int64_t b0 = ctx > 0 ? (ctx - 1) / p.block : 0;
-    const int64_t w0 = ctx >= 0 ? ctx / p.block : 0, w1 = ((int64_t)ctx + len - 1) / p.block;
-    const int last = ctx >= 0 && w1 < p.width ? p.tables[(int64_t)seq * p.width + w1] : -2;
-    live = last != -1;
-    bool bad = false;
+    const int c = p.ctx[seq];
+    ctx = (uint32_t)max(c, 0);
+    b0 = (max(ctx, 1u) - 1) / (uint32_t)p.block;
+    w0 = ctx / (uint32_t)p.block;
+    w1 = (ctx + (uint32_t)len - 1) / (uint32_t)p.block;
+    live = c < 0 || w1 >= (uint32_t)p.width || p.tables[(int64_t)seq * p.width + w1] != -1;
     if (live) {
-      for (int64_t j = b0; j <= w1; ++j) bad |= page_of(p, seq, j) < 0;
-      bad |= ctx < 0;
-      for (int r = tid; r < p.N_seq && !bad; r += kThreads) {
-        const int rc = p.ctx[r];
-        if (r == seq || rc < 0) continue;
-        const int64_t r1 = ((int64_t)rc + len - 1) / p.block;
-        if (page_of(p, r, r1) < 0) continue;
-        for (int64_t i = rc > 0 ? (rc - 1) / p.block : 0; i <= r1; ++i) {
-          const int pg = page_of(p, r, i);
-          for (int64_t j = w0; j <= w1; ++j) bad |= pg >= 0 && pg == page_of(p, seq, j);
-        }
-      }
+      bad = c < 0;
+      for (uint32_t j = b0; j <= w1 && !bad; ++j) bad = page_of(p, seq, j) < 0;
     }
-    if (__syncthreads_or(bad)) {
-      if (tid == 0 && p.status) atomicExch(p.status, 1);
-      live = false;
-    }
+    if (live && !bad && ctx > 0) src = p.pool + ((int64_t)page_of(p, seq, b0) * p.HV + hv) * K * V;
   }
-  T* o = static_cast<T*>(p.o) + (int64_t)seq * len * p.HV * V + (int64_t)hv * V;
-  const int64_t orow = (int64_t)p.HV * V;
-  if (!live) {
-    for (int i = tid; i < len * VS; i += kThreads) {
-      const int c = v0 + i % VS;
-      if (c < V) put(o + (i / VS) * orow + c, 0.f);
-    }
-    return;
-  }
-  if (p.pool && ctx > 0)
-    src = p.pool + ((int64_t)page_of(p, seq, (ctx - 1) / p.block) * p.HV + hv) * K * V;
-
+  // the state's loads go out first; everything up to the first step runs behind them
   float s[R][VEC];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int row = rg + RG * i;
-    if (src && col_ok && row < K) {
+    if (src && live && !bad && col_ok && row < K) {
       if (VEC == 4) {
         const float4 x = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)row * V + c0));
         s[i][0] = x.x; s[i][1 % VEC] = x.y; s[i][2 % VEC] = x.z; s[i][3 % VEC] = x.w;
@@ -120,6 +95,48 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
 #pragma unroll
       for (int c = 0; c < VEC; ++c) s[i][c] = 0.f;
     }
+  }
+  if (p.pool && live && !bad) {
+    // a request that writes a page which another one reads or writes would race with it
+    for (int r = tid; r < p.N_seq && !bad; r += kThreads) {
+      const int rc = p.ctx[r];
+      if (r == seq || rc < 0) continue;
+      const uint32_t r1 = ((uint32_t)rc + (uint32_t)len - 1) / (uint32_t)p.block;
+      if (page_of(p, r, r1) < 0) continue;
+      for (uint32_t i = (max((uint32_t)rc, 1u) - 1) / (uint32_t)p.block; i <= r1; ++i) {
+        const int pg = page_of(p, r, i);
+        for (uint32_t j = w0; j <= w1; ++j) bad |= pg >= 0 && pg == page_of(p, seq, j);
+      }
+    }
+  }
+  const T* q = static_cast<const T*>(p.q) + seq * p.qs[0] + h * p.qs[2];
+  const T* k = static_cast<const T*>(p.k) + seq * p.ks[0] + h * p.ks[2];
+  const T* v = static_cast<const T*>(p.v) + seq * p.vs[0] + hv * p.vs[2];
+  for (int t = 0; t < len; ++t) {
+    for (int c = tid; c < K; c += kThreads) {
+      sq[t * K + c] = to_f(q[t * p.qs[1] + c]);
+      sk[t * K + c] = to_f(k[t * p.ks[1] + c]);
+    }
+    if (tid < VS) sv[t * VS + tid] = v0 + tid < V ? to_f(v[t * p.vs[1] + v0 + tid]) : 0.f;
+  }
+  if (tid < len) {
+    const float g = !p.g ? 0.f : p.g_token ? p.g[((int64_t)seq * len + tid) * p.HV + hv] : p.g[hv];
+    const float2 w = linear::exp_pair(g, 0.f);
+    sw[tid] = w.x;
+    sw[kStep + tid] = w.y;
+  }
+  T* o = static_cast<T*>(p.o) + (int64_t)seq * len * p.HV * V + (int64_t)hv * V;
+  const int64_t orow = (int64_t)p.HV * V;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && p.status) atomicExch(p.status, 1);
+    live = false;
+  }
+  if (!live) {
+    for (int i = tid; i < len * VS; i += kThreads) {
+      const int c = v0 + i % VS;
+      if (c < V) put(o + (i / VS) * orow + c, 0.f);
+    }
+    return;
   }
   auto store = [&](float* dst) {
 #pragma unroll
@@ -134,74 +151,51 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const __grid_cons
       }
     }
   };
-
-  const T* q = static_cast<const T*>(p.q) + seq * p.qs[0] + h * p.qs[2];
-  const T* k = static_cast<const T*>(p.k) + seq * p.ks[0] + h * p.ks[2];
-  const T* v = static_cast<const T*>(p.v) + seq * p.vs[0] + hv * p.vs[2];
-  const float* g = !p.g ? nullptr : p.g_token ? p.g + (int64_t)seq * len * p.HV + hv : p.g + hv;
-  for (int base = 0; base < len; base += kStep) {
-    const int m = min(kStep, len - base);
-    __syncthreads();
-    for (int i = tid; i < m * K; i += kThreads) {
-      const int t = i / K, c = i - t * K;
-      sq[i] = to_f(q[(int64_t)(base + t) * p.qs[1] + c]);
-      sk[i] = to_f(k[(int64_t)(base + t) * p.ks[1] + c]);
-    }
-    for (int i = tid; i < m * VS; i += kThreads) {
-      const int t = i / VS, c = i - t * VS;
-      sv[i] = v0 + c < V ? to_f(v[(int64_t)(base + t) * p.vs[1] + v0 + c]) : 0.f;
-    }
-    if (tid < m) {
-      const double w = !g ? 1.0 : exp((double)(p.g_token ? g[(int64_t)(base + tid) * p.HV] : *g));
-      sw[tid] = (float)w;
-      sw[kStep + tid] = isinf(sw[tid]) ? 0.f : (float)(w - (double)sw[tid]);
-    }
-    __syncthreads();
-    for (int t = 0; t < m; ++t) {
-      const float w = sw[t], wl = sw[kStep + t];
-      float vv[VEC], acc[VEC];
+  for (int t = 0; t < len; ++t) {
+    const float w = sw[t], wl = sw[kStep + t];
+    float vv[VEC], acc[VEC];
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        vv[c] = sv[t * VS + cg * VEC + c];
-        acc[c] = 0.f;
-      }
+    for (int c = 0; c < VEC; ++c) {
+      vv[c] = sv[t * VS + cg * VEC + c];
+      acc[c] = 0.f;
+    }
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int row = rg + RG * i;
-        if (row < K) {
-          const float kk = sk[t * K + row], qq = sq[t * K + row];
+    for (int i = 0; i < R; ++i) {
+      const int row = rg + RG * i;
+      if (row < K) {
+        const float kk = sk[t * K + row], qq = sq[t * K + row];
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            s[i][c] = fmaf(w, s[i][c], fmaf(wl, s[i][c], kk * vv[c]));
-            acc[c] = fmaf(qq, s[i][c], acc[c]);
-          }
+        for (int c = 0; c < VEC; ++c) {
+          s[i][c] = fmaf(w, s[i][c], fmaf(wl, s[i][c], kk * vv[c]));
+          acc[c] = fmaf(qq, s[i][c], acc[c]);
         }
       }
-      // lanes of equal columns are CG apart inside a warp
-      for (int off = CG; off < 32; off <<= 1)
+    }
+    float* keep = nullptr;  // where the state after this step goes
+    if (p.pool) {
+      const uint32_t end = ctx + (uint32_t)t + 1;
+      if (end % (uint32_t)p.block == 0 || t + 1 == len)
+        keep = p.pool + ((int64_t)page_of(p, seq, (end - 1) / (uint32_t)p.block) * p.HV + hv) * K * V;
+    } else if (t + 1 == len) {
+      keep = p.sT + ((int64_t)seq * p.HV + hv) * K * V;
+    }
+    if (keep) store(keep);
+    // lanes of equal columns are CG apart inside a warp
+    for (int off = CG; off < 32; off <<= 1)
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], off);
-      float* rb = red + (t & 1) * 8 * VS;
-      if ((tid & 31) < CG)
+      for (int c = 0; c < VEC; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], off);
+    float* rb = red + (t & 1) * 8 * VS;
+    if ((tid & 31) < CG)
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) rb[(tid >> 5) * VS + cg * VEC + c] = acc[c];
-      __syncthreads();
-      if (tid < VS && v0 + tid < V) {
-        float x = 0.f;
+      for (int c = 0; c < VEC; ++c) rb[(tid >> 5) * VS + cg * VEC + c] = acc[c];
+    __syncthreads();
+    if (tid < VS && v0 + tid < V) {
+      float x = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x += rb[i * VS + tid];
-        put(o + (int64_t)(base + t) * orow + v0 + tid, x * p.scale);
-      }
-      if (p.pool) {
-        const int64_t end = (int64_t)ctx + base + t + 1;
-        if (end % p.block == 0 || base + t + 1 == len) {
-          const int pg = page_of(p, seq, (end - 1) / p.block);
-          if (pg >= 0) store(p.pool + ((int64_t)pg * p.HV + hv) * K * V);
-        }
-      }
+      for (int i = 0; i < 8; ++i) x += rb[i * VS + tid];
+      put(o + t * orow + v0 + tid, x * p.scale);
     }
   }
-  if (p.sT) store(p.sT + ((int64_t)seq * p.HV + hv) * K * V);
 }
 
 template <typename T, int VEC, int R>
@@ -218,14 +212,15 @@ template <typename T>
 cudaError_t pick(const LinearProblem& p) {
   WalkArgs a{p, 0, 0};
   const bool vec = p.V % 4 == 0;  // 16-byte state columns (the API checks the base's alignment)
-  int VS = vec ? 128 : 32;
+  // 64 columns: 8 rows of K = 128 per thread, four CTAs per SM; fewer where that leaves SMs idle
+  int VS = vec ? 64 : 32;
   while (vec && VS > 32 && (VS / 2 >= p.V ||
          (int64_t)p.N_seq * p.HV * cdiv(p.V, VS) < 2 * sm_count()))
     VS /= 2;
   a.VS = VS;
   a.slices = (int)cdiv(p.V, VS);
   const int RG = kThreads / (vec ? VS / 4 : VS), rows = (int)cdiv(p.K, RG);
-  const int smem = (2 * kStep * p.K + kStep * VS + 2 * kStep + 16 * VS) * 4;
+  const int smem = (2 * p.T * p.K + p.T * VS + 2 * kStep + 16 * VS) * 4;
   if (!vec) return rows <= 16 ? go<T, 1, 16>(a, smem) : go<T, 1, 32>(a, smem);
   if (rows <= 4) return go<T, 4, 4>(a, smem);
   if (rows <= 8) return go<T, 4, 8>(a, smem);
