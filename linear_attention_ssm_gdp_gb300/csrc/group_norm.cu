@@ -116,11 +116,14 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t n = n0 + u * Nu;
-    float s = 0.f;
+    float f[NV][VEC], s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += to_f(x[u][j].e[e]);
+      for (int e = 0; e < VEC; ++e) {
+        f[j][e] = to_f(x[u][j].e[e]);
+        s += f[j][e];
+      }
 #pragma unroll
     for (int o = TG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float mean = s * inv;
@@ -130,8 +133,8 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
       if (sub + j * TG < nvec)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float d = to_f(x[u][j].e[e]) - mean;
-          m2 = fmaf(d, d, m2);
+          f[j][e] -= mean;
+          m2 = fmaf(f[j][e], f[j][e], m2);
         }
 #pragma unroll
     for (int o = TG / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
       PO out;
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
-        put(&out.e[e], finish<GATE>(a, fmaf((to_f(x[u][j].e[e]) - mean) * rstd, w[j][e], bi[j][e]),
+        put(&out.e[e], finish<GATE>(a, fmaf(f[j][e], rstd * w[j][e], bi[j][e]),
                                     GATE ? to_f(gt[GATE ? u : 0][GATE ? j : 0].e[e]) : 0.f));
       *reinterpret_cast<PO*>(static_cast<TO*>(a.y) + n * a.C + c + vi * VEC) = out;
     }
@@ -165,8 +168,9 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   extern __shared__ __align__(16) uint8_t raw[];
   using PX = Pack<TX, VEC>;
   using PO = Pack<TO, VEC>;
-  __shared__ float part[kMapThreads * VEC];
-  __shared__ float gsum[2][kMaxGS];  // this CTA's group sums: elements, squared distances
+  __shared__ float part[kMapThreads * (VEC + 1)];  // rows of W + 1 (W is at least a vector)
+  __shared__ float total[kMaxGS];                  // the cluster's group sums
+  __shared__ float gsum[2][kMaxGS];                // this CTA's: elements, squared distances
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks();
   const int64_t unit = blockIdx.x / CL;
@@ -181,83 +185,105 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   const int nty = kMapThreads / tc;
   const bool on = ty < nty;
   PX* keep = reinterpret_cast<PX*>(raw);
+  bool kept = false;  // the elements are in shared memory
   const TX* xb = static_cast<const TX*>(a.x) + n * a.x_sn + l0 * a.x_sl + c0;
   const float inv = 1.f / ((float)a.L * (float)a.Cg);
 
   float mean_of[VEC];  // per channel of the thread's column (one group: all the same)
   float acc[VEC];
   auto reduce = [&](int which) {
-    // this CTA's sums by group, then the cluster's
+    // this CTA's sums by group, in a fixed order, then the cluster's
+    if (gs == 1) {
+      float t = 0.f;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) part[threadIdx.x * VEC + e] = on ? acc[e] : 0.f;
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = warp; g < gs; g += kMapThreads / 32) {
-      float s = 0.f;
-      if (gs == 1) {
-        for (int i = lane; i < kMapThreads * VEC; i += 32) s += part[i];
-      } else {  // channels [g Cg, (g + 1) Cg) of every row group
-        for (int i = lane; i < nty * a.Cg; i += 32) {
-          const int y = i / a.Cg, c = g * a.Cg + i - y * a.Cg;
-          s += part[(y * tc + c / VEC) * VEC + c % VEC];
-        }
+      for (int e = 0; e < VEC; ++e) t += on ? acc[e] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        t = 0.f;
+        for (int i = 0; i < kMapThreads / 32; ++i) t += part[i];
+        gsum[which][0] = t;
       }
+    } else {  // one pass of columns: a warp per group, lanes over the rows of W channel sums
+      if (on)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) gsum[which][g] = s;
+        for (int e = 0; e < VEC; ++e) part[ty * (W + 1) + tx * VEC + e] = acc[e];
+      __syncthreads();
+      const int lane = threadIdx.x & 31;
+      for (int g = threadIdx.x >> 5; g < gs; g += kMapThreads / 32) {
+        float t = 0.f;
+        for (int y = lane; y < nty; y += 32)
+          for (int i = 0; i < a.Cg; ++i) t += part[y * (W + 1) + g * a.Cg + i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) gsum[which][g] = t;
+      }
     }
     cl.sync();
-    // `part` takes the cluster's sums
-    for (int g = threadIdx.x; g < gs; g += kMapThreads) {
-      float s = 0.f;
-      for (int r = 0; r < CL; ++r) s += cl.map_shared_rank(&gsum[which][0], r)[g];
-      part[g] = s;
+    for (int g = threadIdx.x >> 3; g < gs; g += kMapThreads / 8) {  // eight lanes, a rank each
+      const int r = threadIdx.x & 7;
+      float t = r < CL ? cl.map_shared_rank(&gsum[which][0], r)[g] : 0.f;
+      const uint32_t m = 0xffu << (threadIdx.x & 24);
+      t += __shfl_xor_sync(m, t, 1);
+      t += __shfl_xor_sync(m, t, 2);
+      t += __shfl_xor_sync(m, t, 4);
+      if (r == 0) total[g] = t;  // the cluster's sums
     }
     __syncthreads();
   };
   auto group_of = [&](int col, int e) { return gs == 1 ? 0 : (col * VEC + e) / a.Cg; };
+  // rows ty, ty + nty, .. of column c: D loads in flight; `use` gets the row's index from ty and its data
+  auto walk = [&](int c, auto use) {
+    constexpr int D = 4;
+    const TX* src = xb + (int64_t)ty * a.x_sl + c * VEC;
+    const int64_t step = (int64_t)nty * a.x_sl;
+    const PX* kp = keep + ty * cols + c;
+    const int kstep = nty * cols;
+    for (int r = ty; r < nrow; r += D * nty) {
+      PX x[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (r + d * nty < nrow) x[d] = kept ? kp[d * kstep] : *reinterpret_cast<const PX*>(src + d * step);
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (r + d * nty < nrow) use(r + d * nty, x[d]);
+      src += D * step;
+      kp += D * kstep;
+    }
+  };
 
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
   if (on)
-    for (int c = tx; c < cols; c += tc) {
-      constexpr int D = 8;  // rows in flight
-      for (int r = ty; r < nrow; r += D * nty) {
-        PX x[D];
+    for (int c = tx; c < cols; c += tc)
+      walk(c, [&](int r, const PX& x) {
+        if (a.resident) keep[r * cols + c] = x;
 #pragma unroll
-        for (int d = 0; d < D; ++d)
-          if (r + d * nty < nrow) x[d] = *reinterpret_cast<const PX*>(xb + (int64_t)(r + d * nty) * a.x_sl + c * VEC);
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-          if (r + d * nty < nrow) {
-            if (a.resident) keep[(int64_t)(r + d * nty) * cols + c] = x[d];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += to_f(x[d].e[e]);
-          }
-      }
-    }
+        for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
+      });
+  kept = a.resident;
   reduce(0);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    mean_of[e] = part[group_of(tx, e)] * inv;
+    mean_of[e] = total[group_of(tx, e)] * inv;
     acc[e] = 0.f;
   }
   __syncthreads();
   if (on)
     for (int c = tx; c < cols; c += tc)
-      for (int r = ty; r < nrow; r += nty) {
-        const PX x = a.resident ? keep[(int64_t)r * cols + c]
-                                : *reinterpret_cast<const PX*>(xb + (int64_t)r * a.x_sl + c * VEC);
+      walk(c, [&](int, const PX& x) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float d = to_f(x.e[e]) - mean_of[e];
           acc[e] = fmaf(d, d, acc[e]);
         }
-      }
+      });
   reduce(1);
   float rstd[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(part[group_of(tx, e)] * inv + a.eps);
+  for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(total[group_of(tx, e)] * inv + a.eps);
   const TO* gb = static_cast<const TO*>(a.gate);
   if (GATE) gb += n * a.g_sn + l0 * a.g_sl + c0;
   TO* yb = static_cast<TO*>(a.y) + (n * a.L + l0) * a.C + c0;
@@ -266,20 +292,18 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
       float ww[VEC], bb[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        ww[e] = a.w ? a.w[c0 + c * VEC + e] : 1.f;
+        ww[e] = rstd[e] * (a.w ? a.w[c0 + c * VEC + e] : 1.f);
         bb[e] = a.b ? a.b[c0 + c * VEC + e] : 0.f;
       }
-      for (int r = ty; r < nrow; r += nty) {
-        const PX x = a.resident ? keep[(int64_t)r * cols + c]
-                                : *reinterpret_cast<const PX*>(xb + (int64_t)r * a.x_sl + c * VEC);
+      walk(c, [&](int r, const PX& x) {
         PO gt, out;
         if (GATE) gt = *reinterpret_cast<const PO*>(gb + (int64_t)r * a.g_sl + c * VEC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-          put(&out.e[e], finish<GATE>(a, fmaf((to_f(x.e[e]) - mean_of[e]) * rstd[e], ww[e], bb[e]),
+          put(&out.e[e], finish<GATE>(a, fmaf(to_f(x.e[e]) - mean_of[e], ww[e], bb[e]),
                                       GATE ? to_f(gt.e[e]) : 0.f));
         *reinterpret_cast<PO*>(yb + (int64_t)r * a.C + c * VEC) = out;
-      }
+      });
     }
   cl.sync();  // no CTA leaves while another may still read its sums
 }
@@ -295,7 +319,7 @@ cudaError_t go_rows(const NormArgs& a, cudaStream_t s) {
 template <typename TX, typename TO, int VEC, bool GATE>
 cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
   auto kern = norm_map_kernel<TX, TO, VEC, GATE>;
-  if (smem > 32 * 1024) {
+  if (smem > 24 * 1024) {  // beside up to 20 KB of static shared memory
     const cudaError_t e = allow_smem<norm_map_kernel<TX, TO, VEC, GATE>>(kMapSmem);
     if (e != cudaSuccess) return e;
   }
@@ -328,9 +352,10 @@ cudaError_t go_map(NormArgs a, cudaStream_t s) {
   a.sets = (int)cdiv(a.G, a.GS);
   const int64_t units = a.N * a.sets;
   const int64_t seg = (int64_t)a.GS * a.Cg * sizeof(TX);
-  // CTAs per cluster: until the machine is filled twice, or 64 rows of work are left each
+  // CTAs per cluster: until every SM has one, or 8 KB of work are left each (clusters of 16 found
+  // few places: 4 x 4096 x 320 took 34 us)
   int CL = 1;
-  while (CL < 8 && units * CL < 2 * sm_count() && a.L * seg > (int64_t)CL * 8192) CL *= 2;
+  while (CL < 8 && units * CL < sm_count() && a.L * seg > (int64_t)CL * 8192) CL *= 2;
   while (CL < 8 && cdiv(a.L, CL) * seg > 96 * 1024) CL *= 2;
   a.rows = (int)cdiv(a.L, CL);
   const int64_t bytes = (int64_t)a.rows * seg;
@@ -351,13 +376,13 @@ cudaError_t run(NormArgs a, cudaStream_t s) {
                        (!a.gate || (a.g_sn % VEC == 0 && a.g_sl % VEC == 0 && aligned(a.gate, GA)));
   if (a.L == 1 && rows_ok && a.Cg % VEC == 0 && aligned(a.w, 16) && aligned(a.b, 16)) {
     const int nvec = a.Cg / VEC;
-    if (nvec <= 1) return go_rows<TX, TO, 1, 1, 4>(a, s);
-    if (nvec <= 2) return go_rows<TX, TO, 2, 1, 4>(a, s);
-    if (nvec <= 4) return go_rows<TX, TO, 4, 1, 4>(a, s);
-    if (nvec <= 8) return go_rows<TX, TO, 8, 1, 4>(a, s);
-    if (nvec <= 16) return go_rows<TX, TO, 16, 1, 4>(a, s);
-    if (nvec <= 32) return go_rows<TX, TO, 32, 1, 4>(a, s);
-    if (nvec <= 64) return go_rows<TX, TO, 32, 2, 2>(a, s);
+    if (nvec <= 1) return go_rows<TX, TO, 1, 1, 2>(a, s);
+    if (nvec <= 2) return go_rows<TX, TO, 2, 1, 2>(a, s);
+    if (nvec <= 4) return go_rows<TX, TO, 4, 1, 2>(a, s);
+    if (nvec <= 8) return go_rows<TX, TO, 8, 1, 2>(a, s);
+    if (nvec <= 16) return go_rows<TX, TO, 16, 1, 2>(a, s);
+    if (nvec <= 32) return go_rows<TX, TO, 32, 1, 2>(a, s);
+    if (nvec <= 64) return go_rows<TX, TO, 32, 2, 1>(a, s);
     if (nvec <= 128) return go_rows<TX, TO, 32, 4, 1>(a, s);
   }
   // several groups share a vector only where the set of groups ends on one

@@ -14,7 +14,7 @@ bool dtype_ok(gdp_dtype dt) { return dt == GDP_BF16 || dt == GDP_F16 || dt == GD
 // Workspace: status word, then what the kernel that takes the problem lays out. The size does
 // not depend on the strides, so it is the larger of the two kernels' where both may.
 size_t linear_ws(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
-  const size_t m = linear_mma_workspace(N_seq, B, T, HV, K, V);
+  const size_t m = linear_mma_workspace(N_seq, B, T, HV, K, V, dt);
   return linear_tc_shape(K, V, dt) ? std::max(m, linear_tc_workspace(N_seq, B, T, HV, K, V)) : m;
 }
 

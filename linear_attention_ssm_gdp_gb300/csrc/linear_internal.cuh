@@ -40,7 +40,7 @@ struct LinearProblem {
 cudaError_t launch_linear_walk(const LinearProblem& p);
 
 // The chunked form for any type, size and stride.
-size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V);
+size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt);
 cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws);
 
 // The chunked form on the tensor cores: whether sizes and type fit it, whether the

@@ -81,7 +81,7 @@ struct MmaLay {
 };
 
 template <typename T, int KD, bool OUT>
-__global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ ChunkArgs a, int vec) {
+__global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ? 2 : 1) linear_mma_kernel(const __grid_constant__ ChunkArgs a, int vec) {
   pdl_wait();
   using L = MmaLay<T, KD>;
   constexpr bool EX = sizeof(T) == 2;  // inputs are exact in tf32
@@ -332,17 +332,22 @@ cudaError_t go_t(const ChunkArgs& a, int vec) {
 
 constexpr double kStateCost = 0.5;  // the state pass leaves out scores and read-out
 int slice_of(int K) { return K <= 128 ? 64 : 32; }
+// CTAs that share an SM, by their shared memory (91 KB; 141 KB and more otherwise)
+int per_sm(int K, gdp_dtype dt) { return K <= 64 && dt != GDP_F32 ? 2 : 1; }
+Plan plan(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt, bool packed) {
+  return plan_of(N_seq, B, T, HV, K, V, packed, slice_of(K), per_sm(K, dt), kStateCost);
+}
 
 }  // namespace
 
-size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V) {
+size_t linear_mma_workspace(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
   // the query does not say whether the batch is packed
-  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, slice_of(K), kStateCost).total : 0;
-  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, slice_of(K), kStateCost).total : 0);
+  const size_t d = N_seq == B ? plan(N_seq, B, T, HV, K, V, dt, false).total : 0;
+  return std::max(d, B == 1 ? plan(N_seq, B, T, HV, K, V, dt, true).total : 0);
 }
 
 cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
-  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, slice_of(p.K), kStateCost);
+  const Plan x = plan(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt, p.cu != nullptr);
   ChunkArgs a{};
   a.p = p;
   a.nseg = x.nseg;

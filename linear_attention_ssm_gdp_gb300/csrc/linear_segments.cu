@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_consta
 
 }  // namespace
 
-Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, double state_cost) {
+Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, int per_sm, double state_cost) {
   Plan x{};
-  const int G = sm_count();
+  const int G = sm_count() * per_sm;
   x.slices = (int)cdiv(V, vt);
   const int chunks = (int)cdiv(T, C);
   const int64_t heads = (int64_t)HV * x.slices;
@@ -190,7 +190,7 @@ Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt,
     // that and the two extra launches at about eight chunks
     const int64_t units = heads * B;
     double best = (double)cdiv(units, G) * (chunks + 3);
-    for (int n = 2; n <= chunks && n <= 64; ++n) {
+    for (int n = 2; n <= chunks && n <= 256; ++n) {
       const int64_t per = cdiv(chunks, n);
       if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
       const double t =
