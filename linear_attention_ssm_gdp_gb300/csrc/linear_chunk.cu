@@ -769,14 +769,14 @@ cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
 
 }  // namespace
 
-constexpr double kStateCost = 0.6;
+constexpr Cost kCost = {1.9, 1.3, 5.0, 9.0};
 
 bool linear_tc_shape(int K, int V, gdp_dtype dt) { return dt == GDP_BF16 && K <= 128 && K % 8 == 0 && V % 8 == 0; }
 
 size_t linear_tc_workspace(int N_seq, int B, int T, int HV, int K, int V) {
   // the query does not say whether the batch is packed
-  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, kVT, 1, kStateCost).total : 0;
-  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, kVT, 1, kStateCost).total : 0);
+  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, kVT, kCost).total : 0;
+  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, kVT, kCost).total : 0);
 }
 
 bool linear_tc_ok(const LinearProblem& p) {
@@ -785,7 +785,7 @@ bool linear_tc_ok(const LinearProblem& p) {
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
-  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, 1, kStateCost);
+  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, kCost);
   TcArgs a{};
   a.p = p;
   a.nseg = x.nseg;

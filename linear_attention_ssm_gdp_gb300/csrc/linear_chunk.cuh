@@ -32,9 +32,13 @@ struct Plan {
   int nseg, Lseg, bound, slices;  // segments per dense sequence, tokens, segments in all at most
   size_t recs, seqs, segS, segW, total;
 };
-// vt: value columns per item; per_sm: items that an SM works on at once; state_cost: a chunk of the
-// state pass in chunks of the whole one.
-Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, int per_sm, double state_cost);
+// What a kernel's items take, in microseconds: a chunk, a chunk of the state pass, an item's start
+// and states, the two extra launches of a split.
+struct Cost {
+  double chunk, state_chunk, item, split;
+};
+// vt: value columns per item.
+Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, const Cost& cost);
 
 // The two kernels around the state pass: segment records of a packed batch, and the states at
 // the segment starts.

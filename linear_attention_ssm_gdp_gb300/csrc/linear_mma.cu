@@ -1,18 +1,21 @@
 // Linear attention with a decay for each head, chunked form for every type, size and stride
 // that the tensor-memory kernel does not take: fp32 and fp16 inputs, K up to 256, odd sizes.
 //
-// The same algebra on chunks of 64 tokens (see linear_chunk.cu), one CTA of eight warps per
+// The same algebra on chunks of 64 tokens (see linear_chunk.cu), one CTA of sixteen warps per
 // (segment, value head, slice of value columns), the products with mma.sync in tf32: an
 // operand that has more than tf32's 11 bits goes in as two parts (x = hi + lo to 2^-22)
 // and a product of two such operands takes three instructions, so that sums are fp32 to a few
-// 2^-22 whatever the input type. 16-bit inputs are exact in one part. The state stays in
-// registers as the accumulator fragments of U, in fp32, with a copy in shared memory that the
-// read-out q S takes its operands from.
+// 2^-22 whatever the input type. 16-bit inputs are exact in one part, and their scores q k^T come
+// from 16-bit instructions (exact products, fp32 sums). The state stays in registers as the
+// accumulator fragments of U, in fp32. What several warps read as an operand (the state for
+// the read-out q S, the decayed values v') is split into its parts once, into shared memory.
 //
-// What bounds it: the latency of its phases (a chunk is loaded, scored, read out and
-// added up by the same eight warps); tiles of the next chunk stream in by cp.async
-// meanwhile where two fit in shared memory.
+// What bounds it: mma.sync's own rate, 16 cycles of an SM quarter per m16n8k8 in tf32
+// (measured: 12,000 cycles a chunk for fp16 K = V = 64, 17,500 for fp32, the same with eight
+// warps, with sixteen and with the loops unrolled). Tiles of the next chunk stream in by
+// cp.async meanwhile where two fit in shared memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_chunk.cuh"
 #include "ptx.cuh"
@@ -22,7 +25,7 @@ namespace {
 
 using namespace linear;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -46,6 +49,26 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, const uint32_t*
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+// The same for 16-bit operands, m16n8k16.
+template <typename T>
+__device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
 // An operand fragment of N registers: hi, and lo unless EXACT.
 template <int N, bool EXACT>
 struct Frag {
@@ -59,11 +82,18 @@ struct Frag {
     }
   }
 };
-template <bool EA, bool EB>
-__device__ __forceinline__ void mma_parts(float* d, const Frag<4, EA>& a, const Frag<2, EB>& b) {
-  if (!EA) mma(d, a.lo, b.hi);
-  if (!EB) mma(d, a.hi, b.lo);
-  mma(d, a.hi, b.hi);
+// N products with the same A, the small terms first; neighbouring instructions have accumulators
+// of their own.
+template <bool EA, bool EB, int N>
+__device__ __forceinline__ void mma_parts(float (*d)[4], const Frag<4, EA>& a, const Frag<2, EB> (&b)[N]) {
+  if (!EA)
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma(d[j], a.lo, b[j].hi);
+  if (!EB)
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma(d[j], a.hi, b[j].lo);
+#pragma unroll
+  for (int j = 0; j < N; ++j) mma(d[j], a.hi, b[j].hi);
 }
 
 template <typename T, int KD>
@@ -73,15 +103,18 @@ struct MmaLay {
   static constexpr int LV = VS + 8;
   static constexpr int Q = 0, Kt = Q + C * LK * (int)sizeof(T), Vt = Kt + C * LK * (int)sizeof(T);
   static constexpr int TILE = Vt + C * LV * (int)sizeof(T);
-  static constexpr int REST = KD * LV * 4 + C * (C + 4) * 4 + 2 * 272 * 4;  // S, P, decays
+  // the state as hi and lo parts where they fit, v' as hi and lo, P, decays
+  static constexpr bool SPLIT = KD <= 128;
+  static constexpr int SB = KD * LV * 4, VB = C * LV * 4;
+  static constexpr int REST = (SPLIT ? 2 : 1) * SB + 2 * VB + C * (C + 4) * 4 + 2 * 272 * 4;
   static constexpr int STAGES = 2 * TILE + REST <= 227 * 1024 ? 2 : 1;
-  static constexpr int S = STAGES * TILE, P = S + KD * LV * 4, G = P + C * (C + 4) * 4;
+  static constexpr int S = STAGES * TILE, W = S + (SPLIT ? 2 : 1) * SB, P = W + 2 * VB, G = P + C * (C + 4) * 4;
   static constexpr int BYTES = G + 2 * 272 * 4;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
 };
 
 template <typename T, int KD, bool OUT>
-__global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ? 2 : 1) linear_mma_kernel(const __grid_constant__ ChunkArgs a, int vec) {
+__global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ ChunkArgs a, int vec) {
   pdl_wait();
   using L = MmaLay<T, KD>;
   constexpr bool EX = sizeof(T) == 2;  // inputs are exact in tf32
@@ -94,6 +127,8 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
   if (!get_item(a, blockIdx.x, x) || skip<OUT>(x)) return;
   float* sS = reinterpret_cast<float*>(sm + L::S);
   float* sP = reinterpret_cast<float*>(sm + L::P);
+  uint32_t* sW = reinterpret_cast<uint32_t*>(sm + L::W);  // v' parts: hi, then lo
+  constexpr int SL = L::SB / 4, WL = L::VB / 4;
   const int K = p.K, V = p.V;
   const T* gq = static_cast<const T*>(p.q) + x.b * p.qs[0] + x.h * p.qs[2];
   const T* gk = static_cast<const T*>(p.k) + x.b * p.ks[0] + x.h * p.ks[2];
@@ -101,11 +136,12 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
   const int nv = min(VS, V - x.v0);
 
   // tile rows of `cols` elements (the rest of the tile's width and rows outside the sequence zero)
-  auto tile = [&](int off, int ld, int width, const T* src, int64_t step, int cols, int base) {
+  auto tile = [&](int off, int ld, auto wide, const T* src, int64_t step, int cols, int base) {
     T* dst = reinterpret_cast<T*>(sm + off);
-    constexpr int VEC = 16 / sizeof(T);
+    constexpr int VEC = 16 / sizeof(T), width = decltype(wide)::value;
     if (vec) {
-      const int per = width / VEC;
+      constexpr int per = width / VEC;
+#pragma unroll
       for (int i = tid; i < C * per; i += kThreads) {
         const int r = i / per, c = (i - r * per) * VEC, row = base + r;
         T* d = dst + r * ld + c;
@@ -117,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
                      : "memory");
       }
     } else {
+#pragma unroll 1
       for (int i = tid; i < C * width; i += kThreads) {
         const int r = i / width, c = i - r * width, row = base + r;
         if (row >= x.r.t0 && row < x.r.t0 + x.r.n && c < cols) dst[r * ld + c] = src[row * step + c];
@@ -126,57 +163,68 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
   };
   auto load = [&](int c) {
     const int base = x.r.t0 - x.off + c * C, o = (c % L::STAGES) * L::TILE;
-    if (OUT) tile(o + L::Q, LK, KD, gq, p.qs[1], K, base);
-    tile(o + L::Kt, LK, KD, gk, p.ks[1], K, base);
-    tile(o + L::Vt, LV, VS, gv, p.vs[1], nv, base);
+    if (OUT) tile(o + L::Q, LK, std::integral_constant<int, KD>(), gq, p.qs[1], K, base);
+    tile(o + L::Kt, LK, std::integral_constant<int, KD>(), gk, p.ks[1], K, base);
+    tile(o + L::Vt, LV, std::integral_constant<int, VS>(), gv, p.vs[1], nv, base);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  // state fragments: U's accumulators. KD = 64: warps 4 x 2 over (k, v); otherwise over k
-  constexpr int MT = KD / 64 <= 2 ? 1 : KD / 128;  // 16-row tiles of k per warp
-  constexpr int NT = KD == 64 ? VS / 16 : VS / 8;  // 8-column tiles of v per warp
-  const int m0 = KD == 64 ? 16 * (warp & 3) : 16 * MT * warp, n0 = KD == 64 ? (VS / 2) * (warp >> 2) : 0;
-  float s[MT][NT][4];
+  // state fragments: U's accumulators, one 16-row tile of k and NT 8-column tiles of v per warp
+  constexpr int MW = KD / 16 < 16 ? KD / 16 : 16;  // warps along k, the rest along v
+  constexpr int NT = VS / 8 * MW / 16;
+  const int m0 = 16 * (warp % MW), n0 = 8 * NT * (warp / MW);
+  float s[NT][4];
   const int64_t at = (int64_t)x.hv * K * V + x.v0;
   auto each_state = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = m0 + 16 * i + gr + 8 * (e >> 1), v = n0 + 8 * j + 2 * tq + (e & 1);
-          f(s[i][j][e], k, v, k < K && v < nv);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int k = m0 + gr + 8 * (e >> 1), v = n0 + 8 * j + 2 * tq + (e & 1);
+        f(s[j][e], k, v, k < K && v < nv);
+      }
   };
   {
     const float* src = state_src<OUT>(a, x);
     each_state([&](float& y, int k, int v, bool in) { y = src && in ? __ldcg(src + at + (int64_t)k * V + v) : 0.f; });
   }
   float2 wseg = make_float2(1.f, 0.f);
+  // the decays of a chunk, a chunk ahead, by a warp that has no scores (its tile is above the diagonal)
+  constexpr int kDecay = 12;
+  float* sG = reinterpret_cast<float*>(sm + L::G);
   float g0 = 0.f, g1 = 0.f;
-  if (warp == 0) {
-    g0 = load_g(p, x, x.r.t0 - x.off, 2 * lane);
-    g1 = load_g(p, x, x.r.t0 - x.off, 2 * lane + 1);
-  }
+  auto fetch_g = [&](int c) {
+    g0 = load_g(p, x, x.r.t0 - x.off + c * C, 2 * lane);
+    g1 = load_g(p, x, x.r.t0 - x.off + c * C, 2 * lane + 1);
+  };
+  auto decays = [&](int c) {
+    const int base = x.r.t0 - x.off + c * C;
+    chunk_decays(g0, g1, p.scale, max(0, x.r.t0 - base), min(C, x.r.t0 + x.r.n - base), lane, sG + (c & 1) * 272);
+  };
   if (x.chunks > 0) load(0);
+  if (warp == kDecay && x.chunks > 0) {
+    fetch_g(0);
+    decays(0);
+    fetch_g(1);
+  }
   for (int c = 0; c < x.chunks; ++c) {
     const int base = x.r.t0 - x.off + c * C;
     const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
-    float* g = reinterpret_cast<float*>(sm + L::G) + (c & 1) * 272;
+    const float* g = sG + (c & 1) * 272;
     if (L::STAGES == 1 && c > 0) {
       __syncthreads();  // the last chunk's readers are done with the tiles
       load(c);
     }
     if (OUT)  // the state before the chunk, for the read-out
-      each_state([&](float& y, int k, int v, bool) { sS[k * LV + v] = y; });
-    if (warp == 0) {
-      chunk_decays(g0, g1, p.scale, lo, hi, lane, g);
-      if (c + 1 < x.chunks) {
-        g0 = load_g(p, x, base + C, 2 * lane);
-        g1 = load_g(p, x, base + C, 2 * lane + 1);
-      }
-    }
+      each_state([&](float& y, int k, int v, bool) {
+        if (L::SPLIT) {
+          const uint32_t y0 = tf32(y);
+          sS[k * LV + v] = __uint_as_float(y0);
+          sS[SL + k * LV + v] = __uint_as_float(tf32(y - __uint_as_float(y0)));
+        } else {
+          sS[k * LV + v] = y;
+        }
+      });
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     if (L::STAGES == 2 && c + 1 < x.chunks) load(c + 1);  // its stage was last read before this barrier
@@ -185,41 +233,72 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
     const T* tK = reinterpret_cast<const T*>(st + L::Kt);
     const T* tV = reinterpret_cast<const T*>(st + L::Vt);
     const int kk = (K + 7) / 8;  // steps over K
-    if (OUT) {
-      // scores: rows 16 (warp % 4), columns 32 (warp / 4), only tiles that reach the diagonal
-      const int r0 = 16 * (warp & 3), c0 = 32 * (warp >> 2);
-      float d[4][4] = {};
-      if (c0 <= r0 + 15) {
-        for (int k0 = 0; k0 < 8 * kk; k0 += 8) {
-          Frag<4, EX> fa;
-          const T* qa = tQ + (r0 + gr) * LK + k0 + tq;
-          fa.set(0, to_f(qa[0]));
-          fa.set(1, to_f(qa[8 * LK]));
-          fa.set(2, to_f(qa[4]));
-          fa.set(3, to_f(qa[8 * LK + 4]));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            Frag<2, EX> fb;
-            const T* kb = tK + (c0 + 8 * j + gr) * LK + k0 + tq;
-            fb.set(0, to_f(kb[0]));
-            fb.set(1, to_f(kb[4]));
-            mma_parts<EX, EX>(d[j], fa, fb);
+    for (int i = tid; i < C * VS; i += kThreads) {  // v' = e^{Gam - Gam_i} v_i in two parts
+      const int t = i / VS, v = i % VS;
+      const float y = g[128 + t] * to_f(tV[t * LV + v]);
+      const uint32_t y0 = tf32(y);
+      sW[t * LV + v] = y0;
+      sW[WL + t * LV + v] = tf32(y - __uint_as_float(y0));
+    }
+    if (warp == kDecay && c + 1 < x.chunks) {
+      decays(c + 1);
+      fetch_g(c + 2);
+    }
+    if (OUT) {
+      // scores: rows 16 (warp % 4), columns 16 (warp / 4), only tiles that reach the diagonal
+      const int r0 = 16 * (warp & 3), c0 = 16 * (warp >> 2);
+      float d[2][4] = {};
+      if (c0 <= r0 + 15) {
+        if constexpr (EX) {
+          // lanes 8 m ..: rows 8 (m % 2) .. of the A tile, columns 8 (m / 2); of B rows 8 (m / 2) ..
+          const uint32_t qa = ptx::smem_u32(tQ + (r0 + (lane & 15)) * LK + 8 * (lane >> 4));
+          const uint32_t kb = ptx::smem_u32(tK + (c0 + (lane & 7) + 8 * (lane >> 4)) * LK + 8 * ((lane >> 3) & 1));
+#pragma unroll 1
+          for (int k0 = 0; k0 < (K + 15) / 16; ++k0) {
+            uint32_t fa[4], fb[4];
+            ldmatrix_x4(qa + 32 * k0, fa);
+            ldmatrix_x4(kb + 32 * k0, fb);
+            mma16<T>(d[0], fa, fb[0], fb[1]);
+            mma16<T>(d[1], fa, fb[2], fb[3]);
+          }
+        } else {
+#pragma unroll 1
+          for (int k0 = 0; k0 < 8 * kk; k0 += 8) {
+            Frag<4, EX> fa;
+            const T* qa = tQ + (r0 + gr) * LK + k0 + tq;
+            fa.set(0, to_f(qa[0]));
+            fa.set(1, to_f(qa[8 * LK]));
+            fa.set(2, to_f(qa[4]));
+            fa.set(3, to_f(qa[8 * LK + 4]));
+            Frag<2, EX> fb[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const T* kb = tK + (c0 + 8 * j + gr) * LK + k0 + tq;
+              fb[j].set(0, to_f(kb[0]));
+              fb[j].set(1, to_f(kb[4]));
+            }
+            mma_parts(d, fa, fb);
           }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = r0 + gr + 8 * (e >> 1), i = c0 + 8 * j + 2 * tq + (e & 1);
           const float f = ex2_approx((g[t] - g[i]) + (g[64 + t] - g[64 + i]));
           sP[t * LP + i] = i <= t ? d[j][e] * (p.scale * f) : 0.f;
         }
-      __syncthreads();
-      // o: rows r0, value columns of this warp's half
-      constexpr int NO = VS / 16;
-      const int v0 = (VS / 2) * (warp >> 2);
+    }
+    __syncthreads();
+    if (OUT) {
+      const int r0 = 16 * (warp & 3);
+      // o: rows r0, value columns of this warp's quarter
+      constexpr int NO = VS / 32;
+      const int v0 = (VS / 4) * (warp >> 2);
       float o[NO][4] = {};
+#pragma unroll 1
       for (int k0 = 0; k0 < 8 * kk; k0 += 8) {
         Frag<4, EX> fa;
         const T* qa = tQ + (r0 + gr) * LK + k0 + tq;
@@ -227,14 +306,21 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
         fa.set(1, to_f(qa[8 * LK]));
         fa.set(2, to_f(qa[4]));
         fa.set(3, to_f(qa[8 * LK + 4]));
+        Frag<2, false> fb[NO];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-          Frag<2, false> fb;
           const float* sb = sS + (k0 + tq) * LV + v0 + 8 * j + gr;
-          fb.set(0, sb[0]);
-          fb.set(1, sb[4 * LV]);
-          mma_parts<EX, false>(o[j], fa, fb);
+          if (L::SPLIT) {
+            fb[j].hi[0] = __float_as_uint(sb[0]);
+            fb[j].hi[1] = __float_as_uint(sb[4 * LV]);
+            fb[j].lo[0] = __float_as_uint(sb[SL]);
+            fb[j].lo[1] = __float_as_uint(sb[SL + 4 * LV]);
+          } else {
+            fb[j].set(0, sb[0]);
+            fb[j].set(1, sb[4 * LV]);
+          }
         }
+        mma_parts(o, fa, fb);
       }
       const float e0 = g[192 + r0 + gr], e1 = g[192 + r0 + gr + 8];
 #pragma unroll
@@ -244,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
         o[j][2] *= e1;
         o[j][3] *= e1;
       }
+#pragma unroll 1
       for (int i0 = 0; i0 < r0 + 16; i0 += 8) {
         Frag<4, false> fa;
         const float* pa = sP + (r0 + gr) * LP + i0 + tq;
@@ -251,14 +338,14 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
         fa.set(1, pa[8 * LP]);
         fa.set(2, pa[4]);
         fa.set(3, pa[8 * LP + 4]);
+        Frag<2, EX> fb[NO];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-          Frag<2, EX> fb;
           const T* vb = tV + (i0 + tq) * LV + v0 + 8 * j + gr;
-          fb.set(0, to_f(vb[0]));
-          fb.set(1, to_f(vb[4 * LV]));
-          mma_parts<false, EX>(o[j], fa, fb);
+          fb[j].set(0, to_f(vb[0]));
+          fb[j].set(1, to_f(vb[4 * LV]));
         }
+        mma_parts(o, fa, fb);
       }
       T* og = static_cast<T*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
 #pragma unroll
@@ -271,37 +358,38 @@ __global__ void __launch_bounds__(kThreads, MmaLay<T, KD>::BYTES <= 113 * 1024 ?
     }
     // U = k^T (w v), then S = e^Gam S + U
     const float wh = g[256], wl = g[257];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    {
       float u[NT][4] = {};
+#pragma unroll 1
       for (int t0 = 0; t0 < C; t0 += 8) {
         Frag<4, EX> fa;
-        const T* ka = tK + (t0 + tq) * LK + m0 + 16 * i + gr;
+        const T* ka = tK + (t0 + tq) * LK + m0 + gr;
         fa.set(0, to_f(ka[0]));
         fa.set(1, to_f(ka[8]));
         fa.set(2, to_f(ka[4 * LK]));
         fa.set(3, to_f(ka[4 * LK + 8]));
-        const float w0 = g[128 + t0 + tq], w1 = g[128 + t0 + tq + 4];
+        Frag<2, false> fb[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          Frag<2, false> fb;
-          const T* vb = tV + (t0 + tq) * LV + n0 + 8 * j + gr;
-          fb.set(0, w0 * to_f(vb[0]));
-          fb.set(1, w1 * to_f(vb[4 * LV]));
-          mma_parts<EX, false>(u[j], fa, fb);
+          const uint32_t* wb = sW + (t0 + tq) * LV + n0 + 8 * j + gr;
+          fb[j].hi[0] = wb[0];
+          fb[j].hi[1] = wb[4 * LV];
+          fb[j].lo[0] = wb[WL];
+          fb[j].lo[1] = wb[WL + 4 * LV];
         }
+        mma_parts(u, fa, fb);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][j][e] = fmaf(wh, s[i][j][e], fmaf(wl, s[i][j][e], u[j][e]));
+        for (int e = 0; e < 4; ++e) s[j][e] = fmaf(wh, s[j][e], fmaf(wl, s[j][e], u[j][e]));
     }
     if (!OUT) wseg = mul_pair(wseg, make_float2(wh, wl));
     if (float* dst = state_dst<OUT>(a, x, c))
       each_state([&](float& y, int k, int v, bool in) {
         if (in) dst[at + (int64_t)k * V + v] = y;
       });
-    if (OUT) __syncthreads();  // S and P are rewritten next
+    __syncthreads();  // S, P and v' are rewritten next
   }
   if (!OUT && tid == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
   if (OUT && x.chunks == 0 && x.r.last && !p.pool && p.sT)  // an empty sequence keeps its state
@@ -330,12 +418,14 @@ cudaError_t go_t(const ChunkArgs& a, int vec) {
   }
 }
 
-constexpr double kStateCost = 0.5;  // the state pass leaves out scores and read-out
+// Measured at K = V = 64: 5.9 us a chunk for 16-bit inputs, 8.7 for fp32; products over K grow with it.
+Cost cost_of(int K, gdp_dtype dt) {
+  const double k = K / 64.0;
+  return dt == GDP_F32 ? Cost{3.0 + 5.5 * k, 1.3 + 2.2 * k, 4.0, 8.0} : Cost{2.5 + 3.2 * k, 1.0 + 1.3 * k, 4.0, 8.0};
+}
 int slice_of(int K) { return K <= 128 ? 64 : 32; }
-// CTAs that share an SM, by their shared memory (91 KB; 141 KB and more otherwise)
-int per_sm(int K, gdp_dtype dt) { return K <= 64 && dt != GDP_F32 ? 2 : 1; }
 Plan plan(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt, bool packed) {
-  return plan_of(N_seq, B, T, HV, K, V, packed, slice_of(K), per_sm(K, dt), kStateCost);
+  return plan_of(N_seq, B, T, HV, K, V, packed, slice_of(K), cost_of(K, dt));
 }
 
 }  // namespace

@@ -176,25 +176,23 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_consta
 
 }  // namespace
 
-Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, int per_sm, double state_cost) {
+Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, const Cost& cost) {
   Plan x{};
-  const int G = sm_count() * per_sm;
+  const int G = sm_count();
   x.slices = (int)cdiv(V, vt);
   const int chunks = (int)cdiv(T, C);
   const int64_t heads = (int64_t)HV * x.slices;
   x.nseg = 1;
   x.Lseg = std::max(1, chunks) * C;
   if (!packed) {
-    // time in units of a chunk of the second pass: rounds of items over the SMs, each item with
-    // about three chunks' time for its states and its start, the state pass at state_cost of
-    // that and the two extra launches at about eight chunks
+    // rounds of items over the SMs, of both passes
     const int64_t units = heads * B;
-    double best = (double)cdiv(units, G) * (chunks + 3);
+    double best = (double)cdiv(units, G) * (chunks * cost.chunk + cost.item);
     for (int n = 2; n <= chunks && n <= 256; ++n) {
       const int64_t per = cdiv(chunks, n);
       if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
-      const double t =
-          ((double)cdiv(units * n, G) + state_cost * cdiv(units * (n - 1), G)) * (per + 3) + 8.0;
+      const double t = (double)cdiv(units * n, G) * (per * cost.chunk + cost.item) +
+                       (double)cdiv(units * (n - 1), G) * (per * cost.state_chunk + cost.item) + cost.split;
       if (t < 0.95 * best) {
         best = t;
         x.nseg = n;
