@@ -368,6 +368,10 @@ gdp_status gdp_debug_wait_fault(int arm, double budget_seconds);
  *   o       [B, T, HV, V] contiguous, dtype `dt`; sums and states are fp32.
  *   K <= 256, V <= 1024, HV % H == 0, T and B T below 2^31; state bases 16-byte
  *   aligned.
+ * Values that are not finite stay in their sequence: one in q spoils its own
+ * token's o, one in k or v the state and every later token of its head; the
+ * chunked calls may also spoil the earlier tokens of the same 64-token chunk
+ * (a masked score is an exact 0, and 0 times infinity is not).
  *
  * Paged states. state_pool [n_pages, HV, K, V] fp32; block_tables [n,
  * max_blocks] int32 names the page of each block of block_size tokens of a
@@ -458,7 +462,7 @@ gdp_status gdp_linear_recurrent_update_paged(const void* q, const void* k, const
  * slot_map [max_tokens] int64: a token's request, its position and its slot
  * page * block_size + position % block_size in a per-token cache (-1 where the
  * table names no page), all -1 past the last token; free_used_out [1] int32
- * (may not alias free_used); status (nullable int32): 0, or the sum of 1 (a request
+ * (another word than free_used); status (nullable int32): 0, or the sum of 1 (a request
  * with a negative length, or longer than its table: it is planned as empty; or a
  * negative free_used) and 2 (pages or tokens ran out: requests are planned in
  * order while they fit, and the first that does not and all after it are planned

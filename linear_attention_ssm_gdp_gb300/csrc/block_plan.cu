@@ -162,7 +162,8 @@ extern "C" gdp_status gdp_block_plan(const int32_t* context_lens, const int32_t*
                                      cudaStream_t stream) {
   if (n < 0 || max_blocks < 0 || n_free < 0 || block_size <= 0 || max_tokens < 0)
     return GDP_ERR_INVALID_ARG;
-  if (!cu_seqlens || !free_used || !free_used_out) return GDP_ERR_INVALID_ARG;
+  // (one CTA writes free_used_out while others read free_used)
+  if (!cu_seqlens || !free_used || !free_used_out || free_used == free_used_out) return GDP_ERR_INVALID_ARG;
   if (n > 0 && (!context_lens || !query_lens)) return GDP_ERR_INVALID_ARG;
   if (n > 0 && max_blocks > 0 && !block_tables) return GDP_ERR_INVALID_ARG;
   if (n_free > 0 && !free_pages) return GDP_ERR_INVALID_ARG;

@@ -22,9 +22,8 @@
 // What bounds it: q, k, v, o are 64 KB per chunk and head, 1.5 us of an SM's share of HBM.
 // A product with both operands in shared memory runs at that memory's 128 bytes a clock
 // ((A + B) / 128 cycles, measured), more than the tensor pipe needs, so the operands that
-// are made on chip (S, v') live in tensor memory, where they cost none of it: about 2300
-// cycles of shared memory a chunk with both there, 3200 without. Nothing in the state's
-// chain depends on the state but one multiply-add per element (U does not), so a CTA is
+// are made on chip (S, v') live in tensor memory, where they cost none of it. Nothing in the
+// state's chain depends on the state but one multiply-add per element (U does not), so a CTA is
 // split into groups that meet at mbarriers and work on neighbouring chunks at once:
 //     8 state warps   the state update, S as bf16; o = e^{Gam_t} INTER + INTRA, stores
 //     4 v' warps      v' of the next chunk
@@ -34,6 +33,11 @@
 // The roles' loops are rolled where they can be: together they have to fit the 32 KB
 // first-level instruction cache, or the SMs of a GPC wait for their common next level (with
 // them unrolled a third of the warps' time went there, at 80 % of that cache's bandwidth).
+// Measured: 1.9 us a chunk (K = V = 128) on a CTA of its own SM, 10 us for a call of one chunk;
+// 2 x 4096 tokens, 16 heads: 78 us with the state pass and the combine kernel. What is left
+// above the 1.5 us is the state warps' loop (U's read, the update, S's write, the output's
+// read and staging, one after another); sixteen state warps and four output warps at 64
+// registers take the same time.
 //
 // Sequences are cut into segments when there are too few (sequence, head) pairs to
 // fill the GPU: a first launch of the same kernel without its output half (OUT =
@@ -53,8 +57,8 @@ using namespace linear;
 using bf16 = __nv_bfloat16;
 
 constexpr int kVT = 128;       // value columns per CTA
-constexpr int kSW = 8, kVW = 4;    // state warps, v' warps (multiples of 4)
-constexpr int kScore = kSW + kVW;  // first of the four score warps
+constexpr int kSW = 8;             // state warps; then the v' warps
+constexpr int kScore = kSW + 4;    // first of the four score warps
 constexpr int kLoad = kScore + 4;  // loads and decays; then the issuers of U, QK, INTER and INTRA
 constexpr int kThreads = (kLoad + 4) * 32;
 
@@ -291,20 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       if (!warp_item(a, it, &x) || skip<OUT>(x)) continue;
       const int chunks = x.chunks;
       const bool von = x.v0 + row < V;
-      const int64_t page_sz = (int64_t)K * V, at = (int64_t)x.hv * page_sz + x.v0 + row;
-      auto page = [&](uint32_t end) {  // page of the state after token end - 1
-        return p.pool + (int64_t)p.tables[(int64_t)x.r.seq * p.width + (end - 1) / (uint32_t)p.block] * p.HV * page_sz;
-      };
-      const float* src = nullptr;
-      if (OUT) {
-        // a split sequence's states all come from the scratch: its first page may be written by
-        // its last segment meanwhile
-        if (!(x.r.first && x.r.last)) src = a.segS + (int64_t)x.r.id * p.HV * page_sz;
-        else if (p.pool) src = x.r.pos0 > 0 && x.r.n > 0 ? page(x.r.pos0) : nullptr;
-        else if (p.s0) src = p.s0 + (int64_t)x.r.seq * p.HV * page_sz;
-      }
+      const int64_t at = ((int64_t)x.hv * K + cb) * V + x.v0 + row;
       {
-        const float* q = src ? src + at + (int64_t)cb * V : nullptr;
+        const float* src = state_src<OUT>(a, x);
+        const float* q = src ? src + at : nullptr;
 #pragma unroll
         for (int c = 0; c < NC; ++c, q += V) s[c] = src && von && cb + c < K ? __ldcg(q) : 0.f;
       }
@@ -350,103 +344,90 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
             d[1] = f.y;
           }
         }
-        const bool more = c + 1 < chunks;
-        float* dst = nullptr;  // where the state after this chunk is kept
-        if (!OUT) {            // the segment's whole decay, pair by pair
-          const float ph = wseg.x * wh;
-          const float pl = fmaf(wseg.x, wh, -ph) + (wseg.x * wl + wseg.y * wh);
-          wseg.x = ph + pl;
-          wseg.y = pl - (wseg.x - ph);
-          if (!more) {
-            dst = a.segS + (int64_t)x.r.id * p.HV * page_sz;
-            if (row == 0 && cb == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
-          }
-        } else if (p.pool) {
-          const uint32_t end = (uint32_t)(x.r.pos0 - x.off) + (uint32_t)(c + 1) * C;
-          if ((!more && x.r.last) || end % (uint32_t)p.block == 0) dst = page(min(end, (uint32_t)x.r.pos0 + (uint32_t)x.r.n));
-        } else if (!more && x.r.last && p.sT) {
-          dst = p.sT + (int64_t)x.r.seq * p.HV * page_sz;
-        }
+        if (!OUT) wseg = mul_pair(wseg, make_float2(wh, wl));
         if (OUT) {
-        ok = sy.wait_warp(&bars[B_O + (n & 1)], (n >> 1) & 1) && ok;
-        tc_fence_after();
-        if (more && ok) publish();
-        // the previous chunk's stores have read the tile
-        if (tid == 0) tma_store_wait_read();
-        if (!(ok = state_and(ok))) break;
-        // eight rows t at a time, as fragments: pairs of rows in a register, by value block of 8
-        const float* ein = g + 192 + (64 / NP) * part + 2 * (lane & 3);
+          ok = sy.wait_warp(&bars[B_O + (n & 1)], (n >> 1) & 1) && ok;
+          tc_fence_after();
+          if (ok && c + 1 < chunks) publish();
+          // the previous chunk's stores have read the tile
+          if (tid == 0) tma_store_wait_read();
+          if (!(ok = state_and(ok))) break;
+          // eight rows t at a time, as fragments: pairs of rows in a register, by value block of 8
+          const float* ein = g + 192 + (64 / NP) * part + 2 * (lane & 3);
 #pragma unroll 1
-        for (int z = 0; z < 8 / NP; ++z) {
-          const uint32_t col = (64 / NP) * part + 8 * z;
-          uint32_t r[8], w[8], out[4];
+          for (int z = 0; z < 8 / NP; ++z) {
+            const uint32_t col = (64 / NP) * part + 8 * z;
+            uint32_t r[8], w[8], out[4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTER + col, (r + 4 * q));
-            GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTRA + col, (w + 4 * q));
-          }
-          const float2 e = *reinterpret_cast<const float2*>(ein + 8 * z);
-          tmem_wait_ld();
-          if (z == 8 / NP - 1) {  // the next products may overwrite these
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_OREAD]);
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 f = upk2(fma2(pk2(e.x, e.y), pk2(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])),
-                                       pk2(__uint_as_float(w[2 * u]), __uint_as_float(w[2 * u + 1]))));
-            out[u] = cvt2(f.x, f.y);
-          }
-          // lanes 8 m .. address value block m
-          stmatrix_x4_trans(orow + z * 1024 + ((oc ^ (lane & 7)) << 4), out[0], out[1], out[2], out[3]);
-        }
-        // rows of the tile inside the sequence
-        const int base = x.r.t0 - x.off + c * C;
-        const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
-        const bool whole = lo == 0 && (hi == C || (!a.recs && x.r.last));
-        if (whole) {  // rows past a dense batch's end are clipped by the map
-          fence_async_smem();
-          state_and(true);
-          if (tid == 0) {
-            if (a.v_halves == 1) {
-              tma_store_5d(&map_o, sm + L::O, x.v0, x.hv, base, x.b, 0);
-              if (x.v0 + 64 < V) tma_store_5d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b, 0);
-            } else {
-              tma_store_5d(&map_o, sm + L::O, 0, x.hv, base, x.b, x.v0 >> 6);
+            for (int q = 0; q < 2; ++q) {
+              GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTER + col, (r + 4 * q));
+              GDP_TMEM_LD_16X256_X1(lb + (q << 20) + T_INTRA + col, (w + 4 * q));
             }
-            tma_store_commit();
-          }
-        } else {
-          state_and(true);
-          bf16* og = static_cast<bf16*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
-          const int j = tid & 15, c8 = 8 * j;  // 16-byte piece of the row (V is a multiple of 8)
-          if (x.v0 + c8 < V)
-            for (int t = lo + (tid >> 4); t < hi; t += 2 * kSW)
-              *reinterpret_cast<uint4*>(og + (int64_t)t * p.HV * V + c8) =
-                  *reinterpret_cast<const uint4*>(sm + L::O + (j >> 3) * 8192 + t * 128 + (((j & 7) ^ (t & 7)) << 4));
-          // the next chunk's barrier orders these reads before its writes
-        }
-        }
-        if (dst && von) {
-          dst += at + (int64_t)cb * V;
+            const float2 e = *reinterpret_cast<const float2*>(ein + 8 * z);
+            tmem_wait_ld();
+            if (z == 8 / NP - 1) {  // the next products may overwrite these
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[B_OREAD]);
+            }
 #pragma unroll
-          for (int c2 = 0; c2 < NC; ++c2, dst += V)
-            if (cb + c2 < K) *dst = s[c2];
+            for (int u = 0; u < 4; ++u) {
+              const float2 f = upk2(fma2(pk2(e.x, e.y), pk2(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])),
+                                         pk2(__uint_as_float(w[2 * u]), __uint_as_float(w[2 * u + 1]))));
+              out[u] = cvt2(f.x, f.y);
+            }
+            // lanes 8 m .. address value block m
+            stmatrix_x4_trans(orow + z * 1024 + ((oc ^ (lane & 7)) << 4), out[0], out[1], out[2], out[3]);
+          }
+          // rows of the tile inside the sequence
+          const int base = x.r.t0 - x.off + c * C;
+          const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
+          const bool whole = lo == 0 && (hi == C || (!a.recs && x.r.last));
+          if (whole) {  // rows past a dense batch's end are clipped by the map
+            fence_async_smem();
+            state_and(true);
+            if (tid == 0) {
+              if (a.v_halves == 1) {
+                tma_store_5d(&map_o, sm + L::O, x.v0, x.hv, base, x.b, 0);
+                if (x.v0 + 64 < V) tma_store_5d(&map_o, sm + L::O + 8192, x.v0 + 64, x.hv, base, x.b, 0);
+              } else {
+                tma_store_5d(&map_o, sm + L::O, 0, x.hv, base, x.b, x.v0 >> 6);
+              }
+              tma_store_commit();
+            }
+          } else {
+            state_and(true);
+            bf16* og = static_cast<bf16*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
+            const int j = tid & 15, c8 = 8 * j;  // 16-byte piece of the row (V is a multiple of 8)
+            if (x.v0 + c8 < V)
+              for (int t = lo + (tid >> 4); t < hi; t += 2 * kSW)
+                *reinterpret_cast<uint4*>(og + (int64_t)t * p.HV * V + c8) =
+                    *reinterpret_cast<const uint4*>(sm + L::O + (j >> 3) * 8192 + t * 128 + (((j & 7) ^ (t & 7)) << 4));
+            // the next chunk's barrier orders these reads before its writes
+          }
+        }
+        if (float* dst = state_dst<OUT>(a, x, c)) {
+          if (von) {
+            dst += at;
+#pragma unroll
+            for (int c2 = 0; c2 < NC; ++c2, dst += V)
+              if (cb + c2 < K) *dst = s[c2];
+          }
         }
       }
       if (!ok) break;
-      if (OUT && chunks == 0 && p.sT && von && x.r.last) {  // an empty sequence keeps its state
-        float* dst = p.sT + (int64_t)x.r.seq * p.HV * page_sz + at;
-        src += src ? at : 0;
-#pragma unroll 1
-        for (int k = cb; k < min(cb + NC, K); ++k) dst[(int64_t)k * V] = src ? __ldcg(src + (int64_t)k * V) : 0.f;
+      if (!OUT && chunks > 0 && row == 0 && cb == 0) a.segW[(int64_t)x.r.id * p.HV + x.hv] = wseg;
+      if (OUT && chunks == 0 && !p.pool && p.sT && von && x.r.last) {  // an empty sequence keeps its state
+        float* dst = p.sT + (int64_t)x.r.seq * p.HV * K * V + at;
+#pragma unroll
+        for (int c2 = 0; c2 < NC; ++c2, dst += V)
+          if (cb + c2 < K) *dst = s[c2];
       }
     }
     if (OUT && tid == 0) tma_store_wait_all();
   } else if (warp < kScore) {
     // ---------------------------------------------------------------- v'
-    const int quarter = warp & 3, ks0 = (warp - kSW) / 4 * (16 / kVW);  // first of this warp's steps
+    const int quarter = warp & 3;
     const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16) + T_V;
     // transposing loads: lanes 8 m .. 8 m + 7 address rows i of value block m (16-byte chunk
     // 4 (quarter % 2) + m, permuted by i % 8)
@@ -455,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     bool ok = true;
     for (int n = 0; n < total && ok; ++n) {
       if (!tiles(n)) break;
-      uint32_t va = smb + (n % L::NST) * L::STG + vrow + ks0 * 2048;
-      const float* g = gates(n) + 128 + ks0 * 16 + 2 * (lane & 3);
+      uint32_t va = smb + (n % L::NST) * L::STG + vrow;
+      const float* g = gates(n) + 128 + 2 * (lane & 3);
       // a step of U (16 positions) at a time, each as soon as U(n - 1) has read its own
 #pragma unroll 1
-      for (int ks = ks0; ks < ks0 + 16 / kVW; ++ks, va += 2048, g += 16) {
+      for (int ks = 0; ks < 4; ++ks, va += 2048, g += 16) {
         // register 4 hh + m: positions 8 hh + 2 (l % 4), + 1 of value column 8 m + l / 4
         uint32_t e[8], h[8], m[8], l[8];
         ldmatrix_x4_trans(va, e);
@@ -769,6 +750,7 @@ cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
 
 }  // namespace
 
+// As measured at K = V = 128 (smaller ones take as long: the roles' steps, not the bytes, set it).
 constexpr Cost kCost = {1.9, 1.3, 5.0, 9.0};
 
 bool linear_tc_shape(int K, int V, gdp_dtype dt) { return dt == GDP_BF16 && K <= 128 && K % 8 == 0 && V % 8 == 0; }
@@ -781,7 +763,7 @@ size_t linear_tc_workspace(int N_seq, int B, int T, int HV, int K, int V) {
 
 bool linear_tc_ok(const LinearProblem& p) {
   return linear_tc_shape(p.K, p.V, p.dt) && map_ok(p.q, p.H, p.T, p.B, p.qs) && map_ok(p.k, p.H, p.T, p.B, p.ks) &&
-         map_ok(p.v, p.HV, p.T, p.B, p.vs) && p.N_seq <= 65535 && p.HV <= 65535 && reinterpret_cast<uintptr_t>(p.o) % 16 == 0;
+         map_ok(p.v, p.HV, p.T, p.B, p.vs) && reinterpret_cast<uintptr_t>(p.o) % 16 == 0;
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
@@ -794,7 +776,7 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   a.vt = kVT;
   if ((int64_t)x.bound * p.HV * x.slices > INT32_MAX - 65536) return cudaErrorInvalidValue;
   a.items = x.bound * p.HV * x.slices;
-  if (a.items == 0) return cudaSuccess;
+  if (a.items == 0) return cudaMemsetAsync(p.status, 0, sizeof(int32_t), p.stream);  // kDevOk
   int2* seqs = nullptr;
   if (p.cu) {
     SegRec* recs = reinterpret_cast<SegRec*>(ws + x.recs);

@@ -130,7 +130,6 @@ __device__ __forceinline__ float2 exp_pair(float hi, float lo) {
   return make_float2(h * sc, l * sc);
 }
 
-
 // g at position i of the chunk whose position 0 is row `base`; 0 outside the sequence.
 __device__ __forceinline__ float load_g(const LinearProblem& p, const Item& x, int base, int i) {
   const int r = base + i;

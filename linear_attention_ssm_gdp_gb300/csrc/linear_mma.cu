@@ -446,7 +446,7 @@ cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
   a.vt = slice_of(p.K);
   if ((int64_t)x.bound * p.HV * x.slices > INT32_MAX) return cudaErrorInvalidValue;
   a.items = x.bound * p.HV * x.slices;
-  if (a.items == 0) return cudaSuccess;
+  if (a.items == 0) return cudaMemsetAsync(p.status, 0, sizeof(int32_t), p.stream);  // kDevOk
   int2* seqs = nullptr;
   if (p.cu) {
     SegRec* recs = reinterpret_cast<SegRec*>(ws + x.recs);

@@ -116,61 +116,65 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
 }
 
 // States at the segment starts: S_0 = the sequence's initial state, S_{j+1} = w_j S_j + U_j,
-// in place of the U's. A thread per VEC state elements.
+// in place of the U's. A thread per VEC state elements. HBM-bound (a read and a write of the
+// scratch), eight segments' loads in flight per thread.
 template <int VEC>
 __global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
   pdl_wait();
   const LinearProblem& p = a.p;
   const int64_t sz = (int64_t)p.K * p.V;
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-  const int hv = blockIdx.y, seq = blockIdx.z;
-  int first, cnt;
-  if (a.recs) {
-    const int2 x = seqs[seq];
-    first = x.x;
-    cnt = x.y;
-  } else {
-    first = seq * a.nseg;
-    cnt = a.nseg;
-  }
-  if (cnt < 2 || e >= sz) return;
-  const float* src = nullptr;
-  if (p.pool) {
-    const int c = p.ctx[seq];
-    if (c > 0) src = p.pool + (int64_t)p.tables[(int64_t)seq * p.width + (c - 1) / p.block] * p.HV * sz;
-  } else if (p.s0) {
-    src = p.s0 + (int64_t)seq * p.HV * sz;
-  }
-  float s[VEC];
+  if (e >= sz) return;
+  for (int64_t pair = blockIdx.y; pair < (int64_t)p.N_seq * p.HV; pair += gridDim.y) {
+    const int seq = (int)(pair / p.HV), hv = (int)(pair - (int64_t)seq * p.HV);
+    int first, cnt;
+    if (a.recs) {
+      const int2 x = seqs[seq];
+      first = x.x;
+      cnt = x.y;
+    } else {
+      first = seq * a.nseg;
+      cnt = a.nseg;
+    }
+    if (cnt < 2) continue;
+    const float* src = nullptr;
+    if (p.pool) {
+      const int c = p.ctx[seq];
+      if (c > 0) src = p.pool + (int64_t)p.tables[(int64_t)seq * p.width + (c - 1) / p.block] * p.HV * sz;
+    } else if (p.s0) {
+      src = p.s0 + (int64_t)seq * p.HV * sz;
+    }
+    float s[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) s[i] = 0.f;
-  auto load = [](float* d, const float* q) {
-    if (VEC == 4) *reinterpret_cast<float4*>(d) = __ldcg(reinterpret_cast<const float4*>(q));
-    else *d = __ldcg(q);
-  };
-  if (src) load(s, src + hv * sz + e);
-  float* seg = a.segS + ((int64_t)first * p.HV + hv) * sz + e;
-  const int64_t step = (int64_t)p.HV * sz;
-  const float2* w = a.segW + (int64_t)first * p.HV + hv;
-  for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight segments' loads in flight
-    const int m = min(8, cnt - 1 - j0);
-    alignas(16) float u[8][VEC];
-    float2 f[8];
+    for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+    auto load = [](float* d, const float* q) {
+      if (VEC == 4) *reinterpret_cast<float4*>(d) = __ldcg(reinterpret_cast<const float4*>(q));
+      else *d = __ldcg(q);
+    };
+    if (src) load(s, src + hv * sz + e);
+    float* seg = a.segS + ((int64_t)first * p.HV + hv) * sz + e;
+    const int64_t step = (int64_t)p.HV * sz;
+    const float2* w = a.segW + (int64_t)first * p.HV + hv;
+    for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight segments' loads in flight
+      const int m = min(8, cnt - 1 - j0);
+      alignas(16) float u[8][VEC];
+      float2 f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < m) {
-        load(u[j], seg + (j0 + j) * step);
-        f[j] = __ldcg(w + (int64_t)(j0 + j) * p.HV);
-      }
+      for (int j = 0; j < 8; ++j)
+        if (j < m) {
+          load(u[j], seg + (j0 + j) * step);
+          f[j] = __ldcg(w + (int64_t)(j0 + j) * p.HV);
+        }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < cnt) {
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < cnt) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) seg[(j0 + j) * step + i] = s[i];
-        if (j < m)
+          for (int i = 0; i < VEC; ++i) seg[(j0 + j) * step + i] = s[i];
+          if (j < m)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) s[i] = fmaf(f[j].x, s[i], fmaf(f[j].y, s[i], u[j][i]));
-      }
+            for (int i = 0; i < VEC; ++i) s[i] = fmaf(f[j].x, s[i], fmaf(f[j].y, s[i], u[j][i]));
+        }
+    }
   }
 }
 
@@ -216,7 +220,6 @@ Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt,
   return x;
 }
 
-
 cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs) {
   return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs);
 }
@@ -224,7 +227,7 @@ cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs,
 cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs) {
   const int64_t sz = (int64_t)a.p.K * a.p.V;
   const bool vec = sz % 4 == 0;
-  const dim3 grid((unsigned)cdiv(sz, vec ? 1024 : 256), a.p.HV, a.p.N_seq);
+  const dim3 grid((unsigned)cdiv(sz, vec ? 1024 : 256), (unsigned)std::min<int64_t>((int64_t)a.p.N_seq * a.p.HV, 65535));
   return vec ? launch_pdl(linear_combine_kernel<4>, grid, dim3(256), 0, a.p.stream, a, seqs)
              : launch_pdl(linear_combine_kernel<1>, grid, dim3(256), 0, a.p.stream, a, seqs);
 }

@@ -6,7 +6,7 @@
 //
 // The work is the state's read and write (8 bytes per element and call, against
 // 5 operations), so the kernel is an HBM stream: a CTA of 256 threads takes one
-// (request, value head, slice of up to 128 columns) and holds it in registers,
+// (request, value head, slice of up to 64 columns) and holds it in registers,
 // four columns (16 bytes) by R rows per thread, all loads in flight at once.
 // The sum over K of a read-out is in-thread over R rows, then shuffles across
 // the lanes of equal columns, then the eight warps through shared memory in a
@@ -200,8 +200,6 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : R <= 16 ? 2 : 1) linear
 
 template <typename T, int VEC, int R>
 cudaError_t go(const WalkArgs& a, int smem) {
-  cudaError_t e = allow_smem<linear_walk_kernel<T, VEC, R>>(52 * 1024);  // K = 256: 49 KB
-  if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)a.p.N_seq * a.p.HV * a.slices;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(linear_walk_kernel<T, VEC, R>, dim3((unsigned)grid), dim3(kThreads), smem,
@@ -220,12 +218,11 @@ cudaError_t pick(const LinearProblem& p) {
   a.VS = VS;
   a.slices = (int)cdiv(p.V, VS);
   const int RG = kThreads / (vec ? VS / 4 : VS), rows = (int)cdiv(p.K, RG);
-  const int smem = (2 * p.T * p.K + p.T * VS + 2 * kStep + 16 * VS) * 4;
+  const int smem = (2 * p.T * p.K + p.T * VS + 2 * kStep + 16 * VS) * 4;  // 40 KB for K = 256, 16 steps
   if (!vec) return rows <= 16 ? go<T, 1, 16>(a, smem) : go<T, 1, 32>(a, smem);
   if (rows <= 4) return go<T, 4, 4>(a, smem);
   if (rows <= 8) return go<T, 4, 8>(a, smem);
-  if (rows <= 16) return go<T, 4, 16>(a, smem);
-  return go<T, 4, 32>(a, smem);
+  return go<T, 4, 16>(a, smem);  // K <= 256: 16 rows at most
 }
 
 }  // namespace
