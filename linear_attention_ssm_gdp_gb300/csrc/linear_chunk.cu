@@ -28,8 +28,9 @@
 //     8 state warps   the state update, S as bf16; o = e^{Gam_t} INTER + INTRA, stores
 //     4 v' warps      v' of the next chunk
 //     4 score warps   P
-//     1 warp          TMA loads, decays of the chunk, rows outside the sequence zeroed
-//     3 warps         issue U, QK, and INTER with INTRA
+//     1 warp          decays of the chunk, rows outside the sequence zeroed
+//     1 warp          TMA loads, issues QK
+//     2 warps         issue U, and INTER with INTRA
 // The roles' loops are rolled where they can be: together they have to fit the 32 KB
 // first-level instruction cache, or the SMs of a GPC wait for their common next level (with
 // them unrolled a third of the warps' time went there, at 80 % of that cache's bandwidth).
@@ -59,8 +60,8 @@ using bf16 = __nv_bfloat16;
 constexpr int kVT = 128;       // value columns per CTA
 constexpr int kSW = 8;             // state warps; then the v' warps
 constexpr int kScore = kSW + 4;    // first of the four score warps
-constexpr int kLoad = kScore + 4;  // loads and decays; then the issuers of U, QK, INTER and INTRA
-constexpr int kThreads = (kLoad + 4) * 32;
+constexpr int kDecay = kScore + 4;  // decays; then the issuers of U, of loads and QK, of INTER and INTRA
+constexpr int kThreads = (kDecay + 4) * 32;
 
 // ------------------------------------------------------------------ arithmetic
 typedef unsigned long long f2;
@@ -103,6 +104,13 @@ __device__ __forceinline__ uint32_t cvt2(float a, float b) {
 __device__ __forceinline__ f2 wide(uint32_t h) {  // the two bf16 as floats
   return pk2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u));
 }
+// 4 bytes to shared memory, zeros unless `on` (src is not read then).
+__device__ __forceinline__ void cp_async4(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 // ------------------------------------------------------------------ work items
 // (Kept in shared memory, not in registers: with 220 KB of that in use the first-level cache is
 // too small for anything that would spill to local memory.)
@@ -199,19 +207,22 @@ struct Lay {
   static constexpr int G = O + (OUT ? 16384 : 0);
   static constexpr int GS = 272 * 4;                    // hi2, lo2, wend, ein [64] each, e^Gam hi, lo
   static constexpr int BAR = G + 8 * GS;
-  static constexpr int ITEM = BAR + 256;                // work items, one slot per state warp and two more
+  static constexpr int RAW = BAR + 256;                 // g as loaded, four chunks
+  static constexpr int ITEM = RAW + 1024;               // work items, one slot per state warp and two more
   static constexpr int BYTES = ITEM + (kSW + 2) * 64 + 1024;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 // full, ready, free by stage; v' ready and free by step; INTER and INTRA done, P done by parity;
-// the rest single
+// U done and read by buffer; the rest single
 enum {
   B_FULL = 0, B_READY = 3, B_FREE = 6, B_V = 9, B_VFREE = 13, B_O = 17, B_P = 19, B_QK = 21, B_SREAD, B_OREAD, B_S, B_U,
-  B_UREAD, B_N
+  B_UREAD = B_U + 2, B_N = B_UREAD + 2
 };
 
 // TMEM columns: scores [64], INTER and INTRA [64] each, U [KD], S [KD / 2], v' [3][32]
 constexpr uint32_t T_QK = 0, T_INTER = 64, T_INTRA = 128, T_U = 192, T_S = 320, T_V = 384;
+// (the state pass has no scores and outputs: two U's [128] in their place, so that one is formed while
+// the other is read)
 
 template <int KD, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
@@ -236,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     for (int i = 0; i < B_N; ++i) {
       int n = 1;
       if (i >= B_FREE && i < B_V) n = OUT ? 2 : 1;                   // both issuing warps
-      if (i == B_OREAD || i == B_S || i == B_UREAD) n = kSW;         // state warps
+      if (i == B_OREAD || i == B_S || i >= B_UREAD) n = kSW;         // state warps
       if ((i >= B_V && i < B_VFREE) || i == B_P || i == B_P + 1 || i == B_SREAD) n = 4;  // v' or score warps
       mbar_init(&bars[i], n);
     }
     fence_mbar_init();
     *s_dead = 0;
   }
-  if (warp == kLoad && lane == 0) {
+  if (warp == kDecay && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
     if (OUT) prefetch_tmap(&map_q);
@@ -274,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     return sy.wait_warp(&bars[B_READY + n % L::NST], ph) && sy.wait_warp(&bars[B_FULL + n % L::NST], ph);
   };
   const int K = p.K, V = p.V;
+  constexpr int NU = OUT ? 1 : 2;  // U's
+  auto u_at = [&](int n) { return tmem + (OUT ? T_U : (uint32_t)(128 * (n & 1))); };
 
   if (warp < kSW) {
     // ---------------------------------------------------------------- state, output
@@ -319,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       float2 wseg = make_float2(1.f, 0.f);
       for (int c = 0; c < chunks; ++c, ++n) {
         // a failed wait leaves through the barrier below, with the whole group
-        ok = sy.wait_warp(&bars[B_U], n & 1);
+        ok = sy.wait_warp(&bars[B_U + n % NU], (n / NU) & 1);
         if (!OUT && !ok) break;
         tc_fence_after();
         const float* g = gates(n);
@@ -328,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
 #pragma unroll
         for (int q = 0; q < NC; q += 16) {
           uint32_t r[16];
-          GDP_TMEM_LD16(lb + T_U + cb + q, r);
+          GDP_TMEM_LD16(u_at(n) + ((uint32_t)(quarter * 32) << 16) + cb + q, r);
           tmem_wait_ld();
           if (q + 16 == NC) {
             tc_fence_before();  // the next U may overwrite this one
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_UREAD]);
+            if (lane == 0) mbar_arrive(&bars[B_UREAD + n % NU]);
           }
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
@@ -425,9 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       }
     }
     if (OUT && tid == 0) tma_store_wait_all();
-  } else if (warp < kScore) {
+  } else if (warp < (OUT ? kScore : kDecay)) {
     // ---------------------------------------------------------------- v'
-    const int quarter = warp & 3;
+    // (in the state pass by the score warps too, two of a chunk's four steps each)
+    constexpr int KS = OUT ? 4 : 2;
+    const int quarter = warp & 3, ks0 = (warp - kSW) / 4 * KS;
     const uint32_t lb = tmem + ((uint32_t)(quarter * 32) << 16) + T_V;
     // transposing loads: lanes 8 m .. 8 m + 7 address rows i of value block m (16-byte chunk
     // 4 (quarter % 2) + m, permuted by i % 8)
@@ -436,11 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     bool ok = true;
     for (int n = 0; n < total && ok; ++n) {
       if (!tiles(n)) break;
-      uint32_t va = smb + (n % L::NST) * L::STG + vrow;
-      const float* g = gates(n) + 128 + 2 * (lane & 3);
+      uint32_t va = smb + (n % L::NST) * L::STG + vrow + ks0 * 2048;
+      const float* g = gates(n) + 128 + ks0 * 16 + 2 * (lane & 3);
       // a step of U (16 positions) at a time, each as soon as U(n - 1) has read its own
 #pragma unroll 1
-      for (int ks = 0; ks < 4; ++ks, va += 2048, g += 16) {
+      for (int ks = ks0; ks < ks0 + KS; ++ks, va += 2048, g += 16) {
         // register 4 hh + m: positions 8 hh + 2 (l % 4), + 1 of value column 8 m + l / 4
         uint32_t e[8], h[8], m[8], l[8];
         ldmatrix_x4_trans(va, e);
@@ -472,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         if (lane == 0) mbar_arrive(&bars[B_V + ks]);
       }
     }
-  } else if (warp < kLoad) {
+  } else if (warp < kDecay) {
     // ---------------------------------------------------------------- scores
     if (OUT) {
       // rows t0 + l / 4 (+ 8) of the chunk, columns 2 (l % 4) (+ 1) of a block of 8, as fragments
@@ -522,70 +537,36 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         if (lane == 0) mbar_arrive(&bars[B_P + (n & 1)]);
       }
     }
-  } else if (warp == kLoad) {
-    // ---------------------------------------------------------------- loads, decays
+  } else if (warp == kDecay) {
+    // ---------------------------------------------------------------- decays
+    float* ring = reinterpret_cast<float*>(sm + L::RAW) + 2 * lane;  // g as loaded, four chunks
     int n = 0;
     bool ok = true;
-    int nl = 0, lk = -1, lc = 0;  // next load: chunk lc of this CTA's item lk
-    Item& lx = *reinterpret_cast<Item*>(sm + L::ITEM + kSW * 64);
-    int lchunks = 0;
-    // the tiles of the next chunks, up to a ring ahead of chunk n; a stage that is not free yet is
-    // waited for only if chunk n itself is still to load
-    auto loads = [&](int now) {
-      while (nl < total && nl < now + L::NST) {
-        const int st = nl % L::NST;
-        if (nl >= L::NST) {
-          const uint32_t ph = (nl / L::NST - 1) & 1;
-          if (nl > now) {
-            if (!__all_sync(0xffffffffu, mbar_poll(&bars[B_FREE + st], ph))) return true;
-          } else if (!sy.wait_warp(&bars[B_FREE + st], ph)) {
-            return false;
-          }
-        }
-        while (lc >= lchunks) {
-          ++lk;
-          lc = 0;
-          lchunks = warp_item(a, nth_item(lk), &lx) && !skip<OUT>(lx) ? lx.chunks : 0;
-        }
-        if (elect_one()) {
-          const int t = lx.r.t0 - lx.off + lc * C;
-          uint8_t* tile = sm + st * L::STG;
-          uint64_t* bar = &bars[B_FULL + st];
-          // a tensor whose width is whole halves comes by one load, both halves in its box; of
-          // another the second half is its own load (zeros past the width), if there is one
-          const bool two = a.v_halves == 1 && lx.v0 + 64 < V, twok = KD == 128 && a.k_halves == 1;
-          mbar_expect_tx(bar, (OUT ? 2 : 1) * L::KT + 8192 * (two ? 2 : a.v_halves));
-          if (OUT) tma_load_5d(tile, &map_q, 0, lx.h, t, lx.b, 0, bar);
-          tma_load_5d(tile + L::KT, &map_k, 0, lx.h, t, lx.b, 0, bar);
-          if (a.v_halves == 1) tma_load_5d(tile + L::VT, &map_v, lx.v0, lx.hv, t, lx.b, 0, bar);
-          else tma_load_5d(tile + L::VT, &map_v, 0, lx.hv, t, lx.b, lx.v0 >> 6, bar);
-          if (twok) {
-            if (OUT) tma_load_5d(tile + 8192, &map_q, 64, lx.h, t, lx.b, 0, bar);
-            tma_load_5d(tile + L::KT + 8192, &map_k, 64, lx.h, t, lx.b, 0, bar);
-          }
-          if (two) tma_load_5d(tile + L::VT + 8192, &map_v, lx.v0 + 64, lx.hv, t, lx.b, 0, bar);
-        }
-        __syncwarp();
-        ++lc;
-        ++nl;
-      }
-      return true;
-    };
     for (int kk = 0; ok && (int64_t)kk * gridDim.x < a.items; ++kk) {
-      const int it = nth_item(kk);
-      Item& x = *reinterpret_cast<Item*>(sm + L::ITEM + (kSW + 1) * 64);
-      if (!warp_item(a, it, &x) || skip<OUT>(x)) continue;
-      const int chunks = x.chunks, base0 = x.r.t0 - x.off;
-      float g0 = load_g(p, x, base0, 2 * lane), g1 = load_g(p, x, base0, 2 * lane + 1);
+      Item& x = *reinterpret_cast<Item*>(sm + L::ITEM + kSW * 64);
+      if (!warp_item(a, nth_item(kk), &x) || skip<OUT>(x)) continue;
+      const int chunks = x.chunks, base0 = x.r.t0 - x.off, t1 = x.r.t0 + x.r.n;
+      auto fetch = [&](int c) {  // zeros outside the sequence
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = base0 + c * C + 2 * lane + u;
+          const bool on = p.g && t >= x.r.t0 && t < t1;
+          const int64_t at = p.g_token ? ((int64_t)x.b * p.T + t) * p.HV + x.hv : x.hv;
+          cp_async4(ring + (c & 3) * C + u, on ? p.g + at : static_cast<const float*>(p.k), on);
+        }
+        cp_async_commit();
+      };
+      fetch(0);
+      fetch(1);
       for (int c = 0; c < chunks; ++c, ++n) {
         const int st = n % L::NST, base = base0 + c * C;
-        const int lo = max(0, x.r.t0 - base), hi = min(C, x.r.t0 + x.r.n - base);
-        const float n0 = load_g(p, x, base + C, 2 * lane), n1 = load_g(p, x, base + C, 2 * lane + 1);
-        // (once chunk n's load has gone out, the decays of chunk n - 8 have been used)
-        if (!(ok = loads(n))) break;
-        chunk_decays(g0, g1, p.scale, lo, hi, lane, gates(n));
-        g0 = n0;
-        g1 = n1;
+        const int lo = max(0, x.r.t0 - base), hi = min(C, t1 - base);
+        fetch(c + 2);
+        // chunk n - 3's products are done, so the decays of chunk n - 8 have been used
+        if (n >= L::NST && !(ok = sy.wait_warp(&bars[B_FREE + st], (n / L::NST - 1) & 1))) break;
+        cp_async_wait<2>();
+        const float2 g = *reinterpret_cast<const float2*>(ring + (c & 3) * C);
+        chunk_decays(g.x, g.y, p.scale, lo, hi, lane, gates(n));
         if (!(ok = sy.wait_warp(&bars[B_FULL + st], (n / L::NST) & 1))) break;
         if (lo > 0 || hi < C) {
           // rows of other sequences, or past the end: k and v as zeros, so that nothing in
@@ -605,18 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_READY + st]);
       }
+      cp_async_wait<0>();
     }
-    // nothing may still write shared memory when the CTA leaves
-    for (int m = max(0, nl - L::NST); m < nl; ++m) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
-    }
-  } else if (warp == kLoad + 1) {
+  } else if (warp == kDecay + 1) {
     // ---------------------------------------------------------------- U
     const uint32_t id_u = idesc_bf16(128, KD, false, true);
     for (int n = 0; n < total; ++n) {
       bool ok = tiles(n);
-      if (n > 0) ok = sy.wait_warp(&bars[B_UREAD], (n - 1) & 1) && ok;
+      if (n >= NU) ok = sy.wait_warp(&bars[B_UREAD + n % NU], (n / NU - 1) & 1) && ok;
       const uint64_t kd = sdesc_sw128(smb + (n % L::NST) * L::STG + L::KT, 8192, 1024);
 #pragma unroll 1
       for (int ks = 0; ks < 4; ++ks) {
@@ -626,12 +603,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           tc_fence_after();
           const uint64_t k = kd + (uint64_t)(ks * (2048 >> 4));
           const uint32_t av = tmem + T_V + 8 * ks;
-          mma_bf16_ts(tmem + T_U, av + 64, k, id_u, ks > 0);
-          mma_bf16_ts(tmem + T_U, av + 32, k, id_u, 1);
-          mma_bf16_ts(tmem + T_U, av, k, id_u, 1);
+          mma_bf16_ts(u_at(n), av + 64, k, id_u, ks > 0);
+          mma_bf16_ts(u_at(n), av + 32, k, id_u, 1);
+          mma_bf16_ts(u_at(n), av, k, id_u, 1);
           mma_commit(&bars[B_VFREE + ks]);
           if (ks == 3) {
-            mma_commit(&bars[B_U]);
+            mma_commit(&bars[B_U + n % NU]);
             mma_commit(&bars[B_FREE + n % L::NST]);
           }
         }
@@ -639,24 +616,68 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       }
       if (!ok) break;
     }
-  } else if (OUT && warp == kLoad + 2) {
-    // ---------------------------------------------------------------- QK
+  } else if (warp == kDecay + 2) {
+    // ---------------------------------------------------------------- loads, QK
     const uint32_t id = idesc_bf16(64, 64, false, false);
-    for (int n = 0; n < total; ++n) {
-      if (!tiles(n)) break;
-      if (n > 0 && !sy.wait_warp(&bars[B_SREAD], (n - 1) & 1)) break;
+    int next = 0, kk = -1, c = 0, chunks = 0;  // the next load: chunk c of the CTA's item kk
+    Item& x = *reinterpret_cast<Item*>(sm + L::ITEM + (kSW + 1) * 64);
+    auto load = [&] {
+      const int st = next % L::NST;
+      if (next >= L::NST && !sy.wait_warp(&bars[B_FREE + st], (next / L::NST - 1) & 1)) return false;
+      while (c >= chunks) {
+        c = 0;
+        chunks = warp_item(a, nth_item(++kk), &x) && !skip<OUT>(x) ? x.chunks : 0;
+      }
       if (elect_one()) {
-        tc_fence_after();
-        const uint32_t tl = smb + (n % L::NST) * L::STG;
-        const uint64_t qd = sdesc_sw128(tl, 16, 1024), kd = sdesc_sw128(tl + L::KT, 16, 1024);
-#pragma unroll 1
-        for (int i = 0; i < KD / 16; ++i) {
-          const uint64_t o = (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2);
-          mma_bf16(tmem + T_QK, qd + o, kd + o, id, i > 0);
-        }
-        mma_commit(&bars[B_QK]);
+          const int t = x.r.t0 - x.off + c * C;
+          uint8_t* tile = sm + st * L::STG;
+          uint64_t* bar = &bars[B_FULL + st];
+          // a tensor whose width is whole halves comes by one load, both halves in its box; of
+          // another the second half is its own load (zeros past the width), if there is one
+          const bool two = a.v_halves == 1 && x.v0 + 64 < V, twok = KD == 128 && a.k_halves == 1;
+          mbar_expect_tx(bar, (OUT ? 2 : 1) * L::KT + 8192 * (two ? 2 : a.v_halves));
+          if (OUT) tma_load_5d(tile, &map_q, 0, x.h, t, x.b, 0, bar);
+          tma_load_5d(tile + L::KT, &map_k, 0, x.h, t, x.b, 0, bar);
+          if (a.v_halves == 1) tma_load_5d(tile + L::VT, &map_v, x.v0, x.hv, t, x.b, 0, bar);
+          else tma_load_5d(tile + L::VT, &map_v, 0, x.hv, t, x.b, x.v0 >> 6, bar);
+          if (twok) {
+            if (OUT) tma_load_5d(tile + 8192, &map_q, 64, x.h, t, x.b, 0, bar);
+            tma_load_5d(tile + L::KT + 8192, &map_k, 64, x.h, t, x.b, 0, bar);
+          }
+          if (two) tma_load_5d(tile + L::VT + 8192, &map_v, x.v0 + 64, x.hv, t, x.b, 0, bar);
       }
       __syncwarp();
+      ++c;
+      ++next;
+      return true;
+    };
+    // the scores of chunk n, then the load of the chunk after the next one into the stage that chunk
+    // n - 1 leaves: by then its products are done, or nearly
+    bool ok = true;
+    while (ok && next < min(total, L::NST)) ok = load();
+    for (int n = 0; ok && n < total; ++n) {
+      if (OUT) {
+        if (!(ok = tiles(n))) break;
+        if (n > 0 && !(ok = sy.wait_warp(&bars[B_SREAD], (n - 1) & 1))) break;
+        if (elect_one()) {
+          tc_fence_after();
+          const uint32_t tl = smb + (n % L::NST) * L::STG;
+          const uint64_t qd = sdesc_sw128(tl, 16, 1024), kd = sdesc_sw128(tl + L::KT, 16, 1024);
+#pragma unroll 1
+          for (int i = 0; i < KD / 16; ++i) {
+            const uint64_t o = (uint64_t)((i >> 2) * (8192 >> 4) + (i & 3) * 2);
+            mma_bf16(tmem + T_QK, qd + o, kd + o, id, i > 0);
+          }
+          mma_commit(&bars[B_QK]);
+        }
+        __syncwarp();
+      }
+      if (n > 0 && next < total) ok = load();
+    }
+    // nothing may still write shared memory when the CTA leaves
+    for (int m = max(0, next - L::NST); m < next; ++m) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
     }
   } else if (OUT) {
     // ---------------------------------------------------------------- INTER, INTRA
@@ -686,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   }
   __syncwarp();
   if (*s_dead) {  // products in flight end before their operands and columns go away
-    if (warp == kLoad + 1 && lane == 0) {
+    if (warp == kDecay + 1 && lane == 0) {
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) {}  // a chunk's products take microseconds
     }
