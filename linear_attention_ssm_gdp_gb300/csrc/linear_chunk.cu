@@ -34,11 +34,12 @@
 // The roles' loops are rolled where they can be: together they have to fit the 32 KB
 // first-level instruction cache, or the SMs of a GPC wait for their common next level (with
 // them unrolled a third of the warps' time went there, at 80 % of that cache's bandwidth).
-// Measured: 1.9 us a chunk (K = V = 128) on a CTA of its own SM, 10 us for a call of one chunk;
-// 2 x 4096 tokens, 16 heads: 78 us with the state pass and the combine kernel. What is left
-// above the 1.5 us is the state warps' loop (U's read, the update, S's write, the output's
-// read and staging, one after another); sixteen state warps and four output warps at 64
-// registers take the same time.
+// Measured: 1.8 us a chunk (K = V = 128), 1.2 in the state pass, 9.4 us for a call of one chunk;
+// 2 x 4096 tokens, 16 heads: 70 us with the state pass and the combine kernel. What is left above
+// the 1.5 us is a stage's round trip over its three places: 1.4 us for a load to land, as long
+// again for v' at the rate that four warps reach beside the others, then U and INTRA. Measured in
+// place of it: four stages with one P buffer, 73 us; a step of v' on the score warps, 72; sixteen
+// state and four output warps at 64 registers, 78 (as eight then were).
 //
 // Sequences are cut into segments when there are too few (sequence, head) pairs to
 // fill the GPU: a first launch of the same kernel without its output half (OUT =
@@ -623,7 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     Item& x = *reinterpret_cast<Item*>(sm + L::ITEM + (kSW + 1) * 64);
     auto load = [&] {
       const int st = next % L::NST;
-      if (next >= L::NST && !sy.wait_warp(&bars[B_FREE + st], (next / L::NST - 1) & 1)) return false;
       while (c >= chunks) {
         c = 0;
         chunks = warp_item(a, nth_item(++kk), &x) && !skip<OUT>(x) ? x.chunks : 0;
@@ -649,16 +649,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       __syncwarp();
       ++c;
       ++next;
-      return true;
     };
-    // the scores of chunk n, then the load of the chunk after the next one into the stage that chunk
-    // n - 1 leaves: by then its products are done, or nearly
-    bool ok = true;
-    while (ok && next < min(total, L::NST)) ok = load();
-    for (int n = 0; ok && n < total; ++n) {
-      if (OUT) {
-        if (!(ok = tiles(n))) break;
-        if (n > 0 && !(ok = sy.wait_warp(&bars[B_SREAD], (n - 1) & 1))) break;
+    // loads and scores as each becomes possible, whichever is first
+    auto all = [](bool yes) { return __all_sync(0xffffffffu, yes); };
+    uint64_t since = 0;  // nothing was possible since then
+    for (int n = 0, spins = 0; OUT ? n < total : next < total;) {
+      const bool qk = OUT && n < next && all(mbar_poll(&bars[B_READY + n % L::NST], (n / L::NST) & 1) &&
+                                             mbar_poll(&bars[B_FULL + n % L::NST], (n / L::NST) & 1) &&
+                                             (n == 0 || mbar_poll(&bars[B_SREAD], (n - 1) & 1)));
+      if (qk) {
         if (elect_one()) {
           tc_fence_after();
           const uint32_t tl = smb + (n % L::NST) * L::STG;
@@ -671,8 +670,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           mma_commit(&bars[B_QK]);
         }
         __syncwarp();
+        ++n;
+      } else if (next < total && (next < L::NST || all(mbar_poll(&bars[B_FREE + next % L::NST], (next / L::NST - 1) & 1)))) {
+        load();
+      } else {
+        if ((++spins & 63) == 0) {  // a bounded wait like the others
+          const uint64_t t = globaltimer_ns();
+          if (spins == 64) since = t;
+          if (__any_sync(0xffffffffu, *sy.dead || t - since > kWaitBudgetNs)) {
+            if (lane == 0 && !*sy.dead) {
+              if (p.status) atomicExch(p.status, kDevTimeout);
+              *sy.dead = 1;
+            }
+            break;
+          }
+        }
+        continue;
       }
-      if (n > 0 && next < total) ok = load();
+      spins = 0;
     }
     // nothing may still write shared memory when the CTA leaves
     for (int m = max(0, next - L::NST); m < next; ++m) {
@@ -771,8 +786,10 @@ cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
 
 }  // namespace
 
-// As measured at K = V = 128 (smaller ones take as long: the roles' steps, not the bytes, set it).
-constexpr Cost kCost = {1.9, 1.3, 5.0, 9.0};
+// As measured at K = V = 128 (smaller ones take as long: the roles' steps, not the bytes, set it); an
+// item's and a split's fixed times are the best of a sweep over 16 sizes from 16 heads x 192 tokens to
+// 32 x 16384 (1 x 700 tokens, 16 heads: 20.4 us, against 25.8 with 5 and 9).
+constexpr Cost kCost = {1.85, 1.2, 3.0, 6.0};
 
 bool linear_tc_shape(int K, int V, gdp_dtype dt) { return dt == GDP_BF16 && K <= 128 && K % 8 == 0 && V % 8 == 0; }
 
