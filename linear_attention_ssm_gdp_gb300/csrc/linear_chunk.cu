@@ -240,6 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const LinearProblem& p = a.p;
 
+  if (!OUT) {
+    pdl_wait();
+    if (no_split(a)) return;
+  }
   if (warp == 0) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
@@ -820,7 +824,9 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
     SegRec* recs = reinterpret_cast<SegRec*>(ws + x.recs);
     seqs = reinterpret_cast<int2*>(ws + x.seqs);
     a.recs = recs;
-    const cudaError_t e = launch_segments(p, x, recs, seqs);
+    int* split = reinterpret_cast<int*>(ws) + 1;  // beside the status word
+    a.split = split;
+    const cudaError_t e = launch_segments(p, x, recs, seqs, split);
     if (e != cudaSuccess) return e;
   }
   CUtensorMap m[4];

@@ -20,6 +20,7 @@ struct SegRec {
 struct ChunkArgs {
   LinearProblem p;
   const SegRec* recs;   // packed batches; seq = -1 past the last
+  const int* split;     // packed batches: whether any sequence is in several segments
   int nseg, Lseg;       // dense batches: segments per sequence, tokens per segment
   int slices, vt;       // slices of vt value columns
   int items;            // bound over all CTAs
@@ -42,7 +43,7 @@ Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt,
 
 // The two kernels around the state pass: segment records of a packed batch, and the states at
 // the segment starts.
-cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs);
+cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs, int* split);
 cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs);
 
 struct Item {
@@ -181,6 +182,10 @@ __device__ __forceinline__ void chunk_decays(float g0, float g1, float scale, in
   *reinterpret_cast<float2*>(g + 192 + 2 * lane) = make_float2(ei[0], ei[1]);
   if (lane == 0) *reinterpret_cast<float2*>(g + 256) = w;
 }
+
+// A state pass (or the combine kernel) with nothing to do: only the device knows how a packed
+// batch's sequences came out.
+__device__ __forceinline__ bool no_split(const ChunkArgs& a) { return a.split && __ldcg(a.split) == 0; }
 
 // Where the state after chunk c of an item is kept (null: nowhere), base of [HV, K, V].
 template <bool OUT>

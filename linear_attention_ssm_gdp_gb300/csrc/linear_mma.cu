@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
   extern __shared__ __align__(16) uint8_t sm[];
   const LinearProblem& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+  if (!OUT && no_split(a)) return;
   if (!a.recs && blockIdx.x == 0 && tid == 0 && p.status) *p.status = kDevOk;
   Item x;
   if (!get_item(a, blockIdx.x, x) || skip<OUT>(x)) return;
@@ -452,7 +453,9 @@ cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
     SegRec* recs = reinterpret_cast<SegRec*>(ws + x.recs);
     seqs = reinterpret_cast<int2*>(ws + x.seqs);
     a.recs = recs;
-    const cudaError_t e = launch_segments(p, x, recs, seqs);
+    int* split = reinterpret_cast<int*>(ws) + 1;  // beside the status word
+    a.split = split;
+    const cudaError_t e = launch_segments(p, x, recs, seqs, split);
     if (e != cudaSuccess) return e;
   }
   // 16-byte copies: rows and bases on 16-byte steps, whole vectors in a row

@@ -26,7 +26,8 @@ __device__ __forceinline__ int table_page(const LinearProblem& p, int r, int64_t
 }
 
 __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __grid_constant__ LinearProblem p,
-                                                                      int Lseg, int bound, SegRec* recs, int2* seqs) {
+                                                                      int Lseg, int bound, SegRec* recs, int2* seqs,
+                                                                      int* split) {
   pdl_wait();
   __shared__ int lens[kSortMax];
   __shared__ int wsum[kRecThreads / 32 + 1];
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
     bad |= x < 0 || y < x || y > p.T;
   }
   bad = __syncthreads_or(bad);
-  bool any = bad;
+  bool any = bad, cut = false;
   int base = 0;  // segments before this round of sequences
   for (int i0 = 0; i0 < p.N_seq; i0 += kRecThreads) {
     const int i = i0 + tid;
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
       }
       cnt = n > 0 ? (int)(((int64_t)pos % C + n + Lseg - 1) / Lseg) : 1;
     }
+    cut |= cnt > 1;
     int s = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -91,7 +93,11 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
     __syncthreads();
   }
   any = __syncthreads_or(any);
-  if (tid == 0 && p.status) *p.status = any ? kDevBadSeqlens : kDevOk;
+  cut = __syncthreads_or(cut);
+  if (tid == 0) {
+    *split = cut;
+    if (p.status) *p.status = any ? kDevBadSeqlens : kDevOk;
+  }
   const int count = base;
   if (count <= kSortMax && count > 1) {  // in place: every thread reads its records first
     SegRec mine[kSortMax / kRecThreads];
@@ -121,6 +127,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
 template <int VEC>
 __global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
   pdl_wait();
+  if (no_split(a)) return;
   const LinearProblem& p = a.p;
   const int64_t sz = (int64_t)p.K * p.V;
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
@@ -220,14 +227,17 @@ Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt,
   return x;
 }
 
-cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs) {
-  return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs);
+cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs, int* split) {
+  return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs,
+                    split);
 }
 
 cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs) {
   const int64_t sz = (int64_t)a.p.K * a.p.V;
   const bool vec = sz % 4 == 0;
-  const dim3 grid((unsigned)cdiv(sz, vec ? 1024 : 256), (unsigned)std::min<int64_t>((int64_t)a.p.N_seq * a.p.HV, 65535));
+  // up to eight CTAs per SM (two are resident): a packed batch's may all have nothing to do
+  const int64_t gx = cdiv(sz, vec ? 1024 : 256), gy = std::max<int64_t>(1, 8 * sm_count() / gx);
+  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((int64_t)a.p.N_seq * a.p.HV, gy));
   return vec ? launch_pdl(linear_combine_kernel<4>, grid, dim3(256), 0, a.p.stream, a, seqs)
              : launch_pdl(linear_combine_kernel<1>, grid, dim3(256), 0, a.p.stream, a, seqs);
 }
