@@ -69,8 +69,8 @@ __device__ __forceinline__ float finish(const NormArgs& a, float z, float gt) {
 // ---------------------------------------------------------------- one position per sample
 // TG lanes hold one (sample, group): NV 16-byte vectors each; U samples per lane group are in
 // flight at once, far apart in N so that they share their channels' weights. 8192 x 4096 bf16
-// with a gate: see the table of measured cases; scalar weight loads and an exact exponential
-// made the kernel issue-bound (77 us).
+// with a gate, 32 groups: 37.8 us, 201 MB at 5.3 TB/s, 78 % of a plain copy; issue slots are 73 %
+// used (scalar weight loads and an exact exponential made it issue-bound, 77 us).
 template <typename TX, typename TO, int TG, int NV, int U, bool GATE>
 __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ NormArgs a, int64_t Nu) {
   pdl_wait();
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
 // A cluster of CTAs takes one sample and a set of GS neighbouring groups (enough that its row
 // segments fill whole sectors), each CTA a run of positions; the group sums meet through
 // distributed shared memory. A thread keeps one vector column, so that its channels' groups
-// are fixed, and walks down the positions.
+// are fixed, and walks down the positions. 4 x 4096 x 320 fp16 in 32 groups, 21 MB: 13.1 us;
+// what it waits for is latency: two reductions over a cluster and the loads of a few warps.
 constexpr int kMapThreads = 256;
 constexpr int kMaxGS = 128;
 constexpr int kMapSmem = 200 * 1024;  // most that a CTA keeps
@@ -343,13 +344,17 @@ cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
 
 template <typename TX, typename TO, int VEC>
 cudaError_t go_map(NormArgs a, cudaStream_t s) {
-  // whole sectors per row: at least 128 bytes of neighbouring groups, a multiple of a vector
-  a.GS = 1;
-  while (a.GS < a.G && a.GS < kMaxGS &&
-         ((int64_t)a.GS * a.Cg * sizeof(TX) < 128 || (a.GS * a.Cg) % VEC != 0))
-    ++a.GS;
-  // a thread's channels must keep their groups, so a set of several groups is one pass of columns
-  a.sets = (int)cdiv(a.G, a.GS);
+  // A set's row segment is whole vectors and at least 128 bytes; half and a quarter of that where
+  // even clusters of 8 would leave SMs idle or a CTA with more than 48 KB (4 x 4096 x 320 in 32
+  // groups, fp16: 13.1 us, against 18.2 with 128 bytes; 1 x 16384 x 128, 32 groups: 15.3 / 48.6),
+  // but not beyond (16 x 256 x 1280, 32 groups: 16.2 us with 64 bytes, 12.4 with 128).
+  for (const int64_t least : {128, 64, 32}) {
+    a.GS = 1;
+    while (a.GS < a.G && a.GS < kMaxGS && ((int64_t)a.GS * a.Cg * sizeof(TX) < least || (a.GS * a.Cg) % VEC != 0)) ++a.GS;
+    // a thread's channels must keep their groups, so a set of several groups is one pass of columns
+    a.sets = (int)cdiv(a.G, a.GS);
+    if (a.N * a.sets * 8 >= sm_count() && cdiv(a.L, 8) * a.GS * a.Cg * (int64_t)sizeof(TX) <= 48 * 1024) break;
+  }
   const int64_t units = a.N * a.sets;
   const int64_t seg = (int64_t)a.GS * a.Cg * sizeof(TX);
   // CTAs per cluster: until every SM has one, or 8 KB of work are left each (clusters of 16 found
