@@ -14,7 +14,7 @@
 // (measured: 12,000 cycles a chunk for fp16 K = V = 64, 17,500 for fp32, the same with eight
 // warps, with sixteen and with the loops unrolled). Tiles of the next chunk stream in by
 // cp.async meanwhile where two fit in shared memory. 16384 tokens, 4 heads, K = V = 64, fp16: 66 us
-// with the state pass; 3 x 333 tokens, 6 value heads over 2, K = 48, V = 80, fp32: 30 us.
+// with the state pass; 3 x 333 tokens, 6 value heads over 2, K = 48, V = 80, fp32: 31 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -84,17 +84,26 @@ struct Frag {
   }
 };
 // N products with the same A, the small terms first; neighbouring instructions have accumulators
-// of their own.
-template <bool EA, bool EB, int N>
+// of their own. The instruction cuts its sum off instead of rounding it, which over K = 128 made
+// fp32 outputs 1.1e-6 off (2-norm); with STEP each step's sum starts from zero and is added to the
+// rest by the fp32 units, rounded: 1.7e-7, for 3 % of the time.
+template <bool STEP, bool EA, bool EB, int N>
 __device__ __forceinline__ void mma_parts(float (*d)[4], const Frag<4, EA>& a, const Frag<2, EB> (&b)[N]) {
+  float z[N][4] = {};
+  float(*t)[4] = STEP ? z : d;
   if (!EA)
 #pragma unroll
-    for (int j = 0; j < N; ++j) mma(d[j], a.lo, b[j].hi);
+    for (int j = 0; j < N; ++j) mma(t[j], a.lo, b[j].hi);
   if (!EB)
 #pragma unroll
-    for (int j = 0; j < N; ++j) mma(d[j], a.hi, b[j].lo);
+    for (int j = 0; j < N; ++j) mma(t[j], a.hi, b[j].lo);
 #pragma unroll
-  for (int j = 0; j < N; ++j) mma(d[j], a.hi, b[j].hi);
+  for (int j = 0; j < N; ++j) mma(t[j], a.hi, b[j].hi);
+  if (STEP)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[j][e] += t[j][e];
 }
 
 template <typename T, int KD>
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
               fb[j].set(0, to_f(kb[0]));
               fb[j].set(1, to_f(kb[4]));
             }
-            mma_parts(d, fa, fb);
+            mma_parts<!EX>(d, fa, fb);
           }
         }
       }
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
             fb[j].set(1, sb[4 * LV]);
           }
         }
-        mma_parts(o, fa, fb);
+        mma_parts<!EX>(o, fa, fb);
       }
       const float e0 = g[192 + r0 + gr], e1 = g[192 + r0 + gr + 8];
 #pragma unroll
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
           fb[j].set(0, to_f(vb[0]));
           fb[j].set(1, to_f(vb[4 * LV]));
         }
-        mma_parts(o, fa, fb);
+        mma_parts<!EX>(o, fa, fb);
       }
       T* og = static_cast<T*>(p.o) + (((int64_t)x.b * p.T + base) * p.HV + x.hv) * V + x.v0;
 #pragma unroll
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
           fb[j].lo[0] = wb[WL];
           fb[j].lo[1] = wb[WL + 4 * LV];
         }
-        mma_parts(u, fa, fb);
+        mma_parts<!EX>(u, fa, fb);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)

@@ -124,10 +124,10 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
 
 // States at the segment starts: S_0 = the sequence's initial state, S_{j+1} = w_j S_j + U_j,
 // in place of the U's. A thread per VEC state elements. A read and a write of the scratch,
-// bound by the trips to memory of four segments' loads at a time: 8 us for 32 heads of four segments
-// (15 MB). Six CTAs per SM with four loads each beat two with eight by 1 us.
+// bound by the trips to memory of eight segments' loads at a time: 9 us for 32 heads of four
+// segments (15 MB). With four at a time a sequence of 37 segments takes 2 us longer.
 template <int VEC>
-__global__ void __launch_bounds__(256, 6) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
+__global__ void __launch_bounds__(256, 4) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
   pdl_wait();
   if (no_split(a)) return;
   const LinearProblem& p = a.p;
@@ -164,18 +164,18 @@ __global__ void __launch_bounds__(256, 6) linear_combine_kernel(const __grid_con
     float* seg = a.segS + ((int64_t)first * p.HV + hv) * sz + e;
     const int64_t step = (int64_t)p.HV * sz;
     const float2* w = a.segW + (int64_t)first * p.HV + hv;
-    for (int j0 = 0; j0 < cnt; j0 += 4) {  // four segments' loads in flight
-      const int m = min(4, cnt - 1 - j0);
-      alignas(16) float u[4][VEC];
-      float2 f[4];
+    for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight segments' loads in flight
+      const int m = min(8, cnt - 1 - j0);
+      alignas(16) float u[8][VEC];
+      float2 f[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
         if (j < m) {
           load(u[j], seg + (j0 + j) * step);
           f[j] = __ldcg(w + (int64_t)(j0 + j) * p.HV);
         }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
         if (j0 + j < cnt) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) seg[(j0 + j) * step + i] = s[i];
@@ -238,7 +238,7 @@ cudaError_t launch_combine(const ChunkArgs& a, const int2* seqs) {
   const int64_t sz = (int64_t)a.p.K * a.p.V;
   const bool vec = sz % 4 == 0;
   // what is resident: a packed batch's CTAs may all have nothing to do
-  const int64_t gx = cdiv(sz, vec ? 1024 : 256), gy = std::max<int64_t>(1, 6 * sm_count() / gx);
+  const int64_t gx = cdiv(sz, vec ? 1024 : 256), gy = std::max<int64_t>(1, 4 * sm_count() / gx);
   const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((int64_t)a.p.N_seq * a.p.HV, gy));
   return vec ? launch_pdl(linear_combine_kernel<4>, grid, dim3(256), 0, a.p.stream, a, seqs)
              : launch_pdl(linear_combine_kernel<1>, grid, dim3(256), 0, a.p.stream, a, seqs);
