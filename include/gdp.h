@@ -498,6 +498,20 @@ gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, const void*
                           gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
                           cudaStream_t stream);
 
+/*
+ * gdp_group_norm_ws - the same with a workspace (256-byte aligned), in which the
+ * sums of few groups of many elements meet, so that more CTAs than a cluster has
+ * work on each. gdp_group_norm_workspace_size gives its bytes: 0 where it is not
+ * used (workspace may be NULL then).
+ * Errors: those of gdp_group_norm, GDP_ERR_WORKSPACE.
+ */
+size_t gdp_group_norm_workspace_size(int64_t N, int64_t L, int C, int G, gdp_dtype dt);
+gdp_status gdp_group_norm_ws(const void* x, int64_t x_sn, int64_t x_sl, const void* gate,
+                             int64_t gate_sn, int64_t gate_sl, const float* weight,
+                             const float* bias, int64_t N, int64_t L, int C, int G, float eps,
+                             gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Number of stage-boundary events gdp_set_stage_events takes. */
 #define GDP_STAGE_EVENTS 5
 

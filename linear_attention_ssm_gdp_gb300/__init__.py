@@ -11,6 +11,7 @@ built (``__graft_entry__.build()``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -25,7 +26,7 @@ __all__ = [
     "gdp_decode_conv_prepare",
     "gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged", "gdp_linear_chunk_fwd_workspace_size",
     "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged", "gdp_block_plan",
-    "gdp_group_norm",
+    "gdp_group_norm", "gdp_group_norm_workspace_size",
     "LIB_PATH",
 ]
 
@@ -85,9 +86,12 @@ def load() -> ctypes.CDLL:
             lib.gdp_block_plan.argtypes = [P, P, I, P, I, P, I, P, I, I] + [P] * 7
             lib.gdp_group_norm.argtypes = ([P, I64, I64, P, I64, I64, P, P, I64, I64, I, I, F, I,
                                             I, I, P, P])
+            lib.gdp_group_norm_ws.argtypes = lib.gdp_group_norm.argtypes[:-1] + [P, SZ, P]
+            lib.gdp_group_norm_workspace_size.argtypes = [I64, I64, I, I, I]
+            lib.gdp_group_norm_workspace_size.restype = SZ
             for f in ("gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged",
                       "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged",
-                      "gdp_block_plan", "gdp_group_norm"):
+                      "gdp_block_plan", "gdp_group_norm", "gdp_group_norm_ws"):
                 getattr(lib, f).restype = I
             lib.gdp_read_status.argtypes = [P, P]
             lib.gdp_debug_wait_fault.argtypes = [I, ctypes.c_double]
@@ -710,14 +714,20 @@ def gdp_block_plan(context_lens, query_lens, block_tables, free_pages, free_used
 _ACTIVATION = {"none": 0, "silu": 1}
 
 
+@functools.lru_cache(maxsize=256)
+def gdp_group_norm_workspace_size(N, L, C, num_groups, dtype) -> int:
+    return int(load().gdp_group_norm_workspace_size(N, L, C, num_groups, _DTYPE[dtype]))
+
+
 def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: float = 1e-5,
-                   activation: str = "silu", out_dtype=None, out=None):
+                   activation: str = "silu", out_dtype=None, out=None, workspace=None):
     """Group norm with an activation, channels last: x [N, L, C] (or [N, C]: one
     position per sample, such as a token's heads), statistics over the positions and
     the C / num_groups channels of a group, z = (x - mean) / sqrt(var + eps) * weight
     + bias; returns act(z), or z * act(gate) with a gate. weight, bias [C] fp32;
     out_dtype is x's dtype, or bf16/fp16 for an fp32 x; the gate has it too. Rows of
-    x and gate may be strided (contiguous channels)."""
+    x and gate may be strided (contiguous channels). ``workspace``: uint8 of
+    gdp_group_norm_workspace_size bytes (allocated where it is needed and None)."""
     _need_cuda(x, weight, bias, gate)
     if x.dim() not in (2, 3) or x.stride(-1) != 1:
         raise ValueError("x must be [N, L, C] or [N, C] with contiguous channels")
@@ -742,9 +752,19 @@ def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: f
         out = torch.empty(shape, dtype=dt_out, device=x.device)
     else:
         _out_ok(out, shape, dt_out)
-    st = load().gdp_group_norm(x.data_ptr(), x_sn, x_sl, _a(gate), g_sn, g_sl, _a(weight),
-                               _a(bias), N, L, C, num_groups, eps, _ACTIVATION[activation],
-                               _DTYPE[x.dtype], _DTYPE[dt_out], out.data_ptr(), _raw_stream(x))
+    args = (x.data_ptr(), x_sn, x_sl, _a(gate), g_sn, g_sl, _a(weight), _a(bias), N, L, C,
+            num_groups, eps, _ACTIVATION[activation], _DTYPE[x.dtype], _DTYPE[dt_out],
+            out.data_ptr())
+    if L > 1 and workspace is None:
+        need = gdp_group_norm_workspace_size(N, L, C, num_groups, x.dtype)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is None:
+        st = load().gdp_group_norm(*args, _raw_stream(x))
+    else:
+        _need_cuda(workspace)
+        st = load().gdp_group_norm_ws(*args, workspace.data_ptr(), workspace.numel(),
+                                      _raw_stream(x))
     if st:
         _check("gdp_group_norm", st)
     return out

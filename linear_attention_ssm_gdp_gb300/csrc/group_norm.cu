@@ -57,6 +57,8 @@ struct NormArgs {
   int GS, sets;   // groups per CTA, CTAs along the groups
   int rows;       // positions per CTA
   int resident;   // the CTA's elements stay in shared memory
+  int slices;     // runs of positions per set of groups, where they meet through memory
+  float2* part;   // [sample, set][slice][GS]: mean and squared distances of a slice
 };
 
 template <bool GATE>
@@ -163,7 +165,12 @@ constexpr int kMapThreads = 256;
 constexpr int kMaxGS = 128;
 constexpr int kMapSmem = 200 * 1024;  // most that a CTA keeps
 
-template <typename TX, typename TO, int VEC, bool GATE>
+//
+// PART: a slice's own mean and squared distances from it go to memory, and a second launch (APPLY)
+// merges the slices' in order (Chan's formula) and normalises: as many CTAs per group as it takes.
+enum { WHOLE, PART, APPLY };
+
+template <typename TX, typename TO, int VEC, bool GATE, int STAGE>
 __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_constant__ NormArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t raw[];
@@ -173,8 +180,9 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   __shared__ float total[kMaxGS];                  // the cluster's group sums
   __shared__ float gsum[2][kMaxGS];                // this CTA's: elements, squared distances
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks();
-  const int64_t unit = blockIdx.x / CL;
+  const int CL = (int)cl.num_blocks(), runs = STAGE == WHOLE ? CL : a.slices;
+  const int rank = STAGE == WHOLE ? (int)cl.block_rank() : (int)(blockIdx.x % runs);
+  const int64_t unit = blockIdx.x / runs;
   const int64_t n = unit / a.sets;
   const int set = (int)(unit - n * a.sets);
   const int g0 = set * a.GS, gs = min(a.GS, a.G - g0);
@@ -188,9 +196,9 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   PX* keep = reinterpret_cast<PX*>(raw);
   bool kept = false;  // the elements are in shared memory
   const TX* xb = static_cast<const TX*>(a.x) + n * a.x_sn + l0 * a.x_sl + c0;
-  const float inv = 1.f / ((float)a.L * (float)a.Cg);
+  const float inv = 1.f / ((float)(STAGE == PART ? max(nrow, 1) : a.L) * (float)a.Cg);
 
-  float mean_of[VEC];  // per channel of the thread's column (one group: all the same)
+  float rstd[VEC], mean_of[VEC];  // per channel of the thread's column (one group: all the same)
   float acc[VEC];
   auto reduce = [&](int which) {
     // this CTA's sums by group, in a fixed order, then the cluster's
@@ -255,36 +263,69 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
     }
   };
 
+  if constexpr (STAGE != APPLY) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  if (on)
-    for (int c = tx; c < cols; c += tc)
-      walk(c, [&](int r, const PX& x) {
-        if (a.resident) keep[r * cols + c] = x;
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    if (on)
+      for (int c = tx; c < cols; c += tc)
+        walk(c, [&](int r, const PX& x) {
+          if (a.resident) keep[r * cols + c] = x;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
-      });
-  kept = a.resident;
-  reduce(0);
+          for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
+        });
+    kept = a.resident;
+    reduce(0);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    mean_of[e] = total[group_of(tx, e)] * inv;
-    acc[e] = 0.f;
+    for (int e = 0; e < VEC; ++e) {
+      mean_of[e] = total[group_of(tx, e)] * inv;
+      acc[e] = 0.f;
+    }
+    __syncthreads();
+    if (on)
+      for (int c = tx; c < cols; c += tc)
+        walk(c, [&](int, const PX& x) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float d = to_f(x.e[e]) - mean_of[e];
+            acc[e] = fmaf(d, d, acc[e]);
+          }
+        });
+    reduce(1);
+    if constexpr (STAGE == PART) {
+      for (int g = threadIdx.x; g < gs; g += kMapThreads)
+        a.part[(unit * runs + rank) * a.GS + g] = make_float2(gsum[0][g] * inv, gsum[1][g]);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(total[group_of(tx, e)] * inv + a.eps);
+  } else {
+    for (int g = threadIdx.x >> 5; g < gs; g += kMapThreads / 32) {  // a warp per group, lanes over the slices
+      const float2* q = a.part + unit * runs * a.GS + g;
+      const int lane = threadIdx.x & 31;
+      auto count = [&](int i) { return (float)max((int64_t)0, min(a.L - (int64_t)i * a.rows, (int64_t)a.rows)) * (float)a.Cg; };
+      float t = 0.f, m2 = 0.f;
+      for (int i = lane; i < runs; i += 32) t = fmaf(count(i), __ldcg(q + (int64_t)i * a.GS).x, t);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      const float mean = t * inv;
+      for (int i = lane; i < runs; i += 32) {
+        const float2 x = __ldcg(q + (int64_t)i * a.GS);
+        m2 += fmaf(count(i) * (x.x - mean), x.x - mean, x.y);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+      if (lane == 0) {
+        gsum[0][g] = mean;
+        total[g] = rsqrtf(m2 * inv + a.eps);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      mean_of[e] = gsum[0][group_of(tx, e)];
+      rstd[e] = total[group_of(tx, e)];
+    }
   }
-  __syncthreads();
-  if (on)
-    for (int c = tx; c < cols; c += tc)
-      walk(c, [&](int, const PX& x) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = to_f(x.e[e]) - mean_of[e];
-          acc[e] = fmaf(d, d, acc[e]);
-        }
-      });
-  reduce(1);
-  float rstd[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(total[group_of(tx, e)] * inv + a.eps);
   const TO* gb = static_cast<const TO*>(a.gate);
   if (GATE) gb += n * a.g_sn + l0 * a.g_sl + c0;
   TO* yb = static_cast<TO*>(a.y) + (n * a.L + l0) * a.C + c0;
@@ -306,7 +347,7 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
         *reinterpret_cast<PO*>(yb + (int64_t)r * a.C + c * VEC) = out;
       });
     }
-  cl.sync();  // no CTA leaves while another may still read its sums
+  if (STAGE == WHOLE) cl.sync();  // no CTA leaves while another may still read its sums
 }
 
 template <typename TX, typename TO, int TG, int NV, int U>
@@ -317,14 +358,14 @@ cudaError_t go_rows(const NormArgs& a, cudaStream_t s) {
                 : launch_pdl(norm_rows_kernel<TX, TO, TG, NV, U, false>, dim3((unsigned)grid), dim3(256), 0, s, a, Nu);
 }
 
-template <typename TX, typename TO, int VEC, bool GATE>
+template <typename TX, typename TO, int VEC, bool GATE, int STAGE>
 cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
-  auto kern = norm_map_kernel<TX, TO, VEC, GATE>;
+  auto kern = norm_map_kernel<TX, TO, VEC, GATE, STAGE>;
   if (smem > 24 * 1024) {  // beside up to 20 KB of static shared memory
-    const cudaError_t e = allow_smem<norm_map_kernel<TX, TO, VEC, GATE>>(kMapSmem);
+    const cudaError_t e = allow_smem<norm_map_kernel<TX, TO, VEC, GATE, STAGE>>(kMapSmem);
     if (e != cudaSuccess) return e;
   }
-  const int64_t grid = a.N * a.sets * CL;
+  const int64_t grid = a.N * a.sets * (STAGE == WHOLE ? CL : a.slices);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -342,31 +383,68 @@ cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename TX, typename TO, int VEC>
-cudaError_t go_map(NormArgs a, cudaStream_t s) {
-  // A set's row segment is whole vectors and at least 128 bytes; half and a quarter of that where
-  // even clusters of 8 would leave SMs idle or a CTA with more than 48 KB (4 x 4096 x 320 in 32
-  // groups, fp16: 13.1 us, against 18.2 with 128 bytes; 1 x 16384 x 128, 32 groups: 15.3 / 48.6),
-  // but not beyond (16 x 256 x 1280, 32 groups: 16.2 us with 64 bytes, 12.4 with 128).
-  for (const int64_t least : {128, 64, 32}) {
-    a.GS = 1;
-    while (a.GS < a.G && a.GS < kMaxGS && ((int64_t)a.GS * a.Cg * sizeof(TX) < least || (a.GS * a.Cg) % VEC != 0)) ++a.GS;
+// How a norm over positions is laid out: GS groups per set, and either clusters of CL CTAs (slices =
+// 0) or slices that meet through memory.
+struct MapPlan {
+  int GS, sets, CL, slices, rows;
+  int64_t seg, part_bytes;
+};
+MapPlan plan_map(int64_t N, int64_t L, int G, int Cg, int size, int vec, bool split) {
+  MapPlan m{};
+  auto sets_of = [&](int64_t least) {  // row segments of whole vectors and at least so many bytes
+    m.GS = 1;
+    while (m.GS < G && m.GS < kMaxGS && ((int64_t)m.GS * Cg * size < least || (m.GS * Cg) % vec != 0)) ++m.GS;
     // a thread's channels must keep their groups, so a set of several groups is one pass of columns
-    a.sets = (int)cdiv(a.G, a.GS);
-    if (a.N * a.sets * 8 >= sm_count() && cdiv(a.L, 8) * a.GS * a.Cg * (int64_t)sizeof(TX) <= 48 * 1024) break;
+    m.sets = (int)cdiv(G, m.GS);
+    m.seg = (int64_t)m.GS * Cg * size;
+  };
+  // Row segments of 128 bytes; half and a quarter of that where even clusters of 8 would leave SMs
+  // idle or a CTA with more than 48 KB (4 x 4096 x 320 in 32 groups, fp16: 13.1 us, against 18.2
+  // with 128 bytes), but not beyond (16 x 256 x 1280, 32 groups: 16.2 us with 64 bytes, 12.4 with 128).
+  for (const int64_t least : {128, 64, 32}) {
+    sets_of(least);
+    if (N * m.sets * 8 >= sm_count() && cdiv(L, 8) * m.seg <= 48 * 1024) break;
   }
-  const int64_t units = a.N * a.sets;
-  const int64_t seg = (int64_t)a.GS * a.Cg * sizeof(TX);
+  // Slices where that still leaves a CTA with much: the same work on more SMs, for a second read of
+  // x and a launch. 1 x 16384 x 128 fp16 in one group: 15.9 us, where a cluster has eight SMs for it;
+  // 2 x 9000 x 512 fp32 in four: 20.7 / 42.9. Sets of several small groups cost more to reduce, so
+  // they stay with clusters longer (1 x 16384 x 128, 32 groups: 43 us in slices, 15.3 in clusters).
+  const int64_t much = N * m.sets * 8 >= sm_count() ? 96 : m.GS > 1 ? 64 : 32;
+  if (split && cdiv(L, 8) * m.seg > much * 1024) {
+    sets_of(128);
+    const int64_t units = N * m.sets, most = std::max<int64_t>(1, L * m.seg / 8192);
+    const int64_t want = std::max(cdiv(4 * sm_count(), units), cdiv(L * m.seg, 64 * 1024));
+    m.rows = (int)cdiv(L, std::min<int64_t>(1024, std::min(want, most)));
+    m.slices = (int)cdiv(L, m.rows);
+    m.CL = 1;
+    m.part_bytes = units * m.slices * m.GS * (int64_t)sizeof(float2);
+    return m;
+  }
   // CTAs per cluster: until every SM has one, or 8 KB of work are left each (clusters of 16 found
   // few places: 4 x 4096 x 320 took 34 us)
-  int CL = 1;
-  while (CL < 8 && units * CL < sm_count() && a.L * seg > (int64_t)CL * 8192) CL *= 2;
-  while (CL < 8 && cdiv(a.L, CL) * seg > 96 * 1024) CL *= 2;
-  a.rows = (int)cdiv(a.L, CL);
-  const int64_t bytes = (int64_t)a.rows * seg;
+  m.CL = 1;
+  while (m.CL < 8 && N * m.sets * m.CL < sm_count() && L * m.seg > (int64_t)m.CL * 8192) m.CL *= 2;
+  while (m.CL < 8 && cdiv(L, m.CL) * m.seg > 96 * 1024) m.CL *= 2;
+  m.rows = (int)cdiv(L, m.CL);
+  return m;
+}
+
+template <typename TX, typename TO, int VEC>
+cudaError_t go_map(NormArgs a, cudaStream_t s) {
+  const MapPlan m = plan_map(a.N, a.L, a.G, a.Cg, sizeof(TX), VEC, a.part != nullptr);
+  a.GS = m.GS;
+  a.sets = m.sets;
+  a.rows = m.rows;
+  a.slices = m.slices;
+  const int64_t bytes = (int64_t)m.rows * m.seg;
   a.resident = bytes <= kMapSmem;
   const size_t smem = a.resident ? (size_t)bytes : 0;
-  return a.gate ? go_map2<TX, TO, VEC, true>(a, CL, smem, s) : go_map2<TX, TO, VEC, false>(a, CL, smem, s);
+  if (m.slices > 0) {
+    const cudaError_t e = go_map2<TX, TO, VEC, false, PART>(a, 1, smem, s);
+    if (e != cudaSuccess) return e;
+    return a.gate ? go_map2<TX, TO, VEC, true, APPLY>(a, 1, 0, s) : go_map2<TX, TO, VEC, false, APPLY>(a, 1, 0, s);
+  }
+  return a.gate ? go_map2<TX, TO, VEC, true, WHOLE>(a, m.CL, smem, s) : go_map2<TX, TO, VEC, false, WHOLE>(a, m.CL, smem, s);
 }
 
 bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -400,11 +478,11 @@ cudaError_t run(NormArgs a, cudaStream_t s) {
 
 using namespace gdp;
 
-extern "C" gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate,
-                                     int64_t gate_sn, int64_t gate_sl, const float* weight,
-                                     const float* bias, int64_t N, int64_t L, int C, int G,
-                                     float eps, gdp_activation activation, gdp_dtype dt,
-                                     gdp_dtype dt_out, void* y, cudaStream_t stream) {
+namespace {
+
+gdp_status norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate, int64_t gate_sn, int64_t gate_sl,
+                const float* weight, const float* bias, int64_t N, int64_t L, int C, int G, float eps,
+                gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y, float2* part, cudaStream_t stream) {
   if (N < 0 || L < 0 || C <= 0 || G <= 0 || C % G != 0 || !(eps >= 0.f)) return GDP_ERR_INVALID_ARG;
   if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU) return GDP_ERR_UNSUPPORTED;
   if (N == 0 || L == 0) return GDP_OK;
@@ -416,7 +494,7 @@ extern "C" gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, 
   if (L == 1) x_sl = gate_sl = 0;  // the stride of a single position or sample means nothing
   if (N == 1) x_sn = gate_sn = 0;
   NormArgs a{x, gate, x_sn, x_sl, gate_sn, gate_sl, weight, bias, y, N, L, C, G, C / G, eps,
-             activation == GDP_ACT_SILU, 0, 0, 0, 0};
+             activation == GDP_ACT_SILU, 0, 0, 0, 0, 0, part};
   cudaError_t e;
   if (dt == GDP_BF16 && dt_out == GDP_BF16) e = run<__nv_bfloat16, __nv_bfloat16>(a, stream);
   else if (dt == GDP_F16 && dt_out == GDP_F16) e = run<__half, __half>(a, stream);
@@ -426,3 +504,36 @@ extern "C" gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, 
   else return GDP_ERR_UNSUPPORTED;
   return e == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
 }
+
+}  // namespace
+
+extern "C" {
+
+size_t gdp_group_norm_workspace_size(int64_t N, int64_t L, int C, int G, gdp_dtype dt) {
+  if (N <= 0 || L <= 1 || L > INT32_MAX || C <= 0 || G <= 0 || C % G != 0) return 0;
+  const int size = dt == GDP_F32 ? 4 : 2;
+  // the strides, which this does not know, decide between vectors and single elements
+  return std::max(plan_map(N, L, G, C / G, size, 16 / size, true).part_bytes,
+                  plan_map(N, L, G, C / G, size, 1, true).part_bytes);
+}
+
+gdp_status gdp_group_norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate, int64_t gate_sn,
+                          int64_t gate_sl, const float* weight, const float* bias, int64_t N, int64_t L, int C,
+                          int G, float eps, gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
+                          cudaStream_t stream) {
+  return norm(x, x_sn, x_sl, gate, gate_sn, gate_sl, weight, bias, N, L, C, G, eps, activation, dt, dt_out, y, nullptr,
+              stream);
+}
+
+gdp_status gdp_group_norm_ws(const void* x, int64_t x_sn, int64_t x_sl, const void* gate, int64_t gate_sn,
+                             int64_t gate_sl, const float* weight, const float* bias, int64_t N, int64_t L, int C,
+                             int G, float eps, gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const size_t need = gdp_group_norm_workspace_size(N, L, C, G, dt);
+  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < need))
+    return GDP_ERR_WORKSPACE;
+  return norm(x, x_sn, x_sl, gate, gate_sn, gate_sl, weight, bias, N, L, C, G, eps, activation, dt, dt_out, y,
+              need > 0 ? static_cast<float2*>(workspace) : nullptr, stream);
+}
+
+}  // extern "C"
