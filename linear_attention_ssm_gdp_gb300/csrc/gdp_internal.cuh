@@ -10,12 +10,9 @@
 #include <utility>
 
 #include "gdp.h"
+#include "sizes.h"
 
 namespace gdp {
-
-constexpr size_t kAlign = 256;
-__host__ __device__ inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
-__host__ __device__ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Device status word codes (first int32 of a chunk_fwd workspace).
 enum DeviceStatus : int { kDevOk = 0, kDevBadSeqlens = 1, kDevTimeout = 2 };

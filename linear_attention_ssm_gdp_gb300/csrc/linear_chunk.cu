@@ -799,8 +799,8 @@ bool linear_tc_shape(int K, int V, gdp_dtype dt) { return dt == GDP_BF16 && K <=
 
 size_t linear_tc_workspace(int N_seq, int B, int T, int HV, int K, int V) {
   // the query does not say whether the batch is packed
-  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, kVT, kCost).total : 0;
-  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, kVT, kCost).total : 0);
+  const size_t d = N_seq == B ? plan_of(N_seq, B, T, HV, K, V, false, kVT, kCost, sm_count()).total : 0;
+  return std::max(d, B == 1 ? plan_of(N_seq, B, T, HV, K, V, true, kVT, kCost, sm_count()).total : 0);
 }
 
 bool linear_tc_ok(const LinearProblem& p) {
@@ -809,7 +809,7 @@ bool linear_tc_ok(const LinearProblem& p) {
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
-  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, kCost);
+  const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, kCost, sm_count());
   TcArgs a{};
   a.p = p;
   a.nseg = x.nseg;

@@ -3,19 +3,12 @@
 #pragma once
 
 #include "linear_internal.cuh"
+#include "linear_plan.h"
 
 namespace gdp {
 namespace linear {
 
-constexpr int C = 64;           // tokens per chunk
 constexpr float kGMin = -1e5f;  // e^g is 0 far above this; keeps -inf out of the prefix sums
-
-// A segment of a sequence: t0 = first row, n = rows, pos0 = tokens of the sequence before it
-// (paged states: its context included), id = its place among the segments.
-struct SegRec {
-  int t0, n, seq, pos0;
-  int first, last, id, pad;
-};
 
 struct ChunkArgs {
   LinearProblem p;
@@ -27,19 +20,6 @@ struct ChunkArgs {
   float* segS;          // [segments][HV][K][V]: U of a segment, then the state at its start
   float2* segW;         // [segments][HV]: its whole decay factor
 };
-
-// Segments of a launch and the workspace they need.
-struct Plan {
-  int nseg, Lseg, bound, slices;  // segments per dense sequence, tokens, segments in all at most
-  size_t recs, seqs, segS, segW, total;
-};
-// What a kernel's items take, in microseconds: a chunk, a chunk of the state pass, an item's start
-// and states, the two extra launches of a split.
-struct Cost {
-  double chunk, state_chunk, item, split;
-};
-// vt: value columns per item.
-Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, const Cost& cost);
 
 // The two kernels around the state pass: segment records of a packed batch, and the states at
 // the segment starts.

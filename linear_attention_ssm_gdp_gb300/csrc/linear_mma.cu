@@ -436,7 +436,7 @@ Cost cost_of(int K, gdp_dtype dt) {
 }
 int slice_of(int K) { return K <= 128 ? 64 : 32; }
 Plan plan(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt, bool packed) {
-  return plan_of(N_seq, B, T, HV, K, V, packed, slice_of(K), cost_of(K, dt));
+  return plan_of(N_seq, B, T, HV, K, V, packed, slice_of(K), cost_of(K, dt), sm_count());
 }
 
 }  // namespace

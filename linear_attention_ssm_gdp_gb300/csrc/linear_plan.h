@@ -1,0 +1,80 @@
+// Linear attention, chunked forms: how the host plans segments of sequences and how the device
+// counts them. Plain C++, so that both sides' arithmetic can be checked without a GPU.
+#pragma once
+
+#include <algorithm>
+
+#include "sizes.h"
+
+namespace gdp {
+namespace linear {
+
+constexpr int C = 64;  // tokens per chunk
+
+// A segment of a sequence: t0 = first row, n = rows, pos0 = tokens of the sequence before it
+// (paged states: its context included), id = its place among the segments.
+struct SegRec {
+  int t0, n, seq, pos0;
+  int first, last, id, pad;
+};
+
+// Segments of a launch and the workspace they need.
+struct Plan {
+  int nseg, Lseg, bound, slices;  // segments per dense sequence, tokens, segments in all at most
+  size_t recs, seqs, segS, segW, total;
+};
+// What a kernel's items take, in microseconds: a chunk, a chunk of the state pass, an item's start
+// and states, the two extra launches of a split.
+struct Cost {
+  double chunk, state_chunk, item, split;
+};
+
+// Segments of a sequence of n tokens whose first one is `off` positions into its chunk, cut at
+// multiples of Lseg positions from that chunk's start.
+GDP_HD inline int segment_count(int off, int n, int Lseg) {
+  return n > 0 ? (int)(((int64_t)off + n + Lseg - 1) / Lseg) : 1;
+}
+
+// vt: value columns per item; G: multiprocessors.
+inline Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, const Cost& cost, int G) {
+  Plan x{};
+  x.slices = (int)cdiv(V, vt);
+  const int chunks = (int)cdiv(T, C);
+  const int64_t heads = (int64_t)HV * x.slices;
+  x.nseg = 1;
+  x.Lseg = std::max(1, chunks) * C;
+  if (!packed) {
+    // rounds of items over the SMs, of both passes
+    const int64_t units = heads * B;
+    double best = (double)cdiv(units, G) * (chunks * cost.chunk + cost.item);
+    for (int n = 2; n <= chunks && n <= 256; ++n) {
+      const int64_t per = cdiv(chunks, n);
+      if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
+      const double t = (double)cdiv(units * n, G) * (per * cost.chunk + cost.item) +
+                       (double)cdiv(units * (n - 1), G) * (per * cost.state_chunk + cost.item) + cost.split;
+      if (t < 0.95 * best) {
+        best = t;
+        x.nseg = n;
+        x.Lseg = (int)per * C;
+      }
+    }
+    x.bound = B * x.nseg;
+  } else {
+    // packed: no more than an SM's share of the whole batch in one item; where a sequence of T tokens
+    // fits in one, so it does from any position of a chunk (there is no scratch for a cut then)
+    const int64_t share = cdiv(cdiv((int64_t)T * heads, G), C) * C, most = std::max<int64_t>(share, 512);
+    x.Lseg = most < T ? (int)most : x.Lseg + C;
+    x.bound = (int)(((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq);
+  }
+  const bool split = packed ? x.Lseg < T : x.nseg > 1;
+  x.recs = kAlign;
+  x.seqs = align_up(x.recs + (packed ? (size_t)x.bound * sizeof(SegRec) : 0));
+  x.segW = align_up(x.seqs + (packed ? (size_t)N_seq * 2 * sizeof(int32_t) : 0));
+  x.segS = align_up(x.segW + (split ? (size_t)x.bound * HV * 2 * sizeof(float) : 0));
+  x.total = align_up(x.segS + (split ? (size_t)x.bound * HV * K * V * 4 : 0));
+  if (!split) x.segS = 0;
+  return x;
+}
+
+}  // namespace linear
+}  // namespace gdp

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
         if (off) n = pos = 0;
         any |= off;
       }
-      cnt = n > 0 ? (int)(((int64_t)pos % C + n + Lseg - 1) / Lseg) : 1;
+      cnt = segment_count(pos % C, n, Lseg);
     }
     cut |= cnt > 1;
     int s = cnt;
@@ -188,46 +188,6 @@ __global__ void __launch_bounds__(256, 4) linear_combine_kernel(const __grid_con
 }
 
 }  // namespace
-
-Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, int vt, const Cost& cost) {
-  Plan x{};
-  const int G = sm_count();
-  x.slices = (int)cdiv(V, vt);
-  const int chunks = (int)cdiv(T, C);
-  const int64_t heads = (int64_t)HV * x.slices;
-  x.nseg = 1;
-  x.Lseg = std::max(1, chunks) * C;
-  if (!packed) {
-    // rounds of items over the SMs, of both passes
-    const int64_t units = heads * B;
-    double best = (double)cdiv(units, G) * (chunks * cost.chunk + cost.item);
-    for (int n = 2; n <= chunks && n <= 256; ++n) {
-      const int64_t per = cdiv(chunks, n);
-      if (cdiv(chunks, per) != n) continue;  // fewer segments of this length do
-      const double t = (double)cdiv(units * n, G) * (per * cost.chunk + cost.item) +
-                       (double)cdiv(units * (n - 1), G) * (per * cost.state_chunk + cost.item) + cost.split;
-      if (t < 0.95 * best) {
-        best = t;
-        x.nseg = n;
-        x.Lseg = (int)per * C;
-      }
-    }
-    x.bound = B * x.nseg;
-  } else {
-    // packed: no more than an SM's share of the whole batch in one item
-    const int64_t share = cdiv(cdiv((int64_t)T * heads, G), C) * C;
-    x.Lseg = (int)std::min<int64_t>(x.Lseg + C, std::max<int64_t>(share, 512));
-    x.bound = (int)(((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq);
-  }
-  const bool split = packed ? x.Lseg < T : x.nseg > 1;
-  x.recs = kAlign;
-  x.seqs = align_up(x.recs + (packed ? (size_t)x.bound * sizeof(SegRec) : 0));
-  x.segW = align_up(x.seqs + (packed ? (size_t)N_seq * sizeof(int2) : 0));
-  x.segS = align_up(x.segW + (split ? (size_t)x.bound * HV * sizeof(float2) : 0));
-  x.total = align_up(x.segS + (split ? (size_t)x.bound * HV * K * V * 4 : 0));
-  if (!split) x.segS = 0;
-  return x;
-}
 
 cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs, int* split) {
   return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs,

@@ -1,0 +1,72 @@
+"""Segments of the chunked linear-attention forms, both sides' arithmetic without a GPU: whatever
+the device may cut has its place in the scratch that the host planned."""
+import ctypes
+import os
+import random
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CHUNK = 64
+SOURCE = r"""
+#include "linear_plan.h"
+using namespace gdp::linear;
+extern "C" {
+void plan(int N, int B, int T, int HV, int K, int V, int packed, int vt, int G, long long* out) {
+  const Plan x = plan_of(N, B, T, HV, K, V, packed, vt, Cost{1.85, 1.2, 3.0, 6.0}, G);
+  out[0] = x.nseg, out[1] = x.Lseg, out[2] = x.bound, out[3] = x.segS, out[4] = x.total;
+}
+int segments(int off, int n, int Lseg) { return segment_count(off, n, Lseg); }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(SOURCE)
+    so = str(d / "plan.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "linear_attention_ssm_gdp_gb300", "csrc"), str(d / "plan.cpp"), "-o", so],
+                   check=True)
+    return ctypes.CDLL(so)
+
+
+def plan(lib, N, B, T, HV, K=128, V=128, packed=1, vt=128, G=152):
+    out = (ctypes.c_longlong * 5)()
+    lib.plan(N, B, T, HV, K, V, packed, vt, G, out)
+    return dict(zip(("nseg", "Lseg", "bound", "segS", "total"), out))
+
+
+@pytest.mark.parametrize("G", [148, 152])
+@pytest.mark.parametrize("V,vt", [(128, 128), (128, 64), (80, 32)])
+def test_no_cut_without_scratch(lib, G, V, vt):
+    """A sequence that starts inside a chunk (a paged one with a context) spans up to 63 positions
+    more than it has tokens; where the plan has no scratch, no offset may cut it."""
+    lengths = [1, 63, 64, 65, 448, 449, 450, 500, 511, 512, 513, 575, 576, 577, 640, 1000, 4095, 4096, 16384, 100000]
+    for HV in (1, 2, 16, 32, 74, 75, 76, 148, 150, 152, 160, 304):
+        for T in lengths + [random.Random(HV).randint(1, 20000) for _ in range(40)]:
+            x = plan(lib, 1, 1, T, HV, V=V, vt=vt, G=G)
+            cut = max(lib.segments(off, T, x["Lseg"]) for off in range(CHUNK))
+            assert cut == 1 or x["segS"], (T, HV, x, cut)
+
+
+def test_counts_stay_in_bounds(lib):
+    """Records of every sequence, however lengths and offsets fall."""
+    rng = random.Random(0)
+    for _ in range(3000):
+        N, HV = rng.randint(1, 40), rng.choice([1, 4, 32, 76, 152])
+        lens = [rng.choice([0, 1, rng.randint(1, 700), rng.randint(1, 5000)]) for _ in range(N)]
+        T = max(1, sum(lens))
+        x = plan(lib, N, 1, T, HV)
+        n = sum(lib.segments(rng.choice([0, 63, rng.randint(0, 63)]), n, x["Lseg"]) for n in lens)
+        assert n <= x["bound"]
+
+
+def test_dense_segments_cover_the_sequence(lib):
+    for T in list(range(1, 300)) + [4096, 8191, 16384, 100001]:
+        for B, HV in ((1, 1), (2, 16), (4, 32)):
+            x = plan(lib, B, B, T, HV, packed=0)
+            assert (x["nseg"] - 1) * x["Lseg"] < T <= x["nseg"] * x["Lseg"] and x["bound"] == B * x["nseg"]
+            assert (x["nseg"] > 1) == bool(x["segS"])
