@@ -17,8 +17,8 @@ struct ChunkArgs {
   int nseg, Lseg;       // dense batches: segments per sequence, tokens per segment
   int slices, vt;       // slices of vt value columns
   int items;            // bound over all CTAs
-  float* segS;          // [segments][HV][K][V]: U of a segment, then the state at its start
-  float2* segW;         // [segments][HV]: its whole decay factor
+  float* segS;          // [segments of cut sequences][HV][K][V]: a segment's U, then the state at its start
+  float2* segW;         // [the same][HV]: its whole decay factor
 };
 
 // The two kernels around the state pass: segment records of a packed batch, and the states at

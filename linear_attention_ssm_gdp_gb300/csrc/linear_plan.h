@@ -12,7 +12,7 @@ namespace linear {
 constexpr int C = 64;  // tokens per chunk
 
 // A segment of a sequence: t0 = first row, n = rows, pos0 = tokens of the sequence before it
-// (paged states: its context included), id = its place among the segments.
+// (paged states: its context included), id = its place in the scratch (cut sequences only).
 struct SegRec {
   int t0, n, seq, pos0;
   int first, last, id, pad;
@@ -21,6 +21,7 @@ struct SegRec {
 // Segments of a launch and the workspace they need.
 struct Plan {
   int nseg, Lseg, bound, slices;  // segments per dense sequence, tokens, segments in all at most
+  int slots;                      // segments of cut sequences at most: a state of scratch each
   size_t recs, seqs, segS, segW, total;
 };
 // What a kernel's items take, in microseconds: a chunk, a chunk of the state pass, an item's start
@@ -33,6 +34,13 @@ struct Cost {
 // multiples of Lseg positions from that chunk's start.
 GDP_HD inline int segment_count(int off, int n, int Lseg) {
   return n > 0 ? (int)(((int64_t)off + n + Lseg - 1) / Lseg) : 1;
+}
+
+// Segments at most of the sequences that are cut, of N_seq with T tokens in all. A sequence is cut
+// when it has more than Lseg positions, of which up to C - 1 may lie before its first token.
+inline int64_t cut_bound(int N_seq, int T, int Lseg) {
+  const int64_t cut = std::min<int64_t>(N_seq, T / (Lseg + 2 - C));
+  return (T + cut * (Lseg + C - 2)) / Lseg;  // segment_count summed
 }
 
 // vt: value columns per item; G: multiprocessors.
@@ -59,20 +67,21 @@ inline Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, 
       }
     }
     x.bound = B * x.nseg;
+    x.slots = x.nseg > 1 ? x.bound : 0;
   } else {
     // packed: no more than an SM's share of the whole batch in one item; where a sequence of T tokens
     // fits in one, so it does from any position of a chunk (there is no scratch for a cut then)
     const int64_t share = cdiv(cdiv((int64_t)T * heads, G), C) * C, most = std::max<int64_t>(share, 512);
     x.Lseg = most < T ? (int)most : x.Lseg + C;
     x.bound = (int)(((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq);
+    x.slots = x.Lseg < T ? (int)std::min<int64_t>(x.bound, cut_bound(N_seq, T, x.Lseg)) : 0;
   }
-  const bool split = packed ? x.Lseg < T : x.nseg > 1;
   x.recs = kAlign;
   x.seqs = align_up(x.recs + (packed ? (size_t)x.bound * sizeof(SegRec) : 0));
   x.segW = align_up(x.seqs + (packed ? (size_t)N_seq * 2 * sizeof(int32_t) : 0));
-  x.segS = align_up(x.segW + (split ? (size_t)x.bound * HV * 2 * sizeof(float) : 0));
-  x.total = align_up(x.segS + (split ? (size_t)x.bound * HV * K * V * 4 : 0));
-  if (!split) x.segS = 0;
+  x.segS = align_up(x.segW + (size_t)x.slots * HV * 2 * sizeof(float));
+  x.total = align_up(x.segS + (size_t)x.slots * HV * K * V * 4);
+  if (x.slots == 0) x.segS = 0;
   return x;
 }
 

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
                                                                       int* split) {
   pdl_wait();
   __shared__ int lens[kSortMax];
-  __shared__ int wsum[kRecThreads / 32 + 1];
+  __shared__ int2 wsum[kRecThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   for (int i = tid; i < p.N_seq; i += kRecThreads) {
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
   }
   bad = __syncthreads_or(bad);
   bool any = bad, cut = false;
-  int base = 0;  // segments before this round of sequences
+  int base = 0, sbase = 0;  // segments before this round of sequences, those of cut ones
   for (int i0 = 0; i0 < p.N_seq; i0 += kRecThreads) {
     const int i = i0 + tid;
     int t0 = 0, n = 0, pos = 0, cnt = 0;
@@ -61,32 +61,38 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
       cnt = segment_count(pos % C, n, Lseg);
     }
     cut |= cnt > 1;
-    int s = cnt;
+    const int slots = cnt > 1 ? cnt : 0;
+    int s = cnt, z = slots;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+      const int y = __shfl_up_sync(0xffffffffu, s, o), w = __shfl_up_sync(0xffffffffu, z, o);
+      if (lane >= o) {
+        s += y;
+        z += w;
+      }
     }
-    if (lane == 31) wsum[warp] = s;
+    if (lane == 31) wsum[warp] = make_int2(s, z);
     __syncthreads();
     if (tid == 0) {
-      int run = 0;
+      int2 run = make_int2(0, 0);
       for (int w = 0; w < kRecThreads / 32; ++w) {
-        const int y = wsum[w];
+        const int2 y = wsum[w];
         wsum[w] = run;
-        run += y;
+        run.x += y.x;
+        run.y += y.y;
       }
       wsum[kRecThreads / 32] = run;
     }
     __syncthreads();
-    const int first = base + wsum[warp] + s - cnt;
-    base += wsum[kRecThreads / 32];
+    const int first = base + wsum[warp].x + s - cnt, slot = sbase + wsum[warp].y + z - slots;
+    base += wsum[kRecThreads / 32].x;
+    sbase += wsum[kRecThreads / 32].y;
     if (i < p.N_seq) {
-      if (seqs) seqs[i] = make_int2(first, cnt);
+      if (seqs) seqs[i] = make_int2(slot, cnt);
       const int off = pos % C;
       for (int j = 0; j < cnt; ++j) {
         const int lo = j == 0 ? 0 : j * Lseg - off, hi = min(n, (j + 1) * Lseg - off);
-        SegRec r{t0 + lo, hi - lo, i, p.pool ? pos + lo : lo, j == 0, j == cnt - 1, first + j, 0};
+        SegRec r{t0 + lo, hi - lo, i, p.pool ? pos + lo : lo, j == 0, j == cnt - 1, slots ? slot + j : 0, 0};
         recs[first + j] = r;
         if (first + j < kSortMax) lens[first + j] = r.n;
       }

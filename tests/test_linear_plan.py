@@ -15,7 +15,7 @@ using namespace gdp::linear;
 extern "C" {
 void plan(int N, int B, int T, int HV, int K, int V, int packed, int vt, int G, long long* out) {
   const Plan x = plan_of(N, B, T, HV, K, V, packed, vt, Cost{1.85, 1.2, 3.0, 6.0}, G);
-  out[0] = x.nseg, out[1] = x.Lseg, out[2] = x.bound, out[3] = x.segS, out[4] = x.total;
+  out[0] = x.nseg, out[1] = x.Lseg, out[2] = x.bound, out[3] = x.segS, out[4] = x.total, out[5] = x.slots;
 }
 int segments(int off, int n, int Lseg) { return segment_count(off, n, Lseg); }
 }
@@ -34,9 +34,9 @@ def lib(tmp_path_factory):
 
 
 def plan(lib, N, B, T, HV, K=128, V=128, packed=1, vt=128, G=152):
-    out = (ctypes.c_longlong * 5)()
+    out = (ctypes.c_longlong * 6)()
     lib.plan(N, B, T, HV, K, V, packed, vt, G, out)
-    return dict(zip(("nseg", "Lseg", "bound", "segS", "total"), out))
+    return dict(zip(("nseg", "Lseg", "bound", "segS", "total", "slots"), out))
 
 
 @pytest.mark.parametrize("G", [148, 152])
@@ -70,3 +70,29 @@ def test_dense_segments_cover_the_sequence(lib):
             x = plan(lib, B, B, T, HV, packed=0)
             assert (x["nseg"] - 1) * x["Lseg"] < T <= x["nseg"] * x["Lseg"] and x["bound"] == B * x["nseg"]
             assert (x["nseg"] > 1) == bool(x["segS"])
+
+
+def test_scratch_is_for_cut_sequences(lib):
+    """A state of scratch for each segment of a cut sequence, none for whole ones, and enough for
+    however the lengths fall."""
+    rng = random.Random(1)
+    for _ in range(4000):
+        N, HV = rng.randint(1, 40), rng.choice([1, 4, 32, 76, 152])
+        lens = [rng.choice([0, 1, 450, 451, 512, 513, 1024, 1025, rng.randint(1, 5000)]) for _ in range(N)]
+        T = max(1, sum(lens))
+        x = plan(lib, N, 1, T, HV)
+        counts = [lib.segments(rng.choice([0, 63, rng.randint(0, 63)]), n, x["Lseg"]) for n in lens]
+        assert sum(c for c in counts if c > 1) <= x["slots"]
+        assert x["slots"] <= 2 * T / (x["Lseg"] - 62) + 1
+
+
+@pytest.mark.parametrize("N,T", [(256, 8192), (600, 600), (1000, 1000), (1024, 4096)])
+def test_many_short_requests_need_little(N, T):
+    """Through the library's own query: 32 heads of 128 x 128, a request's state is 2 MB."""
+    import linear_attention_ssm_gdp_gb300 as gdp
+    if not os.path.exists(gdp.LIB_PATH):
+        from linear_attention_ssm_gdp_gb300 import _build
+        _build.build()
+    size = gdp.load().gdp_linear_chunk_fwd_workspace_size
+    for dtype in (0, 1, 2):
+        assert size(1, T, N, 32, 32, 128, 128, dtype) <= max(50 << 20, T // 256 * (3 << 20))
