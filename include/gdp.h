@@ -364,7 +364,9 @@ gdp_status gdp_debug_wait_fault(int arm, double budget_seconds);
  *           projection go in as they are.
  *   g       natural-log decay, fp32: g_per_token != 0: [B, T, HV] contiguous;
  *           0: [HV], one per value head; NULL: no decay. -inf is a reset (the
- *           state before the token is dropped).
+ *           state before the token is dropped: a factor of 0, so what is not
+ *           finite in it becomes NaN). A positive g is a growth, taken as it is
+ *           while e^ of its sum over a chunk or a segment stays finite.
  *   o       [B, T, HV, V] contiguous, dtype `dt`; sums and states are fp32.
  *   K <= 256, V <= 1024, HV % H == 0, T and B T below 2^31; state bases 16-byte
  *   aligned.

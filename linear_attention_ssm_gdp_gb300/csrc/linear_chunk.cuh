@@ -90,7 +90,7 @@ __device__ __forceinline__ float2 log2e_pair(float hi, float lo) {
 }
 // e^(hi + lo) as a pair of floats (error ~2^-27): reduction by n ln 2 (a 16-bit head, so
 // that n head is exact), Taylor's series for the rest, its leading 1 + r added exactly.
-// Below the normal range the result is 0; NaN passes.
+// Below the normal range the result is 0, past the largest float infinite; NaN passes.
 __device__ __forceinline__ float2 exp_pair(float hi, float lo) {
   const float n = rintf(hi * 1.44269504f);
   float rl;
@@ -106,9 +106,11 @@ __device__ __forceinline__ float2 exp_pair(float hi, float lo) {
   const float s = two_sum(1.f, r, e);
   const float h = two_sum(s, fmaf(q, r * r, rl) + e, l);
   if (hi < -87.f) return make_float2(0.f, 0.f);
-  if (hi > 88.7f) return make_float2(__int_as_float(0x7f800000), 0.f);
-  const float sc = __int_as_float((max(min((int)n, 127), -126) + 127) << 23);
-  return make_float2(h * sc, l * sc);
+  if (hi > 89.f) return make_float2(__int_as_float(0x7f800000), 0.f);
+  // 2^n in two halves: n reaches 128, and 2^128 is past the largest float where h 2^128 is not
+  const int m = (int)n, half = m >> 1;
+  const float s0 = __int_as_float((half + 127) << 23), s1 = __int_as_float((m - half + 127) << 23);
+  return make_float2(h * s0 * s1, l * s0 * s1);
 }
 
 // g at position i of the chunk whose position 0 is row `base`; 0 outside the sequence.
