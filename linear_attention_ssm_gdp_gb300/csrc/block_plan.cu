@@ -174,7 +174,8 @@ extern "C" gdp_status gdp_block_plan(const int32_t* context_lens, const int32_t*
                    free_used, block_size, max_tokens, cu_seqlens, token_req, token_pos, slot_map,
                    free_used_out, status};
   const int smem = (2 * n + 1) * 4;
-  if (smem > 48 * 1024 && allow_smem<block_plan_kernel>((2 * kPlanMax + 1) * 4) != cudaSuccess)
+  // (48 KB unasked, the kernel's static part among them)
+  if (smem > 40 * 1024 && allow_smem<block_plan_kernel>((2 * kPlanMax + 1) * 4) != cudaSuccess)
     return GDP_ERR_CUDA;
   const int64_t want = std::max(cdiv(max_tokens, kPlanThreads), cdiv(n, kPlanThreads / 32));
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count()));
