@@ -127,7 +127,9 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const __grid_c
     for (int j = lane; j < need; j += 32)
       a.tables[(int64_t)r * a.width + have + j] = a.free_pages[first[r] + j];
   }
-  for (int t = blockIdx.x * kPlanThreads + tid; t < a.max_tokens; t += gridDim.x * kPlanThreads) {
+  // (64 bits: the last step of the loop passes max_tokens by up to a grid)
+  for (int64_t t64 = blockIdx.x * kPlanThreads + tid; t64 < a.max_tokens; t64 += gridDim.x * kPlanThreads) {
+    const int t = (int)t64;
     int rr = -1, pp = -1;
     int64_t ss = -1;
     if (t < total) {
