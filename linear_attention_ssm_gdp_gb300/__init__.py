@@ -401,11 +401,12 @@ def gdp_recurrent_update_slots(q, k, v, beta, g, state_pool, state_slot, scale=N
     return o
 
 
-def gdp_debug_wait_fault(arm: bool, budget_seconds: float = 0.0):
+def gdp_debug_wait_fault(arm: bool | int, budget_seconds: float = 0.0):
     """Test hook (off by default): arm a one-shot missing tensor-core commit in the
-    next 128-position WY launch so that one bounded device wait runs out, and/or set
-    the wait budget (<= 0: the default 2 s)."""
-    _check("gdp_debug_wait_fault", load().gdp_debug_wait_fault(1 if arm else 0,
+    next 128-position WY launch (True) or the next tensor-core launch of linear
+    attention (2) so that one bounded device wait runs out, and/or set the wait budget
+    (<= 0: the default 2 s)."""
+    _check("gdp_debug_wait_fault", load().gdp_debug_wait_fault(2 if arm == 2 else 1 if arm else 0,
                                                                 float(budget_seconds)))
 
 

@@ -107,6 +107,10 @@ cudaError_t launch_recurrent(const void* q, const void* k, const void* v, const 
                              const int32_t* slot, int n_slots, int32_t* status,
                              cudaStream_t stream);
 
+// Test hook (gdp_debug_wait_fault) of the linear-attention kernel: a wait of its next launch runs
+// out (arm), limit of its waits.
+cudaError_t linear_wait_fault(int arm, unsigned long long budget_ns);
+
 int sm_count();  // multiprocessors on the current device (cached per device)
 
 // Raises a kernel's limit of dynamic shared memory, once per kernel and device (the call takes

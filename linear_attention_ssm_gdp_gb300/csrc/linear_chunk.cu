@@ -46,6 +46,7 @@
 // false) forms each segment's own U, a small kernel turns those into the states
 // at the segment starts, and the segments then run as independent items.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "linear_chunk.cuh"
@@ -163,7 +164,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
     if (*dead) return false;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitBudgetNs) {
+    if (t - t0 > wait_budget_ns()) {
       if (status) atomicExch(status, kDevTimeout);
       *dead = 1;
       return false;
@@ -194,6 +195,7 @@ __device__ __forceinline__ bool state_and(bool pred) {
 // ------------------------------------------------------------------ shared memory
 struct TcArgs : ChunkArgs {
   int k_halves, v_halves;  // 64-column halves in the boxes of q and k, and of v and o
+  int fault;               // test hook (gdp_debug_wait_fault): CTA 0 leaves out the commit of its first U
 };
 
 template <int KD, bool OUT>
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     t = __reduce_add_sync(0xffffffffu, t);
     if (lane == 0) *s_total = t;
   }
-  if (!a.recs && blockIdx.x == 0 && tid == 96 && p.status) *p.status = kDevOk;
+  if (a.clear && blockIdx.x == 0 && tid == 96) *p.status = kDevOk;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           mma_bf16_ts(u_at(n), av, k, id_u, 1);
           mma_commit(&bars[B_VFREE + ks]);
           if (ks == 3) {
-            mma_commit(&bars[B_U + n % NU]);
+            if (!a.fault || n > 0 || blockIdx.x > 0) mma_commit(&bars[B_U + n % NU]);
             mma_commit(&bars[B_FREE + n % L::NST]);
           }
         }
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         if ((++spins & 63) == 0) {  // a bounded wait like the others
           const uint64_t t = globaltimer_ns();
           if (spins == 64) since = t;
-          if (__any_sync(0xffffffffu, *sy.dead || t - since > kWaitBudgetNs)) {
+          if (__any_sync(0xffffffffu, *sy.dead || t - since > wait_budget_ns())) {
             if (lane == 0 && !*sy.dead) {
               if (p.status) atomicExch(p.status, kDevTimeout);
               *sy.dead = 1;
@@ -695,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     }
     // nothing may still write shared memory when the CTA leaves
     for (int m = max(0, next - L::NST); m < next; ++m) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
+      const uint64_t t0 = globaltimer_ns(), budget = wait_budget_ns();
+      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < budget) {}
     }
   } else if (OUT) {
     // ---------------------------------------------------------------- INTER, INTRA
@@ -738,6 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
 }
 
 // ------------------------------------------------------------------ host
+// Test hook state (gdp_debug_wait_fault): armed for the next launch only.
+std::atomic<int> g_fault{0};
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -808,10 +813,16 @@ bool linear_tc_ok(const LinearProblem& p) {
          map_ok(p.v, p.HV, p.T, p.B, p.vs) && reinterpret_cast<uintptr_t>(p.o) % 16 == 0;
 }
 
+cudaError_t linear_wait_fault(int arm, unsigned long long budget_ns) {
+  g_fault.store(arm);
+  return cudaMemcpyToSymbol(ptx::g_wait_budget_ns, &budget_ns, sizeof(budget_ns));
+}
+
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   const Plan x = plan_of(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.cu != nullptr, kVT, kCost, sm_count());
   TcArgs a{};
   a.p = p;
+  a.clear = !p.cu;  // (the segment kernel does it for a packed batch)
   a.nseg = x.nseg;
   a.Lseg = x.Lseg;
   a.slices = x.slices;
@@ -836,12 +847,14 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   if (!map5(&m[0], p.q, p.K, a.k_halves, p.H, p.T, p.B, p.qs) || !map5(&m[1], p.k, p.K, a.k_halves, p.H, p.T, p.B, p.ks) ||
       !map5(&m[2], p.v, p.V, a.v_halves, p.HV, p.T, p.B, p.vs) || !map5(&m[3], p.o, p.V, a.v_halves, p.HV, p.T, p.B, os))
     return cudaErrorInvalidValue;
+  a.fault = g_fault.exchange(0);
   if (x.segS) {
     a.segS = reinterpret_cast<float*>(ws + x.segS);
     a.segW = reinterpret_cast<float2*>(ws + x.segW);
     cudaError_t e = p.K > 64 ? go<128, false>(a, m) : go<64, false>(a, m);
     if (e == cudaSuccess) e = launch_combine(a, seqs);
     if (e != cudaSuccess) return e;
+    a.fault = a.clear = 0;
   }
   return p.K > 64 ? go<128, true>(a, m) : go<64, true>(a, m);
 }

@@ -14,6 +14,7 @@ struct ChunkArgs {
   LinearProblem p;
   const SegRec* recs;   // packed batches; seq = -1 past the last
   const int* split;     // packed batches: whether any sequence is in several segments
+  int clear;            // the first launch of a dense call: sets the status word to kDevOk
   int nseg, Lseg;       // dense batches: segments per sequence, tokens per segment
   int slices, vt;       // slices of vt value columns
   int items;            // bound over all CTAs

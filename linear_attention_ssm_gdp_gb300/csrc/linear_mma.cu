@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
   const LinearProblem& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
   if (!OUT && no_split(a)) return;
-  if (!a.recs && blockIdx.x == 0 && tid == 0 && p.status) *p.status = kDevOk;
+  if (a.clear && blockIdx.x == 0 && tid == 0) *p.status = kDevOk;
   Item x;
   if (!get_item(a, blockIdx.x, x) || skip<OUT>(x)) return;
   float* sS = reinterpret_cast<float*>(sm + L::S);
@@ -451,6 +451,7 @@ cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
   const Plan x = plan(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt, p.cu != nullptr);
   ChunkArgs a{};
   a.p = p;
+  a.clear = !p.cu;  // (the segment kernel does it for a packed batch)
   a.nseg = x.nseg;
   a.Lseg = x.Lseg;
   a.slices = x.slices;
@@ -480,6 +481,7 @@ cudaError_t launch_linear_mma(const LinearProblem& p, uint8_t* ws) {
     cudaError_t e = go_t<false>(a, vec);
     if (e == cudaSuccess) e = launch_combine(a, seqs);
     if (e != cudaSuccess) return e;
+    a.clear = 0;
   }
   return go_t<true>(a, vec);
 }
