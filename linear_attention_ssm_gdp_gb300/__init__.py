@@ -567,6 +567,12 @@ def _linear_out(v, out):
     return out
 
 
+def _copy_status(status, workspace):
+    """The workspace's status word into the caller's."""
+    if status is not None:
+        status.view(-1)[:1].copy_(workspace.view(torch.uint8)[:4].view(torch.int32))
+
+
 def _packed(cu_seqlens, B):
     _need_cuda(cu_seqlens)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
@@ -577,18 +583,21 @@ def _packed(cu_seqlens, B):
 
 def gdp_linear_chunk_fwd(q, k, v, g=None, cu_seqlens=None, scale: float | None = None,
                          initial_state=None, output_final_state: bool = True, workspace=None,
-                         out=None):
+                         out=None, status=None):
     """Chunked linear attention with a decay for each head:
     S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
 
     q, k [B,T,H,K], v [B,T,HV,V] (bf16/fp16/fp32; any strides with a contiguous last
     dimension), g fp32 natural-log decay [B,T,HV] per token, [HV] per head or None,
     cu_seqlens [N+1] int32 on the device (B must be 1), initial_state [N,HV,K,V] fp32.
-    ``scale`` defaults to K**-0.5. Returns (o [B,T,HV,V] in q's dtype, final_state
-    [N,HV,K,V] fp32 or None)."""
+    ``scale`` defaults to K**-0.5. ``status`` (optional int32 device tensor) is set to 0, 1
+    (bad offsets: o is left as it was) or 2 (a wait on the device ran out); without it the
+    word is in the workspace (gdp_read_status). Returns (o [B,T,HV,V] in q's dtype,
+    final_state [N,HV,K,V] fp32 or None)."""
     B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
     N = B if cu_seqlens is None else _packed(cu_seqlens, B)
     _state_ok("initial_state", initial_state, (N, HV, K, V))
+    _status_ok(status)
     ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
     if out is None:
         o = _linear_out(v, None)
@@ -604,21 +613,24 @@ def gdp_linear_chunk_fwd(q, k, v, g=None, cu_seqlens=None, scale: float | None =
         _DTYPE[q.dtype], o.data_ptr(), _a(fs), ws.data_ptr(), ws.numel(), _raw_stream(q))
     if st:
         _check("gdp_linear_chunk_fwd", st)
+    _copy_status(status, ws)
     return o, fs
 
 
 def gdp_linear_chunk_fwd_paged(q, k, v, g, cu_seqlens, state_pool, block_tables, context_lens,
                                block_size: int, scale: float | None = None, workspace=None,
-                               out=None):
+                               out=None, status=None):
     """Chunked linear attention over packed prompts whose states live in pages:
     request r starts from the page of its token context_lens[r] - 1 (zeros for a new
     request) and writes ``state_pool`` [n_pages,HV,K,V] fp32 at every block of
     block_size tokens (a multiple of 64) that it ends and at its last token;
     block_tables [n, max_blocks] names the pages. q, k [1,T,H,K], v [1,T,HV,V].
-    Returns o."""
+    ``status`` as in gdp_linear_chunk_fwd, 1 also for a skipped request (a negative
+    context or a page outside the pool). Returns o."""
     B, T, H, HV, K, V, strides, per_token = _linear_args(q, k, v, g)
     N = _packed(cu_seqlens, B)
     _tables_ok(N, HV, K, V, state_pool, block_tables, context_lens)
+    _status_ok(status)
     ws = _linear_workspace(workspace, B, T, N, H, HV, K, V, q)
     o = _linear_out(v, out)
     st = load().gdp_linear_chunk_fwd_paged(
@@ -629,6 +641,7 @@ def gdp_linear_chunk_fwd_paged(q, k, v, g, cu_seqlens, state_pool, block_tables,
         ws.data_ptr(), ws.numel(), _raw_stream(q))
     if st:
         _check("gdp_linear_chunk_fwd_paged", st)
+    _copy_status(status, ws)
     return o
 
 
