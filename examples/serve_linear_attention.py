@@ -52,7 +52,8 @@ class Server:
         self.pools = [torch.zeros(n_pages, a.HV, a.K, a.V, device=device) for a in layers]
         self.free = torch.arange(n_pages, dtype=torch.int32, device=device)
         self.used = torch.zeros(1, dtype=torch.int32, device=device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)  # of one call
+        self.seen = torch.zeros_like(self.status)  # of all
         self.tables = torch.full((max_requests, max_blocks), -1, dtype=torch.int32, device=device)
         self.ctx = torch.zeros(max_requests, dtype=torch.int32, device=device)
         self.n = 0
@@ -62,7 +63,18 @@ class Server:
         tables, ctx = self.tables[rows], self.ctx[rows]
         cu, _, _, _, self.used = gdp.gdp_block_plan(ctx, query, tables, self.free, self.used,
                                                     self.block, tokens, status=self.status)
+        self.seen |= self.status
         return cu, tables, ctx
+
+    def attend_prompts(self, q, k, v, g, cu, pool, tables, ctx):
+        o = gdp.gdp_linear_chunk_fwd_paged(q[None], k[None], v[None], g[None], cu, pool, tables, ctx,
+                                           self.block, status=self.status)
+        self.seen |= self.status
+        return o[0]
+
+    def errors(self):
+        """What any step has reported so far (synchronises)."""
+        return int(self.seen)
 
     def prompts(self, prompts, share=None):
         """Admits requests with these prompts (token lists); `share` = (request, blocks) of a common
@@ -78,9 +90,7 @@ class Server:
         cu, tables, ctx = self.plan(rows, query, x.shape[0])
         for layer, pool in zip(self.layers, self.pools):
             q, k, v, gate, g = layer.project(x)
-            o = gdp.gdp_linear_chunk_fwd_paged(q[None], k[None], v[None], g[None], cu, pool, tables,
-                                               ctx, self.block)
-            x = layer.finish(x, o[0], gate)
+            x = layer.finish(x, self.attend_prompts(q, k, v, g, cu, pool, tables, ctx), gate)
         self.ctx[rows] += query
         self.n += len(prompts)
         return list(range(rows.start, rows.stop)), (x[cu[1:].long() - 1] @ self.embed.T).argmax(-1)
@@ -95,6 +105,7 @@ class Server:
             o = gdp.gdp_linear_recurrent_update_paged(
                 q[:, None], k[:, None], v[:, None], g[:, None], pool, tables, ctx, self.block,
                 status=self.status)
+            self.seen |= self.status
             x = layer.finish(x, o[:, 0], gate)
         self.ctx[rows] += 1
         return (x @ self.embed.T).argmax(-1)
@@ -141,8 +152,8 @@ def serve(requests=8, prompt=700, new=32, block=128, width=512, H=4, HV=8, K=64,
         token = s.decode(token)
     torch.cuda.synchronize()
     took = time.perf_counter() - start
-    if int(s.status):
-        raise RuntimeError(f"the plan reported {int(s.status)}")
+    if s.errors():
+        raise RuntimeError(f"a step reported {s.errors()}")
     off = []
     for r, stream in enumerate(streams):
         want = dense_states(layers, embed, torch.tensor(stream, device=device))
