@@ -10,6 +10,7 @@
 // and then the squared distances from it, so the variance is the two-pass one, in
 // fp32, and no element is read twice. Sums run in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -45,6 +46,8 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^126, where the quotient is below 1e-36).
 __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + ex2(-1.44269504f * a)); }
 
+// Means are products by __fmul_rn: contracted into the differences from them, they would not be the
+// rounded ones whose rest is taken out below.
 struct NormArgs {
   const void *x, *gate;
   int64_t x_sn, x_sl, g_sn, g_sl;
@@ -58,7 +61,8 @@ struct NormArgs {
   int rows;       // positions per CTA
   int resident;   // the CTA's elements stay in shared memory
   int slices;     // runs of positions per set of groups, where they meet through memory
-  float2* part;   // [sample, set][slice][GS]: mean and squared distances of a slice
+  float pow2, nn, inv_nn, var_of;  // rows: power of two below 1 / Cg, Cg times it, 1 / nn, 1 / (Cg nn^2)
+  float4* part;   // [sample, set][slice][GS]: a slice's mean, what its rounding left, squared distances, elements
 };
 
 template <bool GATE>
@@ -114,33 +118,40 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
       bi[j][e] = b4.x; bi[j][e + 1] = b4.y; bi[j][e + 2] = b4.z; bi[j][e + 3] = b4.w;
     }
   }
-  const float inv = 1.f / (float)a.Cg;
+  // Distances from the mean without its rounding, which a group of equal or close values would show:
+  // z = (n x - sum x) / (n std), with n scaled by a power of two (a.nn, below 1) so that nothing
+  // overflows that did not, is one exact multiply-add where the sum is exact. It is for 16-bit values
+  // of one size (n is at most 1024 here); 32-bit ones are taken from the group's first, which
+  // makes the differences of close values exact, and costs others at most sqrt(n) 2^-24 of a std.
+  constexpr bool kPivot = sizeof(TX) == 4;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t n = n0 + u * Nu;
     float f[NV][VEC], s = 0.f;
+    const float x0 = kPivot ? __shfl_sync(0xffffffffu, to_f(x[u][0].e[0]), 0, TG) : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         f[j][e] = to_f(x[u][j].e[e]);
+        if (kPivot) f[j][e] = sub + j * TG < nvec ? f[j][e] - x0 : 0.f;
         s += f[j][e];
       }
 #pragma unroll
     for (int o = TG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mean = s * inv;
+    const float sn = s * a.pow2;
     float m2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (sub + j * TG < nvec)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          f[j][e] -= mean;
+          f[j][e] = fmaf(a.nn, f[j][e], -sn);
           m2 = fmaf(f[j][e], f[j][e], m2);
         }
 #pragma unroll
     for (int o = TG / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-    const float rstd = rsqrtf(m2 * inv + a.eps);
+    const float rstd = rsqrtf(fmaf(m2, a.var_of, a.eps)) * a.inv_nn;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int vi = sub + j * TG;
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(256) norm_elements_kernel(const __grid_constan
   for (int i = sub; i < len; i += TG) t += to_f(x[i]);
 #pragma unroll
   for (int o = TG / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  const float mean = t * inv;
+  const float mean = __fmul_rn(t, inv);
   // (the mean's own rounding, which a group of a few close values would show, is taken out again)
   float rest = 0.f;
   t = 0.f;
@@ -199,16 +210,22 @@ __global__ void __launch_bounds__(256) norm_elements_kernel(const __grid_constan
 // A cluster of CTAs takes one sample and a set of GS neighbouring groups (enough that its row
 // segments fill whole sectors), each CTA a run of positions; the group sums meet through
 // distributed shared memory. A thread keeps one vector column, so that its channels' groups
-// are fixed, and walks down the positions. 4 x 4096 x 320 fp16 in 32 groups, 21 MB: 13.1 us;
+// are fixed, and walks down the positions. 4 x 4096 x 320 fp16 in 32 groups, 21 MB: 13.2 us;
 // what it waits for is latency: two reductions over a cluster and the loads of a few warps.
 constexpr int kMapThreads = 256;
 constexpr int kMaxGS = 128;
 constexpr int kMapSmem = 200 * 1024;  // most that a CTA keeps
 
 //
+// The second walk sums the distances from the rounded mean beside their squares: what the mean's
+// rounding has left (`rest`) is taken out of the variance and of the elements.
+//
 // PART: a slice's own mean and squared distances from it go to memory, and a second launch (APPLY)
 // merges the slices' in order (Chan's formula) and normalises: as many CTAs per group as it takes.
 enum { WHOLE, PART, APPLY };
+
+// (a variance of nearly equal values may come out just below zero)
+__device__ __forceinline__ float rstd_of(float var, float eps) { return rsqrtf((var < 0.f ? 0.f : var) + eps); }
 
 template <typename TX, typename TO, int VEC, bool GATE, int STAGE>
 __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_constant__ NormArgs a) {
@@ -216,9 +233,9 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   extern __shared__ __align__(16) uint8_t raw[];
   using PX = Pack<TX, VEC>;
   using PO = Pack<TO, VEC>;
-  __shared__ float part[kMapThreads * (VEC + 1)];  // rows of W + 1 (W is at least a vector)
-  __shared__ float total[kMaxGS];                  // the cluster's group sums
-  __shared__ float gsum[2][kMaxGS];                // this CTA's: elements, squared distances
+  __shared__ float part[2][kMapThreads * (VEC + 1)];  // rows of W + 1 (W is at least a vector)
+  __shared__ float total[2][kMaxGS];                  // the cluster's group sums
+  __shared__ float gsum[3][kMaxGS];                   // this CTA's: elements, squared distances, distances
   cg::cluster_group cl = cg::this_cluster();
   const int CL = (int)cl.num_blocks(), runs = STAGE == WHOLE ? CL : a.slices;
   const int rank = STAGE == WHOLE ? (int)cl.block_rank() : (int)(blockIdx.x % runs);
@@ -238,47 +255,66 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
   const TX* xb = static_cast<const TX*>(a.x) + n * a.x_sn + l0 * a.x_sl + c0;
   const float inv = 1.f / ((float)(STAGE == PART ? max(nrow, 1) : a.L) * (float)a.Cg);
 
-  float rstd[VEC], mean_of[VEC];  // per channel of the thread's column (one group: all the same)
-  float acc[VEC];
-  auto reduce = [&](int which) {
-    // this CTA's sums by group, in a fixed order, then the cluster's
+  float mean_of[VEC];  // per channel of the thread's column (one group: all the same)
+  float acc[VEC], dev[VEC];
+  // this CTA's sums of acc (and of dev, with two) by group, in a fixed order, then the cluster's: into
+  // gsum[which ..] and total
+  auto reduce = [&](int which, auto two) {
+    constexpr int S = decltype(two)::value;
     if (gs == 1) {
-      float t = 0.f;
+      float t[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) t += on ? acc[e] : 0.f;
+      for (int e = 0; e < VEC; ++e) {
+        t[0] += on ? acc[e] : 0.f;
+        if (S == 2) t[1] += on ? dev[e] : 0.f;
+      }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < S; ++i) t[i] += __shfl_xor_sync(0xffffffffu, t[i], o);
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < S; ++i) part[i][threadIdx.x >> 5] = t[i];
       __syncthreads();
-      if (threadIdx.x == 0) {
-        t = 0.f;
-        for (int i = 0; i < kMapThreads / 32; ++i) t += part[i];
-        gsum[which][0] = t;
+      if (threadIdx.x < S) {
+        float u = 0.f;
+        for (int i = 0; i < kMapThreads / 32; ++i) u += part[threadIdx.x][i];
+        gsum[which + threadIdx.x][0] = u;
       }
     } else {  // one pass of columns: a warp per group, lanes over the rows of W channel sums
       if (on)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) part[ty * (W + 1) + tx * VEC + e] = acc[e];
+        for (int e = 0; e < VEC; ++e) {
+          part[0][ty * (W + 1) + tx * VEC + e] = acc[e];
+          if (S == 2) part[1][ty * (W + 1) + tx * VEC + e] = dev[e];
+        }
       __syncthreads();
       const int lane = threadIdx.x & 31;
       for (int g = threadIdx.x >> 5; g < gs; g += kMapThreads / 32) {
-        float t = 0.f;
+        float t[2] = {0.f, 0.f};
         for (int y = lane; y < nty; y += 32)
-          for (int i = 0; i < a.Cg; ++i) t += part[y * (W + 1) + g * a.Cg + i];
+          for (int i = 0; i < a.Cg; ++i)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) gsum[which][g] = t;
+            for (int j = 0; j < S; ++j) t[j] += part[j][y * (W + 1) + g * a.Cg + i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int j = 0; j < S; ++j) t[j] += __shfl_xor_sync(0xffffffffu, t[j], o);
+        if (lane < S) gsum[which + lane][g] = lane == 0 ? t[0] : t[1];
       }
     }
     cl.sync();
     for (int g = threadIdx.x >> 3; g < gs; g += kMapThreads / 8) {  // eight lanes, a rank each
       const int r = threadIdx.x & 7;
-      float t = r < CL ? cl.map_shared_rank(&gsum[which][0], r)[g] : 0.f;
       const uint32_t m = 0xffu << (threadIdx.x & 24);
-      t += __shfl_xor_sync(m, t, 1);
-      t += __shfl_xor_sync(m, t, 2);
-      t += __shfl_xor_sync(m, t, 4);
-      if (r == 0) total[g] = t;  // the cluster's sums
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        float t = r < CL ? cl.map_shared_rank(&gsum[which + j][0], r)[g] : 0.f;
+        t += __shfl_xor_sync(m, t, 1);
+        t += __shfl_xor_sync(m, t, 2);
+        t += __shfl_xor_sync(m, t, 4);
+        if (r == 0) total[j][g] = t;  // the cluster's sums
+      }
     }
     __syncthreads();
   };
@@ -314,11 +350,11 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
           for (int e = 0; e < VEC; ++e) acc[e] += to_f(x.e[e]);
         });
     kept = a.resident;
-    reduce(0);
+    reduce(0, std::integral_constant<int, 1>());
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      mean_of[e] = total[group_of(tx, e)] * inv;
-      acc[e] = 0.f;
+      mean_of[e] = __fmul_rn(total[0][group_of(tx, e)], inv);
+      acc[e] = dev[e] = 0.f;
     }
     __syncthreads();
     if (on)
@@ -327,44 +363,51 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const float d = to_f(x.e[e]) - mean_of[e];
+            dev[e] += d;
             acc[e] = fmaf(d, d, acc[e]);
           }
         });
-    reduce(1);
+    reduce(1, std::integral_constant<int, 2>());
     if constexpr (STAGE == PART) {
-      for (int g = threadIdx.x; g < gs; g += kMapThreads)
-        a.part[(unit * runs + rank) * a.GS + g] = make_float2(gsum[0][g] * inv, gsum[1][g]);
+      for (int g = threadIdx.x; g < gs; g += kMapThreads) {
+        const float r = gsum[2][g] * inv;
+        a.part[(unit * runs + rank) * a.GS + g] = make_float4(__fmul_rn(gsum[0][g], inv), r, fmaf(-r, gsum[2][g], gsum[1][g]),
+                                                             (float)nrow * (float)a.Cg);
+      }
       return;
     }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) rstd[e] = rsqrtf(total[group_of(tx, e)] * inv + a.eps);
   } else {
     for (int g = threadIdx.x >> 5; g < gs; g += kMapThreads / 32) {  // a warp per group, lanes over the slices
-      const float2* q = a.part + unit * runs * a.GS + g;
+      const float4* q = a.part + unit * runs * a.GS + g;
       const int lane = threadIdx.x & 31;
-      auto count = [&](int i) { return (float)max((int64_t)0, min(a.L - (int64_t)i * a.rows, (int64_t)a.rows)) * (float)a.Cg; };
-      float t = 0.f, m2 = 0.f;
-      for (int i = lane; i < runs; i += 32) t = fmaf(count(i), __ldcg(q + (int64_t)i * a.GS).x, t);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      const float mean = t * inv;
+      float t = 0.f, m2 = 0.f, rest = 0.f;
       for (int i = lane; i < runs; i += 32) {
-        const float2 x = __ldcg(q + (int64_t)i * a.GS);
-        m2 += fmaf(count(i) * (x.x - mean), x.x - mean, x.y);
+        const float4 x = __ldcg(q + (int64_t)i * a.GS);
+        t = fmaf(x.w, x.x, t);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      const float mean = __fmul_rn(t, inv);
+      for (int i = lane; i < runs; i += 32) {
+        const float4 x = __ldcg(q + (int64_t)i * a.GS);
+        const float d = (x.x - mean) + x.y, cd = x.w * d;
+        rest += cd;
+        m2 += fmaf(cd, d, x.z);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      }
       if (lane == 0) {
         gsum[0][g] = mean;
-        total[g] = rsqrtf(m2 * inv + a.eps);
+        total[0][g] = m2;
+        total[1][g] = rest;
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      mean_of[e] = gsum[0][group_of(tx, e)];
-      rstd[e] = total[group_of(tx, e)];
-    }
+    for (int e = 0; e < VEC; ++e) mean_of[e] = gsum[0][group_of(tx, e)];
   }
   const TO* gb = static_cast<const TO*>(a.gate);
   if (GATE) gb += n * a.g_sn + l0 * a.g_sl + c0;
@@ -374,8 +417,10 @@ __global__ void __launch_bounds__(kMapThreads) norm_map_kernel(const __grid_cons
       float ww[VEC], bb[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        ww[e] = rstd[e] * (a.w ? a.w[c0 + c * VEC + e] : 1.f);
-        bb[e] = a.b ? a.b[c0 + c * VEC + e] : 0.f;
+        const int g = group_of(c, e);
+        const float rest = total[1][g] * inv, rstd = rstd_of(fmaf(-rest, rest, total[0][g] * inv), a.eps);
+        ww[e] = rstd * (a.w ? a.w[c0 + c * VEC + e] : 1.f);
+        bb[e] = fmaf(-rest, ww[e], a.b ? a.b[c0 + c * VEC + e] : 0.f);
       }
       walk(c, [&](int r, const PX& x) {
         PO gt, out;
@@ -409,7 +454,7 @@ cudaError_t go_elements(const NormArgs& a, cudaStream_t s) {
 template <typename TX, typename TO, int VEC, bool GATE, int STAGE>
 cudaError_t go_map2(const NormArgs& a, int CL, size_t smem, cudaStream_t s) {
   auto kern = norm_map_kernel<TX, TO, VEC, GATE, STAGE>;
-  if (smem > 24 * 1024) {  // beside up to 20 KB of static shared memory
+  if (smem > 24 * 1024) {  // beside up to 21 KB of static shared memory
     const cudaError_t e = allow_smem<norm_map_kernel<TX, TO, VEC, GATE, STAGE>>(kMapSmem);
     if (e != cudaSuccess) return e;
   }
@@ -447,15 +492,15 @@ MapPlan plan_map(int64_t N, int64_t L, int G, int Cg, int size, int vec, bool sp
     m.seg = (int64_t)m.GS * Cg * size;
   };
   // Row segments of 128 bytes; half and a quarter of that where even clusters of 8 would leave SMs
-  // idle or a CTA with more than 48 KB (4 x 4096 x 320 in 32 groups, fp16: 13.1 us, against 18.2
+  // idle or a CTA with more than 48 KB (4 x 4096 x 320 in 32 groups, fp16: 13.2 us, against 18.2
   // with 128 bytes), but not beyond (16 x 256 x 1280, 32 groups: 16.2 us with 64 bytes, 12.4 with 128).
   for (const int64_t least : {128, 64, 32}) {
     sets_of(least);
     if (N * m.sets * 8 >= sm_count() && cdiv(L, 8) * m.seg <= 48 * 1024) break;
   }
   // Slices where that still leaves a CTA with much: the same work on more SMs, for a second read of
-  // x and a launch. 1 x 16384 x 128 fp16 in one group: 15.9 us, where a cluster has eight SMs for it;
-  // 2 x 9000 x 512 fp32 in four: 20.7 / 42.9. Sets of several small groups cost more to reduce, so
+  // x and a launch. 1 x 16384 x 128 fp16 in one group: 17.7 us, where a cluster has eight SMs for it;
+  // 2 x 9000 x 512 fp32 in four: 21.4 / 42.9. Sets of several small groups cost more to reduce, so
   // they stay with clusters longer (1 x 16384 x 128, 32 groups: 43 us in slices, 15.3 in clusters).
   const int64_t much = N * m.sets * 8 >= sm_count() ? 96 : m.GS > 1 ? 64 : 32;
   if (split && cdiv(L, 8) * m.seg > much * 1024) {
@@ -465,7 +510,7 @@ MapPlan plan_map(int64_t N, int64_t L, int G, int Cg, int size, int vec, bool sp
     m.rows = (int)cdiv(L, std::min<int64_t>(1024, std::min(want, most)));
     m.slices = (int)cdiv(L, m.rows);
     m.CL = 1;
-    m.part_bytes = units * m.slices * m.GS * (int64_t)sizeof(float2);
+    m.part_bytes = units * m.slices * m.GS * (int64_t)sizeof(float4);
     return m;
   }
   // CTAs per cluster: until every SM has one, or 8 KB of work are left each (clusters of 16 found
@@ -532,7 +577,7 @@ namespace {
 
 gdp_status norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate, int64_t gate_sn, int64_t gate_sl,
                 const float* weight, const float* bias, int64_t N, int64_t L, int C, int G, float eps,
-                gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y, float2* part, cudaStream_t stream) {
+                gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y, float4* part, cudaStream_t stream) {
   if (N < 0 || L < 0 || C <= 0 || G <= 0 || C % G != 0 || !(eps >= 0.f)) return GDP_ERR_INVALID_ARG;
   if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU) return GDP_ERR_UNSUPPORTED;
   if (N == 0 || L == 0) return GDP_OK;
@@ -543,8 +588,11 @@ gdp_status norm(const void* x, int64_t x_sn, int64_t x_sl, const void* gate, int
   if (L > INT32_MAX) return GDP_ERR_UNSUPPORTED;
   if (L == 1) x_sl = gate_sl = 0;  // the stride of a single position or sample means nothing
   if (N == 1) x_sn = gate_sn = 0;
+  float pow2 = 1.f;
+  while (pow2 * (float)(C / G) > 1.f) pow2 *= 0.5f;
+  const float nn = pow2 * (float)(C / G);
   NormArgs a{x, gate, x_sn, x_sl, gate_sn, gate_sl, weight, bias, y, N, L, C, G, C / G, eps,
-             activation == GDP_ACT_SILU, 0, 0, 0, 0, 0, part};
+             activation == GDP_ACT_SILU, 0, 0, 0, 0, 0, pow2, nn, 1.f / nn, 1.f / ((float)(C / G) * nn * nn), part};
   cudaError_t e;
   if (dt == GDP_BF16 && dt_out == GDP_BF16) e = run<__nv_bfloat16, __nv_bfloat16>(a, stream);
   else if (dt == GDP_F16 && dt_out == GDP_F16) e = run<__half, __half>(a, stream);
@@ -583,7 +631,7 @@ gdp_status gdp_group_norm_ws(const void* x, int64_t x_sn, int64_t x_sl, const vo
   if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < need))
     return GDP_ERR_WORKSPACE;
   return norm(x, x_sn, x_sl, gate, gate_sn, gate_sl, weight, bias, N, L, C, G, eps, activation, dt, dt_out, y,
-              need > 0 ? static_cast<float2*>(workspace) : nullptr, stream);
+              need > 0 ? static_cast<float4*>(workspace) : nullptr, stream);
 }
 
 }  // extern "C"
