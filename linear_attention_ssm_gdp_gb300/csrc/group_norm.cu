@@ -5,10 +5,11 @@
 // L = 1 is the norm of a token's heads (the output norm and gate of a linear
 // attention layer).
 //
-// The bound is HBM: x (and the gate) read once, y written once. Both kernels hold
-// what they have read (in registers, or in shared memory) while they form the mean
-// and then the squared distances from it, so the variance is the two-pass one, in
-// fp32, and no element is read twice. Sums run in a fixed order.
+// The bound is HBM: x (and the gate) read once, y written once. norm_rows keeps what it has
+// read in registers and norm_map in shared memory, where it fits, while they form the
+// mean and then the squared distances from it: the variance is the two-pass one, in
+// fp32. norm_elements, norm_map without room and the slices of norm_map read x again, from a
+// cache where it still is there. Sums run in a fixed order.
 #include <algorithm>
 #include <type_traits>
 
@@ -560,6 +561,12 @@ cudaError_t run(NormArgs a, cudaStream_t s) {
     if (nvec <= 32) return go_rows<TX, TO, 32, 1, 2>(a, s);
     if (nvec <= 64) return go_rows<TX, TO, 32, 2, 1>(a, s);
     if (nvec <= 128) return go_rows<TX, TO, 32, 4, 1>(a, s);
+    // fp32 groups of 516 to 1024 channels: one read where a lane's eight vectors are mostly used, or
+    // where there are few groups and latency counts; else single elements, whose reads overlap
+    // better (us of rows / elements, 4 groups: 400 x 2560 3.3 / 6.6, 32768 x 2560 141.8 / 127.1,
+    // 400 x 3584 3.6 / 8.5, 32768 x 3584 163.0 / 189.7)
+    if constexpr (VEC == 4)
+      if (nvec <= 256 && (nvec > 192 || a.N * a.G <= 16 * sm_count())) return go_rows<TX, TO, 32, 8, 1>(a, s);
   }
   if (a.L == 1 && a.Cg <= 8) return go_elements<TX, TO, 1>(a, s);
   if (a.L == 1 && a.Cg <= 1024) return go_elements<TX, TO, 32>(a, s);
