@@ -370,8 +370,8 @@ gdp_status gdp_debug_wait_fault(int arm, double budget_seconds);
  *           finite in it becomes NaN). A positive g is a growth, taken as it is
  *           while e^ of its sum over a chunk or a segment stays finite.
  *   o       [B, T, HV, V] contiguous, dtype `dt`; sums and states are fp32.
- *   K <= 256, V <= 1024, HV % H == 0, T and B T below 2^31; state bases 16-byte
- *   aligned.
+ *   K <= 256, V <= 1024, HV % H == 0, B T below 2^31 (the chunked calls: at most
+ *   2^31 - 4096, and 2^30 sequences); state bases 16-byte aligned.
  * Values that are not finite stay in their sequence: one in q spoils its own
  * token's o, one in k or v the state and every later token of its head; the
  * chunked calls may also spoil the earlier tokens of the same 64-token chunk

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "linear_internal.cuh"
+#include "linear_plan.h"
 
 using namespace gdp;
 
@@ -16,6 +17,11 @@ bool dtype_ok(gdp_dtype dt) { return dt == GDP_BF16 || dt == GDP_F16 || dt == GD
 size_t linear_ws(int N_seq, int B, int T, int HV, int K, int V, gdp_dtype dt) {
   const size_t m = linear_mma_workspace(N_seq, B, T, HV, K, V, dt);
   return linear_tc_shape(K, V, dt) ? std::max(m, linear_tc_workspace(N_seq, B, T, HV, K, V)) : m;
+}
+
+// Lengths that the chunked kernels count in 32 bits.
+bool lengths_ok(int N_seq, int B, int T) {
+  return (int64_t)B * T <= linear::kMostTokens && N_seq <= linear::kMostSeqs;
 }
 
 bool sizes_ok(int N_seq, int B, int T, int H, int HV, int K, int V) {
@@ -53,6 +59,7 @@ void set_strides(LinearProblem& p, const int64_t* s) {
 gdp_status chunk(LinearProblem& p, const int64_t* strides, void* workspace, size_t bytes) {
   const gdp_status st = check(p, strides);
   if (st != GDP_OK) return st;
+  if (!lengths_ok(p.N_seq, p.B, p.T)) return GDP_ERR_UNSUPPORTED;
   if (p.cu ? p.B != 1 : p.N_seq != p.B) return GDP_ERR_INVALID_ARG;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 ||
       bytes < linear_ws(p.N_seq, p.B, p.T, p.HV, p.K, p.V, p.dt))
@@ -70,7 +77,9 @@ extern "C" {
 
 size_t gdp_linear_chunk_fwd_workspace_size(int B, int T, int N_seq, int H, int HV, int K, int V,
                                            gdp_dtype dt) {
-  if (!sizes_ok(N_seq, B, T, H, HV, K, V) || K > 256 || V > 1024 || !dtype_ok(dt)) return 0;
+  if (!sizes_ok(N_seq, B, T, H, HV, K, V) || K > 256 || V > 1024 || !dtype_ok(dt) ||
+      !lengths_ok(N_seq, B, T))
+    return 0;
   return linear_ws(N_seq, B, T, HV, K, V, dt);
 }
 

@@ -827,8 +827,8 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   a.Lseg = x.Lseg;
   a.slices = x.slices;
   a.vt = kVT;
-  if ((int64_t)x.bound * p.HV * x.slices > INT32_MAX - 65536) return cudaErrorInvalidValue;
-  a.items = x.bound * p.HV * x.slices;
+  if (x.bound * p.HV * x.slices > INT32_MAX - 65536) return cudaErrorInvalidValue;
+  a.items = (int)(x.bound * p.HV * x.slices);
   if (a.items == 0) return cudaMemsetAsync(p.status, 0, sizeof(int32_t), p.stream);  // kDevOk
   int2* seqs = nullptr;
   if (p.cu) {

@@ -10,6 +10,9 @@ namespace gdp {
 namespace linear {
 
 constexpr int C = 64;  // tokens per chunk
+// Most tokens and sequences of a call: positions up to a few chunks past the end, and the number of
+// segments, fit an int.
+constexpr int64_t kMostTokens = INT32_MAX - 4095, kMostSeqs = 1 << 30;
 
 // A segment of a sequence: t0 = first row, n = rows, pos0 = tokens of the sequence before it
 // (paged states: its context included), id = its place in the scratch (cut sequences only).
@@ -20,8 +23,9 @@ struct SegRec {
 
 // Segments of a launch and the workspace they need.
 struct Plan {
-  int nseg, Lseg, bound, slices;  // segments per dense sequence, tokens, segments in all at most
-  int slots;                      // segments of cut sequences at most: a state of scratch each
+  int nseg, Lseg, slices;  // segments per dense sequence, tokens of one
+  int64_t bound;           // segments in all at most
+  int slots;               // segments of cut sequences at most: a state of scratch each
   size_t recs, seqs, segS, segW, total;
 };
 // What a kernel's items take, in microseconds: a chunk, a chunk of the state pass, an item's start
@@ -34,6 +38,13 @@ struct Cost {
 // multiples of Lseg positions from that chunk's start.
 GDP_HD inline int segment_count(int off, int n, int Lseg) {
   return n > 0 ? (int)(((int64_t)off + n + Lseg - 1) / Lseg) : 1;
+}
+
+// Rows of segment j of that sequence.
+GDP_HD inline void segment_span(int off, int n, int Lseg, int j, int* lo, int* hi) {
+  const int64_t a = (int64_t)j * Lseg - off, b = a + Lseg;
+  *lo = j == 0 ? 0 : (int)a;
+  *hi = n < b ? n : (int)b;
 }
 
 // Segments at most of the sequences that are cut, of N_seq with T tokens in all. A sequence is cut
@@ -66,14 +77,14 @@ inline Plan plan_of(int N_seq, int B, int T, int HV, int K, int V, bool packed, 
         x.Lseg = (int)per * C;
       }
     }
-    x.bound = B * x.nseg;
-    x.slots = x.nseg > 1 ? x.bound : 0;
+    x.bound = (int64_t)B * x.nseg;
+    x.slots = x.nseg > 1 ? (int)x.bound : 0;
   } else {
     // packed: no more than an SM's share of the whole batch in one item; where a sequence of T tokens
     // fits in one, so it does from any position of a chunk (there is no scratch for a cut then)
     const int64_t share = cdiv(cdiv((int64_t)T * heads, G), C) * C, most = std::max<int64_t>(share, 512);
     x.Lseg = most < T ? (int)most : x.Lseg + C;
-    x.bound = (int)(((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq);
+    x.bound = ((int64_t)T + (int64_t)N_seq * C) / x.Lseg + N_seq;
     x.slots = x.Lseg < T ? (int)std::min<int64_t>(x.bound, cut_bound(N_seq, T, x.Lseg)) : 0;
   }
   x.recs = kAlign;

@@ -91,8 +91,10 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
       if (seqs) seqs[i] = make_int2(slot, cnt);
       const int off = pos % C;
       for (int j = 0; j < cnt; ++j) {
-        const int lo = j == 0 ? 0 : j * Lseg - off, hi = min(n, (j + 1) * Lseg - off);
-        SegRec r{t0 + lo, hi - lo, i, p.pool ? pos + lo : lo, j == 0, j == cnt - 1, slots ? slot + j : 0, 0};
+        int lo, hi;
+        segment_span(off, n, Lseg, j, &lo, &hi);
+        // (a position past 2^31 stays one of 32 bits; chunks and pages count it unsigned)
+        SegRec r{t0 + lo, hi - lo, i, p.pool ? (int)((uint32_t)pos + (uint32_t)lo) : lo, j == 0, j == cnt - 1, slots ? slot + j : 0, 0};
         recs[first + j] = r;
         if (first + j < kSortMax) lens[first + j] = r.n;
       }
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(256, 4) linear_combine_kernel(const __grid_con
 }  // namespace
 
 cudaError_t launch_segments(const LinearProblem& p, const Plan& x, SegRec* recs, int2* seqs, int* split) {
-  return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, x.bound, recs, seqs,
+  return launch_pdl(linear_segments_kernel, dim3(1), dim3(kRecThreads), 0, p.stream, p, x.Lseg, (int)x.bound, recs, seqs,
                     split);
 }
 

@@ -18,6 +18,7 @@ void plan(int N, int B, int T, int HV, int K, int V, int packed, int vt, int G, 
   out[0] = x.nseg, out[1] = x.Lseg, out[2] = x.bound, out[3] = x.segS, out[4] = x.total, out[5] = x.slots;
 }
 int segments(int off, int n, int Lseg) { return segment_count(off, n, Lseg); }
+void span(int off, int n, int Lseg, int j, int* out) { segment_span(off, n, Lseg, j, &out[0], &out[1]); }
 }
 """
 
@@ -96,3 +97,43 @@ def test_many_short_requests_need_little(N, T):
     size = gdp.load().gdp_linear_chunk_fwd_workspace_size
     for dtype in (0, 1, 2):
         assert size(1, T, N, 32, 32, 128, 128, dtype) <= max(50 << 20, T // 256 * (3 << 20))
+
+
+MOST = 2 ** 31 - 4096  # tokens of a chunked call
+
+
+@pytest.mark.parametrize("T", [MOST, MOST - 63, 1_900_000_000, 2 ** 30 + 1])
+@pytest.mark.parametrize("HV,G", [(1, 152), (100, 152), (151, 152), (152, 152), (400, 152)])
+def test_longest_sequences(lib, T, HV, G):
+    """Lengths that fill an int: segments follow one another and end with the sequence."""
+    for packed, off in ((1, 0), (1, 63), (0, 0)):
+        x = plan(lib, 1, 1, T, HV, packed=packed)
+        assert 0 < x["Lseg"] and (x["bound"] - 1) * x["Lseg"] < T + 2 * x["Lseg"]
+        if not packed:
+            assert (x["nseg"] - 1) * x["Lseg"] < T <= x["nseg"] * x["Lseg"]
+            continue
+        n, at = lib.segments(off, T, x["Lseg"]), 0
+        assert n == -(-(off + T) // x["Lseg"]) <= x["bound"] and (n == 1 or n <= x["slots"])
+        for j in range(n):
+            ends = (ctypes.c_int * 2)()
+            lib.span(off, T, x["Lseg"], j, ends)
+            lo, hi = ends
+            assert lo == at and lo < hi <= T
+            at = hi
+        assert at == T
+
+
+def test_many_sequences(lib):
+    """Records are counted in 64 bits."""
+    x = plan(lib, 2 ** 31 - 2, 1, 64, 1)
+    assert x["bound"] > 2 ** 31 and x["total"] > 32 * 2 ** 31
+
+
+@pytest.mark.parametrize("B,T,N,status", [(1, MOST + 1, 1, 2), (1, 2 ** 31 - 1, 1, 2), (1, 64, 2 ** 31 - 2, 2)])
+def test_refused_lengths(B, T, N, status):
+    import linear_attention_ssm_gdp_gb300 as gdp
+    A = ctypes.c_void_p(1 << 20)
+    st = (ctypes.c_int64 * 9)(*[64] * 9)
+    assert gdp.load().gdp_linear_chunk_fwd(A, A, A, st, None, 0, None, A, N, B, T, 1, 1, 32, 32, 1.0, 0, A, None, A,
+                                           1 << 62, None) == status
+    assert gdp.load().gdp_linear_chunk_fwd_workspace_size(B, T, N, 1, 1, 32, 32, 0) == 0

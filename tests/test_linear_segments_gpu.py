@@ -45,3 +45,19 @@ def test_cut_prompts(gdp, K, V, dtype, bs):
 def test_cut_at_a_larger_share(gdp):
     """As many heads as SMs: segments are as long as an SM's share of the batch."""
     check(gdp, [1000, 200], [45, 130], 256, 2, 152, 16, 8, BF)
+
+
+@pytest.mark.parametrize("K,V,dtype", [(64, 128, BF), (48, 32, F32), (64, 64, FP16)])
+@pytest.mark.parametrize("before", [100, 64, 700])
+def test_context_past_31_bits(gdp, K, V, dtype, before):
+    """Positions that pass 2^31, in blocks of 2^30 tokens, through both forms."""
+    ctx, bs, S = 2 ** 31 - before, 2 ** 30, 3
+    check(gdp, [650], [ctx], bs, 1, 2, K, V, dtype)
+    q, k, v, g, _ = inputs(1, S, 1, 2, K, V, dtype, "token")
+    at = 2 ** 31 - 2
+    tables, pool = paged_case([S], [at], bs, 2, K, V)
+    ro, want = paged_reference(q, k, v, g, [0, S], [at], tables, pool, bs, K ** -0.5)
+    got = pool.to(DEV)
+    o = gdp.gdp_linear_recurrent_update_paged(q, k, v, g, got, tables.to(DEV),
+                                              torch.tensor([at], dtype=torch.int32, device=DEV), bs)
+    assert o_ok(o, ro) and err(got, want) <= TOL_S
