@@ -341,9 +341,10 @@ gdp_status gdp_chunk_fwd_noalloc(const void* q, const void* k, const void* v, co
  *   arm = 1: the next gdp_chunk_fwd that runs the 128-position WY kernel
  *            (tensor-core path, even M) leaves out one tensor-core commit in
  *            its first CTA, so that CTA's wait for it runs out; the hook then
- *            disarms itself. arm = 2: the same in the first launch of the next
- *            linear-attention call that runs the tensor-core kernel (bf16,
- *            K <= 128). arm = 0: disarm.
+ *            disarms itself. arm = 2: the next linear-attention call that runs the
+ *            tensor-core kernel (bf16, K <= 128) waits in the first CTA of its
+ *            first launch for one commit more than are made; likewise one-shot.
+ *            arm = 0: disarm.
  *   budget_seconds: new wait budget (0 < budget <= 10), or <= 0 for the
  *            default 2 s. The budget applies to every later launch until
  *            changed.

@@ -109,7 +109,7 @@ cudaError_t launch_recurrent(const void* q, const void* k, const void* v, const 
 
 // Test hook (gdp_debug_wait_fault) of the linear-attention kernel: a wait of its next launch runs
 // out (arm), limit of its waits.
-cudaError_t linear_wait_fault(int arm, unsigned long long budget_ns);
+void linear_wait_fault(int arm, unsigned long long budget_ns);
 
 int sm_count();  // multiprocessors on the current device (cached per device)
 

@@ -158,13 +158,16 @@ __device__ __forceinline__ int chunks_of(const ChunkArgs& a, int it) {
 
 // ------------------------------------------------------------------ waits
 // (The loop is not inlined: it would be a third of the kernel's code.)
+// (The limit stands beside `dead` in shared memory, in units of 1024 ns: read from device memory it cost
+// the packed prompts 4 %.)
+__device__ __forceinline__ bool past_budget(uint64_t ns, volatile int* dead) { return (ns >> 10) > (uint32_t)dead[2]; }
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, int* status) {
   uint64_t t0 = 0;
   while (!mbar_test_for(bar, parity, 20000)) {
     if (*dead) return false;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > wait_budget_ns()) {
+    if (past_budget(t - t0, dead)) {
       if (status) atomicExch(status, kDevTimeout);
       *dead = 1;
       return false;
@@ -195,7 +198,8 @@ __device__ __forceinline__ bool state_and(bool pred) {
 // ------------------------------------------------------------------ shared memory
 struct TcArgs : ChunkArgs {
   int k_halves, v_halves;  // 64-column halves in the boxes of q and k, and of v and o
-  int fault;               // test hook (gdp_debug_wait_fault): CTA 0 leaves out the commit of its first U
+  int budget;              // limit of a wait, in units of 1024 ns
+  int fault;               // test hook (gdp_debug_wait_fault): CTA 0 waits for a commit more of its first U
 };
 
 template <int KD, bool OUT>
@@ -256,10 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
       if (i >= B_FREE && i < B_V) n = OUT ? 2 : 1;                   // both issuing warps
       if (i == B_OREAD || i == B_S || i >= B_UREAD) n = kSW;         // state warps
       if ((i >= B_V && i < B_VFREE) || i == B_P || i == B_P + 1 || i == B_SREAD) n = 4;  // v' or score warps
+      if (i == B_U && a.fault && blockIdx.x == 0) n = 2;
       mbar_init(&bars[i], n);
     }
     fence_mbar_init();
     *s_dead = 0;
+    s_dead[2] = a.budget;
   }
   if (warp == kDecay && lane == 0) {
     prefetch_tmap(&map_k);
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
           mma_bf16_ts(u_at(n), av, k, id_u, 1);
           mma_commit(&bars[B_VFREE + ks]);
           if (ks == 3) {
-            if (!a.fault || n > 0 || blockIdx.x > 0) mma_commit(&bars[B_U + n % NU]);
+            mma_commit(&bars[B_U + n % NU]);
             mma_commit(&bars[B_FREE + n % L::NST]);
           }
         }
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
         if ((++spins & 63) == 0) {  // a bounded wait like the others
           const uint64_t t = globaltimer_ns();
           if (spins == 64) since = t;
-          if (__any_sync(0xffffffffu, *sy.dead || t - since > wait_budget_ns())) {
+          if (__any_sync(0xffffffffu, *sy.dead || past_budget(t - since, sy.dead))) {
             if (lane == 0 && !*sy.dead) {
               if (p.status) atomicExch(p.status, kDevTimeout);
               *sy.dead = 1;
@@ -697,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
     }
     // nothing may still write shared memory when the CTA leaves
     for (int m = max(0, next - L::NST); m < next; ++m) {
-      const uint64_t t0 = globaltimer_ns(), budget = wait_budget_ns();
-      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && globaltimer_ns() - t0 < budget) {}
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_test(&bars[B_FULL + m % L::NST], (m / L::NST) & 1) && !past_budget(globaltimer_ns() - t0, s_dead)) {}
     }
   } else if (OUT) {
     // ---------------------------------------------------------------- INTER, INTRA
@@ -742,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(
 // ------------------------------------------------------------------ host
 // Test hook state (gdp_debug_wait_fault): armed for the next launch only.
 std::atomic<int> g_fault{0};
+std::atomic<unsigned long long> g_budget_ns{kWaitBudgetNs};
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -813,9 +820,9 @@ bool linear_tc_ok(const LinearProblem& p) {
          map_ok(p.v, p.HV, p.T, p.B, p.vs) && reinterpret_cast<uintptr_t>(p.o) % 16 == 0;
 }
 
-cudaError_t linear_wait_fault(int arm, unsigned long long budget_ns) {
+void linear_wait_fault(int arm, unsigned long long budget_ns) {
   g_fault.store(arm);
-  return cudaMemcpyToSymbol(ptx::g_wait_budget_ns, &budget_ns, sizeof(budget_ns));
+  g_budget_ns.store(budget_ns);
 }
 
 cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
@@ -847,6 +854,7 @@ cudaError_t launch_linear_tc(const LinearProblem& p, uint8_t* ws) {
   if (!map5(&m[0], p.q, p.K, a.k_halves, p.H, p.T, p.B, p.qs) || !map5(&m[1], p.k, p.K, a.k_halves, p.H, p.T, p.B, p.ks) ||
       !map5(&m[2], p.v, p.V, a.v_halves, p.HV, p.T, p.B, p.vs) || !map5(&m[3], p.o, p.V, a.v_halves, p.HV, p.T, p.B, os))
     return cudaErrorInvalidValue;
+  a.budget = (int)(g_budget_ns.load() >> 10);
   a.fault = g_fault.exchange(0);
   if (x.segS) {
     a.segS = reinterpret_cast<float*>(ws + x.segS);

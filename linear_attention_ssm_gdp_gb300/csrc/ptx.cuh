@@ -81,16 +81,12 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 constexpr uint64_t kWaitBudgetNs = 2000000000ull;
 static __device__ unsigned long long g_wait_budget_ns = kWaitBudgetNs;
 
-__device__ __forceinline__ uint64_t wait_budget_ns() {
-  return *const_cast<volatile unsigned long long*>(&g_wait_budget_ns);
-}
-
 // Bounded wait for `parity`; on timeout stores `code` into *status (if not
 // null) and returns false.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status, int code) {
   if (mbar_test(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  const uint64_t budget = wait_budget_ns();
+  const uint64_t budget = *const_cast<volatile unsigned long long*>(&g_wait_budget_ns);
   while (true) {
     if (mbar_test(bar, parity)) return true;
     if (globaltimer_ns() - t0 > budget) {

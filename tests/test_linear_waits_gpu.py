@@ -1,4 +1,4 @@
-"""Bounded waits of the linear-attention kernel: a commit left out by the test hook makes one run out;
+"""Bounded waits of the linear-attention kernel: the test hook makes one run out;
 the call returns, its status word says so whichever of the call's launches it was in, and the
 next call is right."""
 import time
