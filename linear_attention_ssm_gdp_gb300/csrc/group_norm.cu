@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
 
 // The same for groups or rows that are not whole vectors: TG lanes read one (sample, group) element
 // by element, three times (the second and third reads come from the first-level cache). A CTA per
-// sample, as below, made 138485 x 6 fp16 in 2 groups 760 us; 19 us.
+// sample, as below, made 138485 x 6 fp16 in 2 groups 760 us; 4.1 us with a lane per group. Groups of 9 to
+// 31 leave lanes idle: 200000 x 160 bf16 in groups of 10 takes 758 us, 128 MB that could be read and
+// written in 19.
 template <typename TX, typename TO, int TG, bool GATE>
 __global__ void __launch_bounds__(256) norm_elements_kernel(const __grid_constant__ NormArgs a) {
   pdl_wait();
@@ -500,8 +502,8 @@ MapPlan plan_map(int64_t N, int64_t L, int G, int Cg, int size, int vec, bool sp
     if (N * m.sets * 8 >= sm_count() && cdiv(L, 8) * m.seg <= 48 * 1024) break;
   }
   // Slices where that still leaves a CTA with much: the same work on more SMs, for a second read of
-  // x and a launch. 1 x 16384 x 128 fp16 in one group: 17.7 us, where a cluster has eight SMs for it;
-  // 2 x 9000 x 512 fp32 in four: 21.4 / 42.9. Sets of several small groups cost more to reduce, so
+  // x and a launch. 1 x 16384 x 128 fp16 in one group: 17.7 us / 71.3 in a cluster of 8;
+  // 2 x 9000 x 512 fp32 in four: 21.4 / 46.5. Sets of several small groups cost more to reduce, so
   // they stay with clusters longer (1 x 16384 x 128, 32 groups: 43 us in slices, 15.3 in clusters).
   const int64_t much = N * m.sets * 8 >= sm_count() ? 96 : m.GS > 1 ? 64 : 32;
   if (split && cdiv(L, 8) * m.seg > much * 1024) {

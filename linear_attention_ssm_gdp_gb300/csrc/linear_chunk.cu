@@ -19,7 +19,8 @@
 // for the same reason. Decay exponents are differences of compensated prefix sums, so
 // a strong decay earlier in the chunk costs no digits.
 //
-// What bounds it: q, k, v, o are 64 KB per chunk and head, 1.5 us of an SM's share of HBM.
+// What bounds it: q, k, v, o are 64 KB per chunk and head, 1.5 us of an SM's share of HBM (36 KB, 0.8
+// us, where eight items of a key head share its q and k through the L2).
 // A product with both operands in shared memory runs at that memory's 128 bytes a clock
 // ((A + B) / 128 cycles, measured), more than the tensor pipe needs, so the operands that
 // are made on chip (S, v') live in tensor memory, where they cost none of it. Nothing in the
@@ -36,7 +37,7 @@
 // them unrolled a third of the warps' time went there, at 80 % of that cache's bandwidth).
 // Measured: 1.8 us a chunk (K = V = 128), 1.2 in the state pass, 9.4 us for a call of one chunk;
 // 2 x 4096 tokens, 16 heads: 70 us with the state pass and the combine kernel. What is left above
-// the 1.5 us is a stage's round trip over its three places: 1.4 us for a load to land, as long
+// the bytes is a stage's round trip over its three places: 1.4 us for a load to land, as long
 // again for v' at the rate that four warps reach beside the others, then U and INTRA. Measured in
 // place of it: four stages with one P buffer, 73 us; a step of v' on the score warps, 72; sixteen
 // state and four output warps at 64 registers, 78 (as eight then were).

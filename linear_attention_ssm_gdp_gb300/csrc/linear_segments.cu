@@ -5,7 +5,7 @@
 // GPU: the state pass of a chunked kernel forms each segment's own U from a zero state, the
 // combine kernel here turns those into the states at the segment starts, and the whole pass then
 // runs over all segments at once. Reading k and v twice costs less than idle SMs: 2 x 4096 tokens of
-// 16 heads (K = V = 128) take 69 us in four segments each, as long as half their tokens would in one.
+// 16 heads (K = V = 128) take 70 us in four segments each, as long as half their tokens would in one.
 #include <algorithm>
 
 #include "linear_chunk.cuh"
@@ -14,9 +14,11 @@ namespace gdp {
 namespace linear {
 namespace {
 
-// Segment records of a packed batch (one CTA): offsets and block tables checked as in
-// linear_records_kernel, each sequence cut at multiples of Lseg positions, records sorted by
-// length, longest first.
+// Segment records of a packed batch (one CTA): each sequence cut at multiples of Lseg positions,
+// records sorted by length, longest first (by counting ranks, so up to kSortMax of them; 6 to
+// 8 us for 16 sequences with their tables).
+// Checked on the way: offsets that decrease or leave [0, T] make every sequence empty; a negative
+// context or a page outside the pool makes that sequence empty; either sets the status.
 constexpr int kRecThreads = 512;
 constexpr int kSortMax = 4096;
 
@@ -132,8 +134,8 @@ __global__ void __launch_bounds__(kRecThreads) linear_segments_kernel(const __gr
 
 // States at the segment starts: S_0 = the sequence's initial state, S_{j+1} = w_j S_j + U_j,
 // in place of the U's. A thread per VEC state elements. A read and a write of the scratch,
-// bound by the trips to memory of eight segments' loads at a time: 9 us for 32 heads of four
-// segments (15 MB). With four at a time a sequence of 37 segments takes 2 us longer.
+// bound by the trips to memory of eight segments' loads at a time: 13 us alone with cold caches for 32
+// heads of four segments (15 MB). With four at a time a sequence of 37 segments takes 2 us longer.
 template <int VEC>
 __global__ void __launch_bounds__(256, 4) linear_combine_kernel(const __grid_constant__ ChunkArgs a, const int2* seqs) {
   pdl_wait();

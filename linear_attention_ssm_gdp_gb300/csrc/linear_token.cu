@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : R <= 16 ? 2 : 1)
     }
   }
   if (p.pool && live && !bad) {
-    // a request that writes a page which another one reads or writes would race with it
+    // a request that writes a page which another one reads or writes would race with it (every CTA
+    // looks at all requests: harmless at 256, 19 us in place of 13 for 8 heads of 64 x 64; 750 in place
+    // of 180 at 4096)
     for (int r = tid; r < p.N_seq && !bad; r += kThreads) {
       const int rc = p.ctx[r];
       if (r == seq || rc < 0) continue;
