@@ -122,14 +122,21 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const __grid_constant__ 
   // Distances from the mean without its rounding, which a group of equal or close values would show:
   // z = (n x - sum x) / (n std), with n scaled by a power of two (a.nn, below 1) so that nothing
   // overflows that did not, is one exact multiply-add where the sum is exact. It is for 16-bit values
-  // of one size (n is at most 1024 here); 32-bit ones are taken from the group's first, which
-  // makes the differences of close values exact, and costs others at most sqrt(n) 2^-24 of a std.
+  // of one size (n is at most 1024 here); 32-bit ones are taken from one of the group's, which makes
+  // the differences of close values exact: the middle one of three, since an outlier k stds away would
+  // cost the others k 2^-24 of a std.
   constexpr bool kPivot = sizeof(TX) == 4;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t n = n0 + u * Nu;
     float f[NV][VEC], s = 0.f;
-    const float x0 = kPivot ? __shfl_sync(0xffffffffu, to_f(x[u][0].e[0]), 0, TG) : 0.f;
+    float x0 = 0.f;
+    if (kPivot) {
+      const float p0 = __shfl_sync(0xffffffffu, to_f(x[u][0].e[0]), 0, TG);
+      const float p1 = __shfl_sync(0xffffffffu, to_f(x[u][0].e[VEC - 1]), 0, TG);
+      const float p2 = __shfl_sync(0xffffffffu, to_f(x[u][0].e[1]), min(TG, nvec) - 1, TG);
+      x0 = fmaxf(fminf(p0, p1), fminf(fmaxf(p0, p1), p2));
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll

@@ -36,3 +36,17 @@ def test_a_few_ulps_apart(gdp, N, L, C, G):
     y = gdp.gdp_group_norm(x, G, activation="none")
     ref = norm_reference(x, G, None, None, None, 1e-5, "none")
     assert ((y.double().cpu() - ref).abs() <= 1e-5 * ref.pow(2).mean().sqrt()).all()
+
+
+@pytest.mark.parametrize("N,L,C,G", SIZES + [(300, 1, 2864, 4), (300, 1, 4000, 4), (2000, 1, 1000, 1), (3000, 1, 896, 1)])
+@pytest.mark.parametrize("at", ["first", "second", "last"])
+def test_an_outlier_costs_the_others_nothing(gdp, N, L, C, G, at):
+    """One value 1000 times the others': sums and distances round to a few 2^-24 of the outlier's
+    sqrt(n) stds or of the value itself, 1e-6 of it; the others are held to 4e-6, a few dozen 2^-24."""
+    x = torch.randn(N, L, G, C // G, generator=torch.Generator().manual_seed(L + C))
+    l, c = {"first": (0, 0), "second": (0, 1), "last": (L - 1, C // G - 1)}[at]
+    x[:, l, :, c] *= 1000.0
+    x = x.reshape(N, L, C).to(DEV)
+    ref = norm_reference(x, G, None, None, None, 1e-5, "none")
+    y = gdp.gdp_group_norm(x, G, activation="none").double().cpu()
+    assert ((y - ref).abs() <= 1e-6 * ref.abs() + 4e-6 * ref.pow(2).mean().sqrt()).all()
