@@ -517,6 +517,128 @@ gdp_status gdp_group_norm_ws(const void* x, int64_t x_sn, int64_t x_sl, const vo
                              gdp_activation activation, gdp_dtype dt, gdp_dtype dt_out, void* y,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Attention layers beside the linear ones: position rotation, a paged cache of keys
+ * and values, and attention over it. Positions and slots are those of gdp_block_plan.
+ */
+typedef enum gdp_rotary_scaling {
+  GDP_ROTARY_NONE = 0,
+  GDP_ROTARY_LINEAR = 1,
+  GDP_ROTARY_RAMP = 2,
+  GDP_ROTARY_WAVELENGTH = 3
+} gdp_rotary_scaling;
+
+/*
+ * gdp_rotary_frequencies - the angles per position of the rotary_dim / 2 pairs, and the
+ * amplitude of the rotation. Host arithmetic in fp64: `frequencies` [rotary_dim / 2] and
+ * `amplitude` (nullable) are HOST pointers. With f_i = base^(-2 i / rotary_dim):
+ *   NONE        f_i
+ *   LINEAR      f_i / factor
+ *   RAMP        t_i f_i / factor + (1 - t_i) f_i, t_i rising from 0 to 1 between the pairs
+ *               that turn `high` times within original_length positions and those that
+ *               turn `low` times (rounded down and up to whole pairs); amplitude
+ *               0.1 ln(factor) + 1 for a factor above 1
+ *   WAVELENGTH  the same two with a share of f_i of (r_i - low) / (high - low), held to
+ *               [0, 1], where r_i = original_length f_i / 2 pi are the pair's turns
+ * The amplitude is 1 elsewhere. low < high; both and original_length only for the last two.
+ * Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED (scaling).
+ */
+gdp_status gdp_rotary_frequencies(int rotary_dim, double base, gdp_rotary_scaling scaling,
+                                  double factor, double original_length, double low, double high,
+                                  double* frequencies, double* amplitude);
+
+/*
+ * gdp_rotary - turns the pairs of the elements [offset, offset + rotary_dim) of every head:
+ *     (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),  t = position * frequency_i
+ * with pair i = elements (i, i + rotary_dim / 2), or neighbours (2 i, 2 i + 1) where
+ * `interleaved`. The head's other elements are copied. `backward` != 0 turns by -t: the
+ * gradient of x from y's.
+ *   x, y    [B, T, H, D] in dtype `dt`, the last dimension contiguous; x_strides and
+ *           y_strides are HOST arrays of three element strides (batch, token, head).
+ *           y is x with the same strides (in place), or does not overlap it.
+ *   positions [B, T] int32, any value; frequencies [rotary_dim / 2] fp64, finite, on the
+ *           device. Angles are exact to 2^-52 of a frequency times the position.
+ * D <= 1024. Sums are fp32, rounded once.
+ * Errors: GDP_ERR_INVALID_ARG (sizes, an odd rotary_dim, a part outside the head, an
+ * amplitude that is not finite), GDP_ERR_UNSUPPORTED (dtype, D), GDP_ERR_CUDA.
+ */
+gdp_status gdp_rotary(const void* x, const int64_t* x_strides, const int32_t* positions,
+                      const double* frequencies, int rotary_dim, int offset, int interleaved,
+                      float amplitude, int backward, int B, int T, int H, int D, gdp_dtype dt,
+                      void* y, const int64_t* y_strides, cudaStream_t stream);
+
+/*
+ * gdp_cache_append - writes the keys and values of new tokens into a paged cache, the keys
+ * rotated as by gdp_rotary on the way, and rotates the queries in the same launch.
+ *   k [B, T, HKV, D], v [B, T, HKV, DV], q [B, T, H, D] (nullable: none) in dtype `dt`,
+ *           the last dimension contiguous; `strides`: a HOST array of nine element strides
+ *           (batch, token, head) of q, of k and of v.
+ *   positions, frequencies, rotary_dim, offset, interleaved, amplitude: as gdp_rotary;
+ *           rotary_dim 0: no rotation (both may be NULL).
+ *   slot_map [B, T] int64: a token's slot page * block_size + place; -1: not kept. A slot
+ *           outside the cache is treated so too and sets *status (nullable int32 on the
+ *           device; not cleared) to 1. The slots that are kept must differ: where two tokens
+ *           name one, it holds parts of either.
+ *   k_cache [n_pages, block_size, HKV, D], v_cache [n_pages, block_size, HKV, DV]: dtype
+ *           `dt`, the last dimension contiguous; k_cache_strides and v_cache_strides: HOST
+ *           arrays of three element strides (page, place, head), so views of one buffer and
+ *           head-major pages go in as they are. Other slots are left as they are.
+ *   q_out   [B, T, H, D] contiguous; q itself where that is contiguous.
+ * D, DV <= 1024. Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED (dtype, sizes),
+ * GDP_ERR_CUDA.
+ */
+gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                            const int32_t* positions, const double* frequencies, int rotary_dim,
+                            int offset, int interleaved, float amplitude, int B, int T, int H,
+                            int HKV, int D, int DV, gdp_dtype dt, const int64_t* slot_map,
+                            void* k_cache, const int64_t* k_cache_strides, void* v_cache,
+                            const int64_t* v_cache_strides, int n_pages, int block_size,
+                            void* q_out, int32_t* status, cudaStream_t stream);
+
+/*
+ * gdp_attention_paged - attention of new tokens over a paged cache that holds them already
+ * (gdp_cache_append), softmax(scale q K^T) V: single tokens of a decode step, trees of
+ * drafted tokens, or pieces of prompts.
+ *   q       [B, T, H, D], the last dimension contiguous, q_strides (batch, token, head).
+ *           cu_seqlens (nullable) int32 [N_seq + 1] on the device packs the tokens of
+ *           N_seq requests along T (B == 1); without it N_seq == B requests have T tokens
+ *           each. Query head h reads key head h / (H / HKV).
+ *   caches  as in gdp_cache_append. block_tables [N_seq, max_blocks] int32 names the page of
+ *           each block of block_size positions; -1: the block is not there (none of its
+ *           positions is seen), which also makes padding requests, whose o rows are 0.
+ *   context_lens [N_seq] int32: positions before the request's first new token, which is
+ *           position context_lens[r] of the cache, the next one the position after it.
+ *   tree_mask (nullable) [B, T] int64: bit j of a token: it sees the request's new token j
+ *           (its ancestors in the tree, and itself), beside the whole context; requests of
+ *           at most 64 tokens. NULL: every token sees the new ones up to itself.
+ * Output: o [B, T, H, DV] contiguous, dtype `dt`; a row that sees nothing is 0. Sums and the
+ * softmax's statistics are fp32; 16-bit types round its weights to the type (relative to a
+ * maximum that is at most 2^8 too small) before the product with V.
+ * Refused on the device: a page number of n_pages or more (the block is not there, as for
+ * -1), a negative context, one that its table is too short for, more than 64 tokens with a
+ * tree_mask (the request's o rows are 0): these set *status (nullable int32, not cleared) to
+ * 1. So does a list of offsets that decreases, starts above 0 or ends past T; o is left as it
+ * was then. 2: a bounded wait on the device ran out. Rows of o past cu_seqlens[N_seq] are
+ * left as they were.
+ * Keys and values that are not finite at positions which a request does not have are not
+ * read; one of a new token's values may also reach tokens of the request that do not see
+ * it (0 times infinity is not 0).
+ * workspace: at least gdp_attention_paged_workspace_size() bytes, 256-byte aligned; calls
+ * that share one must not overlap on the GPU.
+ * D, DV <= 256, max_blocks * block_size below 2^31 - 65536.
+ * Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED, GDP_ERR_WORKSPACE, GDP_ERR_CUDA.
+ */
+size_t gdp_attention_paged_workspace_size(int B, int T, int N_seq, int H, int HKV, int D, int DV,
+                                          gdp_dtype dt);
+gdp_status gdp_attention_paged(const void* q, const int64_t* q_strides, const void* k_cache,
+                               const int64_t* k_cache_strides, const void* v_cache,
+                               const int64_t* v_cache_strides, int n_pages, int block_size,
+                               const int32_t* block_tables, int max_blocks,
+                               const int32_t* context_lens, const int32_t* cu_seqlens, int N_seq,
+                               const int64_t* tree_mask, int B, int T, int H, int HKV, int D,
+                               int DV, float scale, gdp_dtype dt, void* o, int32_t* status,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Number of stage-boundary events gdp_set_stage_events takes. */
 #define GDP_STAGE_EVENTS 5
 

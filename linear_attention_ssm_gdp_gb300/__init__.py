@@ -27,6 +27,8 @@ __all__ = [
     "gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged", "gdp_linear_chunk_fwd_workspace_size",
     "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged", "gdp_block_plan",
     "gdp_group_norm", "gdp_group_norm_workspace_size",
+    "gdp_rotary_frequencies", "gdp_rotary", "gdp_cache_append", "gdp_attention_paged",
+    "gdp_attention_paged_workspace_size",
     "LIB_PATH",
 ]
 
@@ -89,9 +91,20 @@ def load() -> ctypes.CDLL:
             lib.gdp_group_norm_ws.argtypes = lib.gdp_group_norm.argtypes[:-1] + [P, SZ, P]
             lib.gdp_group_norm_workspace_size.argtypes = [I64, I64, I, I, I]
             lib.gdp_group_norm_workspace_size.restype = SZ
+            D = ctypes.c_double
+            lib.gdp_rotary_frequencies.argtypes = [I, D, I] + [D] * 4 + [P, P]
+            lib.gdp_rotary.argtypes = [P] * 4 + [I] * 3 + [F] + [I] * 6 + [P] * 3
+            lib.gdp_cache_append.argtypes = ([P] * 6 + [I] * 3 + [F] + [I] * 7 + [P] * 5 + [I, I]
+                                             + [P] * 3)
+            lib.gdp_attention_paged.argtypes = ([P] * 6 + [I, I, P, I, P, P, I, P] + [I] * 6
+                                                + [F, I, P, P, P, SZ, P])
+            lib.gdp_attention_paged_workspace_size.argtypes = [I] * 8
+            lib.gdp_attention_paged_workspace_size.restype = SZ
             for f in ("gdp_linear_chunk_fwd", "gdp_linear_chunk_fwd_paged",
                       "gdp_linear_recurrent_update", "gdp_linear_recurrent_update_paged",
-                      "gdp_block_plan", "gdp_group_norm", "gdp_group_norm_ws"):
+                      "gdp_block_plan", "gdp_group_norm", "gdp_group_norm_ws",
+                      "gdp_rotary_frequencies", "gdp_rotary", "gdp_cache_append",
+                      "gdp_attention_paged"):
                 getattr(lib, f).restype = I
             lib.gdp_read_status.argtypes = [P, P]
             lib.gdp_debug_wait_fault.argtypes = [I, ctypes.c_double]
@@ -403,11 +416,11 @@ def gdp_recurrent_update_slots(q, k, v, beta, g, state_pool, state_slot, scale=N
 
 def gdp_debug_wait_fault(arm: bool | int, budget_seconds: float = 0.0):
     """Test hook (off by default): arm a one-shot missing tensor-core commit in the
-    next 128-position WY launch (True) or the next tensor-core launch of linear
-    attention (2) so that one bounded device wait runs out, and/or set the wait budget
-    (<= 0: the default 2 s)."""
-    _check("gdp_debug_wait_fault", load().gdp_debug_wait_fault(2 if arm == 2 else 1 if arm else 0,
-                                                                float(budget_seconds)))
+    next 128-position WY launch (True) or the next tensor-core launch of linear attention
+    (2) so that one bounded device wait runs out, and/or set
+    the wait budget (<= 0: the default 2 s)."""
+    code = 2 if arm == 2 else 1 if arm else 0
+    _check("gdp_debug_wait_fault", load().gdp_debug_wait_fault(code, float(budget_seconds)))
 
 
 def _conv_common(xp, conv_w, conv_b, ba, A_log, dt_bias, M, H, G, P, N):
@@ -781,4 +794,209 @@ def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: f
                                       _raw_stream(x))
     if st:
         _check("gdp_group_norm", st)
+    return out
+
+
+# ----------------------------------------------------------------------------------
+# attention layers: position rotation, a paged cache, attention over it
+# ----------------------------------------------------------------------------------
+
+_pack3 = struct.Struct("3q").pack
+_SCALING = {"none": 0, "linear": 1, "ramp": 2, "wavelength": 3}
+
+
+def gdp_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                           factor: float = 1.0, original_length: float = 0.0,
+                           low: float = 1.0, high: float = 32.0, device="cuda"):
+    """Angles per position of a rotation's rotary_dim / 2 pairs, base^(-2 i / rotary_dim),
+    or scaled for long contexts: "linear" (all divided by factor), "ramp" (pairs that turn
+    at most ``low`` times within original_length positions divided, those that turn
+    ``high`` times or more kept, between them a ramp over the pairs; amplitude
+    0.1 ln(factor) + 1), "wavelength" (the same by the pairs' own turns, amplitude 1). Host
+    arithmetic in fp64. Returns (frequencies [rotary_dim / 2] fp64 on ``device``, amplitude)."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    f = (ctypes.c_double * max(rotary_dim // 2, 1))()
+    amplitude = ctypes.c_double()
+    _check("gdp_rotary_frequencies",
+           load().gdp_rotary_frequencies(rotary_dim, base, _SCALING[scaling], factor,
+                                         original_length, low, high, f,
+                                         ctypes.byref(amplitude)))
+    return (torch.tensor(f[:rotary_dim // 2], dtype=torch.float64, device=device),
+            amplitude.value)
+
+
+def _heads(name, t, dtype):
+    """[T, H, D] or [B, T, H, D] as (B, T, H, D, three strides)."""
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda:
+        raise ValueError("libgdp works on CUDA tensors only")
+    if t.dtype != dtype or len(shape) not in (3, 4) or (stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be [T, H, D] or [B, T, H, D] in one dtype of "
+                         "{bf16, fp16, fp32} with a contiguous last dimension")
+    if len(shape) == 3:
+        return 1, *shape, (0, stride[0], stride[1])
+    return *shape, stride[:3]
+
+
+def _rotation(lead, positions, frequencies, D, offset):
+    """Checks of a rotation's arguments: (positions, frequencies, rotary_dim)."""
+    if frequencies is None:
+        return None, None, 0
+    if frequencies.dtype != torch.float64 or frequencies.dim() != 1 \
+            or not frequencies.is_contiguous() or not frequencies.is_cuda:
+        raise ValueError("frequencies must be a contiguous fp64 CUDA tensor [rotary_dim / 2]")
+    if positions is None or positions.dtype != torch.int32 or not positions.is_cuda \
+            or positions.shape != lead or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous int32 CUDA tensor {list(lead)}")
+    R = 2 * frequencies.numel()
+    if offset < 0 or offset + R > D:
+        raise ValueError("the rotated part must lie inside the head")
+    return positions.data_ptr(), frequencies.data_ptr(), R
+
+
+def gdp_rotary(x, positions, frequencies, offset: int = 0, interleaved: bool = False,
+               amplitude: float = 1.0, backward: bool = False, out=None):
+    """Position rotation of heads: x [T, H, D] or [B, T, H, D] (rows may be strided),
+    positions [T] or [B, T] int32, frequencies [R / 2] fp64 (gdp_rotary_frequencies). Pair i
+    of the elements [offset, offset + R), (i, i + R / 2) or neighbours (2 i, 2 i + 1) where
+    ``interleaved``, turns by position * frequency; ``backward`` turns back (the gradient's
+    pass, or undoing). ``out``: contiguous, or x itself. Returns y in x's dtype."""
+    if x.dtype not in _DTYPE or frequencies is None:
+        raise ValueError("x must be bf16, fp16 or fp32, with frequencies")
+    B, T, H, D, xs = _heads("x", x, x.dtype)
+    pos, freq, R = _rotation(x.shape[:-2], positions, frequencies, D, offset)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out is not x:
+        _out_ok(out, x.shape, x.dtype)
+    ys = xs if out is x else (T * H * D, H * D, D)
+    st = load().gdp_rotary(x.data_ptr(), _pack3(*xs), pos, freq, R, offset, interleaved, amplitude,
+                           backward, B, T, H, D, _DTYPE[x.dtype], out.data_ptr(), _pack3(*ys),
+                           _raw_stream(x))
+    if st:
+        _check("gdp_rotary", st)
+    return out
+
+
+def _cache_ok(k_cache, v_cache, dtype):
+    """Caches [n_pages, block_size, HKV, D]: (n_pages, block_size, HKV, D, DV)."""
+    for t in (k_cache, v_cache):
+        if not t.is_cuda:
+            raise ValueError("libgdp works on CUDA tensors only")
+        if t.dtype != dtype or t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+            raise ValueError("caches must be [n_pages, block_size, HKV, D] in q, k, v's dtype with "
+                             "a contiguous last dimension")
+    if k_cache.shape[:3] != v_cache.shape[:3]:
+        raise ValueError("the caches must have the same pages, block size and heads")
+    return *k_cache.shape, v_cache.shape[3]
+
+
+def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequencies=None,
+                     offset: int = 0, interleaved: bool = False, amplitude: float = 1.0, q=None,
+                     q_out=None, status=None):
+    """Writes new tokens' keys and values into a paged cache, the keys (and ``q``, in the same
+    launch) rotated as by gdp_rotary on the way; without frequencies nothing is rotated.
+
+    k [T, HKV, D], v [T, HKV, DV], q [T, H, D] or None (or with a batch dimension in front;
+    rows may be strided), k_cache [n_pages, block_size, HKV, D] and v_cache [n_pages,
+    block_size, HKV, DV] with any strides of the first three dimensions, slot_map [T] int64
+    and positions [T] int32 as gdp_block_plan gives them (-1: not kept). ``status`` (optional
+    int32 device tensor) is set to 1 by a slot outside the cache, which is not kept either.
+    Slots must differ. Returns the rotated q (None without one)."""
+    dt = k.dtype
+    if dt not in _DTYPE:
+        raise ValueError("k, v and q must be bf16, fp16 or fp32")
+    B, T, HKV, D, ks = _heads("k", k, dt)
+    vB, vT, vH, DV, vs = _heads("v", v, dt)
+    pages, block, cH, cD, cDV = _cache_ok(k_cache, v_cache, dt)
+    if v.shape[:-1] != k.shape[:-1] or (cH, cD, cDV) != (HKV, D, DV):
+        raise ValueError("k and v must have the same tokens and the caches' heads")
+    lead = k.shape[:-2]
+    if slot_map.dtype != torch.int64 or slot_map.shape != lead or not slot_map.is_contiguous() \
+            or not slot_map.is_cuda:
+        raise ValueError(f"slot_map must be a contiguous int64 CUDA tensor {list(lead)}")
+    _status_ok(status)
+    pos, freq, R = _rotation(lead, positions, frequencies, D, offset)
+    H, qs = 0, (0, 0, 0)
+    if q is not None:
+        _, _, H, qD, qs = _heads("q", q, dt)
+        if q.shape[:-2] != lead or qD != D:
+            raise ValueError("q must have k's tokens and head size")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        else:
+            _out_ok(q_out, q.shape, dt)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = load().gdp_cache_append(
+        _a(q), k.data_ptr(), v.data_ptr(), _pack_strides(*qs, *ks, *vs), pos, freq, R, offset,
+        interleaved, amplitude, B, T, H, HKV, D, DV, _DTYPE[dt], slot_map.data_ptr(),
+        k_cache.data_ptr(), _pack3(*k_cache.stride()[:3]), v_cache.data_ptr(),
+        _pack3(*v_cache.stride()[:3]), pages, block, _a(q_out), _a(status), _raw_stream(k))
+    if st:
+        _check("gdp_cache_append", st)
+    return q_out
+
+
+@functools.lru_cache(maxsize=256)
+def gdp_attention_paged_workspace_size(B, T, N_seq, H, HKV, D, DV, dtype) -> int:
+    return int(load().gdp_attention_paged_workspace_size(B, T, N_seq, H, HKV, D, DV,
+                                                         _DTYPE[dtype]))
+
+
+def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens=None,
+                        tree_mask=None, scale: float | None = None, workspace=None, out=None,
+                        status=None):
+    """Attention of new tokens over a paged cache that holds them already (gdp_cache_append):
+    single tokens, trees of drafted tokens, or pieces of prompts.
+
+    q [B, T, H, D] (rows may be strided): T new tokens for each of B requests, or with
+    cu_seqlens [n+1] int32 on the device the tokens of n requests packed along T (B must be
+    1). k_cache [n_pages, block_size, HKV, D], v_cache [n_pages, block_size, HKV, DV],
+    block_tables [n, max_blocks] int32 (-1: not there), context_lens [n] int32: tokens before
+    the new ones. tree_mask [B, T] int64: bit j of a token set where it sees its request's new
+    token j (at most 64 tokens a request); without it each sees the new ones up to itself.
+    ``scale`` defaults to D**-0.5. ``status`` (optional int32 device tensor) is set to 1 by
+    bad pages, contexts or offsets and to 2 where a wait on the device ran out; it is not
+    cleared. Returns o [B, T, H, DV] in q's dtype; rows that see nothing are 0."""
+    dt = q.dtype
+    if dt not in _DTYPE or q.dim() != 4:
+        raise ValueError("q must be [B, T, H, D] in bf16, fp16 or fp32")
+    B, T, H, D, qs = _heads("q", q, dt)
+    pages, block, HKV, cD, DV = _cache_ok(k_cache, v_cache, dt)
+    if cD != D:
+        raise ValueError("q and k_cache must have the same head size")
+    n = B if cu_seqlens is None else _packed(cu_seqlens, B)
+    if not (block_tables.is_cuda and context_lens.is_cuda):
+        raise ValueError("libgdp works on CUDA tensors only")
+    if (block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.shape != (n,)
+            or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or not block_tables.is_contiguous() or not context_lens.is_contiguous()):
+        raise ValueError("block_tables must be int32 [n, max_blocks] and context_lens int32 [n]")
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int64 or tree_mask.shape != (B, T) \
+                or not tree_mask.is_contiguous() or not tree_mask.is_cuda:
+            raise ValueError("tree_mask must be a contiguous int64 CUDA tensor [B, T]")
+        if cu_seqlens is None and T > 64:
+            raise ValueError("a tree has at most 64 tokens")
+    _status_ok(status)
+    shape = (B, T, H, DV)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    else:
+        _out_ok(out, shape, dt)
+    if workspace is None:
+        need = gdp_attention_paged_workspace_size(B, T, n, H, HKV, D, DV, dt)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    else:
+        _need_cuda(workspace)
+    st = load().gdp_attention_paged(
+        q.data_ptr(), _pack3(*qs), k_cache.data_ptr(), _pack3(*k_cache.stride()[:3]),
+        v_cache.data_ptr(), _pack3(*v_cache.stride()[:3]), pages, block, block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), _a(cu_seqlens), n, _a(tree_mask), B, T, H,
+        HKV, D, DV, D ** -0.5 if scale is None else scale, _DTYPE[dt], out.data_ptr(), _a(status),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(q))
+    if st:
+        _check("gdp_attention_paged", st)
     return out

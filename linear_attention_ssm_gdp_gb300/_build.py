@@ -38,6 +38,8 @@ UNITS = {
     "linear_token.cu": [],
     "block_plan.cu": [],
     "group_norm.cu": [],
+    "rotary.cu": [],
+    "attention.cu": [],
 }
 
 

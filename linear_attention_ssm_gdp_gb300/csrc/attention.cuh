@@ -1,0 +1,280 @@
+// Shared by the kernels of attention over a paged cache: the problem, and how its work is cut.
+//
+// An item is a tile of BM rows (a row: a token and one of the G query heads that share a key head)
+// of one request and key head, and costs as many units as it has tiles of KT keys to see. The units
+// of all items in order are cut into equal shares, one per CTA, so that a long context is spread
+// over many CTAs and a batch of ragged ones ends evenly; contexts are known on the device only, so
+// every CTA adds up the requests' units by itself and finds the start of its share. A share covers
+// whole items and at most two cut ones (its first and its last piece). Pieces of cut items leave
+// their row maxima, sums and unnormalised outputs in the workspace, and the combine kernel joins
+// them in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gdp_internal.cuh"
+
+namespace gdp {
+namespace attn {
+
+struct Problem {
+  const void* q;
+  int64_t qs[3];                  // batch, token, head
+  const void *k, *v;              // caches
+  int64_t ks[3], vs[3];           // page, token, head
+  int n_pages, block;
+  const int32_t* tables;          // [n, width]
+  int width;
+  const int32_t* ctx;             // [n]
+  const int32_t* cu;              // null: n == B requests of T tokens
+  int n, B, T, H, HKV, G, D, DV;
+  const int64_t* tree;            // [B, T] or null: a chain
+  float c;                        // scale log2 e
+  gdp_dtype dt;
+  void* o;                        // [B, T, H, DV]
+  int32_t* status;                // may be null
+  cudaStream_t stream;
+};
+
+// A cut item's record, in the entry of the CTA where it begins.
+struct Rec {
+  long long first;                // the request's first row of tokens in [B T]
+  int row0, rows, head, more;     // rows == 0: none; more: CTAs after this one that hold pieces
+};
+
+struct Args {
+  Problem p;
+  Rec* recs;                      // [ctas]
+  float* part;                    // [ctas][2][cap][dvp] outputs
+  float2* ml;                     // [ctas][2][cap] row maximum (log2) and sum
+  int ctas, cap, dvp;             // cap: rows of a piece that are kept
+  int least;                      // units that a CTA takes at least
+};
+
+struct Layout {
+  size_t recs, ml, part, total;
+  int cap, dvp;
+};
+inline Layout layout(int ctas, int64_t rows, int bm, int DV) {
+  Layout x;
+  x.cap = (int)(rows < bm ? rows : bm);
+  x.dvp = (DV + 3) / 4 * 4;
+  x.recs = 0;
+  x.ml = align_up(sizeof(Rec) * (size_t)ctas);
+  x.part = align_up(x.ml + sizeof(float2) * 2 * (size_t)ctas * x.cap);
+  x.total = align_up(x.part + sizeof(float) * 2 * (size_t)ctas * x.cap * x.dvp);
+  return x;
+}
+
+// What the rows of one request are; L == 0: nothing to see (an invalid request, whose rows are 0).
+struct Req {
+  int S, ctx;
+  bool ok;
+};
+__device__ __forceinline__ Req request(const Problem& p, int r) {
+  Req x;
+  x.S = p.cu ? p.cu[r + 1] - p.cu[r] : p.T;
+  x.ctx = p.ctx[r];
+  x.ok = x.ctx >= 0 && (int64_t)x.ctx + x.S <= (int64_t)p.width * p.block && !(p.tree && x.S > 64);
+  return x;
+}
+__device__ __forceinline__ int64_t first_row(const Problem& p, int r) {
+  return p.cu ? p.cu[r] : (int64_t)r * p.T;
+}
+
+template <int BM, int KT>
+struct Cut {
+  __device__ static __forceinline__ int tiles(const Problem& p, int S) { return (int)(((int64_t)S * p.G + BM - 1) / BM); }
+  // keys that the rows of a tile see at most
+  __device__ static __forceinline__ int keys(const Problem& p, const Req& x, int tile) {
+    if (!x.ok) return 0;
+    if (p.tree) return x.ctx + x.S;
+    const int64_t last = min((int64_t)(tile + 1) * BM, (int64_t)x.S * p.G) - 1;
+    return x.ctx + (int)(last / p.G) + 1;
+  }
+  __device__ static __forceinline__ int units(int keys) { return keys > 0 ? (keys + KT - 1) / KT : 1; }
+  __device__ static __forceinline__ int64_t request_units(const Problem& p, int r) {
+    const Req x = request(p, r);
+    if (x.S <= 0) return 0;
+    const int n = tiles(p, x.S);
+    int64_t u = 0;
+    for (int i = 0; i < n; ++i) u += units(keys(p, x, i));
+    return u * p.HKV;
+  }
+};
+
+// Where a CTA's share begins, and its length.
+struct Start {
+  int r, head, tile, j;
+  long long left, total, ctas;
+  long long at;  // absolute unit
+  int bad;
+};
+
+// By all NT threads of the CTA. (64-bit sums: requests times heads times tiles may pass 2^31.)
+template <int BM, int KT, int NT>
+__device__ __forceinline__ void find_start(const Args& a, Start* out, long long* scratch /* [NT / 32 + 1] */) {
+  const Problem& p = a.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.n + NT - 1) / NT;
+  const int r0 = (int)min((int64_t)tid * per, (int64_t)p.n), r1 = min(r0 + per, p.n);
+  long long mine = 0;
+  int bad = 0, odd = 0;
+  for (int r = r0; r < r1; ++r) {
+    if (p.cu) {
+      const int a0 = p.cu[r], a1 = p.cu[r + 1];
+      if (a0 < 0 || a1 < a0 || a1 > p.T || (r == 0 && a0 != 0)) { bad = 1; break; }
+    }
+    if (!request(p, r).ok) odd = 1;
+    mine += Cut<BM, KT>::request_units(p, r);
+  }
+  if (blockIdx.x == 0 && (odd || bad) && p.status) *p.status = GDP_ERR_INVALID_ARG;
+  bad = __syncthreads_or(bad);
+  long long sum = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) scratch[warp] = sum;
+  if (tid == 0) { out->bad = bad; out->left = 0; }
+  __syncthreads();
+  long long before = sum - mine, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const long long ctas = min((long long)a.ctas, (total + a.least - 1) / a.least);
+  if (tid == 0) { out->total = total; out->ctas = ctas; }
+  if (!bad && total > 0 && blockIdx.x < ctas) {
+    const long long u0 = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
+    const long long u1 = total / ctas * (blockIdx.x + 1) + total % ctas * (blockIdx.x + 1) / ctas;
+    if (before <= u0 && u0 < before + mine) {  // the thread whose requests hold the start
+      long long at = u0 - before;
+      int r = r0;
+      for (;; ++r) {
+        const long long u = Cut<BM, KT>::request_units(p, r);
+        if (at < u) break;
+        at -= u;
+      }
+      const Req x = request(p, r);
+      const long long per_head = Cut<BM, KT>::request_units(p, r) / p.HKV;
+      out->head = (int)(at / per_head);
+      at %= per_head;
+      int tile = 0;
+      for (;; ++tile) {
+        const int u = Cut<BM, KT>::units(Cut<BM, KT>::keys(p, x, tile));
+        if (at < u) break;
+        at -= u;
+      }
+      out->r = r;
+      out->tile = tile;
+      out->j = (int)at;
+      out->left = u1 - u0;
+      out->at = u0;
+    }
+  }
+  __syncthreads();
+}
+
+// First unit of CTA c's share is floor(total c / ctas), so the last CTA with a unit before `end` is
+// ceil(end ctas / total) - 1.
+__device__ __forceinline__ int last_cta(long long end, long long ctas, long long total) {
+  return (int)((end * ctas + total - 1) / total) - 1;
+}
+
+// One piece of an item, and the walk over the pieces of a share.
+struct Piece {
+  Req x;
+  int64_t first;       // the request's first row in [B T]
+  int r, head, tile;
+  int row0, rows;      // rows of the request's S G that the tile holds
+  int keys;            // that the tile sees
+  int j0, j1, units;   // key tiles of this piece, of the item
+  int slot;            // of the partial results; -1: the item is whole
+};
+
+template <int BM, int KT>
+struct Walk {
+  int r, head, tile, j;
+  long long left, at;
+  bool fresh;
+  __device__ __forceinline__ explicit Walk(const Start& s)
+      : r(s.r), head(s.head), tile(s.tile), j(s.j), left(s.left), at(s.at), fresh(true) {}
+  __device__ __forceinline__ bool next(const Problem& p, Piece& x) {
+    if (left <= 0) return false;
+    x.x = request(p, r);
+    while (x.x.S <= 0) x.x = request(p, ++r);  // (units are left, so there is one)
+    x.first = first_row(p, r);
+    x.r = r;
+    x.head = head;
+    x.tile = tile;
+    x.row0 = tile * BM;
+    x.rows = (int)min((int64_t)BM, (int64_t)x.x.S * p.G - x.row0);
+    x.keys = Cut<BM, KT>::keys(p, x.x, tile);
+    x.units = Cut<BM, KT>::units(x.keys);
+    x.j0 = j;
+    x.j1 = (int)min((long long)x.units, j + left);
+    x.slot = j == 0 && x.j1 == x.units ? -1 : j == 0 ? 1 : 0;
+    left -= x.j1 - j;
+    at += x.j1 - j;
+    j = 0;
+    if (++tile == Cut<BM, KT>::tiles(p, x.x.S)) {
+      tile = 0;
+      if (++head == p.HKV) { head = 0; ++r; }
+    }
+    return true;
+  }
+};
+
+// Row R of a request: token R / G, query head head G + R % G.
+__device__ __forceinline__ int64_t out_at(const Problem& p, int64_t first, int head, int row) {
+  const int t = row / p.G;
+  return ((first + t) * p.H + head * p.G + (row - t * p.G)) * (int64_t)p.DV;
+}
+
+// The record of a CTA's share: the piece that begins an item which goes on elsewhere, if there is one.
+__device__ __forceinline__ void write_rec(const Args& a, const Start& s, const Piece* x, long long begin) {
+  Rec& r = a.recs[blockIdx.x];
+  if (!x) {
+    r.rows = 0;
+    return;
+  }
+  r.first = x->first;
+  r.row0 = x->row0;
+  r.rows = x->rows;
+  r.head = x->head;
+  r.more = last_cta(begin + x->units, s.ctas, s.total) - (int)blockIdx.x;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T x);
+template <> __device__ __forceinline__ float to_f(float x) { return x; }
+template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+
+void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas, int least);
+
+// The kernel for any type and size, and the one on the tensor cores: whether sizes and type fit it,
+// whether addresses and strides do too (for TMA). Workspaces for requests of up to `rows` rows.
+cudaError_t launch_simple(const Problem& p, uint8_t* ws);
+size_t simple_workspace(int64_t rows, int DV);
+bool tc_shape(int D, int DV, gdp_dtype dt);
+bool tc_ok(const Problem& p);
+size_t tc_workspace(int64_t rows, int DV);
+cudaError_t launch_tc(const Problem& p, uint8_t* ws);
+// Test hook (gdp_debug_wait_fault): a wait of its next launch runs out (arm), limit of its waits.
+void wait_fault(int arm, unsigned long long budget_ns);
+cudaError_t launch_combine(const Args& a);
+
+}  // namespace attn
+}  // namespace gdp
