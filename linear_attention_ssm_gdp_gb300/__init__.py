@@ -416,10 +416,10 @@ def gdp_recurrent_update_slots(q, k, v, beta, g, state_pool, state_slot, scale=N
 
 def gdp_debug_wait_fault(arm: bool | int, budget_seconds: float = 0.0):
     """Test hook (off by default): arm a one-shot missing tensor-core commit in the
-    next 128-position WY launch (True) or the next tensor-core launch of linear attention
-    (2) so that one bounded device wait runs out, and/or set
+    next 128-position WY launch (True), the next tensor-core launch of linear attention
+    (2) or of gdp_attention_paged (3) so that one bounded device wait runs out, and/or set
     the wait budget (<= 0: the default 2 s)."""
-    code = 2 if arm == 2 else 1 if arm else 0
+    code = int(arm) if arm in (2, 3) else 1 if arm else 0
     _check("gdp_debug_wait_fault", load().gdp_debug_wait_fault(code, float(budget_seconds)))
 
 

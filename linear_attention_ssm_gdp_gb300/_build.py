@@ -40,6 +40,7 @@ UNITS = {
     "group_norm.cu": [],
     "rotary.cu": [],
     "attention.cu": [],
+    "attention_tc.cu": [],
 }
 
 

@@ -302,7 +302,7 @@ bool sizes_built(int B, int T, int H, int HKV, int D, int DV, gdp_dtype dt) {
 size_t workspace_of(int T, int H, int HKV, int D, int DV, gdp_dtype dt) {
   const int64_t rows = (int64_t)T * (H / HKV);
   const size_t s = attn::simple_workspace(rows, DV);
-  return s;
+  return attn::tc_shape(D, DV, dt) ? std::max(s, attn::tc_workspace(rows, DV)) : s;
 }
 
 }  // namespace
@@ -345,7 +345,7 @@ gdp_status gdp_attention_paged(const void* q, const int64_t* q_strides, const vo
   p.cu = cu_seqlens; p.n = N_seq; p.B = B; p.T = T; p.H = H; p.HKV = HKV; p.G = H / HKV; p.D = D; p.DV = DV;
   p.tree = tree_mask; p.c = scale * 1.44269504088896341f; p.dt = dt; p.o = o; p.status = status; p.stream = stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const cudaError_t e = attn::launch_simple(p, ws);
+  const cudaError_t e = attn::tc_ok(p) ? attn::launch_tc(p, ws) : attn::launch_simple(p, ws);
   return e == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
 }
 

@@ -2243,6 +2243,8 @@ cudaError_t launch_chunk_tc(const ChunkProblem& p, const WsLayout& L, uint8_t* w
 
 }  // namespace gdp
 
+namespace gdp { namespace attn { void wait_fault(int arm, unsigned long long budget_ns); } }
+
 extern "C" gdp_status gdp_debug_wait_fault(int arm, double budget_seconds) {
   unsigned long long ns = gdp::ptx::kWaitBudgetNs;
   if (budget_seconds > 0.0) {
@@ -2253,6 +2255,7 @@ extern "C" gdp_status gdp_debug_wait_fault(int arm, double budget_seconds) {
   if (cudaMemcpyToSymbol(gdp::ptx::g_wait_budget_ns, &ns, sizeof(ns)) != cudaSuccess)
     return GDP_ERR_CUDA;
   gdp::linear_wait_fault(arm == 2 ? 1 : 0, ns);
-  gdp::g_wy_fault.store(arm != 0 && arm != 2 ? 1 : 0);
+  gdp::attn::wait_fault(arm == 3 ? 1 : 0, ns);
+  gdp::g_wy_fault.store(arm != 0 && arm != 2 && arm != 3 ? 1 : 0);
   return GDP_OK;
 }
