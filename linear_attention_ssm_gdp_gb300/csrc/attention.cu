@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
       const int row = i / L.sd, d = i - row * L.sd;
       float f = 0.f;
       if (row < x.rows && d < p.D) {
-        const int R = x.row0 + row, t = R / p.G, h = x.head * p.G + R - t * p.G;
+        const int R = x.row0 + row, t = (int)quot(R, p.by_G), h = x.head * p.G + R - t * p.G;
         const int64_t at = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
         f = to_f(static_cast<const T*>(p.q)[at + h * p.qs[2] + d]);
       }
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
         const int key = j * kKeys + tid;
         int64_t ko = -1, vo = -1;
         if (key < x.keys) {
-          const int b = key / p.block, page = p.tables[(int64_t)x.r * p.width + b];
+          const int b = (int)quot(key, p.by_block), page = p.tables[(int64_t)x.r * p.width + b];
           if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
           if (page >= 0 && page < p.n_pages) {
             ko = page * p.ks[0] + (key - b * p.block) * p.ks[1] + x.head * p.ks[2];
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
         for (int i = 0; i < 4; ++i) {
           bool sees = s_ko[key] >= 0 && r0 + i < x.rows;
           if (sees && back >= 0) {
-            const int t = (x.row0 + r0 + i) / p.G;
+            const int t = (int)quot(x.row0 + r0 + i, p.by_G);
             sees = p.tree ? (p.tree[x.first + t] >> back) & 1 : back <= t;
           }
           ss[(r0 + i) * (kKeys + 1) + key] = sees ? s[i] * p.c : -INFINITY;
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
         const int row = rg + RG * i;
         if (row >= x.rows) continue;
         if (x.slot >= 0) {
-          float* dst = a.part + (((int64_t)blockIdx.x * 2 + x.slot) * a.cap + row) * a.dvp;
-          *reinterpret_cast<float4*>(dst + 4 * c) = acc[i];
+          float4* dst = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * 2 + x.slot) * a.cap * quads;
+          dst[c * a.cap + row] = acc[i];
           continue;
         }
         const float sum = s_sum[row], f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
@@ -191,48 +191,84 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ joining cut items
-// A CTA of the grid's x per record, a warp per row: the pieces' maxima give the factors 2^(m_i - m),
-// which the lanes apply to their columns in the order of the pieces.
-constexpr int kJoinWarps = 8;
+// A CTA of the grid's x per record and 32 rows (or fewer: kJoinRows), a thread per row and quad of
+// columns: the pieces' maxima give the factors 2^(m_i - m), applied in the order of the pieces. Maxima
+// and factors of 32 pieces at a time go through shared memory; outputs lie with rows side by side.
+constexpr int kJoin = 256, kJoinPieces = 32;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Args a) {
+struct alignas(4 * sizeof(T)) Quad {
+  T e[4];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Args a, int rows /* power of two */) {
+  __shared__ float s_f[kJoinPieces][33];
+  __shared__ float s_m[kJoin], s_l[kJoin];
   pdl_wait();
   const Rec r = a.recs[blockIdx.x];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= r.rows) return;
+  const int row0 = blockIdx.y * rows, tid = threadIdx.x;
+  if (row0 >= r.rows) return;
   const Problem& p = a.p;
+  const int here = min(rows, r.rows - row0), pieces = r.more + 1;
   // piece i: slot 1 of this CTA, slot 0 of the next ones
-  auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * a.cap + row; };
+  auto at = [&](int i) { return (int64_t)(blockIdx.x + i) * 2 + (i == 0); };
+  const int row = tid & (rows - 1), part = tid / rows, parts = kJoin / rows;
+  const bool on = row < here;
   float m = -INFINITY;
-  for (int i = lane; i <= r.more; i += 32) m = fmaxf(m, a.ml[at(i)].x);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (on)
+    for (int i = part; i < pieces; i += parts) m = fmaxf(m, a.ml[at(i) * a.cap + row0 + row].x);
+  s_m[tid] = m;
+  __syncthreads();
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, s_m[i * rows + row]);
   const float base = m == -INFINITY ? 0.f : m;
-  float4 acc[2] = {};
+  // a thread's quads: part, part + parts, ..
+  const int quads = a.dvp / 4;
+  const bool even = p.DV % 4 == 0 && reinterpret_cast<uintptr_t>(p.o) % sizeof(Quad<T>) == 0;
   float sum = 0.f;
-  for (int i = 0; i <= r.more; ++i) {
-    const float2 ml = a.ml[at(i)];
-    const float f = ex2(ml.x - base);
-    sum += f * ml.y;
-    const float4* src = reinterpret_cast<const float4*>(a.part + at(i) * a.dvp);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      if (lane + 32 * n < a.dvp / 4) {
-        const float4 v = src[lane + 32 * n];
-        acc[n].x = fmaf(f, v.x, acc[n].x);
-        acc[n].y = fmaf(f, v.y, acc[n].y);
-        acc[n].z = fmaf(f, v.z, acc[n].z);
-        acc[n].w = fmaf(f, v.w, acc[n].w);
+  for (int q0 = part; q0 - part < quads; q0 += parts) {
+    const bool mine = on && q0 < quads;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < pieces; i0 += kJoinPieces) {
+      const int n = min(kJoinPieces, pieces - i0);
+      __syncthreads();
+      for (int i = part; i < n; i += parts) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (on) ml = a.ml[at(i0 + i) * a.cap + row0 + row];
+        s_f[i][row] = ex2(ml.x - base);
+        if (q0 == part) sum += s_f[i][row] * ml.y;
       }
-  }
-  const float f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-  T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row);
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int e = 4 * (lane + 32 * n);
-    const float y[4] = {acc[n].x, acc[n].y, acc[n].z, acc[n].w};
-    for (int k = 0; k < 4; ++k)
-      if (e + k < p.DV) dst[e + k] = from_f<T>(y[k] * f);
+      __syncthreads();
+      if (mine) {
+        const float4* src = reinterpret_cast<const float4*>(a.part) + (int64_t)q0 * a.cap + row0 + row;
+        const int64_t step = (int64_t)a.cap * quads;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+          const float4 v = src[at(i0 + i) * step];
+          const float f = s_f[i][row];
+          acc.x = fmaf(f, v.x, acc.x);
+          acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z);
+          acc.w = fmaf(f, v.w, acc.w);
+        }
+      }
+    }
+    if (q0 == part) {  // the parts' sums, in order
+      s_l[tid] = sum;
+      __syncthreads();
+      sum = 0.f;
+      for (int i = 0; i < parts; ++i) sum += s_l[i * rows + row];
+      sum = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    }
+    if (mine) {
+      T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row0 + row) + 4 * q0;
+      const Quad<T> y = {from_f<T>(acc.x * sum), from_f<T>(acc.y * sum), from_f<T>(acc.z * sum), from_f<T>(acc.w * sum)};
+      if (even)
+        *reinterpret_cast<Quad<T>*>(dst) = y;
+      else
+        for (int k = 0; k < 4; ++k)
+          if (4 * q0 + k < p.DV) dst[k] = y.e[k];
+    }
   }
 }
 
@@ -250,28 +286,29 @@ int simple_ctas() { return 2 * sm_count(); }
 size_t simple_workspace(int64_t rows, int DV) { return layout(simple_ctas(), rows, kRows, DV).total; }
 
 cudaError_t launch_combine(const Args& a) {
-  const dim3 grid(a.ctas, (a.cap + kJoinWarps - 1) / kJoinWarps), block(kJoinWarps * 32);
+  int rows = 1;
+  while (rows < 32 && rows < a.cap) rows *= 2;
+  const dim3 grid(a.ctas, (a.cap + rows - 1) / rows), block(kJoin);
   switch (a.p.dt) {
-    case GDP_BF16: return launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, a.p.stream, a);
-    case GDP_F16: return launch_pdl(join_kernel<__half>, grid, block, 0, a.p.stream, a);
-    default: return launch_pdl(join_kernel<float>, grid, block, 0, a.p.stream, a);
+    case GDP_BF16: return launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, a.p.stream, a, rows);
+    case GDP_F16: return launch_pdl(join_kernel<__half>, grid, block, 0, a.p.stream, a, rows);
+    default: return launch_pdl(join_kernel<float>, grid, block, 0, a.p.stream, a, rows);
   }
 }
 
-void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas, int least) {
+void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas) {
   a.recs = reinterpret_cast<Rec*>(ws + x.recs);
   a.ml = reinterpret_cast<float2*>(ws + x.ml);
   a.part = reinterpret_cast<float*>(ws + x.part);
   a.ctas = ctas;
   a.cap = x.cap;
   a.dvp = x.dvp;
-  a.least = least;
 }
 
 cudaError_t launch_simple(const Problem& p, uint8_t* ws) {
   Args a{};
   a.p = p;
-  set_layout(a, layout(simple_ctas(), (int64_t)p.T * p.G, kRows, p.DV), ws, simple_ctas(), 1);
+  set_layout(a, layout(simple_ctas(), (int64_t)p.T * p.G, kRows, p.DV), ws, simple_ctas());
   cudaError_t e;
   switch (p.dt) {
     case GDP_BF16: e = go<__nv_bfloat16>(a); break;
@@ -343,6 +380,7 @@ gdp_status gdp_attention_paged(const void* q, const int64_t* q_strides, const vo
   }
   p.n_pages = n_pages; p.block = block_size; p.tables = block_tables; p.width = max_blocks; p.ctx = context_lens;
   p.cu = cu_seqlens; p.n = N_seq; p.B = B; p.T = T; p.H = H; p.HKV = HKV; p.G = H / HKV; p.D = D; p.DV = DV;
+  p.by_G = div_by(p.G); p.by_block = div_by(block_size);
   p.tree = tree_mask; p.c = scale * 1.44269504088896341f; p.dt = dt; p.o = o; p.status = status; p.stream = stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaError_t e = attn::tc_ok(p) ? attn::launch_tc(p, ws) : attn::launch_simple(p, ws);

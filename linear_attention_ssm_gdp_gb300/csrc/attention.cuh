@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fast_div.cuh"
 #include "gdp_internal.cuh"
 
 namespace gdp {
@@ -29,6 +30,7 @@ struct Problem {
   const int32_t* ctx;             // [n]
   const int32_t* cu;              // null: n == B requests of T tokens
   int n, B, T, H, HKV, G, D, DV;
+  Div by_G, by_block;
   const int64_t* tree;            // [B, T] or null: a chain
   float c;                        // scale log2 e
   gdp_dtype dt;
@@ -46,10 +48,9 @@ struct Rec {
 struct Args {
   Problem p;
   Rec* recs;                      // [ctas]
-  float* part;                    // [ctas][2][cap][dvp] outputs
+  float* part;                    // [ctas][2][dvp / 4][cap][4] outputs
   float2* ml;                     // [ctas][2][cap] row maximum (log2) and sum
   int ctas, cap, dvp;             // cap: rows of a piece that are kept
-  int least;                      // units that a CTA takes at least
 };
 
 struct Layout {
@@ -83,24 +84,25 @@ __device__ __forceinline__ int64_t first_row(const Problem& p, int r) {
   return p.cu ? p.cu[r] : (int64_t)r * p.T;
 }
 
+// (Rows of a request, S G, stay below 2^31 - 1024.)
 template <int BM, int KT>
 struct Cut {
-  __device__ static __forceinline__ int tiles(const Problem& p, int S) { return (int)(((int64_t)S * p.G + BM - 1) / BM); }
+  __device__ static __forceinline__ int tiles(const Problem& p, int S) { return (S * p.G + BM - 1) / BM; }
   // keys that the rows of a tile see at most
   __device__ static __forceinline__ int keys(const Problem& p, const Req& x, int tile) {
     if (!x.ok) return 0;
     if (p.tree) return x.ctx + x.S;
-    const int64_t last = min((int64_t)(tile + 1) * BM, (int64_t)x.S * p.G) - 1;
-    return x.ctx + (int)(last / p.G) + 1;
+    const int last = min((tile + 1) * BM, x.S * p.G) - 1;
+    return x.ctx + (int)quot(last, p.by_G) + 1;
   }
   __device__ static __forceinline__ int units(int keys) { return keys > 0 ? (keys + KT - 1) / KT : 1; }
-  __device__ static __forceinline__ int64_t request_units(const Problem& p, int r) {
-    const Req x = request(p, r);
+  // of one head of a request
+  __device__ static __forceinline__ int64_t head_units(const Problem& p, const Req& x) {
     if (x.S <= 0) return 0;
     const int n = tiles(p, x.S);
     int64_t u = 0;
     for (int i = 0; i < n; ++i) u += units(keys(p, x, i));
-    return u * p.HKV;
+    return u;
   }
 };
 
@@ -112,26 +114,36 @@ struct Start {
   int bad;
 };
 
+// (32 bits where they do: the 64-bit division is a call of a hundred instructions.)
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (a | b) >> 31 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // By all NT threads of the CTA. (64-bit sums: requests times heads times tiles may pass 2^31.)
 template <int BM, int KT, int NT>
 __device__ __forceinline__ void find_start(const Args& a, Start* out, long long* scratch /* [NT / 32 + 1] */) {
   const Problem& p = a.p;
+  using C = Cut<BM, KT>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.n + NT - 1) / NT;
   const int r0 = (int)min((int64_t)tid * per, (int64_t)p.n), r1 = min(r0 + per, p.n);
   long long mine = 0;
   int bad = 0, odd = 0;
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
+    const Req x = request(p, r);
     if (p.cu) {
-      const int a0 = p.cu[r], a1 = p.cu[r + 1];
-      if (a0 < 0 || a1 < a0 || a1 > p.T || (r == 0 && a0 != 0)) { bad = 1; break; }
+      const int a0 = p.cu[r];
+      if (a0 < 0 || x.S < 0 || x.S > p.T - a0 || (r == 0 && a0 != 0)) { bad = 1; break; }
     }
-    if (!request(p, r).ok) odd = 1;
-    mine += Cut<BM, KT>::request_units(p, r);
+    if (!x.ok) odd = 1;
+    mine += C::head_units(p, x);
   }
+  mine *= p.HKV;
   if (blockIdx.x == 0 && (odd || bad) && p.status) *p.status = GDP_ERR_INVALID_ARG;
   bad = __syncthreads_or(bad);
   long long sum = mine;
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += x;
@@ -140,37 +152,43 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
   if (tid == 0) { out->bad = bad; out->left = 0; }
   __syncthreads();
   long long before = sum - mine, total = 0;
+#pragma unroll 1
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  const long long ctas = min((long long)a.ctas, (total + a.least - 1) / a.least);
+  const long long ctas = min((long long)a.ctas, total);
   if (tid == 0) { out->total = total; out->ctas = ctas; }
-  if (!bad && total > 0 && blockIdx.x < ctas) {
-    const long long u0 = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
-    const long long u1 = total / ctas * (blockIdx.x + 1) + total % ctas * (blockIdx.x + 1) / ctas;
+  if (!bad && blockIdx.x < ctas) {
+    // first unit of CTA c: floor(total c / ctas)
+    const long long q = divide(total, ctas), rest = total - q * ctas;
+    const long long u0 = q * blockIdx.x + divide(rest * blockIdx.x, ctas);
     if (before <= u0 && u0 < before + mine) {  // the thread whose requests hold the start
       long long at = u0 - before;
       int r = r0;
+      Req x;
+      long long head;
+#pragma unroll 1
       for (;; ++r) {
-        const long long u = Cut<BM, KT>::request_units(p, r);
-        if (at < u) break;
-        at -= u;
+        x = request(p, r);
+        head = C::head_units(p, x);
+        if (at < head * p.HKV) break;
+        at -= head * p.HKV;
       }
-      const Req x = request(p, r);
-      const long long per_head = Cut<BM, KT>::request_units(p, r) / p.HKV;
-      out->head = (int)(at / per_head);
-      at %= per_head;
+      const long long h = divide(at, head);
+      at -= h * head;
       int tile = 0;
+#pragma unroll 1
       for (;; ++tile) {
-        const int u = Cut<BM, KT>::units(Cut<BM, KT>::keys(p, x, tile));
+        const int u = C::units(C::keys(p, x, tile));
         if (at < u) break;
         at -= u;
       }
       out->r = r;
+      out->head = (int)h;
       out->tile = tile;
       out->j = (int)at;
-      out->left = u1 - u0;
+      out->left = q * (blockIdx.x + 1ll) + divide(rest * (blockIdx.x + 1ll), ctas) - u0;
       out->at = u0;
     }
   }
@@ -180,7 +198,7 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
 // First unit of CTA c's share is floor(total c / ctas), so the last CTA with a unit before `end` is
 // ceil(end ctas / total) - 1.
 __device__ __forceinline__ int last_cta(long long end, long long ctas, long long total) {
-  return (int)((end * ctas + total - 1) / total) - 1;
+  return (int)divide(end * ctas + total - 1, total) - 1;
 }
 
 // One piece of an item, and the walk over the pieces of a share.
@@ -210,7 +228,7 @@ struct Walk {
     x.head = head;
     x.tile = tile;
     x.row0 = tile * BM;
-    x.rows = (int)min((int64_t)BM, (int64_t)x.x.S * p.G - x.row0);
+    x.rows = min(BM, x.x.S * p.G - x.row0);
     x.keys = Cut<BM, KT>::keys(p, x.x, tile);
     x.units = Cut<BM, KT>::units(x.keys);
     x.j0 = j;
@@ -229,7 +247,7 @@ struct Walk {
 
 // Row R of a request: token R / G, query head head G + R % G.
 __device__ __forceinline__ int64_t out_at(const Problem& p, int64_t first, int head, int row) {
-  const int t = row / p.G;
+  const int t = (int)quot(row, p.by_G);
   return ((first + t) * p.H + head * p.G + (row - t * p.G)) * (int64_t)p.DV;
 }
 
@@ -262,7 +280,7 @@ template <> __device__ __forceinline__ float from_f(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 
-void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas, int least);
+void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas);
 
 // The kernel for any type and size, and the one on the tensor cores: whether sizes and type fit it,
 // whether addresses and strides do too (for TMA). Workspaces for requests of up to `rows` rows.

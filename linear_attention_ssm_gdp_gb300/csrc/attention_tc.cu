@@ -33,28 +33,32 @@ namespace attn {
 namespace {
 using namespace ptx;
 
-constexpr int kRows = 256, kKeys = 128;
+constexpr int kRows = 256, kKeys = 64;
 constexpr int kLoad = 8, kMma = 9;  // warps; 0 to 3 and 4 to 7 are the slots'
 constexpr int kThreads = 320;
-constexpr int kMeta = 8;            // tiles whose absent boxes are on record
+constexpr int kAhead = 4;           // scores formed before their outputs: two buffers for each slot
 constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
 
 template <int KD>
 struct Lay {
-  static constexpr int NB = KD == 128 ? 5 : 8;   // buffers of the ring, each a tile of K or of V
-  static constexpr int TILE = KD / 64 * 16384;   // halves of 64 columns: 128 rows of 128 bytes
-  static constexpr int Q = 0;                    // two tiles of rows
-  static constexpr int RING = 2 * TILE;
-  static constexpr int BAR = RING + NB * TILE;
-  static constexpr int BYTES = BAR + 1536 + 1024;       // (barriers, maxima and sums; alignment)
+  static constexpr int NB = KD == 128 ? 5 : 10;  // stages of the ring, a tile of K and one of V each
+  static constexpr int HALF = kKeys * 128;       // 64 columns of a tile: 64 rows of 128 bytes
+  static constexpr int TILE = KD / 64 * HALF;
+  static constexpr int QT = KD / 64 * 16384;     // 128 rows of queries
+  static constexpr int Q = 0, RING = 2 * QT;
+  static constexpr int BAR = RING + NB * 2 * TILE;
+  static constexpr int ML = BAR + 384;           // maxima and sums [2][128]
+  static constexpr int START = ML + 2048;        // the share, and the sums that lead to it
+  static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-enum { B_FULL = 0, B_EMPTY = 8, B_S = 16, B_P = 18, B_O = 20, B_Q = 22, B_META = 24, B_JOIN = 32, B_END, B_N };
-constexpr uint32_t T_S = 0, T_O = 256;  // columns: S [2][128], O [2][128]
+// by stage: full, empty; by slot and buffer: scores, weights; by slot: outputs, queries; a piece's two slots
+// have left their maxima, have read each other's outputs
+enum { B_FULL = 0, B_EMPTY = 10, B_S = 20, B_P = 24, B_O = 28, B_Q = 30, B_JOIN = 32, B_DONE, B_END, B_N };
+constexpr uint32_t T_S = 0, T_O = 256;  // columns: S [2][2][64], O [2][128]
 
 struct TcArgs : Args {
   int g;          // keys of a box
-  int box_bytes;
   int budget;     // limit of a wait, in units of 1024 ns
   int fault;      // test hook (gdp_debug_wait_fault): CTA 0 waits for a commit more of its first scores
 };
@@ -113,11 +117,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // How a piece's tiles are spread over the slots.
 struct Spread {
   bool two;       // tiles of rows of their own, the same keys
-  int first, step, n, rows, row0;
+  int n, rows, row0;
   __device__ __forceinline__ Spread(const Piece& x, int slot) {
     two = x.rows > 128;
-    first = two ? x.j0 : x.j0 + slot;
-    step = two ? 1 : 2;
     n = two ? x.j1 - x.j0 : (x.j1 - x.j0 + 1 - slot) / 2;
     rows = two ? (slot ? x.rows - 128 : 128) : x.rows;
     row0 = x.row0 + (two ? 128 * slot : 0);
@@ -129,15 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ TcArgs a) {
   using L = Lay<KD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];  // (nothing static beside it: the array begins on a swizzle atom)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + B_N);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint32_t* s_absent = s_tmem + 2;                               // [kMeta]
-  float2* s_ml = reinterpret_cast<float2*>(sm + L::BAR + 384);   // [128]: the second slot's
-  __shared__ Start s_start;
-  __shared__ long long s_scan[kThreads / 32 + 1];
+  uint32_t* s_absent = s_tmem + 2;                                     // [NB]
+  float2* s_ml = reinterpret_cast<float2*>(sm + L::ML);                // [2][128]
+  Start& s_start = *reinterpret_cast<Start*>(sm + L::START);
+  long long* s_scan = reinterpret_cast<long long*>(sm + L::START + 96);  // [kThreads / 32]
+  static_assert(sizeof(Start) <= 96 && kThreads / 32 * 8 <= 96 && B_N * 8 + 8 + L::NB * 4 <= 384, "shared memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const Problem& p = a.p;
 
@@ -145,18 +147,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int i = 0; i < B_N; ++i) {
-      int n = 1;
-      if (i >= B_P && i < B_O) n = 4;                            // warps of the slot
-      if (i >= B_Q && i < B_META) n = 4;
-      if (i == B_JOIN) n = 8;
-      if (i == B_S && a.fault && blockIdx.x == 0) n = 2;
-      mbar_init(&bars[i], n);
-    }
+  if (tid < B_N) {
+    int n = 1;
+    if (tid >= B_P && tid < B_O) n = 4;                                // warps of the slot
+    if (tid >= B_Q && tid < B_JOIN) n = 4;
+    if (tid == B_JOIN || tid == B_DONE) n = 8;
+    if (tid == B_S && a.fault && blockIdx.x == 0) n = 2;
+    mbar_init(&bars[tid], n);
     fence_mbar_init();
-    *s_dead = 0;
   }
+  if (tid == 64) *s_dead = 0;
   if (warp == kLoad && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -176,75 +176,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- softmax, outputs
     const int slot = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + lanes + T_S + 128 * slot, to = tmem + lanes + T_O + 128 * slot;
-    const float c = fabsf(p.c);
-    const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
-    uint8_t* sq = sm + L::Q + slot * L::TILE;
-    float* so = reinterpret_cast<float*>(sm + L::Q);             // [KD][128]: the second slot's outputs
-    uint32_t n = 0, tile0 = 0, joins = 0;  // this slot's tiles so far, the CTA's at the piece's start
-    bool rec = false;
+    const uint32_t ts = tmem + lanes + T_S + 128 * slot, to = tmem + lanes + T_O;
+    // a scale of 0 as the least that keeps 0 times -inf (not seen) at -inf
+    const float c = fmaxf(fabsf(p.c), 1e-37f);
+    uint8_t* sq = sm + L::Q + slot * L::QT;
+    const uint32_t sqa = smem_u32(sq);
+    uint32_t n = 0, tile0 = 0, joins = 0, other = 0;  // tiles of this slot, of the CTA; joins; tiles of the other slot
+    bool rec = false, owe = false;
+#pragma unroll 1
     while (ok && walk.next(p, x)) {
       const Spread d(x, slot);
       if (d.n > 0) {  // Q: 16-byte chunks of the rows, zero behind the head's end
+#pragma unroll 1
         for (int i = tid & 127; i < d.rows * (KD / 8); i += 128) {
-          const int r = i / (KD / 8), ch = i % (KD / 8), R = d.row0 + r, t = R / p.G, h = x.head * p.G + R - t * p.G;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (8 * ch < p.D) {
-            const int64_t at = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
-            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at + h * p.qs[2] + 8 * ch);
-            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-          }
-          *reinterpret_cast<uint4*>(sq + (ch >> 3) * 16384 + sw128_offset(r, (ch & 7) * 16)) = v;
+          const int r = i / (KD / 8), ch = i % (KD / 8), R = d.row0 + r, t = (int)quot(R, p.by_G);
+          const int h = x.head * p.G + R - t * p.G;
+          const int64_t at = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
+          const T* src = static_cast<const T*>(p.q) + at + h * p.qs[2] + (8 * ch < p.D ? 8 * ch : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           sqa + (ch >> 3) * 16384 + sw128_offset(r, (ch & 7) * 16)),
+                       "l"(src), "r"(8 * ch < p.D ? 16 : 0)
+                       : "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_Q + slot]);
       }
       const bool live = quarter * 32 < d.rows;
-      const int t = (d.row0 + min(row, d.rows - 1)) / p.G;
+      const int t = (int)quot(d.row0 + min(row, d.rows - 1), p.by_G);
       const uint64_t bits = p.tree && x.x.ok ? (uint64_t)p.tree[x.first + t] : 0ull;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int k = 0; ok && k < d.n; ++k, ++n) {
-        const int j = d.first + k * d.step, key0 = j * kKeys;
-        const uint32_t tile = tile0 + (uint32_t)(j - x.j0);
-        ok = sy.wait(&bars[B_META + tile % kMeta], (tile / kMeta) & 1);
-        const uint32_t absent = s_absent[tile % kMeta];
-        ok = ok && sy.wait(&bars[B_S + slot], n & 1);
+        const int j = d.two ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
+        const uint32_t stage = (tile0 + j) % L::NB, turn = (tile0 + j) / L::NB;
+        const uint32_t buf = n & 1, tb = ts + 64 * buf;
+        ok = sy.wait(&bars[B_S + 2 * slot + buf], (n >> 1) & 1) && sy.wait(&bars[B_FULL + stage], turn & 1);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t absent = s_absent[stage];
         if (live) {
-          uint32_t s[kKeys];
-#pragma unroll
-          for (int q = 0; q < kKeys; q += 32) GDP_TMEM_LD32(ts + q, (s + q));
-          tmem_wait_ld();
-          float ce = c;
           if (key0 + kKeys > x.x.ctx || absent) {  // some of the keys are not seen by some row
-            ce = 1.f;
-#pragma unroll
-            for (int q = 0; q < kKeys; q += 32) {
+#pragma unroll 1
+            for (int q = 0; q < kKeys; q += 8) {
               const int k0 = key0 + q;
               uint32_t see;
               if (p.tree) {
                 const int back = k0 - x.x.ctx;
                 see = low_bits(-back);
-                if (back > -32 && back < 64) see |= (uint32_t)(back >= 0 ? bits >> back : bits << -back);
+                if (back > -8 && back < 64) see |= (uint32_t)(back >= 0 ? bits >> back : bits << -back);
               } else {
                 see = low_bits(x.x.ctx + t + 1 - k0);
               }
               see &= low_bits(x.keys - k0);
-              if (absent)
-                for (int b = 0; b < 32; b += 8)
-                  if (absent >> ((q + b) / a.g) & 1) see &= ~(0xffu << b);
+              if (absent >> (q / a.g) & 1) see = 0;
+              uint32_t s[8];
+              GDP_TMEM_LD8(tb + q, s);
+              tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[q + e] = __float_as_uint(see >> e & 1 ? __uint_as_float(s[q + e]) * c : -INFINITY);
+              for (int e = 0; e < 8; ++e) s[e] = see >> e & 1 ? s[e] : __float_as_uint(-INFINITY);
+              GDP_TMEM_ST8(tb + q, s);
             }
+            tmem_wait_st();
           }
+          uint32_t s[kKeys];
+          GDP_TMEM_LD32(tb, s);
+          GDP_TMEM_LD32(tb + 32, (s + 32));
+          tmem_wait_ld();
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
-          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          const float mt = most == -INFINITY ? -INFINITY : most * ce;
+          const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
           const bool grow = mt > m + kGrow;  // (from -inf: as soon as anything is seen)
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mt : m, f = grow ? ex2(m - mn) : 1.f;
@@ -255,180 +258,160 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int q = 0; q < KD; q += 16) {
-                uint32_t o[16];
-                GDP_TMEM_LD16(to + q, o);
+              for (int q = 0; q < KD; q += 8) {
+                uint32_t o[8];
+                GDP_TMEM_LD8(to + 128 * slot + q, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                GDP_TMEM_ST8(to + q, o);
-                GDP_TMEM_ST8(to + q + 8, (o + 8));
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                GDP_TMEM_ST8(to + 128 * slot + q, o);
               }
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t w[32];
 #pragma unroll
-          for (int q = 0; q < kKeys; q += 64) {
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float p0 = ex2(fmaf(__uint_as_float(s[q + 2 * e]), ce, -base));
-              const float p1 = ex2(fmaf(__uint_as_float(s[q + 2 * e + 1]), ce, -base));
-              sum[2 * (e & 1)] += p0;
-              sum[2 * (e & 1) + 1] += p1;
-              w[e] = pack<T>(p0, p1);
-            }
-            GDP_TMEM_ST32(ts + q / 2, w);
+          for (int e = 0; e < 32; ++e) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), c, -base));
+            const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), c, -base));
+            sum[2 * (e & 1)] += p0;
+            sum[2 * (e & 1) + 1] += p1;
+            w[e] = pack<T>(p0, p1);
           }
+          GDP_TMEM_ST32(tb, w);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
-        if (key0 + kKeys > x.keys && x.keys > 0) {  // rows of V behind the last key, in the last box
-          const int z0 = x.keys - key0, z1 = (z0 + a.g - 1) / a.g * a.g;
-          if (z0 > 0 && z1 > z0) {
-            const uint32_t i = 2 * tile + 1;
-            ok = sy.wait(&bars[B_FULL + i % L::NB], (i / L::NB) & 1);
-            if (!ok) break;
-            uint8_t* sv = sm + L::RING + (i % L::NB) * L::TILE;
-            for (int e = tid & 127; e < (z1 - z0) * (KD / 8); e += 128) {
-              const int r = z0 + e / (KD / 8), ch = e % (KD / 8);
-              *reinterpret_cast<uint4*>(sv + (ch >> 3) * 16384 + sw128_offset(r, (ch & 7) * 16)) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
+        const int z0 = x.keys - key0;
+        if (z0 > 0 && z0 < kKeys && z0 % a.g) {  // rows of V behind the last key, in the last box
+          uint8_t* sv = sm + L::RING + stage * 2 * L::TILE + L::TILE;
+          const int z1 = (z0 + a.g - 1) / a.g * a.g;
+#pragma unroll 1
+          for (int e = tid & 127; e < (z1 - z0) * (KD / 8); e += 128) {
+            const int r = z0 + e / (KD / 8), ch = e % (KD / 8);
+            *reinterpret_cast<uint4*>(sv + (ch >> 3) * L::HALF + sw128_offset(r, (ch & 7) * 16)) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_async_smem();
+        }
+        if (owe) {  // the other slot has read this one's outputs of the last piece
+          owe = false;
+          ok = sy.wait(&bars[B_DONE], (joins - 1) & 1);
+          if (!ok) break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_P + slot]);
+        if (lane == 0) mbar_arrive(&bars[B_P + 2 * slot + buf]);
       }
-      tile0 += x.j1 - x.j0;
+      const int nt = x.j1 - x.j0;
+      tile0 += nt;
+      other += d.two ? nt : nt - d.n;
       if (!ok) break;
-      if (d.n > 0) {
-        ok = sy.wait(&bars[B_O + slot], (n - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      // Two slots on the same rows: the second leaves its results in the first ones' shared memory
-      // (no product reads Q any more), column by column so that lanes are side by side.
-      const bool join = !d.two && x.j1 - x.j0 > 1;
-      auto meet = [&]() {
+      // Two slots on the same rows: each leaves its maxima and sums, then joins half of the columns. (Both
+      // slots' outputs lie in the same lanes of tensor memory.)
+      const bool join = !d.two && nt > 1;
+      float f0 = 1.f, f1 = 0.f;  // of this slot's and of the other's outputs
+      if (d.n > 0) ok = sy.wait(&bars[B_O + slot], (n - 1) & 1);
+      if (join) {
+        s_ml[slot * 128 + row] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_JOIN]);
-        const bool met = sy.wait(&bars[B_JOIN], joins & 1);
+        ok = ok && sy.wait(&bars[B_JOIN], joins & 1) && sy.wait(&bars[B_O + (slot ^ 1)], (other - 1) & 1);
+        if (!ok) break;
         ++joins;
-        return met;
-      };
-      float f0 = 1.f, f1 = 0.f;
-      if (join) {
-        ok = meet();
-        if (!ok) break;
-        if (slot == 1 && live) {
-#pragma unroll 1
-          for (int q = 0; q < KD; q += 16) {
-            uint32_t o[16];
-            GDP_TMEM_LD16(to + q, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) so[(q + e) * 128 + row] = __uint_as_float(o[e]);
-          }
-          s_ml[row] = make_float2(m, l);
-        }
-        ok = meet();
-        if (!ok) break;
-        if (slot == 0 && live) {
-          const float2 u = s_ml[row];
-          const float mn = fmaxf(m, u.x), base = mn == -INFINITY ? 0.f : mn;
-          f0 = ex2(m - base);
-          f1 = ex2(u.x - base);
-          m = mn;
-          l = f0 * l + f1 * u.y;
-        }
+        owe = true;
+        const float2 u = s_ml[(slot ^ 1) * 128 + row];
+        const float mn = fmaxf(m, u.x), base = mn == -INFINITY ? 0.f : mn;
+        f0 = ex2(m - base);
+        f1 = ex2(u.x - base);
+        m = mn;
+        l = f0 * l + f1 * u.y;
       }
-      if ((d.two || slot == 0) && live) {
+      if (!ok) break;
+      tc_fence_after();
+      if ((join || d.n > 0) && live) {
         const bool on = row < d.rows;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         const int at = d.row0 - x.row0 + row;  // of the item's rows
-        float* part = x.slot >= 0 && on ? a.part + (((int64_t)blockIdx.x * 2 + x.slot) * a.cap + at) * a.dvp : nullptr;
-        T* dst = on ? static_cast<T*>(p.o) + out_at(p, x.first, x.head, d.row0 + row) : nullptr;
-        if (part) a.ml[((int64_t)blockIdx.x * 2 + x.slot) * a.cap + at] = make_float2(m, l);
-        const float f = part ? f0 : f0 * inv, g = part ? f1 : f1 * inv;
+        const int64_t cut = (int64_t)blockIdx.x * 2 + x.slot;
+        const bool whole = x.slot < 0;
+        if (!whole && on && (slot == 0 || d.two)) a.ml[cut * a.cap + at] = make_float2(m, l);
+        float4* part = reinterpret_cast<float4*>(a.part + (whole ? 0 : cut * a.cap * a.dvp)) + at;
+        T* dst = static_cast<T*>(p.o) + out_at(p, x.first, x.head, d.row0 + min(row, d.rows - 1));
+        if (whole) { f0 *= inv; f1 *= inv; }
+        const int q0 = join && slot ? KD / 2 : 0, q1 = join && !slot ? KD / 2 : KD;
 #pragma unroll 1
-        for (int q = 0; q < KD; q += 16) {
-          uint32_t o[16];
-          GDP_TMEM_LD16(to + q, o);
+        for (int q = q0; q < q1; q += 8) {
+          uint32_t o[8], u[8];
+          GDP_TMEM_LD8(to + 128 * slot + q, o);
+          if (join) GDP_TMEM_LD8(to + 128 * (slot ^ 1) + q, u);
           tmem_wait_ld();
-          if (!on) continue;
-          float y[16];
+          float y[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            y[e] = __uint_as_float(o[e]) * f;
-            if (join) y[e] = fmaf(g, so[(q + e) * 128 + row], y[e]);
+          for (int e = 0; e < 8; ++e) {
+            y[e] = __uint_as_float(o[e]) * f0;
+            if (join) y[e] = fmaf(f1, __uint_as_float(u[e]), y[e]);
           }
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            if (q + e >= p.DV) break;
-            if (part) {
-              *reinterpret_cast<float4*>(part + q + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-              *reinterpret_cast<float4*>(part + q + e + 4) = make_float4(y[e + 4], y[e + 5], y[e + 6], y[e + 7]);
-            } else {
-              *reinterpret_cast<uint4*>(dst + q + e) =
-                  make_uint4(pack<T>(y[e], y[e + 1]), pack<T>(y[e + 2], y[e + 3]), pack<T>(y[e + 4], y[e + 5]),
-                             pack<T>(y[e + 6], y[e + 7]));
-            }
+          if (!on || q >= p.DV) continue;
+          if (whole) {
+            *reinterpret_cast<uint4*>(dst + q) = make_uint4(pack<T>(y[0], y[1]), pack<T>(y[2], y[3]),
+                                                            pack<T>(y[4], y[5]), pack<T>(y[6], y[7]));
+          } else {  // quads of columns outermost: lanes are side by side
+            part[(q >> 2) * a.cap] = make_float4(y[0], y[1], y[2], y[3]);
+            part[((q >> 2) + 1) * a.cap] = make_float4(y[4], y[5], y[6], y[7]);
           }
         }
       }
       tc_fence_before();
       if (join) {
-        ok = meet();
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_DONE]);
       }
       if (x.slot == 1) {
         rec = true;
-        if (tid == 0) write_rec(a, s_start, &x, walk.at - (x.j1 - x.j0));
+        if (tid == 0) write_rec(a, s_start, &x, walk.at - nt);
       }
     }
     if (!rec && tid == 0) write_rec(a, s_start, nullptr, 0);
   } else if (warp == kLoad) {
     // ---------------------------------------------------------------- loads
-    const int subs = kKeys / a.g;  // boxes of a tile and half: 1 to 16, so a lane's is the same in every round
+    const int subs = kKeys / a.g;  // boxes of a tile and half: 1 to 8, so a lane's is the same in every round
     const int sub = lane % subs;
-    uint32_t i = 0, tile = 0;
+    uint32_t i = 0;
+#pragma unroll 1
     while (ok && walk.next(p, x)) {
+      const int32_t* table = p.tables + (int64_t)x.r * p.width;
       auto page_of = [&](int j, int& place) {  // n_pages: a box of zeros
         const int key = j * kKeys + sub * a.g;
         place = 0;
         if (j >= x.j1 || key >= x.keys) return p.n_pages;
-        const int b = key / p.block, page = p.tables[(int64_t)x.r * p.width + b];
+        const int b = (int)quot(key, p.by_block), page = table[b];
         place = key - b * p.block;
         if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
         return page >= 0 && page < p.n_pages ? page : p.n_pages;
       };
       int place, page = page_of(x.j0, place);
-      for (int j = x.j0; ok && j < x.j1; ++j, ++tile) {
+#pragma unroll 1
+      for (int j = x.j0; j < x.j1; ++j, ++i) {
         int place1;
         const int page1 = page_of(j + 1, place1);
         const uint32_t absent = __ballot_sync(0xffffffffu, page == p.n_pages) & low_bits(subs);
-#pragma unroll
-        for (int v = 0; v < 2; ++v, ++i) {
-          uint64_t* bar = &bars[B_FULL + i % L::NB];
-          ok = sy.wait(&bars[B_EMPTY + i % L::NB], ((i / L::NB) & 1) ^ 1);
-          if (!ok) break;
-          if (lane == 0) {
-            if (v == 0) {
-              s_absent[tile % kMeta] = absent;
-              mbar_arrive(&bars[B_META + tile % kMeta]);
-            }
-            mbar_expect_tx(bar, L::TILE);
-          }
-          __syncwarp();
-          uint8_t* dst = sm + L::RING + (i % L::NB) * L::TILE + sub * a.g * 128;
-          for (int b = lane; b < subs * (KD / 64); b += 32) {
-            const int half = b / subs;
-            tma_load_4d(dst + half * 16384, v ? &map_v : &map_k, half * 64, x.head, place, page, bar);
-          }
+        const uint32_t stage = i % L::NB;
+        ok = sy.wait(&bars[B_EMPTY + stage], ((i / L::NB) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          s_absent[stage] = absent;
+          mbar_expect_tx(&bars[B_FULL + stage], 2 * L::TILE);
+        }
+        __syncwarp();
+        uint8_t* dst = sm + L::RING + stage * 2 * L::TILE + sub * a.g * 128;
+#pragma unroll 1
+        for (int b = lane; b < subs * (KD / 32); b += 32) {  // halves of K, then of V
+          const int half = b / subs;
+          const bool v = half >= KD / 64;
+          tma_load_4d(dst + half * L::HALF, v ? &map_v : &map_k, (v ? half - KD / 64 : half) * 64, x.head, place, page,
+                      &bars[B_FULL + stage]);
         }
         page = page1;
         place = place1;
@@ -439,65 +422,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_FULL + b % L::NB], (b / L::NB) & 1, 20000); ++tries) {}
   } else {
     // ---------------------------------------------------------------- products
-    constexpr uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, KD, true);
+    // Steps of a piece: its tiles in turn, for both slots where they have rows of their own. Scores are
+    // formed up to four steps ahead of the outputs, whichever of the two can be first.
+    const uint32_t id_s = idesc<T>(128, kKeys, false) | (p.c < 0.f ? 1u << 13 : 0u);  // (-Q)
+    constexpr uint32_t id_o = idesc<T>(128, KD, true);
     const uint32_t base = smem_u32(sm);
-    uint32_t i0 = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // ring at the piece's start; weights and queries taken
+    uint32_t tile0 = 0, ns0 = 0, ns1 = 0, np0 = 0, np1 = 0, nq0 = 0, nq1 = 0;  // tiles; per slot: scores, weights, queries
+#pragma unroll 1
     while (ok && walk.next(p, x)) {
       const int nt = x.j1 - x.j0;
       const bool two = x.rows > 128;
-      for (int s = 0; ok && s < 2; ++s)
-        if (two || s < nt) ok = sy.wait(&bars[B_Q + s], nq[s]++ & 1);
-      auto scores = [&](int s, int k) {  // of the piece's tile k in slot s
-        const uint32_t i = i0 + 2 * k;
-        ok = ok && sy.wait(&bars[B_FULL + i % L::NB], (i / L::NB) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_run<KD / 16, false, 16384, 32, 16384, 32>(
-              tmem + T_S + 128 * s, sdesc_sw128(base + L::Q + s * L::TILE, 16, 1024),
-              sdesc_sw128(base + L::RING + (i % L::NB) * L::TILE, 16, 1024), id_s);
-          mma_commit(&bars[B_S + s]);
-          if (!two || s == 1) mma_commit(&bars[B_EMPTY + i % L::NB]);
-        }
-        __syncwarp();
-      };
-      auto outputs = [&](int s, int k) {
-        const uint32_t i = i0 + 2 * k + 1;
-        ok = ok && sy.wait(&bars[B_P + s], np[s] & 1);
-        ok = ok && sy.wait(&bars[B_FULL + i % L::NB], (i / L::NB) & 1);
-        if (!ok) return;
-        ++np[s];
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = sdesc_sw128(base + L::RING + (i % L::NB) * L::TILE, 16384, 1024);
-          const bool add = two ? k > 0 : k > 1;
-#pragma unroll
-          for (int e = 0; e < kKeys / 16; ++e)
-            mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + 8 * e, vd + e * (2048 >> 4), id_o, add || e > 0);
-          mma_commit(&bars[B_O + s]);
-          if (!two || s == 1) mma_commit(&bars[B_EMPTY + i % L::NB]);
-        }
-        __syncwarp();
-      };
-      if (two) {
-        scores(0, 0);
-        scores(1, 0);
-        for (int k = 0; ok && k < nt; ++k)
-          for (int s = 0; ok && s < 2; ++s) {
-            outputs(s, k);
-            if (k + 1 < nt) scores(s, k + 1);
+      const int steps = two ? 2 * nt : nt;
+      int is = 0, io = 0, ready = 0;  // steps whose scores and outputs are under way; slots whose queries are there
+      uint64_t t0 = 0;
+      int spins = 0;
+#pragma unroll 1
+      while (io < steps) {
+        bool moved = false;
+        if (is < steps && is < io + kAhead) {
+          const int s = is & 1;
+          const uint32_t i = tile0 + (two ? is >> 1 : is), stage = i % L::NB;
+          if (!(ready >> s & 1) && mbar_poll(&bars[B_Q + s], (s ? nq1 : nq0) & 1)) {
+            ready |= 1 << s;
+            if (s) ++nq1; else ++nq0;
           }
-      } else {
-        scores(0, 0);
-        if (nt > 1) scores(1, 1);
-        for (int k = 0; ok && k < nt; ++k) {
-          outputs(k & 1, k);
-          if (k + 2 < nt) scores(k & 1, k + 2);
+          if ((ready >> s & 1) && mbar_poll(&bars[B_FULL + stage], (i / L::NB) & 1)) {
+            const uint32_t buf = (s ? ns1 : ns0) & 1;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(
+                  tmem + T_S + 128 * s + 64 * buf, sdesc_sw128(base + L::Q + s * L::QT, 16, 1024),
+                  sdesc_sw128(base + L::RING + stage * 2 * L::TILE, 16, 1024), id_s);
+              mma_commit(&bars[B_S + 2 * s + buf]);
+            }
+            __syncwarp();
+            if (s) ++ns1; else ++ns0;
+            ++is;
+            moved = true;
+          }
+        }
+        if (io < is) {
+          const int s = io & 1;
+          const uint32_t np = s ? np1 : np0, buf = np & 1;
+          if (mbar_poll(&bars[B_P + 2 * s + buf], (np >> 1) & 1)) {
+            const uint32_t i = tile0 + (two ? io >> 1 : io), stage = i % L::NB;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = sdesc_sw128(base + L::RING + stage * 2 * L::TILE + L::TILE, L::HALF, 1024);
+#pragma unroll
+              for (int e = 0; e < kKeys / 16; ++e)
+                mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + 64 * buf + 8 * e, vd + e * (2048 >> 4), id_o,
+                            io > 1 || e > 0);
+              mma_commit(&bars[B_O + s]);
+              if (!two || s == 1) mma_commit(&bars[B_EMPTY + stage]);
+            }
+            __syncwarp();
+            if (s) ++np1; else ++np0;
+            ++io;
+            moved = true;
+          }
+        }
+        if (moved) {
+          spins = 0;
+          t0 = 0;
+        } else if (++spins > 256) {
+          spins = 0;
+          const uint64_t now = globaltimer_ns();
+          if (t0 == 0) t0 = now;
+          const bool over = *s_dead || ((now - t0) >> 10) > (uint32_t)a.budget;
+          if (__any_sync(0xffffffffu, over)) {
+            if (lane == 0 && !*s_dead) {
+              if (p.status) atomicExch(p.status, kDevTimeout);
+              *s_dead = 1;
+            }
+            ok = false;
+            break;
+          }
         }
       }
-      i0 += 2 * nt;
+      tile0 += nt;
     }
-    if (*s_dead) {  // products in flight end before their operands and columns go away
+    if (!ok) {  // products in flight end before their operands and columns go away
       if (elect_one()) mma_commit(&bars[B_END]);
       for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END], 0, 20000); ++tries) {}
     }
@@ -579,7 +584,7 @@ void wait_fault(int arm, unsigned long long budget_ns) {
 cudaError_t launch_tc(const Problem& p, uint8_t* ws) {
   TcArgs a{};
   a.p = p;
-  set_layout(a, layout(sm_count(), (int64_t)p.T * p.G, kRows, p.DV), ws, sm_count(), 1);
+  set_layout(a, layout(sm_count(), (int64_t)p.T * p.G, kRows, p.DV), ws, sm_count());
   a.g = 8;
   while (a.g < kKeys && p.block % (2 * a.g) == 0) a.g *= 2;
   a.budget = (int)(g_budget_ns.load() >> 10);

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "fast_div.cuh"
 #include "gdp_internal.cuh"
 
 namespace gdp {
@@ -29,20 +30,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostDim = 1024;  // of a head
-
-// Division by a number that the launch knows: n / d for n < 2^31.
-struct Div {
-  uint32_t d, mul, shift;
-};
-Div div_by(uint32_t d) {
-  uint32_t l = 0;
-  while (l < 32 && (1ull << l) < d) ++l;
-  const uint64_t m = (((1ull << l) - d) << 32) / d + 1;
-  return {d, (uint32_t)m, l};
-}
-__device__ __forceinline__ uint32_t quot(uint32_t n, const Div& v) {
-  return (uint32_t)(((uint64_t)__umulhi(n, v.mul) + n) >> v.shift);
-}
 
 // One tensor [B, T, H, D] of a call: rows of `per_head` steps, the first `pairs` of them rotated.
 struct Rows {
