@@ -34,9 +34,8 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 256, kKeys = 64;
-constexpr int kLoad = 8, kMma = 9;  // warps; 0 to 3 and 4 to 7 are the slots'
-constexpr int kThreads = 320;
-constexpr int kAhead = 4;           // scores formed before their outputs: two buffers for each slot
+constexpr int kLoad = 8, kMma = 9;  // warps; 0 to 3 and 4 to 7 are the slots', 9 and 10 issue their products
+constexpr int kThreads = 352;
 constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
 
 template <int KD>
@@ -52,9 +51,10 @@ struct Lay {
   static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-// by stage: full, empty; by slot and buffer: scores, weights; by slot: outputs, queries; a piece's two slots
-// have left their maxima, have read each other's outputs
-enum { B_FULL = 0, B_EMPTY = 10, B_S = 20, B_P = 24, B_O = 28, B_Q = 30, B_JOIN = 32, B_DONE, B_END, B_N };
+// by stage: full, empty; by slot and buffer: scores, weights, outputs (of the buffer's tile: a waiter may be two
+// tiles behind, which one barrier's parity cannot tell from none); by slot: queries; a piece's two slots have left
+// their maxima, have read each other's outputs
+enum { B_FULL = 0, B_EMPTY = 10, B_S = 20, B_P = 24, B_O = 28, B_Q = 32, B_JOIN = 34, B_DONE, B_END, B_N = B_END + 2 };
 constexpr uint32_t T_S = 0, T_O = 256;  // columns: S [2][2][64], O [2][128]
 
 struct TcArgs : Args {
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid >= B_P && tid < B_O) n = 4;                                // warps of the slot
     if (tid >= B_Q && tid < B_JOIN) n = 4;
     if (tid == B_JOIN || tid == B_DONE) n = 8;
+    if (tid >= B_EMPTY && tid < B_S) n = 2;                            // both slots
     if (tid == B_S && a.fault && blockIdx.x == 0) n = 2;
     mbar_init(&bars[tid], n);
     fence_mbar_init();
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mn;
             l *= f;
             if (k > 0) {  // the last product into O is done, then O is scaled
-              ok = sy.wait(&bars[B_O + slot], (n - 1) & 1);
+              ok = sy.wait(&bars[B_O + 2 * slot + (buf ^ 1)], (n - 1) >> 1 & 1);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -312,12 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // slots' outputs lie in the same lanes of tensor memory.)
       const bool join = !d.two && nt > 1;
       float f0 = 1.f, f1 = 0.f;  // of this slot's and of the other's outputs
-      if (d.n > 0) ok = sy.wait(&bars[B_O + slot], (n - 1) & 1);
+      if (d.n > 0) ok = sy.wait(&bars[B_O + 2 * slot + ((n - 1) & 1)], (n - 1) >> 1 & 1);
       if (join) {
         s_ml[slot * 128 + row] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_JOIN]);
-        ok = ok && sy.wait(&bars[B_JOIN], joins & 1) && sy.wait(&bars[B_O + (slot ^ 1)], (other - 1) & 1);
+        ok = ok && sy.wait(&bars[B_JOIN], joins & 1) && 
+             sy.wait(&bars[B_O + 2 * (slot ^ 1) + ((other - 1) & 1)], (other - 1) >> 1 & 1);
         if (!ok) break;
         ++joins;
         owe = true;
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         T* dst = static_cast<T*>(p.o) + out_at(p, x.first, x.head, d.row0 + min(row, d.rows - 1));
         if (whole) { f0 *= inv; f1 *= inv; }
         const int q0 = join && slot ? KD / 2 : 0, q1 = join && !slot ? KD / 2 : KD;
+        __syncwarp();
 #pragma unroll 1
         for (int q = q0; q < q1; q += 8) {
           uint32_t o[8], u[8];
@@ -353,14 +356,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[e] = __uint_as_float(o[e]) * f0;
             if (join) y[e] = fmaf(f1, __uint_as_float(u[e]), y[e]);
           }
-          if (!on || q >= p.DV) continue;
-          if (whole) {
-            *reinterpret_cast<uint4*>(dst + q) = make_uint4(pack<T>(y[0], y[1]), pack<T>(y[2], y[3]),
-                                                            pack<T>(y[4], y[5]), pack<T>(y[6], y[7]));
-          } else {  // quads of columns outermost: lanes are side by side
-            part[(q >> 2) * a.cap] = make_float4(y[0], y[1], y[2], y[3]);
-            part[((q >> 2) + 1) * a.cap] = make_float4(y[4], y[5], y[6], y[7]);
+          if (on && q < p.DV) {
+            if (whole) {
+              *reinterpret_cast<uint4*>(dst + q) = make_uint4(pack<T>(y[0], y[1]), pack<T>(y[2], y[3]),
+                                                              pack<T>(y[4], y[5]), pack<T>(y[6], y[7]));
+            } else {  // quads of columns outermost: lanes are side by side
+              part[(q >> 2) * a.cap] = make_float4(y[0], y[1], y[2], y[3]);
+              part[((q >> 2) + 1) * a.cap] = make_float4(y[4], y[5], y[6], y[7]);
+            }
           }
+          __syncwarp();  // (the loads from tensor memory are the whole warp's)
         }
       }
       tc_fence_before();
@@ -417,70 +422,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         place = place1;
       }
     }
-    if (*s_dead)  // copies in flight land before the CTA leaves
+    // the last stages' commits land before the CTA leaves, and so do copies in flight where a wait ran out
+    for (uint32_t b = i > L::NB ? i - L::NB : 0; ok && b < i; ++b)
+      ok = sy.wait(&bars[B_EMPTY + b % L::NB], (b / L::NB) & 1);
+    if (*s_dead)
       for (uint32_t b = i > L::NB ? i - L::NB : 0; b < i; ++b)
         for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_FULL + b % L::NB], (b / L::NB) & 1, 20000); ++tries) {}
   } else {
     // ---------------------------------------------------------------- products
-    // Steps of a piece: its tiles in turn, for both slots where they have rows of their own. Scores are
-    // formed up to four steps ahead of the outputs, whichever of the two can be first.
+    // A warp for each slot (a step of its loop, four waits and twelve products, takes 1000 cycles: with one
+    // warp for both a tile of 2 x 128 rows took 2800, and a decode step's tile 1400). Scores are formed up to two
+    // tiles ahead of the outputs, whichever of the two can be first.
+    const int slot = warp - kMma;
     const uint32_t id_s = idesc<T>(128, kKeys, false) | (p.c < 0.f ? 1u << 13 : 0u);  // (-Q)
     constexpr uint32_t id_o = idesc<T>(128, KD, true);
-    const uint32_t base = smem_u32(sm);
-    uint32_t tile0 = 0, ns0 = 0, ns1 = 0, np0 = 0, np1 = 0, nq0 = 0, nq1 = 0;  // tiles; per slot: scores, weights, queries
+    const uint32_t base = smem_u32(sm), ts = tmem + T_S + 128 * slot, to = tmem + T_O + 128 * slot;
+    const uint64_t qd = sdesc_sw128(base + L::Q + slot * L::QT, 16, 1024);
+    const uint64_t kd = sdesc_sw128(base + L::RING, 16, 1024);
+    const uint64_t vd = sdesc_sw128(base + L::RING + L::TILE, L::HALF, 1024);
+    auto poll = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_poll(bar, parity)); };
+    uint32_t tile0 = 0, ns = 0, np = 0, nq = 0;  // tiles of the CTA; this slot's scores, weights, queries
 #pragma unroll 1
     while (ok && walk.next(p, x)) {
+      const Spread d(x, slot);
       const int nt = x.j1 - x.j0;
-      const bool two = x.rows > 128;
-      const int steps = two ? 2 * nt : nt;
-      int is = 0, io = 0, ready = 0;  // steps whose scores and outputs are under way; slots whose queries are there
+      // stages of the next tile and of the next outputs
+      uint32_t ks = tile0 % L::NB, kt = tile0 / L::NB & 1, os = (tile0 + (d.two ? 0 : slot)) % L::NB;
+      int k = 0, is = 0, io = 0, done = 0;  // tiles whose scores and outputs are under way, whose outputs are complete
+      bool queries = false;
       uint64_t t0 = 0;
       int spins = 0;
 #pragma unroll 1
-      while (io < steps) {
-        bool moved = false;
-        if (is < steps && is < io + kAhead) {
-          const int s = is & 1;
-          const uint32_t i = tile0 + (two ? is >> 1 : is), stage = i % L::NB;
-          if (!(ready >> s & 1) && mbar_poll(&bars[B_Q + s], (s ? nq1 : nq0) & 1)) {
-            ready |= 1 << s;
-            if (s) ++nq1; else ++nq0;
+      while (io < d.n || k < nt) {
+        bool moved = false, seen = false;
+        // (products into different columns may overtake one another: scores go over weights only once those
+        // have been multiplied)
+        if (done < io && poll(&bars[B_O + 2 * slot + ((np - 1) & 1)], (np - 1) >> 1 & 1)) done = io;
+        // Every tile is waited for in turn, the other slot's too, and both slots release its stage: a warp that
+        // skipped tiles could take a stage's last but one load for the last (a parity tells only two apart).
+        if (k < nt && (!d.two && (k & 1) != slot)) {
+          if (poll(&bars[B_FULL + ks], kt)) {
+            if (lane == 0) mbar_arrive(&bars[B_EMPTY + ks]);
+            seen = true;
           }
-          if ((ready >> s & 1) && mbar_poll(&bars[B_FULL + stage], (i / L::NB) & 1)) {
-            const uint32_t buf = (s ? ns1 : ns0) & 1;
+        } else if (k < nt && is < done + 2) {
+          if (!queries) queries = poll(&bars[B_Q + slot], nq & 1);
+          if (queries && poll(&bars[B_FULL + ks], kt)) {
+            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
-              mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(
-                  tmem + T_S + 128 * s + 64 * buf, sdesc_sw128(base + L::Q + s * L::QT, 16, 1024),
-                  sdesc_sw128(base + L::RING + stage * 2 * L::TILE, 16, 1024), id_s);
-              mma_commit(&bars[B_S + 2 * s + buf]);
+              mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(ts + 64 * (ns & 1), qd, kd + ks * (2 * L::TILE >> 4), id_s);
+              mma_commit(&bars[B_S + 2 * slot + (ns & 1)]);
             }
             __syncwarp();
-            if (s) ++ns1; else ++ns0;
+            ++ns;
             ++is;
-            moved = true;
+            seen = true;
           }
         }
-        if (io < is) {
-          const int s = io & 1;
-          const uint32_t np = s ? np1 : np0, buf = np & 1;
-          if (mbar_poll(&bars[B_P + 2 * s + buf], (np >> 1) & 1)) {
-            const uint32_t i = tile0 + (two ? io >> 1 : io), stage = i % L::NB;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t vd = sdesc_sw128(base + L::RING + stage * 2 * L::TILE + L::TILE, L::HALF, 1024);
+        if (seen) {
+          ++k;
+          if (++ks == L::NB) { ks = 0; kt ^= 1; }
+          moved = true;
+        }
+        if (io < is && done == io && poll(&bars[B_P + 2 * slot + (np & 1)], np >> 1 & 1)) {
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v = vd + os * (2 * L::TILE >> 4);
 #pragma unroll
-              for (int e = 0; e < kKeys / 16; ++e)
-                mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + 64 * buf + 8 * e, vd + e * (2048 >> 4), id_o,
-                            io > 1 || e > 0);
-              mma_commit(&bars[B_O + s]);
-              if (!two || s == 1) mma_commit(&bars[B_EMPTY + stage]);
-            }
-            __syncwarp();
-            if (s) ++np1; else ++np0;
-            ++io;
-            moved = true;
+            for (int e = 0; e < kKeys / 16; ++e)
+              mma_bf16_ts(to, ts + 64 * (np & 1) + 8 * e, v + e * (2048 >> 4), id_o, io > 0 || e > 0);
+            mma_commit(&bars[B_O + 2 * slot + (np & 1)]);
+            mma_commit(&bars[B_EMPTY + os]);
           }
+          __syncwarp();
+          ++np;
+          ++io;
+          os += d.two ? 1 : 2;
+          if (os >= L::NB) os -= L::NB;
+          moved = true;
         }
         if (moved) {
           spins = 0;
@@ -500,11 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (queries) ++nq;
       tile0 += nt;
     }
     if (!ok) {  // products in flight end before their operands and columns go away
-      if (elect_one()) mma_commit(&bars[B_END]);
-      for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END], 0, 20000); ++tries) {}
+      if (elect_one()) mma_commit(&bars[B_END + slot]);
+      for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END + slot], 0, 20000); ++tries) {}
     }
   }
   __syncwarp();

@@ -380,3 +380,21 @@ def test_step_of_a_server(gdp):
     step([4, 4, 4], torch.tensor([bits * 3], device=DEV), torch.tensor([0, 1, 1, 2] * 3, **i32),
          [[0, 2], [0, 1, 3], [0]])
     step([1, 1, 1])
+
+
+@pytest.mark.parametrize("lens,ctx", [([1] * 96, list(range(40, 4840, 50))), ([64, 33, 64, 50], [3000, 700, 64, 2000]),
+                                      ([500, 260], [100, 900])])
+def test_many_pieces_many_times(gdp, lens, ctx):
+    """Many pieces on every CTA, launched back to back and from idle with cold caches: the same bits."""
+    d = problem(lens, ctx, 32, 8, 128, 128, 64, BF)
+    want = gdp.gdp_attention_paged(**d)
+    flush = torch.empty(400 << 20, dtype=torch.uint8, device=DEV)
+    got = []
+    for i in range(30):
+        if i % 3 == 1:
+            flush.zero_()
+        if i % 5 == 1:
+            torch.cuda.synchronize()
+        got.append(gdp.gdp_attention_paged(**d))
+    assert all(torch.equal(x, want) for x in got)
+    check(gdp, d)
