@@ -344,8 +344,8 @@ gdp_status gdp_chunk_fwd_noalloc(const void* q, const void* k, const void* v, co
  *            disarms itself. arm = 2: the next linear-attention call that runs the
  *            tensor-core kernel (bf16, K <= 128) waits in the first CTA of its
  *            first launch for one commit more than are made; likewise one-shot. arm = 3:
- *            the same for gdp_attention_paged on the tensor cores (16-bit types, D and DV
- *            <= 128).
+ *            the same in every CTA of the next gdp_attention_paged on the tensor cores
+ *            (16-bit types, D and DV <= 128).
  *            arm = 0: disarm.
  *   budget_seconds: new wait budget (0 < budget <= 10), or <= 0 for the
  *            default 2 s. The budget applies to every later launch until
@@ -607,7 +607,8 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  *           each. Query head h reads key head h / (H / HKV).
  *   caches  as in gdp_cache_append. block_tables [N_seq, max_blocks] int32 names the page of
  *           each block of block_size positions; -1: the block is not there (none of its
- *           positions is seen), which also makes padding requests, whose o rows are 0.
+ *           positions is seen). A request whose last new token has no page (-1) is padding:
+ *           its o rows are 0.
  *   context_lens [N_seq] int32: positions before the request's first new token, which is
  *           position context_lens[r] of the cache, the next one the position after it.
  *   tree_mask (nullable) [B, T] int64: bit j of a token: it sees the request's new token j

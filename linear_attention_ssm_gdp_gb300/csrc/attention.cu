@@ -33,7 +33,6 @@ __host__ __device__ inline SimpleSmem simple_smem(int D, int DV) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant__ Args a) {
-  using C = Cut<kRows, kKeys>;
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Start s_start;
   __shared__ long long s_scan[kThreads / 32 + 1];
@@ -50,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   find_start<kRows, kKeys, kThreads>(a, &s_start, s_scan);
-  Walk<kRows, kKeys> walk(s_start);
+  Walk<kRows, kKeys> walk(s_start, a.cost);
   Piece x;
   bool rec = false;
   const int quads = L.sv / 4;
@@ -184,17 +183,17 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
       }
     if (x.slot == 1) {
       rec = true;
-      if (tid == 0) write_rec(a, s_start, &x, walk.at - (x.j1 - x.j0));
+      if (tid == 0) write_rec(a, s_start, &x);
     }
   }
-  if (!rec && tid == 0) write_rec(a, s_start, nullptr, 0);
+  if (!rec && tid == 0) write_rec(a, s_start, nullptr);
 }
 
 // ------------------------------------------------------------------ joining cut items
-// A CTA of the grid's x per record and 32 rows (or fewer: kJoinRows), a thread per row and quad of
-// columns: the pieces' maxima give the factors 2^(m_i - m), applied in the order of the pieces. Maxima
-// and factors of 32 pieces at a time go through shared memory; outputs lie with rows side by side.
-constexpr int kJoin = 256, kJoinPieces = 32;
+// A CTA of the grid's x per record and 8 rows (so that one cut item is joined by several), a thread per
+// row and quad of columns: the pieces' maxima give the factors 2^(m_i - m), applied in the order of the pieces. Maxima
+// and factors of 64 pieces at a time go through shared memory; outputs lie with rows side by side.
+constexpr int kJoin = 256, kJoinPieces = 64, kJoinRows = 8;
 
 template <typename T>
 struct alignas(4 * sizeof(T)) Quad {
@@ -203,7 +202,7 @@ struct alignas(4 * sizeof(T)) Quad {
 
 template <typename T>
 __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Args a, int rows /* power of two */) {
-  __shared__ float s_f[kJoinPieces][33];
+  __shared__ float s_f[kJoinPieces][kJoinRows + 1];
   __shared__ float s_m[kJoin], s_l[kJoin];
   pdl_wait();
   const Rec r = a.recs[blockIdx.x];
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Arg
       if (mine) {
         const float4* src = reinterpret_cast<const float4*>(a.part) + (int64_t)q0 * a.cap + row0 + row;
         const int64_t step = (int64_t)a.cap * quads;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < n; ++i) {
           const float4 v = src[at(i0 + i) * step];
           const float f = s_f[i][row];
@@ -287,7 +286,7 @@ size_t simple_workspace(int64_t rows, int DV) { return layout(simple_ctas(), row
 
 cudaError_t launch_combine(const Args& a) {
   int rows = 1;
-  while (rows < 32 && rows < a.cap) rows *= 2;
+  while (rows < kJoinRows && rows < a.cap) rows *= 2;
   const dim3 grid(a.ctas, (a.cap + rows - 1) / rows), block(kJoin);
   switch (a.p.dt) {
     case GDP_BF16: return launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, a.p.stream, a, rows);
@@ -309,6 +308,7 @@ cudaError_t launch_simple(const Problem& p, uint8_t* ws) {
   Args a{};
   a.p = p;
   set_layout(a, layout(simple_ctas(), (int64_t)p.T * p.G, kRows, p.DV), ws, simple_ctas());
+  a.cost = {4, 8, 4, 8};
   cudaError_t e;
   switch (p.dt) {
     case GDP_BF16: e = go<__nv_bfloat16>(a); break;

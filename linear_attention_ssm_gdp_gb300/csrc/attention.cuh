@@ -1,13 +1,13 @@
 // Shared by the kernels of attention over a paged cache: the problem, and how its work is cut.
 //
 // An item is a tile of BM rows (a row: a token and one of the G query heads that share a key head)
-// of one request and key head, and costs as many units as it has tiles of KT keys to see. The units
-// of all items in order are cut into equal shares, one per CTA, so that a long context is spread
-// over many CTAs and a batch of ragged ones ends evenly; contexts are known on the device only, so
-// every CTA adds up the requests' units by itself and finds the start of its share. A share covers
-// whole items and at most two cut ones (its first and its last piece). Pieces of cut items leave
-// their row maxima, sums and unnormalised outputs in the workspace, and the combine kernel joins
-// them in order.
+// of one request and key head. Its cost is what it takes to begin and end it and its tiles of KT keys,
+// in units of about 0.3 us. The costs of all items in order are cut into equal shares, one per CTA, so
+// that a long context is spread over many CTAs and a batch of ragged ones ends evenly; contexts are
+// known on the device only, so every CTA adds up the requests' costs by itself and finds the start of
+// its share. A share covers whole items and at most two cut ones (its first and its last piece). Pieces
+// of cut items leave their row maxima, sums and unnormalised outputs in the workspace, and the join
+// kernel joins them in order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -45,8 +45,14 @@ struct Rec {
   int row0, rows, head, more;     // rows == 0: none; more: CTAs after this one that hold pieces
 };
 
+// The begin and end of an item and a tile of keys, for items of up to 128 rows and for larger ones.
+struct Cost {
+  int begin, tile, begin2, tile2;
+};
+
 struct Args {
   Problem p;
+  Cost cost;
   Rec* recs;                      // [ctas]
   float* part;                    // [ctas][2][dvp / 4][cap][4] outputs
   float2* ml;                     // [ctas][2][cap] row maximum (log2) and sum
@@ -68,16 +74,19 @@ inline Layout layout(int ctas, int64_t rows, int bm, int DV) {
   return x;
 }
 
-// What the rows of one request are; L == 0: nothing to see (an invalid request, whose rows are 0).
+// What the rows of one request are. A request that is not `live` sees nothing (its rows are 0): padding, whose
+// last new token has no page, or `bad` lengths.
 struct Req {
   int S, ctx;
-  bool ok;
+  bool live, bad;
 };
 __device__ __forceinline__ Req request(const Problem& p, int r) {
   Req x;
   x.S = p.cu ? p.cu[r + 1] - p.cu[r] : p.T;
   x.ctx = p.ctx[r];
-  x.ok = x.ctx >= 0 && (int64_t)x.ctx + x.S <= (int64_t)p.width * p.block && !(p.tree && x.S > 64);
+  x.bad = x.ctx < 0 || (int64_t)x.ctx + x.S > (int64_t)p.width * p.block || (p.tree && x.S > 64);
+  x.live = !x.bad && x.S > 0 &&
+           p.tables[(int64_t)r * p.width + quot(x.ctx + x.S - 1, p.by_block)] >= 0;
   return x;
 }
 __device__ __forceinline__ int64_t first_row(const Problem& p, int r) {
@@ -90,28 +99,42 @@ struct Cut {
   __device__ static __forceinline__ int tiles(const Problem& p, int S) { return (S * p.G + BM - 1) / BM; }
   // keys that the rows of a tile see at most
   __device__ static __forceinline__ int keys(const Problem& p, const Req& x, int tile) {
-    if (!x.ok) return 0;
+    if (!x.live) return 0;
     if (p.tree) return x.ctx + x.S;
     const int last = min((tile + 1) * BM, x.S * p.G) - 1;
     return x.ctx + (int)quot(last, p.by_G) + 1;
   }
   __device__ static __forceinline__ int units(int keys) { return keys > 0 ? (keys + KT - 1) / KT : 1; }
+  __device__ static __forceinline__ bool large(const Problem& p, const Req& x, int tile) {
+    return BM > 128 && x.S * p.G - tile * BM > 128;
+  }
+  __device__ static __forceinline__ int begin(const Cost& c, bool large) { return large ? c.begin2 : c.begin; }
+  __device__ static __forceinline__ int each(const Cost& c, bool large) { return large ? c.tile2 : c.tile; }
+  __device__ static __forceinline__ int64_t cost(const Problem& p, const Cost& c, const Req& x, int tile) {
+    const bool l = large(p, x, tile);
+    return begin(c, l) + (int64_t)units(keys(p, x, tile)) * each(c, l);
+  }
   // of one head of a request
-  __device__ static __forceinline__ int64_t head_units(const Problem& p, const Req& x) {
+  __device__ static __forceinline__ int64_t head_cost(const Problem& p, const Cost& c, const Req& x) {
     if (x.S <= 0) return 0;
     const int n = tiles(p, x.S);
     int64_t u = 0;
-    for (int i = 0; i < n; ++i) u += units(keys(p, x, i));
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) u += cost(p, c, x, i);
     return u;
+  }
+  // tiles of an item's keys that lie before a cut `at` units behind its begin
+  __device__ static __forceinline__ int before(const Cost& c, bool large, long long at, int units) {
+    const int each_ = each(c, large);
+    at -= begin(c, large);
+    return at <= 0 ? 0 : at >= (long long)units * each_ ? units : ((int)at + each_ - 1) / each_;
   }
 };
 
-// Where a CTA's share begins, and its length.
+// Where a CTA's share begins: an item, and how far in it; its length in units.
 struct Start {
-  int r, head, tile, j;
-  long long left, total, ctas;
-  long long at;  // absolute unit
-  int bad;
+  int r, head, tile, bad;
+  long long in, left, total, ctas, at;  // at: the share's first unit
 };
 
 // (32 bits where they do: the 64-bit division is a call of a hundred instructions.)
@@ -131,13 +154,13 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
   int bad = 0, odd = 0;
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
-    const Req x = request(p, r);
     if (p.cu) {
-      const int a0 = p.cu[r];
-      if (a0 < 0 || x.S < 0 || x.S > p.T - a0 || (r == 0 && a0 != 0)) { bad = 1; break; }
+      const int a0 = p.cu[r], a1 = p.cu[r + 1];
+      if (a0 < 0 || a1 < a0 || a1 > p.T || (r == 0 && a0 != 0)) { bad = 1; break; }
     }
-    if (!x.ok) odd = 1;
-    mine += C::head_units(p, x);
+    const Req x = request(p, r);
+    if (x.bad) odd = 1;
+    mine += C::head_cost(p, a.cost, x);
   }
   mine *= p.HKV;
   if (blockIdx.x == 0 && (odd || bad) && p.status) *p.status = GDP_ERR_INVALID_ARG;
@@ -157,9 +180,10 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  const long long ctas = min((long long)a.ctas, total);
+  // (no share is shorter than a tile, so that every CTA between a cut item's first and last has a piece)
+  const long long ctas = max(1ll, min((long long)a.ctas, total / max(a.cost.tile, a.cost.tile2)));
   if (tid == 0) { out->total = total; out->ctas = ctas; }
-  if (!bad && blockIdx.x < ctas) {
+  if (!bad && total > 0 && blockIdx.x < ctas) {
     // first unit of CTA c: floor(total c / ctas)
     const long long q = divide(total, ctas), rest = total - q * ctas;
     const long long u0 = q * blockIdx.x + divide(rest * blockIdx.x, ctas);
@@ -171,7 +195,7 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
 #pragma unroll 1
       for (;; ++r) {
         x = request(p, r);
-        head = C::head_units(p, x);
+        head = C::head_cost(p, a.cost, x);
         if (at < head * p.HKV) break;
         at -= head * p.HKV;
       }
@@ -180,14 +204,14 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
       int tile = 0;
 #pragma unroll 1
       for (;; ++tile) {
-        const int u = C::units(C::keys(p, x, tile));
+        const long long u = C::cost(p, a.cost, x, tile);
         if (at < u) break;
         at -= u;
       }
       out->r = r;
       out->head = (int)h;
       out->tile = tile;
-      out->j = (int)at;
+      out->in = at;
       out->left = q * (blockIdx.x + 1ll) + divide(rest * (blockIdx.x + 1ll), ctas) - u0;
       out->at = u0;
     }
@@ -210,38 +234,47 @@ struct Piece {
   int keys;            // that the tile sees
   int j0, j1, units;   // key tiles of this piece, of the item
   int slot;            // of the partial results; -1: the item is whole
+  long long end;       // the unit behind the first one of the item's last tile
 };
 
 template <int BM, int KT>
 struct Walk {
-  int r, head, tile, j;
-  long long left, at;
-  bool fresh;
-  __device__ __forceinline__ explicit Walk(const Start& s)
-      : r(s.r), head(s.head), tile(s.tile), j(s.j), left(s.left), at(s.at), fresh(true) {}
+  using C = Cut<BM, KT>;
+  Cost cost;
+  int r, head, tile;
+  long long in, left, at;  // at: the item's first unit
+  __device__ __forceinline__ Walk(const Start& s, const Cost& c)
+      : cost(c), r(s.r), head(s.head), tile(s.tile), in(s.in), left(s.left), at(s.at - s.in) {}
   __device__ __forceinline__ bool next(const Problem& p, Piece& x) {
-    if (left <= 0) return false;
-    x.x = request(p, r);
-    while (x.x.S <= 0) x.x = request(p, ++r);  // (units are left, so there is one)
-    x.first = first_row(p, r);
-    x.r = r;
-    x.head = head;
-    x.tile = tile;
-    x.row0 = tile * BM;
-    x.rows = min(BM, x.x.S * p.G - x.row0);
-    x.keys = Cut<BM, KT>::keys(p, x.x, tile);
-    x.units = Cut<BM, KT>::units(x.keys);
-    x.j0 = j;
-    x.j1 = (int)min((long long)x.units, j + left);
-    x.slot = j == 0 && x.j1 == x.units ? -1 : j == 0 ? 1 : 0;
-    left -= x.j1 - j;
-    at += x.j1 - j;
-    j = 0;
-    if (++tile == Cut<BM, KT>::tiles(p, x.x.S)) {
-      tile = 0;
-      if (++head == p.HKV) { head = 0; ++r; }
+#pragma unroll 1
+    while (left > 0) {
+      x.x = request(p, r);
+      while (x.x.S <= 0) x.x = request(p, ++r);  // (units are left, so there is one)
+      x.first = first_row(p, r);
+      x.r = r;
+      x.head = head;
+      x.tile = tile;
+      x.row0 = tile * BM;
+      x.rows = min(BM, x.x.S * p.G - x.row0);
+      x.keys = C::keys(p, x.x, tile);
+      x.units = C::units(x.keys);
+      const bool large = C::large(p, x.x, tile);
+      const long long all = C::begin(cost, large) + (long long)x.units * C::each(cost, large);
+      x.j0 = C::before(cost, large, in, x.units);
+      x.j1 = C::before(cost, large, in + left, x.units);
+      x.slot = x.j0 == 0 && x.j1 == x.units ? -1 : x.j0 == 0 ? 1 : 0;
+      // the unit in which the last tile begins, for the record of a cut item
+      x.end = at + all - C::each(cost, large) + 1;
+      left -= all - in;
+      at += all;
+      in = 0;
+      if (++tile == C::tiles(p, x.x.S)) {
+        tile = 0;
+        if (++head == p.HKV) { head = 0; ++r; }
+      }
+      if (x.j1 > x.j0) return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -252,7 +285,7 @@ __device__ __forceinline__ int64_t out_at(const Problem& p, int64_t first, int h
 }
 
 // The record of a CTA's share: the piece that begins an item which goes on elsewhere, if there is one.
-__device__ __forceinline__ void write_rec(const Args& a, const Start& s, const Piece* x, long long begin) {
+__device__ __forceinline__ void write_rec(const Args& a, const Start& s, const Piece* x) {
   Rec& r = a.recs[blockIdx.x];
   if (!x) {
     r.rows = 0;
@@ -262,7 +295,7 @@ __device__ __forceinline__ void write_rec(const Args& a, const Start& s, const P
   r.row0 = x->row0;
   r.rows = x->rows;
   r.head = x->head;
-  r.more = last_cta(begin + x->units, s.ctas, s.total) - (int)blockIdx.x;
+  r.more = last_cta(x->end, s.ctas, s.total) - (int)blockIdx.x;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -34,33 +34,41 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 256, kKeys = 64;
-constexpr int kLoad = 8, kMma = 9;  // warps; 0 to 3 and 4 to 7 are the slots', 9 and 10 issue their products
-constexpr int kThreads = 352;
+constexpr int kLoad = 8, kScores = 10, kOutputs = 11;  // warps; 0 to 3 and 4 to 7 are the slots', 8 and 9 load K and V
+constexpr int kThreads = 384;
+constexpr Cost kCost = {10, 2, 22, 3};
 constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
 
 template <int KD>
 struct Lay {
-  static constexpr int NB = KD == 128 ? 5 : 10;  // stages of the ring, a tile of K and one of V each
+  // Buffers of K and of V. A tile of K is free when its scores are formed, one of V two thousand cycles later:
+  // with as many of V as of K in common stages a decode step had too few loads in flight.
+  static constexpr int NK = KD == 128 ? 4 : 8, NV = KD == 128 ? 6 : 12;
   static constexpr int HALF = kKeys * 128;       // 64 columns of a tile: 64 rows of 128 bytes
   static constexpr int TILE = KD / 64 * HALF;
   static constexpr int QT = KD / 64 * 16384;     // 128 rows of queries
-  static constexpr int Q = 0, RING = 2 * QT;
-  static constexpr int BAR = RING + NB * 2 * TILE;
-  static constexpr int ML = BAR + 384;           // maxima and sums [2][128]
+  static constexpr int Q = 0, K = 2 * QT, V = K + NK * TILE;
+  static constexpr int BAR = V + NV * TILE;
+  static constexpr int ML = BAR + 640;           // maxima and sums [2][128]
   static constexpr int START = ML + 2048;        // the share, and the sums that lead to it
   static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-// by stage: full, empty; by slot and buffer: scores, weights, outputs (of the buffer's tile: a waiter may be two
-// tiles behind, which one barrier's parity cannot tell from none); by slot: queries; a piece's two slots have left
-// their maxima, have read each other's outputs
-enum { B_FULL = 0, B_EMPTY = 10, B_S = 20, B_P = 24, B_O = 28, B_Q = 32, B_JOIN = 34, B_DONE, B_END, B_N = B_END + 2 };
-constexpr uint32_t T_S = 0, T_O = 256;  // columns: S [2][2][64], O [2][128]
+// by buffer: K full, empty, V full, empty, absent boxes known; by slot: scores formed, read; by slot and buffer:
+// weights, outputs (of that tile: a waiter may be two tiles behind, which one barrier's parity cannot tell from
+// none); by slot: queries; a piece's two slots have left their maxima, have read each other's outputs
+enum {
+  B_KFULL = 0, B_KEMPTY = 8, B_VFULL = 16, B_VEMPTY = 28, B_META = 40, B_S = 52, B_R = 54, B_P = 56, B_O = 60, B_Q = 64,
+  B_JOIN = 66, B_DONE, B_END, B_N = B_END + 2
+};
+// columns: by slot, scores [64] and weights [2][32] (16-bit pairs); outputs [2][128]
+constexpr uint32_t T_S = 0, T_P = 64, T_O = 256;
 
 struct TcArgs : Args {
   int g;          // keys of a box
+  int halves;     // of 64 columns in a box
   int budget;     // limit of a wait, in units of 1024 ns
-  int fault;      // test hook (gdp_debug_wait_fault): CTA 0 waits for a commit more of its first scores
+  int fault;      // test hook (gdp_debug_wait_fault): every CTA waits for a commit more of its first scores
 };
 
 // ------------------------------------------------------------------ waits
@@ -103,16 +111,8 @@ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return sizeof(T) == 2 && std::is_same<T, __half>::value ? idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10))
                                                           : idesc_bf16(M, N, false, b_mn);
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-// The lowest n bits (n outside 0 .. 32 is held to it).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// The lowest n of 64 bits (n outside 0 .. 64 is held to it).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
 // How a piece's tiles are spread over the slots.
 struct Spread {
@@ -135,29 +135,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + B_N);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint32_t* s_absent = s_tmem + 2;                                     // [NB]
+  uint32_t* s_absent = s_tmem + 2;                                     // [NV]
   float2* s_ml = reinterpret_cast<float2*>(sm + L::ML);                // [2][128]
   Start& s_start = *reinterpret_cast<Start*>(sm + L::START);
   long long* s_scan = reinterpret_cast<long long*>(sm + L::START + 96);  // [kThreads / 32]
-  static_assert(sizeof(Start) <= 96 && kThreads / 32 * 8 <= 96 && B_N * 8 + 8 + L::NB * 4 <= 384, "shared memory");
+  static_assert(sizeof(Start) <= 96 && kThreads / 32 * 8 <= 96 && B_N * 8 + 8 + L::NV * 4 <= 640, "shared memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const Problem& p = a.p;
 
-  if (warp == kMma) {
+  if (warp == kScores) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
   if (tid < B_N) {
     int n = 1;
-    if (tid >= B_P && tid < B_O) n = 4;                                // warps of the slot
-    if (tid >= B_Q && tid < B_JOIN) n = 4;
+    if ((tid >= B_R && tid < B_O) || (tid >= B_Q && tid < B_JOIN)) n = 4;                // warps of the slot
     if (tid == B_JOIN || tid == B_DONE) n = 8;
-    if (tid >= B_EMPTY && tid < B_S) n = 2;                            // both slots
-    if (tid == B_S && a.fault && blockIdx.x == 0) n = 2;
+    if (tid == B_S && a.fault) n = 2;
     mbar_init(&bars[tid], n);
     fence_mbar_init();
   }
-  if (tid == 64) *s_dead = 0;
+  if (tid == 96) *s_dead = 0;
   if (warp == kLoad && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -169,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const Sync sy{s_dead, a.budget, p.status};
-  Walk<kRows, kKeys> walk(s_start);
+  Walk<kRows, kKeys> walk(s_start, a.cost);
   Piece x;
   bool ok = true;
 
@@ -188,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(p, x)) {
       const Spread d(x, slot);
       if (d.n > 0) {  // Q: 16-byte chunks of the rows, zero behind the head's end
-#pragma unroll 1
+#pragma unroll 4
         for (int i = tid & 127; i < d.rows * (KD / 8); i += 128) {
           const int r = i / (KD / 8), ch = i % (KD / 8), R = d.row0 + r, t = (int)quot(R, p.by_G);
           const int h = x.head * p.G + R - t * p.G;
@@ -206,45 +204,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool live = quarter * 32 < d.rows;
       const int t = (int)quot(d.row0 + min(row, d.rows - 1), p.by_G);
-      const uint64_t bits = p.tree && x.x.ok ? (uint64_t)p.tree[x.first + t] : 0ull;
+      const uint64_t bits = p.tree && x.x.live ? (uint64_t)p.tree[x.first + t] : 0ull;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int k = 0; ok && k < d.n; ++k, ++n) {
         const int j = d.two ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
-        const uint32_t stage = (tile0 + j) % L::NB, turn = (tile0 + j) / L::NB;
-        const uint32_t buf = n & 1, tb = ts + 64 * buf;
-        ok = sy.wait(&bars[B_S + 2 * slot + buf], (n >> 1) & 1) && sy.wait(&bars[B_FULL + stage], turn & 1);
+        const uint32_t stage = (tile0 + j) % L::NV, turn = (tile0 + j) / L::NV;
+        const uint32_t buf = n & 1;
+        ok = sy.wait(&bars[B_S + slot], n & 1) && (!live || sy.wait(&bars[B_META + stage], turn & 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t absent = s_absent[stage];
+        const uint32_t absent = live ? s_absent[stage] : 0u;
+        uint32_t s[kKeys];
+        if (live) {
+          GDP_TMEM_LD32(ts, s);
+          GDP_TMEM_LD32(ts + 32, (s + 32));
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_R + slot]);  // the next tile's scores may come
         if (live) {
           if (key0 + kKeys > x.x.ctx || absent) {  // some of the keys are not seen by some row
-#pragma unroll 1
-            for (int q = 0; q < kKeys; q += 8) {
-              const int k0 = key0 + q;
-              uint32_t see;
-              if (p.tree) {
-                const int back = k0 - x.x.ctx;
-                see = low_bits(-back);
-                if (back > -8 && back < 64) see |= (uint32_t)(back >= 0 ? bits >> back : bits << -back);
-              } else {
-                see = low_bits(x.x.ctx + t + 1 - k0);
-              }
-              see &= low_bits(x.keys - k0);
-              if (absent >> (q / a.g) & 1) see = 0;
-              uint32_t s[8];
-              GDP_TMEM_LD8(tb + q, s);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) s[e] = see >> e & 1 ? s[e] : __float_as_uint(-INFINITY);
-              GDP_TMEM_ST8(tb + q, s);
+            uint64_t see;
+            if (p.tree) {
+              const int back = key0 - x.x.ctx;
+              see = low_bits(-back);
+              if (back > -kKeys && back < 64) see |= back >= 0 ? bits >> back : bits << -back;
+            } else {
+              see = low_bits(x.x.ctx + t + 1 - key0);
             }
-            tmem_wait_st();
+            see &= low_bits(x.keys - key0);
+            if (absent)
+#pragma unroll 1
+              for (int b = 0; b < kKeys; b += 8)
+                if (absent >> (b / a.g) & 1) see &= ~(0xffull << b);
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) {
+              const uint32_t half = (uint32_t)(see >> (e & 32));
+              s[e] = half >> (e & 31) & 1 ? s[e] : __float_as_uint(-INFINITY);
+            }
           }
-          uint32_t s[kKeys];
-          GDP_TMEM_LD32(tb, s);
-          GDP_TMEM_LD32(tb + 32, (s + 32));
-          tmem_wait_ld();
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
@@ -280,13 +280,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[2 * (e & 1) + 1] += p1;
             w[e] = pack<T>(p0, p1);
           }
-          GDP_TMEM_ST32(tb, w);
+          if (k > 1) {  // the weights that lie there have been multiplied
+            ok = sy.wait(&bars[B_O + 2 * slot + buf], (n >> 1) - 1 & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          GDP_TMEM_ST32(ts + T_P + 32 * buf, w);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
         const int z0 = x.keys - key0;
         if (z0 > 0 && z0 < kKeys && z0 % a.g) {  // rows of V behind the last key, in the last box
-          uint8_t* sv = sm + L::RING + stage * 2 * L::TILE + L::TILE;
+          ok = sy.wait(&bars[B_VFULL + stage], turn & 1);
+          if (!ok) break;
+          uint8_t* sv = sm + L::V + stage * L::TILE;
           const int z1 = (z0 + a.g - 1) / a.g * a.g;
 #pragma unroll 1
           for (int e = tid & 127; e < (z1 - z0) * (KD / 8); e += 128) {
@@ -345,24 +352,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q0 = join && slot ? KD / 2 : 0, q1 = join && !slot ? KD / 2 : KD;
         __syncwarp();
 #pragma unroll 1
-        for (int q = q0; q < q1; q += 8) {
-          uint32_t o[8], u[8];
-          GDP_TMEM_LD8(to + 128 * slot + q, o);
-          if (join) GDP_TMEM_LD8(to + 128 * (slot ^ 1) + q, u);
-          tmem_wait_ld();
-          float y[8];
+        for (int q = q0; q < q1; q += 32) {
+          uint32_t o[32];
+          GDP_TMEM_LD32(to + 128 * slot + q, o);
+          if (join) {
+            uint32_t u[32];
+            GDP_TMEM_LD32(to + 128 * (slot ^ 1) + q, u);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = __uint_as_float(o[e]) * f0;
-            if (join) y[e] = fmaf(f1, __uint_as_float(u[e]), y[e]);
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(f1, __uint_as_float(u[e]), __uint_as_float(o[e]) * f0));
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           }
-          if (on && q < p.DV) {
-            if (whole) {
-              *reinterpret_cast<uint4*>(dst + q) = make_uint4(pack<T>(y[0], y[1]), pack<T>(y[2], y[3]),
-                                                              pack<T>(y[4], y[5]), pack<T>(y[6], y[7]));
-            } else {  // quads of columns outermost: lanes are side by side
-              part[(q >> 2) * a.cap] = make_float4(y[0], y[1], y[2], y[3]);
-              part[((q >> 2) + 1) * a.cap] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const float* y = reinterpret_cast<const float*>(o + e);
+            if (on && q + e < p.DV) {
+              if (whole) {
+                *reinterpret_cast<uint4*>(dst + q + e) = make_uint4(pack<T>(y[0], y[1]), pack<T>(y[2], y[3]),
+                                                                    pack<T>(y[4], y[5]), pack<T>(y[6], y[7]));
+              } else {  // quads of columns outermost: lanes are side by side
+                part[((q + e) >> 2) * a.cap] = make_float4(y[0], y[1], y[2], y[3]);
+                part[(((q + e) >> 2) + 1) * a.cap] = make_float4(y[4], y[5], y[6], y[7]);
+              }
             }
           }
           __syncwarp();  // (the loads from tensor memory are the whole warp's)
@@ -375,165 +390,128 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (x.slot == 1) {
         rec = true;
-        if (tid == 0) write_rec(a, s_start, &x, walk.at - nt);
+        if (tid == 0) write_rec(a, s_start, &x);
       }
     }
-    if (!rec && tid == 0) write_rec(a, s_start, nullptr, 0);
-  } else if (warp == kLoad) {
+    if (!rec && tid == 0) write_rec(a, s_start, nullptr);
+  } else if (warp < kScores) {
     // ---------------------------------------------------------------- loads
+    // (One warp for K and V took 1350 cycles for a tile, longer than HBM.)
+    const bool v = warp > kLoad;
     const int subs = kKeys / a.g;  // boxes of a tile and half: 1 to 8, so a lane's is the same in every round
-    const int sub = lane % subs;
-    uint32_t i = 0;
+    const int sub = lane % subs, boxes = subs * (KD / 64) / a.halves, col = lane / subs * 64;
+    const CUtensorMap* map = v ? &map_v : &map_k;
+    uint8_t* dst = sm + (v ? L::V : L::K) + sub * a.g * 128 + lane / subs * L::HALF;
+    uint64_t* full = &bars[v ? B_VFULL : B_KFULL];
+    const int n = v ? L::NV : L::NK, empty = v ? B_VEMPTY - B_VFULL : B_KEMPTY - B_KFULL;
+    int stage = 0;
+    uint32_t turn = 1, loads = 0;
 #pragma unroll 1
     while (ok && walk.next(p, x)) {
       const int32_t* table = p.tables + (int64_t)x.r * p.width;
-      auto page_of = [&](int j, int& place) {  // n_pages: a box of zeros
+      // page of this lane's box in tile j; -1: none
+      auto page_of = [&](int j) {
         const int key = j * kKeys + sub * a.g;
-        place = 0;
-        if (j >= x.j1 || key >= x.keys) return p.n_pages;
-        const int b = (int)quot(key, p.by_block), page = table[b];
-        place = key - b * p.block;
-        if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
-        return page >= 0 && page < p.n_pages ? page : p.n_pages;
+        return j < x.j1 && key < x.keys ? table[quot(key, p.by_block)] : -1;
       };
-      int place, page = page_of(x.j0, place);
+      int page = page_of(x.j0);
 #pragma unroll 1
-      for (int j = x.j0; j < x.j1; ++j, ++i) {
-        int place1;
-        const int page1 = page_of(j + 1, place1);
-        const uint32_t absent = __ballot_sync(0xffffffffu, page == p.n_pages) & low_bits(subs);
-        const uint32_t stage = i % L::NB;
-        ok = sy.wait(&bars[B_EMPTY + stage], ((i / L::NB) & 1) ^ 1);
+      for (int j = x.j0; j < x.j1; ++j) {
+        const int next = page_of(j + 1), key = j * kKeys + sub * a.g;
+        ok = sy.wait(full + empty + stage, turn);
         if (!ok) break;
+        if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
+        const bool there = (uint32_t)page < (uint32_t)p.n_pages;
+        const uint32_t absent = ~__ballot_sync(0xffffffffu, there) & ((1u << subs) - 1u);
         if (lane == 0) {
-          s_absent[stage] = absent;
-          mbar_expect_tx(&bars[B_FULL + stage], 2 * L::TILE);
+          if (v) {
+            s_absent[stage] = absent;
+            mbar_arrive(&bars[B_META + stage]);
+          }
+          mbar_expect_tx(full + stage, L::TILE);
         }
         __syncwarp();
-        uint8_t* dst = sm + L::RING + stage * 2 * L::TILE + sub * a.g * 128;
-#pragma unroll 1
-        for (int b = lane; b < subs * (KD / 32); b += 32) {  // halves of K, then of V
-          const int half = b / subs;
-          const bool v = half >= KD / 64;
-          tma_load_4d(dst + half * L::HALF, v ? &map_v : &map_k, (v ? half - KD / 64 : half) * 64, x.head, place, page,
-                      &bars[B_FULL + stage]);
-        }
-        page = page1;
-        place = place1;
+        if (lane < boxes)  // (a box past the last page arrives as zeros)
+          tma_load_5d(dst + stage * L::TILE, map, col, x.head, key - (int)quot(key, p.by_block) * p.block,
+                      there ? page : p.n_pages, 0, full + stage);
+        if (++stage == n) { stage = 0; turn ^= 1; }
+        ++loads;
+        page = next;
       }
     }
-    // the last stages' commits land before the CTA leaves, and so do copies in flight where a wait ran out
-    for (uint32_t b = i > L::NB ? i - L::NB : 0; ok && b < i; ++b)
-      ok = sy.wait(&bars[B_EMPTY + b % L::NB], (b / L::NB) & 1);
+    // the last buffers' commits land before the CTA leaves, and so do copies in flight where a wait ran out
+    for (uint32_t b = loads > n ? loads - n : 0; ok && b < loads; ++b) ok = sy.wait(full + empty + b % n, (b / n) & 1);
     if (*s_dead)
-      for (uint32_t b = i > L::NB ? i - L::NB : 0; b < i; ++b)
-        for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_FULL + b % L::NB], (b / L::NB) & 1, 20000); ++tries) {}
+      for (uint32_t b = loads > n ? loads - n : 0; b < loads; ++b)
+        for (int tries = 0; tries < 1000 && !mbar_test_for(full + b % n, (b / n) & 1, 20000); ++tries) {}
   } else {
     // ---------------------------------------------------------------- products
-    // A warp for each slot (a step of its loop, four waits and twelve products, takes 1000 cycles: with one
-    // warp for both a tile of 2 x 128 rows took 2800, and a decode step's tile 1400). Scores are formed up to two
-    // tiles ahead of the outputs, whichever of the two can be first.
-    const int slot = warp - kMma;
+    // One warp forms the scores, another the outputs, each tile by tile for both slots in turn. Scores come as
+    // soon as those before have been read to registers, beside their softmax; weights have columns of their own, so
+    // no order between the two warps is needed. (One warp for everything took 2800 cycles for a tile of 2 x 128
+    // rows, one for each slot 1750: its waits and issues one after another.)
+    const bool pv = warp == kOutputs;
     const uint32_t id_s = idesc<T>(128, kKeys, false) | (p.c < 0.f ? 1u << 13 : 0u);  // (-Q)
     constexpr uint32_t id_o = idesc<T>(128, KD, true);
-    const uint32_t base = smem_u32(sm), ts = tmem + T_S + 128 * slot, to = tmem + T_O + 128 * slot;
-    const uint64_t qd = sdesc_sw128(base + L::Q + slot * L::QT, 16, 1024);
-    const uint64_t kd = sdesc_sw128(base + L::RING, 16, 1024);
-    const uint64_t vd = sdesc_sw128(base + L::RING + L::TILE, L::HALF, 1024);
-    auto poll = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_poll(bar, parity)); };
-    uint32_t tile0 = 0, ns = 0, np = 0, nq = 0;  // tiles of the CTA; this slot's scores, weights, queries
+    const uint32_t base = smem_u32(sm);
+    const uint64_t qd = sdesc_sw128(base + L::Q, 16, 1024), kd = sdesc_sw128(base + L::K, 16, 1024);
+    const uint64_t vd = sdesc_sw128(base + L::V, L::HALF, 1024);
+    uint32_t stage = 0, turn = 0, n[2] = {0, 0}, nq[2] = {0, 0};  // buffer of the next tile; per slot: tiles, queries
 #pragma unroll 1
     while (ok && walk.next(p, x)) {
-      const Spread d(x, slot);
       const int nt = x.j1 - x.j0;
-      // stages of the next tile and of the next outputs
-      uint32_t ks = tile0 % L::NB, kt = tile0 / L::NB & 1, os = (tile0 + (d.two ? 0 : slot)) % L::NB;
-      int k = 0, is = 0, io = 0, done = 0;  // tiles whose scores and outputs are under way, whose outputs are complete
-      bool queries = false;
-      uint64_t t0 = 0;
-      int spins = 0;
+      const bool two = x.rows > 128;
+      const int steps = two ? 2 * nt : nt;
 #pragma unroll 1
-      while (io < d.n || k < nt) {
-        bool moved = false, seen = false;
-        // (products into different columns may overtake one another: scores go over weights only once those
-        // have been multiplied)
-        if (done < io && poll(&bars[B_O + 2 * slot + ((np - 1) & 1)], (np - 1) >> 1 & 1)) done = io;
-        // Every tile is waited for in turn, the other slot's too, and both slots release its stage: a warp that
-        // skipped tiles could take a stage's last but one load for the last (a parity tells only two apart).
-        if (k < nt && (!d.two && (k & 1) != slot)) {
-          if (poll(&bars[B_FULL + ks], kt)) {
-            if (lane == 0) mbar_arrive(&bars[B_EMPTY + ks]);
-            seen = true;
+      for (int i = 0; ok && i < steps; ++i) {
+        const int s = i & 1;
+        const uint32_t ni = s ? n[1] : n[0];
+        const bool first = !two || s == 0, last = !two || s == 1;  // of the tile's steps
+        if (pv) {
+          ok = sy.wait(&bars[B_P + 2 * s + (ni & 1)], ni >> 1 & 1) && (!first || sy.wait(&bars[B_VFULL + stage], turn));
+        } else {
+          // (in the first tile of a piece the scores before have been read: its queries are there)
+          if (i < 2) {
+            ok = sy.wait(&bars[B_Q + s], (s ? nq[1] : nq[0]) & 1);
+            if (s) ++nq[1]; else ++nq[0];
+          } else {
+            ok = sy.wait(&bars[B_R + s], (ni - 1) & 1);
           }
-        } else if (k < nt && is < done + 2) {
-          if (!queries) queries = poll(&bars[B_Q + slot], nq & 1);
-          if (queries && poll(&bars[B_FULL + ks], kt)) {
-            __syncwarp();
-            tc_fence_after();
-            if (elect_one()) {
-              mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(ts + 64 * (ns & 1), qd, kd + ks * (2 * L::TILE >> 4), id_s);
-              mma_commit(&bars[B_S + 2 * slot + (ns & 1)]);
-            }
-            __syncwarp();
-            ++ns;
-            ++is;
-            seen = true;
-          }
+          ok = ok && (!first || sy.wait(&bars[B_KFULL + stage], turn));
         }
-        if (seen) {
-          ++k;
-          if (++ks == L::NB) { ks = 0; kt ^= 1; }
-          moved = true;
-        }
-        if (io < is && done == io && poll(&bars[B_P + 2 * slot + (np & 1)], np >> 1 & 1)) {
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t v = vd + os * (2 * L::TILE >> 4);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ts = tmem + T_S + 128 * s;
+        if (elect_one()) {
+          if (pv) {
+            const uint64_t v = vd + stage * (L::TILE >> 4);
 #pragma unroll
             for (int e = 0; e < kKeys / 16; ++e)
-              mma_bf16_ts(to, ts + 64 * (np & 1) + 8 * e, v + e * (2048 >> 4), id_o, io > 0 || e > 0);
-            mma_commit(&bars[B_O + 2 * slot + (np & 1)]);
-            mma_commit(&bars[B_EMPTY + os]);
-          }
-          __syncwarp();
-          ++np;
-          ++io;
-          os += d.two ? 1 : 2;
-          if (os >= L::NB) os -= L::NB;
-          moved = true;
-        }
-        if (moved) {
-          spins = 0;
-          t0 = 0;
-        } else if (++spins > 256) {
-          spins = 0;
-          const uint64_t now = globaltimer_ns();
-          if (t0 == 0) t0 = now;
-          const bool over = *s_dead || ((now - t0) >> 10) > (uint32_t)a.budget;
-          if (__any_sync(0xffffffffu, over)) {
-            if (lane == 0 && !*s_dead) {
-              if (p.status) atomicExch(p.status, kDevTimeout);
-              *s_dead = 1;
-            }
-            ok = false;
-            break;
+              mma_bf16_ts(tmem + T_O + 128 * s, ts + T_P + 32 * (ni & 1) + 8 * e, v + e * (2048 >> 4), id_o,
+                          i > 1 || e > 0);
+            mma_commit(&bars[B_O + 2 * s + (ni & 1)]);
+            if (last) mma_commit(&bars[B_VEMPTY + stage]);
+          } else {
+            mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(ts, qd + s * (L::QT >> 4), kd + stage * (L::TILE >> 4), id_s);
+            mma_commit(&bars[B_S + s]);
+            if (last) mma_commit(&bars[B_KEMPTY + stage]);
           }
         }
+        __syncwarp();
+        if (s) ++n[1]; else ++n[0];
+        if (last && ++stage == (pv ? L::NV : L::NK)) { stage = 0; turn ^= 1; }
       }
-      if (queries) ++nq;
-      tile0 += nt;
     }
     if (!ok) {  // products in flight end before their operands and columns go away
-      if (elect_one()) mma_commit(&bars[B_END + slot]);
-      for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END + slot], 0, 20000); ++tries) {}
+      if (elect_one()) mma_commit(&bars[B_END + pv]);
+      for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END + pv], 0, 20000); ++tries) {}
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMma) tmem_dealloc(tmem, 512);
+  if (warp == kScores) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ host
@@ -556,17 +534,20 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [pages][places][heads][D] with element strides s (page, place, head); boxes of 64 x 1 x g x 1.
-bool map4(CUtensorMap* m, const Problem& p, const void* base, int D, const int64_t* s, int g) {
+// [pages][places][heads][D] with element strides s (page, place, head); boxes of 64 columns of g places, or of
+// both halves of 128 columns side by side.
+bool map5(CUtensorMap* m, const Problem& p, const void* base, int D, const int64_t* s, int g, int halves) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.HKV, (cuuint64_t)p.block, (cuuint64_t)p.n_pages};
+  const bool both = halves == 2;
+  const cuuint64_t dims[5] = {(cuuint64_t)(both ? 64 : D), (cuuint64_t)p.HKV, (cuuint64_t)p.block, (cuuint64_t)p.n_pages,
+                              (cuuint64_t)(both ? 2 : 1)};
   // the stride of a dimension of one entry is never used; the encoder wants a valid one
   const cuuint64_t some = 16;
-  const cuuint64_t st[3] = {p.HKV > 1 ? (cuuint64_t)s[2] * 2 : some, p.block > 1 ? (cuuint64_t)s[1] * 2 : some,
-                            p.n_pages > 1 ? (cuuint64_t)s[0] * 2 : some};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)g, 1}, es[4] = {1, 1, 1, 1};
-  return fn(m, p.dt == GDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  const cuuint64_t st[4] = {p.HKV > 1 ? (cuuint64_t)s[2] * 2 : some, p.block > 1 ? (cuuint64_t)s[1] * 2 : some,
+                            p.n_pages > 1 ? (cuuint64_t)s[0] * 2 : some, both ? (cuuint64_t)128 : some};
+  const cuuint32_t box[5] = {64, 1, (cuuint32_t)g, 1, (cuuint32_t)halves}, es[5] = {1, 1, 1, 1, 1};
+  return fn(m, p.dt == GDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
             const_cast<void*>(base), dims, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -607,12 +588,16 @@ cudaError_t launch_tc(const Problem& p, uint8_t* ws) {
   TcArgs a{};
   a.p = p;
   set_layout(a, layout(sm_count(), (int64_t)p.T * p.G, kRows, p.DV), ws, sm_count());
+  a.cost = kCost;
   a.g = 8;
   while (a.g < kKeys && p.block % (2 * a.g) == 0) a.g *= 2;
   a.budget = (int)(g_budget_ns.load() >> 10);
   a.fault = g_fault.exchange(0);
   CUtensorMap m[2];
-  if (!map4(&m[0], p, p.k, p.D, p.ks, a.g) || !map4(&m[1], p, p.v, p.DV, p.vs, a.g)) return cudaErrorInvalidValue;
+  // (a box of both halves needs its rows to be a whole half's)
+  a.halves = a.g == kKeys && p.D == 128 && p.DV == 128 ? 2 : 1;
+  if (!map5(&m[0], p, p.k, p.D, p.ks, a.g, a.halves) || !map5(&m[1], p, p.v, p.DV, p.vs, a.g, a.halves))
+    return cudaErrorInvalidValue;
   const bool wide = p.D > 64 || p.DV > 64;
   cudaError_t e;
   if (p.dt == GDP_BF16)
