@@ -190,85 +190,96 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ joining cut items
-// A CTA of the grid's x per record and 8 rows (so that one cut item is joined by several), a thread per
-// row and quad of columns: the pieces' maxima give the factors 2^(m_i - m), applied in the order of the pieces. Maxima
-// and factors of 64 pieces at a time go through shared memory; outputs lie with rows side by side.
-constexpr int kJoin = 256, kJoinPieces = 64, kJoinRows = 8;
+// A CTA per record and RB rows, a thread per row, quad of columns and every groups-th piece: batches of
+// pieces, their loads in flight together, are added under a running maximum, in the order of the pieces;
+// then the groups' results in the order of the groups. Rows lie side by side, so a warp reads whole lines.
+constexpr int kJoin = 256, kBatch = 8;
 
 template <typename T>
 struct alignas(4 * sizeof(T)) Quad {
   T e[4];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Args a, int rows /* power of two */) {
-  __shared__ float s_f[kJoinPieces][kJoinRows + 1];
-  __shared__ float s_m[kJoin], s_l[kJoin];
+struct Joined {
+  float m, l;
+  float4 acc;
+  // f0 of this, f1 of x
+  __device__ __forceinline__ void add(float xm, float xl, const float4& x) {
+    const float mn = fmaxf(m, xm), base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2(m - base), f1 = ex2(xm - base);
+    m = mn;
+    l = f0 * l + f1 * xl;
+    acc.x = fmaf(f1, x.x, f0 * acc.x);
+    acc.y = fmaf(f1, x.y, f0 * acc.y);
+    acc.z = fmaf(f1, x.z, f0 * acc.z);
+    acc.w = fmaf(f1, x.w, f0 * acc.w);
+  }
+};
+
+template <typename T, int RB>
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Args a) {
+  constexpr int kSlots = kJoin / RB;
+  __shared__ Joined s_part[kJoin];
   pdl_wait();
   const Rec r = a.recs[blockIdx.x];
-  const int row0 = blockIdx.y * rows, tid = threadIdx.x;
-  if (row0 >= r.rows) return;
+  const int tid = threadIdx.x, row = blockIdx.y * RB + tid % RB;
+  if ((int)blockIdx.y * RB >= r.rows) return;
   const Problem& p = a.p;
-  const int here = min(rows, r.rows - row0), pieces = r.more + 1;
-  // piece i: slot 1 of this CTA, slot 0 of the next ones
-  auto at = [&](int i) { return (int64_t)(blockIdx.x + i) * 2 + (i == 0); };
-  const int row = tid & (rows - 1), part = tid / rows, parts = kJoin / rows;
-  const bool on = row < here;
-  float m = -INFINITY;
-  if (on)
-    for (int i = part; i < pieces; i += parts) m = fmaxf(m, a.ml[at(i) * a.cap + row0 + row].x);
-  s_m[tid] = m;
-  __syncthreads();
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, s_m[i * rows + row]);
-  const float base = m == -INFINITY ? 0.f : m;
-  // a thread's quads: part, part + parts, ..
-  const int quads = a.dvp / 4;
+  const int pieces = r.more + 1, quads = a.dvp / 4;
+  int span = 1;  // slots of a group: a power of two
+  while (span < quads && span < kSlots) span *= 2;
+  const int slot = tid / RB, group = slot / span, groups = kSlots / span;
   const bool even = p.DV % 4 == 0 && reinterpret_cast<uintptr_t>(p.o) % sizeof(Quad<T>) == 0;
-  float sum = 0.f;
-  for (int q0 = part; q0 - part < quads; q0 += parts) {
-    const bool mine = on && q0 < quads;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < pieces; i0 += kJoinPieces) {
-      const int n = min(kJoinPieces, pieces - i0);
-      __syncthreads();
-      for (int i = part; i < n; i += parts) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (on) ml = a.ml[at(i0 + i) * a.cap + row0 + row];
-        s_f[i][row] = ex2(ml.x - base);
-        if (q0 == part) sum += s_f[i][row] * ml.y;
-      }
-      __syncthreads();
-      if (mine) {
-        const float4* src = reinterpret_cast<const float4*>(a.part) + (int64_t)q0 * a.cap + row0 + row;
-        const int64_t step = (int64_t)a.cap * quads;
-#pragma unroll 16
-        for (int i = 0; i < n; ++i) {
-          const float4 v = src[at(i0 + i) * step];
-          const float f = s_f[i][row];
-          acc.x = fmaf(f, v.x, acc.x);
-          acc.y = fmaf(f, v.y, acc.y);
-          acc.z = fmaf(f, v.z, acc.z);
-          acc.w = fmaf(f, v.w, acc.w);
+  // piece i: slot 1 of this CTA, slot 0 of the next ones
+  auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * a.cap; };
+  for (int q0 = 0; q0 < quads; q0 += span) {
+    const int q = q0 + slot % span;
+    const bool on = row < r.rows && q < quads;
+    Joined x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (on)
+      for (int i0 = group; i0 < pieces; i0 += kBatch * groups) {
+        float2 ml[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * groups;
+          if (i < pieces) {
+            ml[k] = a.ml[at(i) + row];
+            v[k] = reinterpret_cast<const float4*>(a.part)[at(i) * quads + (int64_t)q * a.cap + row];
+          }
         }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * groups < pieces) x.add(ml[k].x, ml[k].y, v[k]);
       }
-    }
-    if (q0 == part) {  // the parts' sums, in order
-      s_l[tid] = sum;
+    if (groups > 1) {
       __syncthreads();
-      sum = 0.f;
-      for (int i = 0; i < parts; ++i) sum += s_l[i * rows + row];
-      sum = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      s_part[tid] = x;
+      __syncthreads();
+      if (group == 0)
+        for (int g = 1; g < groups; ++g) {
+          const Joined& y = s_part[tid + g * span * RB];
+          x.add(y.m, y.l, y.acc);
+        }
     }
-    if (mine) {
-      T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row0 + row) + 4 * q0;
-      const Quad<T> y = {from_f<T>(acc.x * sum), from_f<T>(acc.y * sum), from_f<T>(acc.z * sum), from_f<T>(acc.w * sum)};
+    if (on && group == 0) {
+      const float f = x.l > 0.f || x.l != x.l ? 1.f / x.l : 0.f;
+      T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row) + 4 * q;
+      const Quad<T> y = {from_f<T>(x.acc.x * f), from_f<T>(x.acc.y * f), from_f<T>(x.acc.z * f), from_f<T>(x.acc.w * f)};
       if (even)
         *reinterpret_cast<Quad<T>*>(dst) = y;
       else
         for (int k = 0; k < 4; ++k)
-          if (4 * q0 + k < p.DV) dst[k] = y.e[k];
+          if (4 * q + k < p.DV) dst[k] = y.e[k];
     }
   }
+}
+
+template <typename T>
+cudaError_t join(const Args& a) {
+  // (few rows a CTA where an item may be cut often; more where that would be thousands of CTAs)
+  if (a.cap <= 64) return launch_pdl(join_kernel<T, 8>, dim3(a.ctas, (a.cap + 7) / 8), dim3(kJoin), 0, a.p.stream, a);
+  return launch_pdl(join_kernel<T, 16>, dim3(a.ctas, (a.cap + 15) / 16), dim3(kJoin), 0, a.p.stream, a);
 }
 
 template <typename T>
@@ -285,13 +296,10 @@ int simple_ctas() { return 2 * sm_count(); }
 size_t simple_workspace(int64_t rows, int DV) { return layout(simple_ctas(), rows, kRows, DV).total; }
 
 cudaError_t launch_combine(const Args& a) {
-  int rows = 1;
-  while (rows < kJoinRows && rows < a.cap) rows *= 2;
-  const dim3 grid(a.ctas, (a.cap + rows - 1) / rows), block(kJoin);
   switch (a.p.dt) {
-    case GDP_BF16: return launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, a.p.stream, a, rows);
-    case GDP_F16: return launch_pdl(join_kernel<__half>, grid, block, 0, a.p.stream, a, rows);
-    default: return launch_pdl(join_kernel<float>, grid, block, 0, a.p.stream, a, rows);
+    case GDP_BF16: return join<__nv_bfloat16>(a);
+    case GDP_F16: return join<__half>(a);
+    default: return join<float>(a);
   }
 }
 
