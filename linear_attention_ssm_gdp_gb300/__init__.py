@@ -827,7 +827,7 @@ def gdp_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str 
 
 
 def _heads(name, t, dtype):
-    """[T, H, D] or [B, T, H, D] as (B, T, H, D, three strides)."""
+    """[T, H, D] or [B, T, H, D] as (shape, B, T, H, D, three strides)."""
     shape, stride = t.shape, t.stride()
     if not t.is_cuda:
         raise ValueError("libgdp works on CUDA tensors only")
@@ -835,8 +835,8 @@ def _heads(name, t, dtype):
         raise ValueError(f"{name} must be [T, H, D] or [B, T, H, D] in one dtype of "
                          "{bf16, fp16, fp32} with a contiguous last dimension")
     if len(shape) == 3:
-        return 1, *shape, (0, stride[0], stride[1])
-    return *shape, stride[:3]
+        return shape, 1, shape[0], shape[1], shape[2], (0, stride[0], stride[1])
+    return shape, shape[0], shape[1], shape[2], shape[3], stride[:3]
 
 
 def _rotation(lead, positions, frequencies, D, offset):
@@ -864,12 +864,12 @@ def gdp_rotary(x, positions, frequencies, offset: int = 0, interleaved: bool = F
     pass, or undoing). ``out``: contiguous, or x itself. Returns y in x's dtype."""
     if x.dtype not in _DTYPE or frequencies is None:
         raise ValueError("x must be bf16, fp16 or fp32, with frequencies")
-    B, T, H, D, xs = _heads("x", x, x.dtype)
-    pos, freq, R = _rotation(x.shape[:-2], positions, frequencies, D, offset)
+    shape, B, T, H, D, xs = _heads("x", x, x.dtype)
+    pos, freq, R = _rotation(shape[:-2], positions, frequencies, D, offset)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out is not x:
-        _out_ok(out, x.shape, x.dtype)
+        _out_ok(out, shape, x.dtype)
     ys = xs if out is x else (T * H * D, H * D, D)
     st = load().gdp_rotary(x.data_ptr(), _pack3(*xs), pos, freq, R, offset, interleaved, amplitude,
                            backward, B, T, H, D, _DTYPE[x.dtype], out.data_ptr(), _pack3(*ys),
@@ -880,16 +880,17 @@ def gdp_rotary(x, positions, frequencies, offset: int = 0, interleaved: bool = F
 
 
 def _cache_ok(k_cache, v_cache, dtype):
-    """Caches [n_pages, block_size, HKV, D]: (n_pages, block_size, HKV, D, DV)."""
-    for t in (k_cache, v_cache):
-        if not t.is_cuda:
-            raise ValueError("libgdp works on CUDA tensors only")
-        if t.dtype != dtype or t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
-            raise ValueError("caches must be [n_pages, block_size, HKV, D] in q, k, v's dtype with "
-                             "a contiguous last dimension")
-    if k_cache.shape[:3] != v_cache.shape[:3]:
+    """Caches [n_pages, block_size, HKV, D]: (n_pages, block_size, HKV, D, DV, strides of both)."""
+    (ks, kt), (vs, vt) = (k_cache.shape, k_cache.stride()), (v_cache.shape, v_cache.stride())
+    if not (k_cache.is_cuda and v_cache.is_cuda):
+        raise ValueError("libgdp works on CUDA tensors only")
+    if (len(ks) != 4 or len(vs) != 4 or k_cache.dtype != dtype or v_cache.dtype != dtype
+            or (kt[3] != 1 and ks[3] > 1) or (vt[3] != 1 and vs[3] > 1)):
+        raise ValueError("caches must be [n_pages, block_size, HKV, D] in q, k, v's dtype with "
+                         "a contiguous last dimension")
+    if ks[:3] != vs[:3]:
         raise ValueError("the caches must have the same pages, block size and heads")
-    return *k_cache.shape, v_cache.shape[3]
+    return (*ks, vs[3], _pack3(kt[0], kt[1], kt[2]), _pack3(vt[0], vt[1], vt[2]))
 
 
 def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequencies=None,
@@ -907,12 +908,12 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
     dt = k.dtype
     if dt not in _DTYPE:
         raise ValueError("k, v and q must be bf16, fp16 or fp32")
-    B, T, HKV, D, ks = _heads("k", k, dt)
-    vB, vT, vH, DV, vs = _heads("v", v, dt)
-    pages, block, cH, cD, cDV = _cache_ok(k_cache, v_cache, dt)
-    if v.shape[:-1] != k.shape[:-1] or (cH, cD, cDV) != (HKV, D, DV):
+    shape, B, T, HKV, D, ks = _heads("k", k, dt)
+    vshape, _, _, _, DV, vs = _heads("v", v, dt)
+    pages, block, cH, cD, cDV, kst, vst = _cache_ok(k_cache, v_cache, dt)
+    if vshape[:-1] != shape[:-1] or cH != HKV or cD != D or cDV != DV:
         raise ValueError("k and v must have the same tokens and the caches' heads")
-    lead = k.shape[:-2]
+    lead = shape[:-2]
     if slot_map.dtype != torch.int64 or slot_map.shape != lead or not slot_map.is_contiguous() \
             or not slot_map.is_cuda:
         raise ValueError(f"slot_map must be a contiguous int64 CUDA tensor {list(lead)}")
@@ -920,20 +921,20 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
     pos, freq, R = _rotation(lead, positions, frequencies, D, offset)
     H, qs = 0, (0, 0, 0)
     if q is not None:
-        _, _, H, qD, qs = _heads("q", q, dt)
-        if q.shape[:-2] != lead or qD != D:
+        qshape, _, _, H, qD, qs = _heads("q", q, dt)
+        if qshape[:-2] != lead or qD != D:
             raise ValueError("q must have k's tokens and head size")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _out_ok(q_out, q.shape, dt)
+            _out_ok(q_out, qshape, dt)
     elif q_out is not None:
         raise ValueError("q_out without q")
     st = load().gdp_cache_append(
         _a(q), k.data_ptr(), v.data_ptr(), _pack_strides(*qs, *ks, *vs), pos, freq, R, offset,
         interleaved, amplitude, B, T, H, HKV, D, DV, _DTYPE[dt], slot_map.data_ptr(),
-        k_cache.data_ptr(), _pack3(*k_cache.stride()[:3]), v_cache.data_ptr(),
-        _pack3(*v_cache.stride()[:3]), pages, block, _a(q_out), _a(status), _raw_stream(k))
+        k_cache.data_ptr(), kst, v_cache.data_ptr(), vst, pages, block, _a(q_out), _a(status),
+        _raw_stream(k))
     if st:
         _check("gdp_cache_append", st)
     return q_out
@@ -963,8 +964,8 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
     dt = q.dtype
     if dt not in _DTYPE or q.dim() != 4:
         raise ValueError("q must be [B, T, H, D] in bf16, fp16 or fp32")
-    B, T, H, D, qs = _heads("q", q, dt)
-    pages, block, HKV, cD, DV = _cache_ok(k_cache, v_cache, dt)
+    _, B, T, H, D, qs = _heads("q", q, dt)
+    pages, block, HKV, cD, DV, kst, vst = _cache_ok(k_cache, v_cache, dt)
     if cD != D:
         raise ValueError("q and k_cache must have the same head size")
     n = B if cu_seqlens is None else _packed(cu_seqlens, B)
@@ -992,9 +993,8 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
     else:
         _need_cuda(workspace)
     st = load().gdp_attention_paged(
-        q.data_ptr(), _pack3(*qs), k_cache.data_ptr(), _pack3(*k_cache.stride()[:3]),
-        v_cache.data_ptr(), _pack3(*v_cache.stride()[:3]), pages, block, block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), _a(cu_seqlens), n, _a(tree_mask), B, T, H,
+        q.data_ptr(), _pack3(*qs), k_cache.data_ptr(), kst, v_cache.data_ptr(), vst, pages, block,
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), _a(cu_seqlens), n, _a(tree_mask), B, T, H,
         HKV, D, DV, D ** -0.5 if scale is None else scale, _DTYPE[dt], out.data_ptr(), _a(status),
         workspace.data_ptr(), workspace.numel(), _raw_stream(q))
     if st:
