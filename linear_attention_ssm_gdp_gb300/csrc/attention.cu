@@ -13,180 +13,291 @@ namespace attn {
 namespace {
 
 // ------------------------------------------------------------------ any type and size
-constexpr int kRows = 16, kKeys = 64, kThreads = 256;
+// A CTA of eight warps takes up to 8 rows of an item against tiles of 32 keys, which arrive in their own type by
+// cp.async, up to three tiles ahead (rows that are not whole 16-byte chunks are copied by elements). Products are
+// fp32 multiply-adds: for the scores a thread has a key and every eighth chunk of the head, for the outputs four
+// columns (eight above 128) and every eighth key, whose sums meet at the item's end. Up to 8 rows that is HBM's
+// time for fp32: a tile of 32 KB for 128 + 128 columns takes an SM 0.75 us to load and its products 0.4.
+constexpr int kRows = 8, kKeys = 32, kThreads = 256, kWarps = kThreads / 32;
+constexpr Cost kCost = {8, 3, 8, 3};
 
 struct SimpleSmem {
-  int sd, sv;  // row strides of q and k, and of v, in floats
-  size_t k, v, s, bytes;
+  int ks, vs;                 // bytes of a row of K and of V
+  int stage, stages;
+  int q, s, p, off, bytes;    // offsets past the stages
 };
-// sd = 4 mod 8, so that eight keys' vectors fall into different banks
-__host__ __device__ inline SimpleSmem simple_smem(int D, int DV) {
+inline SimpleSmem simple_smem(int D, int DV, int esz) {
   SimpleSmem x;
-  x.sd = (D + 7) / 8 * 8 + 4;
-  x.sv = (DV + 3) / 4 * 4;
-  x.k = sizeof(float) * kRows * x.sd;
-  x.v = x.k + sizeof(float) * kKeys * x.sd;
-  x.s = x.v + sizeof(float) * kKeys * x.sv;
-  x.bytes = x.s + sizeof(float) * kRows * (kKeys + 1) + sizeof(float) * kRows * 2 + sizeof(int64_t) * kKeys * 2;
+  x.ks = (D * esz + 15) / 16 * 16;
+  x.vs = (DV * esz + 15) / 16 * 16;
+  x.stage = kKeys * (x.ks + x.vs);
+  x.stages = std::max(2, std::min(4, 105 * 1024 / x.stage));  // (two CTAs an SM)
+  x.q = std::max(x.stages * x.stage, kWarps * kRows * 512 * (DV > 128 ? 2 : 1));  // (the warps' outputs meet there)
+  x.s = x.q + 4 * kRows * (x.ks / esz);                            // Q, fp32
+  x.p = x.s + 4 * kRows * kKeys;                                   // scores [row][key], weights [key][row]
+  x.off = x.p + 4 * kRows * kKeys + 4 * kRows * 2;                 // factors and sums of the rows
+  x.bytes = x.off + 2 * kKeys * 16 + 16 + 4 * 4;                   // offsets of two tiles' rows; seen keys by stage
   return x;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant__ Args a) {
+template <typename T> struct alignas(16) Chunk { T e[16 / sizeof(T)]; };
+template <typename T> struct alignas(4 * sizeof(T)) Quad { T e[4]; };
+
+struct SimpleArgs : Args {
+  SimpleSmem L;
+  int k_chunks, v_chunks;     // of a row, where rows are whole chunks on the 16-byte grid; else 0
+  Div by_k, by_v;
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+// The tiles [j0, j1) of one piece for R rows (x.rows of them in use), outputs of NQ quads a thread.
+template <typename T, int R, int NQ>
+__device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, const Piece& x) {
+  constexpr int VN = 16 / sizeof(T);
+  const Problem& p = a.p;
+  const SimpleSmem& L = a.L;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NST = L.stages;
+  float* sq = reinterpret_cast<float*>(sm + L.q);
+  float* ss = reinterpret_cast<float*>(sm + L.s);                  // [kRows][kKeys]
+  float* sp = reinterpret_cast<float*>(sm + L.p);                  // [kKeys][kRows]
+  float* s_alpha = sp + kRows * kKeys;
+  float* s_sum = s_alpha + kRows;
+  longlong2* s_off = reinterpret_cast<longlong2*>(sm + L.off);     // [2][kKeys]
+  uint32_t* s_ok = reinterpret_cast<uint32_t*>(s_off + 2 * kKeys); // [stages]
+  const int qs = L.ks / (int)sizeof(T);
+  const T *k0 = static_cast<const T*>(p.k) + x.head * p.ks[2], *v0 = static_cast<const T*>(p.v) + x.head * p.vs[2];
+
+  // where the rows of tile j lie (by the last warp; -1: not there), from page numbers that were asked for a tile before
+  int page = -1;
+  auto ask = [&](int j) {
+    const int key = j * kKeys + lane;
+    if (warp == kWarps - 1) page = j < x.j1 && key < x.keys ? p.tables[(int64_t)x.r * p.width + quot(key, p.by_block)] : -1;
+  };
+  auto find = [&](int j) {
+    if (warp != kWarps - 1) return;
+    const int key = j * kKeys + lane, in = key - (int)quot(key, p.by_block) * p.block;
+    if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
+    const bool there = (uint32_t)page < (uint32_t)p.n_pages;
+    s_off[(j & 1) * kKeys + lane] =
+        there ? make_longlong2(page * p.ks[0] + in * p.ks[1], page * p.vs[0] + in * p.vs[1]) : make_longlong2(-1, -1);
+    const uint32_t ok = __ballot_sync(0xffffffffu, there);
+    if (lane == 0) s_ok[j % NST] = ok;
+    ask(j + 1);
+  };
+  // tile j into its stage; rows that are not there are 0
+  auto load = [&](int j) {
+    if (j < x.j1) {
+      uint8_t* st = sm + (j % NST) * L.stage;
+      const longlong2* off = s_off + (j & 1) * kKeys;
+      if (a.k_chunks) {
+        for (int i = tid; i < kKeys * a.k_chunks; i += kThreads) {
+          const int key = (int)quot(i, a.by_k), c = i - key * a.k_chunks;
+          const int64_t o = off[key].x;
+          cp_async16(st + key * L.ks + 16 * c, k0 + (o < 0 ? 0 : o + c * VN), o >= 0);
+        }
+      } else {
+        for (int key = warp; key < kKeys; key += kWarps)
+          for (int d = lane; d < qs; d += 32)
+            reinterpret_cast<T*>(st + key * L.ks)[d] = off[key].x >= 0 && d < p.D ? k0[off[key].x + d] : from_f<T>(0.f);
+      }
+      st += kKeys * L.ks;
+      if (a.v_chunks) {
+        for (int i = tid; i < kKeys * a.v_chunks; i += kThreads) {
+          const int key = (int)quot(i, a.by_v), c = i - key * a.v_chunks;
+          const int64_t o = off[key].y;
+          cp_async16(st + key * L.vs + 16 * c, v0 + (o < 0 ? 0 : o + c * VN), o >= 0);
+        }
+      } else {
+        for (int key = warp; key < kKeys; key += kWarps)
+          for (int d = lane; d < L.vs / (int)sizeof(T); d += 32)
+            reinterpret_cast<T*>(st + key * L.vs)[d] = off[key].y >= 0 && d < p.DV ? v0[off[key].y + d] : from_f<T>(0.f);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");           // (one for each tile, empty ones too)
+  };
+
+  ask(x.j0);
+  __syncthreads();  // (the last piece's reads are over)
+  for (int i = tid; i < R * qs; i += kThreads) {
+    const int row = i / qs, d = i - row * qs;
+    float f = 0.f;
+    if (row < x.rows && d < p.D) {
+      const int at = x.row0 + row, t = (int)quot(at, p.by_G), h = x.head * p.G + at - t * p.G;
+      const int64_t base = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
+      f = to_f(static_cast<const T*>(p.q)[base + h * p.qs[2] + d]);
+    }
+    sq[i] = f;
+  }
+  for (int i = 0; i + 1 < NST; ++i) {
+    find(x.j0 + i);
+    __syncthreads();
+    load(x.j0 + i);
+  }
+  find(x.j0 + NST - 1);
+  float4 acc[R][NQ];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) acc[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;                                    // of row `warp`
+
+  for (int j = x.j0; j < x.j1; ++j) {
+    if (NST == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (NST == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    __syncthreads();                                               // tile j is there, tile j - 1 has been read
+    load(j + NST - 1);
+    const uint8_t* st = sm + (j % NST) * L.stage;
+    {  // scores: key tid / 8, chunks tid % 8, + 8, ..
+      const int key = tid >> 3, part = tid & 7;
+      float s[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) s[i] = 0.f;
+      const Chunk<T>* kp = reinterpret_cast<const Chunk<T>*>(st + key * L.ks);
+      for (int c = part; c * VN < p.D; c += 8) {
+        const Chunk<T> kk = kp[c];
+#pragma unroll
+        for (int e = 0; e < VN; e += 4) {
+          const float k_0 = to_f(kk.e[e]), k_1 = to_f(kk.e[e + 1]), k_2 = to_f(kk.e[e + 2]), k_3 = to_f(kk.e[e + 3]);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(sq + i * qs + c * VN + e);
+            s[i] = fmaf(q.x, k_0, fmaf(q.y, k_1, fmaf(q.z, k_2, fmaf(q.w, k_3, s[i]))));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
+        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
+        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 4);
+      }
+      const int back = j * kKeys + key - x.x.ctx;
+      const bool there = s_ok[j % NST] >> key & 1;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (i != part) continue;
+        bool sees = there && i < x.rows;
+        if (sees && back >= 0) {
+          const int t = (int)quot(x.row0 + i, p.by_G);
+          sees = p.tree ? (p.tree[x.first + t] >> back) & 1 : back <= t;
+        }
+        ss[i * kKeys + key] = sees ? s[i] * p.c : -INFINITY;
+      }
+    }
+    __syncthreads();
+    find(j + NST);                                                 // (its offsets' place was tile j + NST - 2's)
+    if (warp < R) {                                                // running maximum and sum of row `warp`
+      const float s = ss[warp * kKeys + lane];
+      float top = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+      const float w = ex2(s - base), f = ex2(m - base);
+      sp[lane * kRows + warp] = w;
+      l = l * f + w;                                               // (each lane its own keys' sum)
+      m = mn;
+      if (lane == 0) s_alpha[warp] = f;
+    }
+    __syncthreads();
+    // outputs: columns 4 lane .. + 3 (+ 128), keys warp, + 8, ..
+    float f[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) f[i] = s_alpha[i];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        acc[i][n].x *= f[i]; acc[i][n].y *= f[i]; acc[i][n].z *= f[i]; acc[i][n].w *= f[i];
+      }
+    const uint8_t* sv = st + kKeys * L.ks;
+#pragma unroll 2
+    for (int key = warp; key < kKeys; key += kWarps) {
+      float w[R];
+#pragma unroll
+      for (int i = 0; i < R; i += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(sp + key * kRows + i);
+        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+        if (4 * lane + 128 * n < p.DV) {
+          const Quad<T> u = *reinterpret_cast<const Quad<T>*>(sv + key * L.vs + (4 * lane + 128 * n) * sizeof(T));
+          const float4 v = make_float4(to_f(u.e[0]), to_f(u.e[1]), to_f(u.e[2]), to_f(u.e[3]));
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            acc[i][n].x = fmaf(w[i], v.x, acc[i][n].x);
+            acc[i][n].y = fmaf(w[i], v.y, acc[i][n].y);
+            acc[i][n].z = fmaf(w[i], v.z, acc[i][n].z);
+            acc[i][n].w = fmaf(w[i], v.w, acc[i][n].w);
+          }
+        }
+    }
+  }
+
+  // the warps' sums meet, in their order; outputs of a whole item, or a piece's share of them
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float4* so = reinterpret_cast<float4*>(sm);                      // [warp][R][NQ][32]
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) so[((warp * R + i) * NQ + n) * 32 + lane] = acc[i][n];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (warp < R && lane == 0) {
+    s_sum[warp] = l;
+    if (x.slot >= 0 && warp < x.rows) a.ml[((int64_t)blockIdx.x * 2 + x.slot) * a.cap + warp] = make_float2(m, l);
+  }
+  __syncthreads();
+  for (int e = tid; e < x.rows * NQ * 32; e += kThreads) {
+    const int c = e % 32, n = e / 32 % NQ, row = e / (32 * NQ), col = 4 * c + 128 * n;
+    if (col >= p.DV) continue;
+    float4 y = so[(row * NQ + n) * 32 + c];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 u = so[((w * R + row) * NQ + n) * 32 + c];
+      y.x += u.x; y.y += u.y; y.z += u.z; y.w += u.w;
+    }
+    if (x.slot >= 0) {
+      float4* dst = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * 2 + x.slot) * a.cap * (a.dvp / 4);
+      dst[(int64_t)(col / 4) * a.cap + row] = y;
+    } else {
+      const float sum = s_sum[row], g = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      T* dst = static_cast<T*>(p.o) + out_at(p, x.first, x.head, x.row0 + row) + col;
+      const float u[4] = {y.x, y.y, y.z, y.w};
+      for (int k = 0; k < 4; ++k)
+        if (col + k < p.DV) dst[k] = from_f<T>(u[k] * g);
+    }
+  }
+}
+
+template <typename T, int NQ>
+__global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant__ SimpleArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Start s_start;
   __shared__ long long s_scan[kThreads / 32 + 1];
-  const Problem& p = a.p;
-  const SimpleSmem L = simple_smem(p.D, p.DV);
-  float* sq = reinterpret_cast<float*>(sm);
-  float* sk = reinterpret_cast<float*>(sm + L.k);
-  float* sv = reinterpret_cast<float*>(sm + L.v);
-  float* ss = reinterpret_cast<float*>(sm + L.s);        // [kRows][kKeys + 1]
-  float* s_alpha = ss + kRows * (kKeys + 1);
-  float* s_sum = s_alpha + kRows;
-  int64_t* s_ko = reinterpret_cast<int64_t*>(s_sum + kRows);
-  int64_t* s_vo = s_ko + kKeys;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   find_start<kRows, kKeys, kThreads>(a, &s_start, s_scan);
   Walk<kRows, kKeys> walk(s_start, a.cost);
   Piece x;
   bool rec = false;
-  const int quads = L.sv / 4;
-  // outputs: a thread holds the quad of columns tid % 64 of rows tid / 64 + 4 i
-  constexpr int RG = kThreads / 64, RN = kRows / RG;
-  while (walk.next(p, x)) {
-    float4 acc[RN];
-#pragma unroll
-    for (int i = 0; i < RN; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows 2 warp, 2 warp + 1
-    __syncthreads();  // (the last piece's reads of sq are over)
-    for (int i = tid; i < kRows * L.sd; i += kThreads) {
-      const int row = i / L.sd, d = i - row * L.sd;
-      float f = 0.f;
-      if (row < x.rows && d < p.D) {
-        const int R = x.row0 + row, t = (int)quot(R, p.by_G), h = x.head * p.G + R - t * p.G;
-        const int64_t at = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
-        f = to_f(static_cast<const T*>(p.q)[at + h * p.qs[2] + d]);
-      }
-      sq[i] = f;
-    }
-    for (int j = x.j0; j < x.j1; ++j) {
-      __syncthreads();  // (the last tile's reads are over)
-      if (tid < kKeys) {
-        const int key = j * kKeys + tid;
-        int64_t ko = -1, vo = -1;
-        if (key < x.keys) {
-          const int b = (int)quot(key, p.by_block), page = p.tables[(int64_t)x.r * p.width + b];
-          if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
-          if (page >= 0 && page < p.n_pages) {
-            ko = page * p.ks[0] + (key - b * p.block) * p.ks[1] + x.head * p.ks[2];
-            vo = page * p.vs[0] + (key - b * p.block) * p.vs[1] + x.head * p.vs[2];
-          }
-        }
-        s_ko[tid] = ko;
-        s_vo[tid] = vo;
-      }
-      __syncthreads();
-      // a warp per key row; what is not there is 0
-      for (int key = warp; key < kKeys; key += kThreads / 32) {
-        const int64_t ko = s_ko[key], vo = s_vo[key];
-        for (int d = lane; d < L.sd; d += 32)
-          sk[key * L.sd + d] = ko >= 0 && d < p.D ? to_f(static_cast<const T*>(p.k)[ko + d]) : 0.f;
-        for (int d = lane; d < L.sv; d += 32)
-          sv[key * L.sv + d] = vo >= 0 && d < p.DV ? to_f(static_cast<const T*>(p.v)[vo + d]) : 0.f;
-      }
-      __syncthreads();
-      {  // scores of key tid % 64, rows 4 (tid / 64) .. + 3
-        const int key = tid % kKeys, r0 = tid / kKeys * 4;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float4* kp = reinterpret_cast<const float4*>(sk + key * L.sd);
-        for (int d = 0; d < (p.D + 3) / 4; ++d) {
-          const float4 kk = kp[d];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(sq + (r0 + i) * L.sd + 4 * d);
-            s[i] = fmaf(q.x, kk.x, fmaf(q.y, kk.y, fmaf(q.z, kk.z, fmaf(q.w, kk.w, s[i]))));
-          }
-        }
-        const int at = j * kKeys + key, back = at - x.x.ctx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bool sees = s_ko[key] >= 0 && r0 + i < x.rows;
-          if (sees && back >= 0) {
-            const int t = (int)quot(x.row0 + r0 + i, p.by_G);
-            sees = p.tree ? (p.tree[x.first + t] >> back) & 1 : back <= t;
-          }
-          ss[(r0 + i) * (kKeys + 1) + key] = sees ? s[i] * p.c : -INFINITY;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // running maximum and sum, two rows a warp
-        float* row = ss + (2 * warp + i) * (kKeys + 1);
-        const float s0 = row[lane], s1 = row[lane + 32];
-        float top = fmaxf(s0, s1);
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float mn = fmaxf(m[i], top), base = mn == -INFINITY ? 0.f : mn;
-        const float p0 = ex2(s0 - base), p1 = ex2(s1 - base), alpha = ex2(m[i] - base);
-        row[lane] = p0;
-        row[lane + 32] = p1;
-        float sum = p0 + p1;
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l[i] = l[i] * alpha + sum;
-        m[i] = mn;
-        if (lane == 0) s_alpha[2 * warp + i] = alpha;
-      }
-      __syncthreads();
-      const int c = tid % 64, rg = tid / 64;
-      if (c < quads) {
-#pragma unroll
-        for (int i = 0; i < RN; ++i) {
-          const float f = s_alpha[rg + RG * i];
-          acc[i].x *= f; acc[i].y *= f; acc[i].z *= f; acc[i].w *= f;
-        }
-        for (int key = 0; key < kKeys; ++key) {
-          const float4 vv = *reinterpret_cast<const float4*>(sv + key * L.sv + 4 * c);
-#pragma unroll
-          for (int i = 0; i < RN; ++i) {
-            const float f = ss[(rg + RG * i) * (kKeys + 1) + key];
-            acc[i].x = fmaf(f, vv.x, acc[i].x);
-            acc[i].y = fmaf(f, vv.y, acc[i].y);
-            acc[i].z = fmaf(f, vv.z, acc[i].z);
-            acc[i].w = fmaf(f, vv.w, acc[i].w);
-          }
-        }
-      }
-    }
-    // outputs of a whole item, or a piece's share of them
-    if (lane < 2) s_sum[2 * warp + lane] = lane == 0 ? l[0] : l[1];
-    if (x.slot >= 0 && lane < 2 && 2 * warp + lane < x.rows)
-      a.ml[((int64_t)blockIdx.x * 2 + x.slot) * a.cap + 2 * warp + lane] =
-          lane == 0 ? make_float2(m[0], l[0]) : make_float2(m[1], l[1]);
-    __syncthreads();
-    const int c = tid % 64, rg = tid / 64;
-    if (c < quads)
-#pragma unroll
-      for (int i = 0; i < RN; ++i) {
-        const int row = rg + RG * i;
-        if (row >= x.rows) continue;
-        if (x.slot >= 0) {
-          float4* dst = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * 2 + x.slot) * a.cap * quads;
-          dst[c * a.cap + row] = acc[i];
-          continue;
-        }
-        const float sum = s_sum[row], f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-        T* dst = static_cast<T*>(p.o) + out_at(p, x.first, x.head, x.row0 + row) + 4 * c;
-        const float y[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
-        for (int e = 0; e < 4; ++e)
-          if (4 * c + e < p.DV) dst[e] = from_f<T>(y[e] * f);
-      }
+  while (walk.next(a.p, x)) {
+    if (x.rows <= 4)
+      simple_piece<T, 4, NQ>(a, sm, x);
+    else
+      simple_piece<T, 8, NQ>(a, sm, x);
     if (x.slot == 1) {
       rec = true;
-      if (tid == 0) write_rec(a, s_start, &x);
+      if (threadIdx.x == 0) write_rec(a, s_start, &x);
     }
   }
-  if (!rec && tid == 0) write_rec(a, s_start, nullptr);
+  if (!rec && threadIdx.x == 0) write_rec(a, s_start, nullptr);
 }
 
 // ------------------------------------------------------------------ joining cut items
@@ -194,11 +305,6 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
 // pieces, their loads in flight together, are added under a running maximum, in the order of the pieces;
 // then the groups' results in the order of the groups. Rows lie side by side, so a warp reads whole lines.
 constexpr int kJoin = 256, kBatch = 8;
-
-template <typename T>
-struct alignas(4 * sizeof(T)) Quad {
-  T e[4];
-};
 
 struct Joined {
   float m, l;
@@ -282,18 +388,30 @@ cudaError_t join(const Args& a) {
   return launch_pdl(join_kernel<T, 16>, dim3(a.ctas, (a.cap + 15) / 16), dim3(kJoin), 0, a.p.stream, a);
 }
 
+template <typename T, int NQ>
+cudaError_t go(const SimpleArgs& a) {
+  const cudaError_t e = allow_smem<simple_kernel<T, NQ>>(simple_smem(256, 256, sizeof(T)).bytes);
+  return e != cudaSuccess ? e
+                          : launch_pdl(simple_kernel<T, NQ>, dim3(a.ctas), dim3(kThreads), a.L.bytes, a.p.stream, a);
+}
 template <typename T>
-cudaError_t go(const Args& a) {
-  const int smem = (int)simple_smem(a.p.D, a.p.DV).bytes;
-  const cudaError_t e = allow_smem<simple_kernel<T>>((int)simple_smem(256, 256).bytes);
-  return e != cudaSuccess ? e : launch_pdl(simple_kernel<T>, dim3(a.ctas), dim3(kThreads), smem, a.p.stream, a);
+cudaError_t go(const SimpleArgs& a) {
+  return a.p.DV > 128 ? go<T, 2>(a) : go<T, 1>(a);
 }
 
-int simple_ctas() { return 2 * sm_count(); }
+constexpr int kResident = 2;  // CTAs of an SM at most
+
+// Whether the rows of a cache are whole 16-byte chunks on their grid.
+bool chunks(const Problem& p, const void* base, const int64_t* s, int D, int esz) {
+  const int n[3] = {p.n_pages, p.block, p.HKV};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && s[i] * esz % 16) return false;
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && D * esz % 16 == 0;
+}
 
 }  // namespace
 
-size_t simple_workspace(int64_t rows, int DV) { return layout(simple_ctas(), rows, kRows, DV).total; }
+size_t simple_workspace(int64_t rows, int DV) { return layout(kResident * sm_count(), rows, kRows, DV).total; }
 
 cudaError_t launch_combine(const Args& a) {
   switch (a.p.dt) {
@@ -313,10 +431,18 @@ void set_layout(Args& a, const Layout& x, uint8_t* ws, int ctas) {
 }
 
 cudaError_t launch_simple(const Problem& p, uint8_t* ws) {
-  Args a{};
+  SimpleArgs a{};
   a.p = p;
-  set_layout(a, layout(simple_ctas(), (int64_t)p.T * p.G, kRows, p.DV), ws, simple_ctas());
-  a.cost = {4, 8, 4, 8};
+  const int esz = p.dt == GDP_F32 ? 4 : 2;
+  a.L = simple_smem(p.D, p.DV, esz);
+  // as many CTAs as are resident (a kilobyte of each one's shared memory is the system's)
+  const int ctas = sm_count() * std::max(1, std::min(kResident, (228 * 1024) / (a.L.bytes + 1280)));
+  set_layout(a, layout(ctas, (int64_t)p.T * p.G, kRows, p.DV), ws, ctas);
+  a.cost = kCost;
+  a.k_chunks = chunks(p, p.k, p.ks, p.D, esz) ? p.D * esz / 16 : 0;
+  a.v_chunks = chunks(p, p.v, p.vs, p.DV, esz) ? p.DV * esz / 16 : 0;
+  a.by_k = div_by(std::max(1, a.k_chunks));
+  a.by_v = div_by(std::max(1, a.v_chunks));
   cudaError_t e;
   switch (p.dt) {
     case GDP_BF16: e = go<__nv_bfloat16>(a); break;

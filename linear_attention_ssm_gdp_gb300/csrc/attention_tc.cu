@@ -49,7 +49,7 @@ struct Lay {
   static constexpr int QT = KD / 64 * 16384;     // 128 rows of queries
   static constexpr int Q = 0, K = 2 * QT, V = K + NK * TILE;
   static constexpr int BAR = V + NV * TILE;
-  static constexpr int ML = BAR + 640;           // maxima and sums [2][128]
+  static constexpr int ML = BAR + 704;           // maxima and sums [2][128]
   static constexpr int START = ML + 2048;        // the share, and the sums that lead to it
   static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
@@ -126,20 +126,20 @@ struct Spread {
   }
 };
 
-template <typename T, int KD>
+template <typename T, int KD, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ TcArgs a) {
   using L = Lay<KD>;
   extern __shared__ __align__(1024) uint8_t sm[];  // (nothing static beside it: the array begins on a swizzle atom)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + B_N);
+  uint64_t* s_absent = bars + B_N;                                     // [NV]: keys of a tile that are not there
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_absent + L::NV);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint32_t* s_absent = s_tmem + 2;                                     // [NV]
   float2* s_ml = reinterpret_cast<float2*>(sm + L::ML);                // [2][128]
   Start& s_start = *reinterpret_cast<Start*>(sm + L::START);
   long long* s_scan = reinterpret_cast<long long*>(sm + L::START + 96);  // [kThreads / 32]
-  static_assert(sizeof(Start) <= 96 && kThreads / 32 * 8 <= 96 && B_N * 8 + 8 + L::NV * 4 <= 640, "shared memory");
+  static_assert(sizeof(Start) <= 96 && kThreads / 32 * 8 <= 96 && B_N * 8 + L::NV * 8 + 8 <= 704, "shared memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const Problem& p = a.p;
 
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (tid == 96) *s_dead = 0;
-  if (warp == kLoad && lane == 0) {
+  if (TMA && warp == kLoad && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = sy.wait(&bars[B_S + slot], n & 1) && (!live || sy.wait(&bars[B_META + stage], turn & 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t absent = live ? s_absent[stage] : 0u;
+        const uint64_t absent = live ? s_absent[stage] : 0ull;
         uint32_t s[kKeys];
         if (live) {
           GDP_TMEM_LD32(ts, s);
@@ -234,11 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               see = low_bits(x.x.ctx + t + 1 - key0);
             }
-            see &= low_bits(x.keys - key0);
-            if (absent)
-#pragma unroll 1
-              for (int b = 0; b < kKeys; b += 8)
-                if (absent >> (b / a.g) & 1) see &= ~(0xffull << b);
+            see &= low_bits(x.keys - key0) & ~absent;
 #pragma unroll
             for (int e = 0; e < kKeys; ++e) {
               const uint32_t half = (uint32_t)(see >> (e & 32));
@@ -398,50 +394,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- loads
     // (One warp for K and V took 1350 cycles for a tile, longer than HBM.)
     const bool v = warp > kLoad;
-    const int subs = kKeys / a.g;  // boxes of a tile and half: 1 to 8, so a lane's is the same in every round
-    const int sub = lane % subs, boxes = subs * (KD / 64) / a.halves, col = lane / subs * 64;
-    const CUtensorMap* map = v ? &map_v : &map_k;
-    uint8_t* dst = sm + (v ? L::V : L::K) + sub * a.g * 128 + lane / subs * L::HALF;
-    uint64_t* full = &bars[v ? B_VFULL : B_KFULL];
     const int n = v ? L::NV : L::NK, empty = v ? B_VEMPTY - B_VFULL : B_KEMPTY - B_KFULL;
+    uint64_t* full = &bars[v ? B_VFULL : B_KFULL];
+    uint8_t* tiles = sm + (v ? L::V : L::K);
     int stage = 0;
     uint32_t turn = 1, loads = 0;
+    // keys of the tile that are not there: known before its values are
+    auto tell = [&](uint64_t absent) {
+      if (!v) return;
+      s_absent[stage] = absent;
+      mbar_arrive(&bars[B_META + stage]);
+    };
+    if (TMA) {
+      const int subs = kKeys / a.g;  // boxes of a tile and half: 1 to 8, so a lane's is the same in every round
+      const int sub = lane % subs, boxes = subs * (KD / 64) / a.halves, col = lane / subs * 64;
+      const CUtensorMap* map = v ? &map_v : &map_k;
+      uint8_t* dst = tiles + sub * a.g * 128 + lane / subs * L::HALF;
 #pragma unroll 1
-    while (ok && walk.next(p, x)) {
-      const int32_t* table = p.tables + (int64_t)x.r * p.width;
-      // page of this lane's box in tile j; -1: none
-      auto page_of = [&](int j) {
-        const int key = j * kKeys + sub * a.g;
-        return j < x.j1 && key < x.keys ? table[quot(key, p.by_block)] : -1;
-      };
-      int page = page_of(x.j0);
+      while (ok && walk.next(p, x)) {
+        const int32_t* table = p.tables + (int64_t)x.r * p.width;
+        // page of this lane's box in tile j; -1: none
+        auto page_of = [&](int j) {
+          const int key = j * kKeys + sub * a.g;
+          return j < x.j1 && key < x.keys ? table[quot(key, p.by_block)] : -1;
+        };
+        int page = page_of(x.j0);
 #pragma unroll 1
-      for (int j = x.j0; j < x.j1; ++j) {
-        const int next = page_of(j + 1), key = j * kKeys + sub * a.g;
-        ok = sy.wait(full + empty + stage, turn);
-        if (!ok) break;
-        if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
-        const bool there = (uint32_t)page < (uint32_t)p.n_pages;
-        const uint32_t absent = ~__ballot_sync(0xffffffffu, there) & ((1u << subs) - 1u);
-        if (lane == 0) {
-          if (v) {
-            s_absent[stage] = absent;
-            mbar_arrive(&bars[B_META + stage]);
+        for (int j = x.j0; j < x.j1; ++j) {
+          const int next = page_of(j + 1), key = j * kKeys + sub * a.g;
+          ok = sy.wait(full + empty + stage, turn);
+          if (!ok) break;
+          if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
+          const bool there = (uint32_t)page < (uint32_t)p.n_pages;
+          const uint32_t gone = ~__ballot_sync(0xffffffffu, there) & ((1u << subs) - 1u);
+          if (lane == 0) {
+            uint64_t absent = 0;
+            if (gone)
+              for (int b = 0; b < subs; ++b)
+                if (gone >> b & 1) absent |= low_bits(a.g) << (b * a.g);
+            tell(absent);
+            mbar_expect_tx(full + stage, L::TILE);
           }
-          mbar_expect_tx(full + stage, L::TILE);
+          __syncwarp();
+          if (lane < boxes)  // (a box past the last page arrives as zeros)
+            tma_load_5d(dst + stage * L::TILE, map, col, x.head, key - (int)quot(key, p.by_block) * p.block,
+                        there ? page : p.n_pages, 0, full + stage);
+          if (++stage == n) { stage = 0; turn ^= 1; }
+          ++loads;
+          page = next;
         }
-        __syncwarp();
-        if (lane < boxes)  // (a box past the last page arrives as zeros)
-          tma_load_5d(dst + stage * L::TILE, map, col, x.head, key - (int)quot(key, p.by_block) * p.block,
-                      there ? page : p.n_pages, 0, full + stage);
-        if (++stage == n) { stage = 0; turn ^= 1; }
-        ++loads;
-        page = next;
       }
+    } else {
+      // Pages whose size is not a multiple of 8: 16-byte copies, a row to KD / 8 lanes, three tiles in flight; a
+      // tile is told full once its copies are done and visible to the tensor cores.
+      constexpr int kLag = 3, kRow = KD / 8, kBeside = 32 / kRow;  // tiles; lanes of a row, rows beside each other
+      static_assert(kLag < L::NK, "a tile is told full before the wait for its buffer's next use");
+      const T* base = static_cast<const T*>(v ? p.v : p.k);
+      const int64_t s0 = v ? p.vs[0] : p.ks[0], s1 = v ? p.vs[1] : p.ks[1], s2 = v ? p.vs[2] : p.ks[2];
+      const int ch = lane % kRow, width = v ? p.DV : p.D;
+      int told = 0;       // stage of the next tile to be told
+      uint32_t tell_of = 0;
+      auto tell_full = [&]() {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + told);
+        if (++told == n) told = 0;
+        ++tell_of;
+      };
+#pragma unroll 1
+      while (ok && walk.next(p, x)) {
+        const int32_t* table = p.tables + (int64_t)x.r * p.width;
+        auto page_of = [&](int j, int half) {  // of key j kKeys + 32 half + lane
+          const int key = j * kKeys + 32 * half + lane;
+          return j < x.j1 && key < x.keys ? table[quot(key, p.by_block)] : -1;
+        };
+        int page0 = page_of(x.j0, 0), page1 = page_of(x.j0, 1);
+#pragma unroll 1
+        for (int j = x.j0; j < x.j1; ++j) {
+          const int next0 = page_of(j + 1, 0), next1 = page_of(j + 1, 1), key0 = j * kKeys + lane, key1 = key0 + 32;
+          ok = sy.wait(full + empty + stage, turn);
+          if (!ok) break;
+          if ((page0 >= p.n_pages || page1 >= p.n_pages) && p.status) *p.status = GDP_ERR_INVALID_ARG;
+          const bool there0 = (uint32_t)page0 < (uint32_t)p.n_pages, there1 = (uint32_t)page1 < (uint32_t)p.n_pages;
+          const uint64_t gone = ~(__ballot_sync(0xffffffffu, there0) | (uint64_t)__ballot_sync(0xffffffffu, there1) << 32);
+          if (lane == 0) tell(gone);
+          const long long at0 = there0 ? page0 * s0 + (key0 - (int)quot(key0, p.by_block) * p.block) * s1 : -1;
+          const long long at1 = there1 ? page1 * s0 + (key1 - (int)quot(key1, p.by_block) * p.block) * s1 : -1;
+          const uint32_t dst = smem_u32(tiles + stage * L::TILE) + (ch >> 3) * L::HALF;
+#pragma unroll 4
+          for (int i = 0; i < kKeys; i += kBeside) {
+            const int r = i + lane / kRow;
+            const long long a0 = __shfl_sync(0xffffffffu, i < 32 ? at0 : at1, r & 31);
+            const bool in = a0 >= 0 && 8 * ch < width;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + sw128_offset(r, (ch & 7) * 16)),
+                         "l"(base + (in ? a0 + x.head * s2 + 8 * ch : 0)), "r"(in ? 16 : 0)
+                         : "memory");
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (++stage == n) { stage = 0; turn ^= 1; }
+          if (++loads > kLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+            tell_full();
+          }
+          page0 = next0;
+          page1 = next1;
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (tell_of < loads) tell_full();
     }
     // the last buffers' commits land before the CTA leaves, and so do copies in flight where a wait ran out
     for (uint32_t b = loads > n ? loads - n : 0; ok && b < loads; ++b) ok = sy.wait(full + empty + b % n, (b / n) & 1);
-    if (*s_dead)
+    if (TMA && *s_dead)
       for (uint32_t b = loads > n ? loads - n : 0; b < loads; ++b)
         for (int tries = 0; tries < 1000 && !mbar_test_for(full + b % n, (b / n) & 1, 20000); ++tries) {}
   } else {
@@ -552,12 +616,17 @@ bool map5(CUtensorMap* m, const Problem& p, const void* base, int D, const int64
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int KD>
+template <typename T, int KD, bool TMA>
 cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
-  const cudaError_t e = allow_smem<attention_kernel<T, KD>>(Lay<KD>::BYTES);
+  const cudaError_t e = allow_smem<attention_kernel<T, KD, TMA>>(Lay<KD>::BYTES);
   return e != cudaSuccess ? e
-                          : launch_pdl(attention_kernel<T, KD>, dim3(a.ctas), dim3(kThreads), Lay<KD>::BYTES,
+                          : launch_pdl(attention_kernel<T, KD, TMA>, dim3(a.ctas), dim3(kThreads), Lay<KD>::BYTES,
                                        a.p.stream, m[0], m[1], a);
+}
+template <typename T>
+cudaError_t go(const TcArgs& a, const CUtensorMap* m, bool tma) {
+  if (a.p.D > 64 || a.p.DV > 64) return tma ? go<T, 128, true>(a, m) : go<T, 128, false>(a, m);
+  return tma ? go<T, 64, true>(a, m) : go<T, 64, false>(a, m);
 }
 
 }  // namespace
@@ -569,7 +638,7 @@ bool tc_shape(int D, int DV, gdp_dtype dt) {
 bool tc_ok(const Problem& p) {
   const auto fits = [](int n, int64_t x) { return n <= 1 || (x > 0 && x % 8 == 0 && x < ((int64_t)1 << 38)); };
   const auto even = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
-  if (!tc_shape(p.D, p.DV, p.dt) || p.block % 8 || p.n_pages < 1) return false;
+  if (!tc_shape(p.D, p.DV, p.dt) || p.n_pages < 1) return false;
   if (!even(p.q) || !even(p.k) || !even(p.v) || !even(p.o)) return false;
   const int qn[3] = {p.B, p.T, p.H}, cn[3] = {p.n_pages, p.block, p.HKV};
   for (int i = 0; i < 3; ++i)
@@ -589,21 +658,17 @@ cudaError_t launch_tc(const Problem& p, uint8_t* ws) {
   a.p = p;
   set_layout(a, layout(sm_count(), (int64_t)p.T * p.G, kRows, p.DV), ws, sm_count());
   a.cost = kCost;
-  a.g = 8;
-  while (a.g < kKeys && p.block % (2 * a.g) == 0) a.g *= 2;
   a.budget = (int)(g_budget_ns.load() >> 10);
   a.fault = g_fault.exchange(0);
-  CUtensorMap m[2];
+  CUtensorMap m[2] = {};
+  const bool tma = p.block % 8 == 0;  // (swizzled boxes begin on 8 rows)
+  a.g = tma ? 8 : 1;
+  while (tma && a.g < kKeys && p.block % (2 * a.g) == 0) a.g *= 2;
   // (a box of both halves needs its rows to be a whole half's)
   a.halves = a.g == kKeys && p.D == 128 && p.DV == 128 ? 2 : 1;
-  if (!map5(&m[0], p, p.k, p.D, p.ks, a.g, a.halves) || !map5(&m[1], p, p.v, p.DV, p.vs, a.g, a.halves))
+  if (tma && (!map5(&m[0], p, p.k, p.D, p.ks, a.g, a.halves) || !map5(&m[1], p, p.v, p.DV, p.vs, a.g, a.halves)))
     return cudaErrorInvalidValue;
-  const bool wide = p.D > 64 || p.DV > 64;
-  cudaError_t e;
-  if (p.dt == GDP_BF16)
-    e = wide ? go<__nv_bfloat16, 128>(a, m) : go<__nv_bfloat16, 64>(a, m);
-  else
-    e = wide ? go<__half, 128>(a, m) : go<__half, 64>(a, m);
+  const cudaError_t e = p.dt == GDP_BF16 ? go<__nv_bfloat16>(a, m, tma) : go<__half>(a, m, tma);
   return e != cudaSuccess ? e : launch_combine(a);
 }
 

@@ -398,3 +398,18 @@ def test_many_pieces_many_times(gdp, lens, ctx):
         got.append(gdp.gdp_attention_paged(**d))
     assert all(torch.equal(x, want) for x in got)
     check(gdp, d)
+
+
+@pytest.mark.parametrize("block", [1, 3, 12, 100, 520])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,DV", [(64, 64), (128, 96)])
+def test_block_sizes(gdp, block, dtype, D, DV):
+    """Pages that are not whole boxes: other loads than for multiples of 8, holes among them."""
+    d = problem([3, 1, 40, 0, 2], [500, 64, 1300, 9, 31], 8, 2, D, DV, block, dtype,
+                holes=[(0, 0), (2, 1)] if block > 1 else [(0, 7), (0, 64), (2, 1000)])
+    check(gdp, d)
+    dead = dict(d, k_cache=d["k_cache"].clone(), v_cache=d["v_cache"].clone())
+    last = int(d["block_tables"][0, 502 // block])  # NaN behind the request's last token
+    for c in (dead["k_cache"], dead["v_cache"]):
+        c[last, 502 % block + 1:] = torch.nan
+    assert torch.equal(gdp.gdp_attention_paged(**dead), gdp.gdp_attention_paged(**d))
