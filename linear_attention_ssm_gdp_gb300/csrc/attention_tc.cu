@@ -91,8 +91,11 @@ struct Sync {
   int budget;
   int* status;
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    const bool ok = mbar_test(bar, parity) || wait_slow(bar, parity, dead, budget, status);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, wait1(bar, parity));
+  }
+  // by one thread
+  __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) const {
+    return mbar_test(bar, parity) || wait_slow(bar, parity, dead, budget, status);
   }
 };
 
@@ -514,61 +517,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     // soon as those before have been read to registers, beside their softmax; weights have columns of their own, so
     // no order between the two warps is needed. (One warp for everything took 2800 cycles for a tile of 2 x 128
     // rows, one for each slot 1750: its waits and issues one after another.)
+    // (One thread of each: votes and elections in every step cost a tenth.)
     const bool pv = warp == kOutputs;
     const uint32_t id_s = idesc<T>(128, kKeys, false) | (p.c < 0.f ? 1u << 13 : 0u);  // (-Q)
     constexpr uint32_t id_o = idesc<T>(128, KD, true);
     const uint32_t base = smem_u32(sm);
-    const uint64_t qd = sdesc_sw128(base + L::Q, 16, 1024), kd = sdesc_sw128(base + L::K, 16, 1024);
-    const uint64_t vd = sdesc_sw128(base + L::V, L::HALF, 1024);
-    uint32_t stage = 0, turn = 0, n[2] = {0, 0}, nq[2] = {0, 0};  // buffer of the next tile; per slot: tiles, queries
+    if (elect_one()) {
+      uint32_t stage = 0, turn = 0, n0 = 0, n1 = 0;  // buffer of the next tile; tiles of the slots
+      if (!pv) {
+        const uint64_t qd = sdesc_sw128(base + L::Q, 16, 1024), kd = sdesc_sw128(base + L::K, 16, 1024);
+        uint32_t nq0 = 0, nq1 = 0;
 #pragma unroll 1
-    while (ok && walk.next(p, x)) {
-      const int nt = x.j1 - x.j0;
-      const bool two = x.rows > 128;
-      const int steps = two ? 2 * nt : nt;
+        while (ok && walk.next(p, x)) {
+          const int nt = x.j1 - x.j0;
+          const bool two = x.rows > 128;
+          const int steps = two ? 2 * nt : nt;
 #pragma unroll 1
-      for (int i = 0; ok && i < steps; ++i) {
-        const int s = i & 1;
-        const uint32_t ni = s ? n[1] : n[0];
-        const bool first = !two || s == 0, last = !two || s == 1;  // of the tile's steps
-        if (pv) {
-          ok = sy.wait(&bars[B_P + 2 * s + (ni & 1)], ni >> 1 & 1) && (!first || sy.wait(&bars[B_VFULL + stage], turn));
-        } else {
-          // (in the first tile of a piece the scores before have been read: its queries are there)
-          if (i < 2) {
-            ok = sy.wait(&bars[B_Q + s], (s ? nq[1] : nq[0]) & 1);
-            if (s) ++nq[1]; else ++nq[0];
-          } else {
-            ok = sy.wait(&bars[B_R + s], (ni - 1) & 1);
+          for (int i = 0; i < steps; ++i) {
+            const int s = i & 1;
+            // (in the first tile of a piece the scores before have been read: its queries are there)
+            if (i < 2) {
+              ok = sy.wait1(&bars[B_Q + s], (s ? nq1 : nq0) & 1);
+              if (s) ++nq1; else ++nq0;
+            } else {
+              ok = sy.wait1(&bars[B_R + s], ((s ? n1 : n0) - 1) & 1);
+            }
+            ok = ok && ((two && s) || sy.wait1(&bars[B_KFULL + stage], turn));
+            if (!ok) break;
+            tc_fence_after();
+            mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(tmem + T_S + 128 * s, qd + s * (L::QT >> 4),
+                                                            kd + stage * (L::TILE >> 4), id_s);
+            mma_commit(&bars[B_S + s]);
+            if (s) ++n1; else ++n0;
+            if (!two || s) {  // the last step of the tile
+              mma_commit(&bars[B_KEMPTY + stage]);
+              if (++stage == L::NK) { stage = 0; turn ^= 1; }
+            }
           }
-          ok = ok && (!first || sy.wait(&bars[B_KFULL + stage], turn));
         }
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t ts = tmem + T_S + 128 * s;
-        if (elect_one()) {
-          if (pv) {
+      } else {
+        const uint64_t vd = sdesc_sw128(base + L::V, L::HALF, 1024);
+#pragma unroll 1
+        while (ok && walk.next(p, x)) {
+          const int nt = x.j1 - x.j0;
+          const bool two = x.rows > 128;
+          const int steps = two ? 2 * nt : nt;
+#pragma unroll 1
+          for (int i = 0; i < steps; ++i) {
+            const int s = i & 1;
+            const uint32_t n = s ? n1 : n0;
+            ok = sy.wait1(&bars[B_P + 2 * s + (n & 1)], n >> 1 & 1) &&
+                 ((two && s) || sy.wait1(&bars[B_VFULL + stage], turn));
+            if (!ok) break;
+            tc_fence_after();
             const uint64_t v = vd + stage * (L::TILE >> 4);
 #pragma unroll
             for (int e = 0; e < kKeys / 16; ++e)
-              mma_bf16_ts(tmem + T_O + 128 * s, ts + T_P + 32 * (ni & 1) + 8 * e, v + e * (2048 >> 4), id_o,
-                          i > 1 || e > 0);
-            mma_commit(&bars[B_O + 2 * s + (ni & 1)]);
-            if (last) mma_commit(&bars[B_VEMPTY + stage]);
-          } else {
-            mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(ts, qd + s * (L::QT >> 4), kd + stage * (L::TILE >> 4), id_s);
-            mma_commit(&bars[B_S + s]);
-            if (last) mma_commit(&bars[B_KEMPTY + stage]);
+              mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + T_P + 32 * (n & 1) + 8 * e, v + e * (2048 >> 4),
+                          id_o, i > 1 || e > 0);
+            mma_commit(&bars[B_O + 2 * s + (n & 1)]);
+            if (s) ++n1; else ++n0;
+            if (!two || s) {
+              mma_commit(&bars[B_VEMPTY + stage]);
+              if (++stage == L::NV) { stage = 0; turn ^= 1; }
+            }
           }
         }
-        __syncwarp();
-        if (s) ++n[1]; else ++n[0];
-        if (last && ++stage == (pv ? L::NV : L::NK)) { stage = 0; turn ^= 1; }
       }
-    }
-    if (!ok) {  // products in flight end before their operands and columns go away
-      if (elect_one()) mma_commit(&bars[B_END + pv]);
-      for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END + pv], 0, 20000); ++tries) {}
+      if (!ok) {  // products in flight end before their operands and columns go away
+        mma_commit(&bars[B_END + pv]);
+        for (int tries = 0; tries < 1000 && !mbar_test_for(&bars[B_END + pv], 0, 20000); ++tries) {}
+      }
     }
   }
   __syncwarp();
