@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
   __shared__ Start s_start;
   __shared__ long long s_scan[kThreads / 32 + 1];
   pdl_wait();
+  pdl_trigger();
   find_start<kRows, kKeys, kThreads>(a, &s_start, s_scan);
   Walk<kRows, kKeys> walk(s_start, a.cost);
   Piece x;

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_v);
   }
   pdl_wait();
+  pdl_trigger();
   find_start<kRows, kKeys, kThreads>(a, &s_start, s_scan);
   tc_fence_before();
   __syncthreads();
@@ -189,12 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(p, x)) {
       const Spread d(x, slot);
       if (d.n > 0) {  // Q: 16-byte chunks of the rows, zero behind the head's end
+        const int ch = tid % (KD / 8);
+        const T* q0 = static_cast<const T*>(p.q) + (p.cu ? x.first * p.qs[1] : x.r * p.qs[0]) + x.head * p.G * p.qs[2] +
+                      (8 * ch < p.D ? 8 * ch : 0);
 #pragma unroll 4
-        for (int i = tid & 127; i < d.rows * (KD / 8); i += 128) {
-          const int r = i / (KD / 8), ch = i % (KD / 8), R = d.row0 + r, t = (int)quot(R, p.by_G);
-          const int h = x.head * p.G + R - t * p.G;
-          const int64_t at = p.cu ? (x.first + t) * p.qs[1] : x.r * p.qs[0] + t * p.qs[1];
-          const T* src = static_cast<const T*>(p.q) + at + h * p.qs[2] + (8 * ch < p.D ? 8 * ch : 0);
+        for (int r = (tid & 127) / (KD / 8); r < d.rows; r += 128 / (KD / 8)) {
+          const int R = d.row0 + r, t = (int)quot(R, p.by_G);
+          const T* src = q0 + t * p.qs[1] + (R - t * p.G) * p.qs[2];
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                            sqa + (ch >> 3) * 16384 + sw128_offset(r, (ch & 7) * 16)),
                        "l"(src), "r"(8 * ch < p.D ? 16 : 0)

@@ -127,9 +127,9 @@ cudaError_t allow_smem(int bytes) {
 // writes are still being made visible, so the launch overlaps the flush; it
 // calls pdl_wait() before its first global-memory access, which returns once
 // every earlier kernel of the stream has completed and its writes are visible.
-// No kernel triggers its dependents early: with an early trigger the fused scan's
-// CTAs were placed on SMs as WY-128's CTAs drained and the prefill step took
-// 0.541 ms instead of 0.482 ms.
+// Few kernels trigger their dependents early (pdl_trigger): with an early trigger the
+// fused scan's CTAs were placed on SMs as WY-128's CTAs drained and the prefill step
+// took 0.541 ms instead of 0.482 ms.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args&&... args) {
@@ -146,6 +146,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel of the stream may be placed on SMs as this one's CTAs leave; its pdl_wait still waits for all.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Records stage-boundary event i (gdp_set_stage_events) on `s`; no-op when off.
 // Slots: 0 entry, 1 after the chunk tables, 2 after the WY stage (transition
