@@ -302,24 +302,27 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ joining cut items
-// A CTA per record and RB rows, a thread per row, quad of columns and every groups-th piece: batches of
-// pieces, their loads in flight together, are added under a running maximum, in the order of the pieces;
+// A CTA per record and RB rows, a thread per row, two quads of columns and every groups-th piece: batches of
+// four pieces, their loads in flight together, are added under a running maximum, in the order of the pieces;
 // then the groups' results in the order of the groups. Rows lie side by side, so a warp reads whole lines.
-constexpr int kJoin = 256, kBatch = 8;
+constexpr int kJoin = 256, kBatch = 4;
 
 struct Joined {
   float m, l;
-  float4 acc;
-  // f0 of this, f1 of x
-  __device__ __forceinline__ void add(float xm, float xl, const float4& x) {
+  float4 acc[2];
+  __device__ __forceinline__ void add(float xm, float xl, const float4& x0, const float4& x1) {
     const float mn = fmaxf(m, xm), base = mn == -INFINITY ? 0.f : mn;
     const float f0 = ex2(m - base), f1 = ex2(xm - base);
     m = mn;
     l = f0 * l + f1 * xl;
-    acc.x = fmaf(f1, x.x, f0 * acc.x);
-    acc.y = fmaf(f1, x.y, f0 * acc.y);
-    acc.z = fmaf(f1, x.z, f0 * acc.z);
-    acc.w = fmaf(f1, x.w, f0 * acc.w);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float4& x = n ? x1 : x0;
+      acc[n].x = fmaf(f1, x.x, f0 * acc[n].x);
+      acc[n].y = fmaf(f1, x.y, f0 * acc[n].y);
+      acc[n].z = fmaf(f1, x.z, f0 * acc[n].z);
+      acc[n].w = fmaf(f1, x.w, f0 * acc[n].w);
+    }
   }
 };
 
@@ -333,31 +336,34 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Arg
   if ((int)blockIdx.y * RB >= r.rows) return;
   const Problem& p = a.p;
   const int pieces = r.more + 1, quads = a.dvp / 4;
-  int span = 1;  // slots of a group: a power of two
-  while (span < quads && span < kSlots) span *= 2;
+  int span = 1;  // slots of a group, for two quads each: a power of two
+  while (2 * span < quads && span < kSlots) span *= 2;
   const int slot = tid / RB, group = slot / span, groups = kSlots / span;
   const bool even = p.DV % 4 == 0 && reinterpret_cast<uintptr_t>(p.o) % sizeof(Quad<T>) == 0;
   // piece i: slot 1 of this CTA, slot 0 of the next ones
   auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * a.cap; };
-  for (int q0 = 0; q0 < quads; q0 += span) {
+  for (int q0 = 0; q0 < quads; q0 += 2 * span) {
     const int q = q0 + slot % span;
-    const bool on = row < r.rows && q < quads;
-    Joined x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    const bool on = row < r.rows && q < quads, both = q + span < quads;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    Joined x = {-INFINITY, 0.f, {zero, zero}};
     if (on)
       for (int i0 = group; i0 < pieces; i0 += kBatch * groups) {
         float2 ml[kBatch];
-        float4 v[kBatch];
+        float4 v[kBatch][2];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int i = i0 + k * groups;
           if (i < pieces) {
+            const float4* src = reinterpret_cast<const float4*>(a.part) + at(i) * quads + (int64_t)q * a.cap + row;
             ml[k] = a.ml[at(i) + row];
-            v[k] = reinterpret_cast<const float4*>(a.part)[at(i) * quads + (int64_t)q * a.cap + row];
+            v[k][0] = src[0];
+            v[k][1] = both ? src[(int64_t)span * a.cap] : zero;
           }
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-          if (i0 + k * groups < pieces) x.add(ml[k].x, ml[k].y, v[k]);
+          if (i0 + k * groups < pieces) x.add(ml[k].x, ml[k].y, v[k][0], v[k][1]);
       }
     if (groups > 1) {
       __syncthreads();
@@ -366,18 +372,22 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Arg
       if (group == 0)
         for (int g = 1; g < groups; ++g) {
           const Joined& y = s_part[tid + g * span * RB];
-          x.add(y.m, y.l, y.acc);
+          x.add(y.m, y.l, y.acc[0], y.acc[1]);
         }
     }
     if (on && group == 0) {
       const float f = x.l > 0.f || x.l != x.l ? 1.f / x.l : 0.f;
-      T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row) + 4 * q;
-      const Quad<T> y = {from_f<T>(x.acc.x * f), from_f<T>(x.acc.y * f), from_f<T>(x.acc.z * f), from_f<T>(x.acc.w * f)};
-      if (even)
-        *reinterpret_cast<Quad<T>*>(dst) = y;
-      else
-        for (int k = 0; k < 4; ++k)
-          if (4 * q + k < p.DV) dst[k] = y.e[k];
+      T* dst = static_cast<T*>(p.o) + out_at(p, r.first, r.head, r.row0 + row);
+      for (int n = 0; n < 1 + both; ++n) {
+        const float4 u = n ? x.acc[1] : x.acc[0];
+        const int col = 4 * (q + n * span);
+        const Quad<T> y = {from_f<T>(u.x * f), from_f<T>(u.y * f), from_f<T>(u.z * f), from_f<T>(u.w * f)};
+        if (even)
+          *reinterpret_cast<Quad<T>*>(dst + col) = y;
+        else
+          for (int k = 0; k < 4; ++k)
+            if (col + k < p.DV) dst[col + k] = y.e[k];
+      }
     }
   }
 }
