@@ -54,15 +54,14 @@ struct Lay {
   static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-// by buffer: K full, empty, V full, empty, absent boxes known; by slot: scores formed, read; by slot and buffer:
-// weights, outputs (of that tile: a waiter may be two tiles behind, which one barrier's parity cannot tell from
-// none); by slot: queries; a piece's two slots have left their maxima, have read each other's outputs
+// by buffer: K full, empty, V full, empty, absent keys known; by slot and buffer of its scores: scores, weights,
+// outputs (a waiter may be two tiles behind, which one barrier's parity cannot tell from none); by slot: queries;
+// a piece's two slots have left their maxima, have read each other's outputs
 enum {
-  B_KFULL = 0, B_KEMPTY = 8, B_VFULL = 16, B_VEMPTY = 28, B_META = 40, B_S = 52, B_R = 54, B_P = 56, B_O = 60, B_Q = 64,
+  B_KFULL = 0, B_KEMPTY = 8, B_VFULL = 16, B_VEMPTY = 28, B_META = 40, B_S = 52, B_P = 56, B_O = 60, B_Q = 64,
   B_JOIN = 66, B_DONE, B_END, B_N = B_END + 2
 };
-// columns: by slot, scores [64] and weights [2][32] (16-bit pairs); outputs [2][128]
-constexpr uint32_t T_S = 0, T_P = 64, T_O = 256;
+constexpr uint32_t T_S = 0, T_O = 256;  // columns: scores [2][2][64], weights over them; outputs [2][128]
 
 struct TcArgs : Args {
   int g;          // keys of a box
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid < B_N) {
     int n = 1;
-    if ((tid >= B_R && tid < B_O) || (tid >= B_Q && tid < B_JOIN)) n = 4;                // warps of the slot
+    if ((tid >= B_P && tid < B_O) || (tid >= B_Q && tid < B_JOIN)) n = 4;                // warps of the slot
     if (tid == B_JOIN || tid == B_DONE) n = 8;
     if (tid == B_S && a.fault) n = 2;
     mbar_init(&bars[tid], n);
@@ -215,21 +214,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && k < d.n; ++k, ++n) {
         const int j = d.two ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
         const uint32_t stage = (tile0 + j) % L::NV, turn = (tile0 + j) / L::NV;
-        const uint32_t buf = n & 1;
-        ok = sy.wait(&bars[B_S + slot], n & 1) && (!live || sy.wait(&bars[B_META + stage], turn & 1));
+        const uint32_t buf = n & 1, tb = ts + 64 * buf;
+        ok = sy.wait(&bars[B_S + 2 * slot + buf], n >> 1 & 1) && (!live || sy.wait(&bars[B_META + stage], turn & 1));
         if (!ok) break;
         tc_fence_after();
         const uint64_t absent = live ? s_absent[stage] : 0ull;
-        uint32_t s[kKeys];
         if (live) {
-          GDP_TMEM_LD32(ts, s);
-          GDP_TMEM_LD32(ts + 32, (s + 32));
+          uint32_t s[kKeys];
+          GDP_TMEM_LD32(tb, s);
+          GDP_TMEM_LD32(tb + 32, (s + 32));
           tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_R + slot]);  // the next tile's scores may come
-        if (live) {
           if (key0 + kKeys > x.x.ctx || absent) {  // some of the keys are not seen by some row
             uint64_t see;
             if (p.tree) {
@@ -281,12 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[2 * (e & 1) + 1] += p1;
             w[e] = pack<T>(p0, p1);
           }
-          if (k > 1) {  // the weights that lie there have been multiplied
-            ok = sy.wait(&bars[B_O + 2 * slot + buf], (n >> 1) - 1 & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          GDP_TMEM_ST32(ts + T_P + 32 * buf, w);
+          GDP_TMEM_ST32(tb, w);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
@@ -537,19 +526,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < steps; ++i) {
             const int s = i & 1;
-            // (in the first tile of a piece the scores before have been read: its queries are there)
+            const uint32_t n = s ? n1 : n0, buf = n & 1;
+            // Scores go over the weights of two tiles before, once those have been multiplied; in a piece's first
+            // two tiles they have been, and its queries are there.
             if (i < 2) {
               ok = sy.wait1(&bars[B_Q + s], (s ? nq1 : nq0) & 1);
               if (s) ++nq1; else ++nq0;
-            } else {
-              ok = sy.wait1(&bars[B_R + s], ((s ? n1 : n0) - 1) & 1);
+            } else if (i >= 4) {
+              ok = sy.wait1(&bars[B_O + 2 * s + buf], (n >> 1) - 1 & 1);
             }
             ok = ok && ((two && s) || sy.wait1(&bars[B_KFULL + stage], turn));
             if (!ok) break;
             tc_fence_after();
-            mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(tmem + T_S + 128 * s, qd + s * (L::QT >> 4),
+            mma_run<KD / 16, false, 16384, 32, L::HALF, 32>(tmem + T_S + 128 * s + 64 * buf, qd + s * (L::QT >> 4),
                                                             kd + stage * (L::TILE >> 4), id_s);
-            mma_commit(&bars[B_S + s]);
+            mma_commit(&bars[B_S + 2 * s + buf]);
             if (s) ++n1; else ++n0;
             if (!two || s) {  // the last step of the tile
               mma_commit(&bars[B_KEMPTY + stage]);
@@ -575,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t v = vd + stage * (L::TILE >> 4);
 #pragma unroll
             for (int e = 0; e < kKeys / 16; ++e)
-              mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + T_P + 32 * (n & 1) + 8 * e, v + e * (2048 >> 4),
+              mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + 64 * (n & 1) + 8 * e, v + e * (2048 >> 4),
                           id_o, i > 1 || e > 0);
             mma_commit(&bars[B_O + 2 * s + (n & 1)]);
             if (s) ++n1; else ++n0;
