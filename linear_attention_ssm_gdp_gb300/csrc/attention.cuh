@@ -110,16 +110,18 @@ struct Cut {
   }
   __device__ static __forceinline__ int begin(const Cost& c, bool large) { return large ? c.begin2 : c.begin; }
   __device__ static __forceinline__ int each(const Cost& c, bool large) { return large ? c.tile2 : c.tile; }
-  __device__ static __forceinline__ int64_t cost(const Problem& p, const Cost& c, const Req& x, int tile) {
+  // (fits 32 bits: keys do, and a tile of 32 of them costs at most 8)
+  __device__ static __forceinline__ int cost(const Problem& p, const Cost& c, const Req& x, int tile) {
     const bool l = large(p, x, tile);
-    return begin(c, l) + (int64_t)units(keys(p, x, tile)) * each(c, l);
+    return begin(c, l) + units(keys(p, x, tile)) * each(c, l);
   }
   // of one head of a request
   __device__ static __forceinline__ int64_t head_cost(const Problem& p, const Cost& c, const Req& x) {
     if (x.S <= 0) return 0;
     const int n = tiles(p, x.S);
+    if (p.tree || !x.live) return (int64_t)(n - 1) * cost(p, c, x, 0) + cost(p, c, x, n - 1);
     int64_t u = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < n; ++i) u += cost(p, c, x, i);
     return u;
   }
@@ -150,32 +152,34 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.n + NT - 1) / NT;
   const int r0 = (int)min((int64_t)tid * per, (int64_t)p.n), r1 = min(r0 + per, p.n);
-  long long mine = 0;
+  long long mine = 0, head = 0;  // head: of one head of the last request
   int bad = 0, odd = 0;
+  Req x{};
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     if (p.cu) {
       const int a0 = p.cu[r], a1 = p.cu[r + 1];
       if (a0 < 0 || a1 < a0 || a1 > p.T || (r == 0 && a0 != 0)) { bad = 1; break; }
     }
-    const Req x = request(p, r);
+    x = request(p, r);
     if (x.bad) odd = 1;
-    mine += C::head_cost(p, a.cost, x);
+    head = C::head_cost(p, a.cost, x);
+    mine += head;
   }
   mine *= p.HKV;
   if (blockIdx.x == 0 && (odd || bad) && p.status) *p.status = GDP_ERR_INVALID_ARG;
   bad = __syncthreads_or(bad);
   long long sum = mine;
-#pragma unroll 1
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += x;
+    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
   }
   if (lane == 31) scratch[warp] = sum;
   if (tid == 0) { out->bad = bad; out->left = 0; }
   __syncthreads();
   long long before = sum - mine, total = 0;
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
@@ -190,21 +194,20 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
     if (before <= u0 && u0 < before + mine) {  // the thread whose requests hold the start
       long long at = u0 - before;
       int r = r0;
-      Req x;
-      long long head;
+      if (r1 - r0 > 1)
 #pragma unroll 1
-      for (;; ++r) {
-        x = request(p, r);
-        head = C::head_cost(p, a.cost, x);
-        if (at < head * p.HKV) break;
-        at -= head * p.HKV;
-      }
+        for (;; ++r) {
+          x = request(p, r);
+          head = C::head_cost(p, a.cost, x);
+          if (at < head * p.HKV) break;
+          at -= head * p.HKV;
+        }
       const long long h = divide(at, head);
       at -= h * head;
       int tile = 0;
 #pragma unroll 1
       for (;; ++tile) {
-        const long long u = C::cost(p, a.cost, x, tile);
+        const int u = C::cost(p, a.cost, x, tile);
         if (at < u) break;
         at -= u;
       }
