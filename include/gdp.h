@@ -557,7 +557,8 @@ gdp_status gdp_rotary_frequencies(int rotary_dim, double base, gdp_rotary_scalin
  * gradient of x from y's.
  *   x, y    [B, T, H, D] in dtype `dt`, the last dimension contiguous; x_strides and
  *           y_strides are HOST arrays of three element strides (batch, token, head).
- *           y is x with the same strides (in place), or does not overlap it.
+ *           y is x with the same strides (in place), or does not overlap it; its own elements
+ *           lie apart (strides of 0 are refused).
  *   positions [B, T] int32, any value; frequencies [rotary_dim / 2] fp64, finite, on the
  *           device. Angles are exact to 2^-52 of a frequency times the position.
  * D <= 1024. Sums are fp32, rounded once.
@@ -584,7 +585,8 @@ gdp_status gdp_rotary(const void* x, const int64_t* x_strides, const int32_t* po
  *   k_cache [n_pages, block_size, HKV, D], v_cache [n_pages, block_size, HKV, DV]: dtype
  *           `dt`, the last dimension contiguous; k_cache_strides and v_cache_strides: HOST
  *           arrays of three element strides (page, place, head), so views of one buffer and
- *           head-major pages go in as they are. Other slots are left as they are.
+ *           head-major pages go in as they are (strides of 0 are refused). Other slots are
+ *           left as they are.
  *   q_out   [B, T, H, D] contiguous; q itself where that is contiguous.
  * D, DV <= 1024. Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED (dtype, sizes),
  * GDP_ERR_CUDA.
@@ -614,7 +616,7 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  *   tree_mask (nullable) [B, T] int64: bit j of a token: it sees the request's new token j
  *           (its ancestors in the tree, and itself), beside the whole context; requests of
  *           at most 64 tokens. NULL: every token sees the new ones up to itself.
- * Output: o [B, T, H, DV] contiguous, dtype `dt`; a row that sees nothing is 0. Sums and the
+ * Output: o [B, T, H, DV] contiguous, dtype `dt`, apart from q; a row that sees nothing is 0. Sums and the
  * softmax's statistics are fp32; 16-bit types round its weights to the type (relative to a
  * maximum that is at most 2^8 too small) before the product with V.
  * Refused on the device: a page number of n_pages or more (the block is not there, as for

@@ -16,8 +16,9 @@ namespace {
 // A CTA of eight warps takes up to 8 rows of an item against tiles of 32 keys, which arrive in their own type by
 // cp.async, up to three tiles ahead (rows that are not whole 16-byte chunks are copied by elements). Products are
 // fp32 multiply-adds: for the scores a thread has a key and every eighth chunk of the head, for the outputs four
-// columns (eight above 128) and every eighth key, whose sums meet at the item's end. Up to 8 rows that is HBM's
-// time for fp32: a tile of 32 KB for 128 + 128 columns takes an SM 0.75 us to load and its products 0.4.
+// columns (eight above 128) and every eighth key, whose sums meet at the item's end. Bound by issue slots (half
+// used) and three barriers a tile: 64 requests of up to 4000 keys, 16 heads over 4, 128 columns, fp32: 137 us,
+// where HBM needs 65; 16 requests of 9000 keys, 256 columns, bf16: 240 us, HBM 50.
 constexpr int kRows = 8, kKeys = 32, kThreads = 256, kWarps = kThreads / 32;
 constexpr Cost kCost = {8, 3, 8, 3};
 

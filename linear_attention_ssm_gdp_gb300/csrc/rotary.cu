@@ -331,6 +331,11 @@ gdp_status check(int B, int T, int D, gdp_dtype dt, const int32_t* pos, const do
   return GDP_OK;
 }
 
+// No two elements of a destination in one place, as far as a stride alone says.
+bool apart(const int64_t* s, int n0, int n1, int n2) {
+  return (n0 <= 1 || s[0] > 0) && (n1 <= 1 || s[1] > 0) && (n2 <= 1 || s[2] > 0);
+}
+
 bool strides_ok(const int64_t* s, int n) {
   if (!s) return false;
   for (int i = 0; i < n; ++i)
@@ -385,7 +390,8 @@ gdp_status gdp_rotary(const void* x, const int64_t* x_strides, const int32_t* po
   if (H < 0) return GDP_ERR_INVALID_ARG;
   if ((int64_t)H * D > INT32_MAX / 2) return GDP_ERR_UNSUPPORTED;
   if ((int64_t)B * T * H == 0) return GDP_OK;
-  if (!x || !y || !strides_ok(x_strides, 3) || !strides_ok(y_strides, 3)) return GDP_ERR_INVALID_ARG;
+  if (!x || !y || !strides_ok(x_strides, 3) || !strides_ok(y_strides, 3) || !apart(y_strides, B, T, H))
+    return GDP_ERR_INVALID_ARG;
   if (y == x)  // in place: every element is written where it was read
     for (int i = 0; i < 3; ++i)
       if ((i == 0 ? B : i == 1 ? T : H) > 1 && x_strides[i] != y_strides[i]) return GDP_ERR_INVALID_ARG;
@@ -416,7 +422,8 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
     return GDP_ERR_UNSUPPORTED;
   if ((int64_t)B * T == 0) return GDP_OK;
   if (!k || !v || !slot_map || (n_pages > 0 && (!k_cache || !v_cache)) || !strides_ok(strides, 9) || !strides_ok(k_cache_strides, 3) ||
-      !strides_ok(v_cache_strides, 3))
+      !strides_ok(v_cache_strides, 3) || !apart(k_cache_strides, n_pages, block_size, HKV) ||
+      !apart(v_cache_strides, n_pages, block_size, HKV))
     return GDP_ERR_INVALID_ARG;
   const int QH = q ? H : 0;
   const int64_t qo[3] = {(int64_t)T * H * D, (int64_t)H * D, D};

@@ -40,6 +40,7 @@ NAN, INF = float("nan"), float("inf")
     (dict(R=16, offset=17), 1), (dict(a=NAN), 1), (dict(a=INF), 1), (dict(B=-1), 1), (dict(T=-1), 1), (dict(H=-1), 1),
     (dict(D=0, R=0), 1), (dict(D=1025), 2), (dict(dt=3), 2), (dict(B=1 << 16, T=1 << 15), 2), (dict(H=1 << 26), 2),
     (dict(y=A, ys=st(0, 128, 32)), 1),        # in place with other strides
+    (dict(ys=st(0, 64, 0)), 1), (dict(ys=st(0, 0, 32)), 1), (dict(B=2, ys=st(0, 64, 32)), 1),  # elements in one place
 ])
 def test_rotary_rejects(so, kw, status):
     a = dict(x=A, xs=st(0, 64, 32), pos=A, f=A, R=32, offset=0, a=1.0, B=1, T=4, H=2, D=32, dt=0, y=2 * A,
@@ -55,7 +56,7 @@ def test_rotary_rejects(so, kw, status):
     (dict(vc=None), 1), (dict(ks=None), 1), (dict(vs=st(64, -32, 32)), 1), (dict(pos=None), 1), (dict(f=None), 1),
     (dict(R=40), 1), (dict(offset=1), 1), (dict(a=NAN), 1), (dict(pages=-1), 1), (dict(block=0), 1), (dict(HKV=0), 1),
     (dict(DV=0), 1), (dict(H=-1), 1), (dict(T=-1), 1), (dict(dt=7), 2), (dict(D=2000), 2), (dict(DV=1025), 2),
-    (dict(HKV=1 << 25), 2),
+    (dict(HKV=1 << 25), 2), (dict(ks=st(256, 64, 0)), 1), (dict(vs=st(0, 64, 32)), 1),  # slots in one place
 ])
 def test_append_rejects(so, kw, status):
     a = dict(q=None, k=A, v=A, st=st(*[0, 64, 32] * 3), pos=A, f=A, R=32, offset=0, a=1.0, B=1, T=4, H=2, HKV=2, D=32,
