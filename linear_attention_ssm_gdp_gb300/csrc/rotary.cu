@@ -14,10 +14,10 @@
 // Bound by HBM: every element is read and written once. A warp takes a token (or a share of its heads, where
 // tokens are few): its lanes form the token's cosines and sines in shared memory, and each keeps those of one
 // place in the head, eight pairs of two 16-byte vectors or one vector of neighbours, in registers for all the
-// heads that it then walks, four heads' loads in flight. Elements whose sizes, strides or addresses are not
-// whole 16-byte vectors go one pair at a time in the same walk. (With a CTA for a few tokens and the cosines
-// read from shared memory for every head: 35 us for 8192 tokens of 32 heads
-// of 128 in bf16, in place of 24, 84 % of the copy rate.)
+// heads that it then walks, two heads' loads in flight. Where sizes, strides or addresses are not whole
+// 16-byte vectors, smaller ones or single elements go in the same walk, more heads at a time. 8192 tokens of 32
+// heads of 128 in bf16: 24 us, 84 % of the copy rate (35 with a CTA for a few tokens and the cosines read from
+// shared memory for every head).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __gri
   using V = Vec<T, VN>;
   constexpr bool kPairs = !(INTER && VN > 1);    // a rotated place is two vectors
   constexpr int kTurns = kPairs ? VN : VN / 2;   // pairs of a place
-  constexpr int kBatch = 2;                      // heads whose loads are in flight
+  constexpr int kBatch = sizeof(V) >= 16 ? 2 : sizeof(V) >= 8 ? 4 : 8;  // heads whose loads are in flight
   extern __shared__ unsigned long long sm[];
   unsigned long long* turns = sm;                // [half]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -252,11 +252,19 @@ cudaError_t go(const RotaryArgs& a, bool inter, cudaStream_t stream) {
                : launch_pdl(rotary_kernel<T, VN, false>, dim3(grid), dim3(kThreads), smem, stream, a);
 }
 
+template <typename T>
+cudaError_t go16(const RotaryArgs& a, int vn, bool inter, cudaStream_t stream) {
+  return vn == 8   ? go<T, 8>(a, inter, stream)
+         : vn == 4 ? go<T, 4>(a, inter, stream)
+         : vn == 2 ? go<T, 2>(a, inter, stream)
+                   : go<T, 1>(a, inter, stream);
+}
+
 bool dtype_ok(gdp_dtype dt) { return dt == GDP_BF16 || dt == GDP_F16 || dt == GDP_F32; }
 
-// Whether a tensor's rows are whole 16-byte vectors.
-bool whole(const void* p, const int64_t* s, const int* n, int D, int vn) {
-  if (reinterpret_cast<uintptr_t>(p) % 16 || D % vn) return false;
+// Whether a tensor's rows are whole vectors of vn elements on their grid.
+bool whole(const void* p, const int64_t* s, const int* n, int D, int vn, int esz) {
+  if (reinterpret_cast<uintptr_t>(p) % (vn * esz) || D % vn) return false;
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && s[i] % vn) return false;
   return true;
@@ -274,17 +282,21 @@ struct Side {
 
 cudaError_t launch(RotaryArgs& a, const Side* sides, int n, int B, int T, int R, bool inter, gdp_dtype dt,
                    cudaStream_t stream) {
-  const int esz = dt == GDP_F32 ? 4 : 2, vn = 16 / esz;
-  bool vec = true;
-  for (int i = 0; i < n; ++i) {
-    const Side& s = sides[i];
-    if (s.H == 0) continue;
-    const int xn[3] = {B, T, s.H}, yn[3] = {s.dst[0], s.dst[1], s.H};
-    vec = vec && whole(s.x, s.xs, xn, s.D, vn) && whole(s.y, s.ys, yn, s.D, vn);
-    if (s.rotated && R > 0)
-      vec = vec && (inter ? a.offset % 2 == 0 : a.offset % vn == 0 && (R / 2) % vn == 0);
-  }
-  const int w = vec ? vn : 1;
+  // vectors of up to 16 bytes, as sizes, strides and addresses allow (72 elements with a rotated half of 18 in bf16:
+  // vectors of 2)
+  const int esz = dt == GDP_F32 ? 4 : 2;
+  int w = 16 / esz;
+  const auto fits = [&](int vn) {
+    for (int i = 0; i < n; ++i) {
+      const Side& s = sides[i];
+      if (s.H == 0) continue;
+      const int xn[3] = {B, T, s.H}, yn[3] = {s.dst[0], s.dst[1], s.H};
+      if (!whole(s.x, s.xs, xn, s.D, vn, esz) || !whole(s.y, s.ys, yn, s.D, vn, esz)) return false;
+      if (s.rotated && R > 0 && (inter ? a.offset % 2 != 0 : a.offset % vn != 0 || (R / 2) % vn != 0)) return false;
+    }
+    return true;
+  };
+  while (w > 1 && !fits(w)) w /= 2;
   a.half = R / 2;
   int walks = 1;  // batches of heads that a token's longest walk takes
   for (int i = 0; i < 3; ++i) {
@@ -300,7 +312,7 @@ cudaError_t launch(RotaryArgs& a, const Side* sides, int n, int B, int T, int R,
     const int rot = s.rotated ? R : 0;
     r.pairs = rot / 2 / w;
     r.places = r.pairs + (s.D - rot) / w;
-    if (inter && vec) {
+    if (inter && w > 1) {
       r.pairs = rot > 0;  // (only whether any pair of the head turns)
       r.places = s.D / w;
     }
@@ -314,9 +326,9 @@ cudaError_t launch(RotaryArgs& a, const Side* sides, int n, int B, int T, int R,
   a.log_parts = 0;
   while ((a.tokens << a.log_parts) < 4ll * sm_count() && (1 << a.log_parts) < walks) ++a.log_parts;
   switch (dt) {
-    case GDP_BF16: return vec ? go<__nv_bfloat16, 8>(a, inter, stream) : go<__nv_bfloat16, 1>(a, inter, stream);
-    case GDP_F16: return vec ? go<__half, 8>(a, inter, stream) : go<__half, 1>(a, inter, stream);
-    default: return vec ? go<float, 4>(a, inter, stream) : go<float, 1>(a, inter, stream);
+    case GDP_BF16: return go16<__nv_bfloat16>(a, w, inter, stream);
+    case GDP_F16: return go16<__half>(a, w, inter, stream);
+    default: return w == 4 ? go<float, 4>(a, inter, stream) : w == 2 ? go<float, 2>(a, inter, stream) : go<float, 1>(a, inter, stream);
   }
 }
 
