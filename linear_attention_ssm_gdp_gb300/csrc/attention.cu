@@ -485,7 +485,7 @@ bool sizes_built(int B, int T, int H, int HKV, int D, int DV, gdp_dtype dt) {
 size_t workspace_of(int T, int H, int HKV, int D, int DV, gdp_dtype dt) {
   const int64_t rows = (int64_t)T * (H / HKV);
   const size_t s = attn::simple_workspace(rows, DV);
-  return attn::tc_shape(D, DV, dt) ? std::max(s, attn::tc_workspace(rows, DV)) : s;
+  return attn::tc_shape(D, DV, dt) ? std::max(s, attn::tc_workspace(rows, D, DV)) : s;
 }
 
 }  // namespace

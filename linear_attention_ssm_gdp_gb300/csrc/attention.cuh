@@ -324,7 +324,7 @@ cudaError_t launch_simple(const Problem& p, uint8_t* ws);
 size_t simple_workspace(int64_t rows, int DV);
 bool tc_shape(int D, int DV, gdp_dtype dt);
 bool tc_ok(const Problem& p);
-size_t tc_workspace(int64_t rows, int DV);
+size_t tc_workspace(int64_t rows, int D, int DV);
 cudaError_t launch_tc(const Problem& p, uint8_t* ws);
 // Test hook (gdp_debug_wait_fault): a wait of its next launch runs out (arm), limit of its waits.
 void wait_fault(int arm, unsigned long long budget_ns);

@@ -1,4 +1,4 @@
-// Attention of new tokens over a paged cache on the tensor cores: bf16 and fp16, heads of up to 128
+// Attention of new tokens over a paged cache on the tensor cores: bf16 and fp16, heads of up to 256
 // elements in steps of 8.
 //
 // A CTA walks the pieces of its share (attention.cuh) with two slots, each with four warps of its own,
@@ -6,6 +6,7 @@
 //   more than 128 rows: the slots are two tiles of 128 rows that read the same keys;
 //   fewer: both slots have the same rows and take the tiles of 64 keys in turn, and their two maxima, sums
 //   and outputs are joined at the piece's end (they lie in the same lanes of tensor memory).
+// Heads above 128 have one slot, whose outputs take the second one's columns.
 // So one slot's softmax runs beside the other's products either way, and a decode step's few rows cost
 // what streaming their keys costs: the products of a padded tile of 128 rows keep the tensor pipe busy a
 // third of the time that HBM needs for its keys.
@@ -41,24 +42,25 @@ namespace attn {
 namespace {
 using namespace ptx;
 
-constexpr int kRows = 256, kKeys = 64;
+constexpr int kKeys = 64;
 constexpr int kLoad = 8, kScores = 10, kOutputs = 11;  // warps; 0 to 3 and 4 to 7 are the slots', 8 and 9 load K and V
 constexpr int kThreads = 384;
 // Shares are of equal cost, in units of about 0.3 us as measured: up to 128 rows 3 us to begin and end an item and
 // 0.6 a tile, more rows 6.5 and 0.95. (With tiles alone the slowest CTA of a decode batch took 870 us, the median
 // 566, and 216 and 130 of pieces of prompts; now 610 and 588, 132 and 122.)
-constexpr Cost kCost = {10, 2, 22, 3};
+constexpr Cost kCost = {10, 2, 22, 3}, kCostWide = {10, 5, 10, 5};
 constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
 
 template <int KD>
 struct Lay {
   // Buffers of K and of V. A tile of K is free when its scores are formed, one of V two thousand cycles later:
   // with as many of V as of K in common stages a decode step had too few loads in flight.
-  static constexpr int NK = KD == 128 ? 4 : 8, NV = KD == 128 ? 6 : 12;
+  static constexpr int NK = KD == 256 ? 2 : KD == 128 ? 4 : 8, NV = KD == 256 ? 3 : KD == 128 ? 6 : 12;
+  static constexpr int SLOTS = KD == 256 ? 1 : 2, ROWS = 128 * SLOTS;
   static constexpr int HALF = kKeys * 128;       // 64 columns of a tile: 64 rows of 128 bytes
   static constexpr int TILE = KD / 64 * HALF;
   static constexpr int QT = KD / 64 * 16384;     // 128 rows of queries
-  static constexpr int Q = 0, K = 2 * QT, V = K + NK * TILE;
+  static constexpr int Q = 0, K = SLOTS * QT, V = K + NK * TILE;
   static constexpr int BAR = V + NV * TILE;
   static constexpr int ML = BAR + 704;           // maxima and sums [2][128]
   static constexpr int START = ML + 2048;        // the share, and the sums that lead to it
@@ -72,7 +74,7 @@ enum {
   B_KFULL = 0, B_KEMPTY = 8, B_VFULL = 16, B_VEMPTY = 28, B_META = 40, B_S = 52, B_P = 56, B_O = 60, B_Q = 64,
   B_JOIN = 66, B_DONE, B_END, B_N = B_END + 2
 };
-constexpr uint32_t T_S = 0, T_O = 256;  // columns: scores [2][2][64], weights over them; outputs [2][128]
+constexpr uint32_t T_S = 0, T_O = 256;  // columns: scores [2][2][64], weights over them; outputs [2][128] or [256]
 
 struct TcArgs : Args {
   int g;          // keys of a box
@@ -128,12 +130,13 @@ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
 // How a piece's tiles are spread over the slots.
+template <int SLOTS>
 struct Spread {
   bool two;       // tiles of rows of their own, the same keys
   int n, rows, row0;
   __device__ __forceinline__ Spread(const Piece& x, int slot) {
-    two = x.rows > 128;
-    n = two ? x.j1 - x.j0 : (x.j1 - x.j0 + 1 - slot) / 2;
+    two = SLOTS == 2 && x.rows > 128;
+    n = two ? x.j1 - x.j0 : SLOTS == 2 ? (x.j1 - x.j0 + 1 - slot) / 2 : slot ? 0 : x.j1 - x.j0;
     rows = two ? (slot ? x.rows - 128 : 128) : x.rows;
     row0 = x.row0 + (two ? 128 * slot : 0);
   }
@@ -175,13 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  find_start<kRows, kKeys, kThreads>(a, &s_start, s_scan);
+  find_start<L::ROWS, kKeys, kThreads>(a, &s_start, s_scan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const Sync sy{s_dead, a.budget, p.status};
-  Walk<kRows, kKeys> walk(s_start, a.cost);
+  Walk<L::ROWS, kKeys> walk(s_start, a.cost);
   Piece x;
   bool ok = true;
 
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool rec = false, owe = false;
 #pragma unroll 1
     while (ok && walk.next(p, x)) {
-      const Spread d(x, slot);
+      const Spread<L::SLOTS> d(x, slot);
       if (d.n > 0) {  // Q: 16-byte chunks of the rows, zero behind the head's end
         const int ch = tid % (KD / 8);
         const T* q0 = static_cast<const T*>(p.q) + (p.cu ? x.first * p.qs[1] : x.r * p.qs[0]) + x.head * p.G * p.qs[2] +
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int k = 0; ok && k < d.n; ++k, ++n) {
-        const int j = d.two ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
+        const int j = d.two || L::SLOTS == 1 ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
         const uint32_t stage = (tile0 + j) % L::NV, turn = (tile0 + j) / L::NV;
         const uint32_t buf = n & 1, tb = ts + 64 * buf;
         ok = sy.wait(&bars[B_S + 2 * slot + buf], n >> 1 & 1) && (!live || sy.wait(&bars[B_META + stage], turn & 1));
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // Two slots on the same rows: each leaves its maxima and sums, then joins half of the columns. (Both
       // slots' outputs lie in the same lanes of tensor memory.)
-      const bool join = !d.two && nt > 1;
+      const bool join = L::SLOTS == 2 && !d.two && nt > 1;
       float f0 = 1.f, f1 = 0.f;  // of this slot's and of the other's outputs
       if (d.n > 0) ok = sy.wait(&bars[B_O + 2 * slot + ((n - 1) & 1)], (n - 1) >> 1 & 1);
       if (join) {
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // Pages whose size is not a multiple of 8: 16-byte copies, a row to KD / 8 lanes, three tiles in flight; a
       // tile is told full once its copies are done and visible to the tensor cores.
-      constexpr int kLag = 3, kRow = KD / 8, kBeside = 32 / kRow;  // tiles; lanes of a row, rows beside each other
+      constexpr int kLag = L::NK > 3 ? 3 : L::NK - 1, kRow = KD / 8, kBeside = 32 / kRow;  // tiles; lanes of a row, rows beside each other
       static_assert(kLag < L::NK, "a tile is told full before the wait for its buffer's next use");
       const T* base = static_cast<const T*>(v ? p.v : p.k);
       const int64_t s0 = v ? p.vs[0] : p.ks[0], s1 = v ? p.vs[1] : p.ks[1], s2 = v ? p.vs[2] : p.ks[2];
@@ -530,18 +533,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (ok && walk.next(p, x)) {
           const int nt = x.j1 - x.j0;
-          const bool two = x.rows > 128;
+          const bool two = L::SLOTS == 2 && x.rows > 128;
           const int steps = two ? 2 * nt : nt;
 #pragma unroll 1
           for (int i = 0; i < steps; ++i) {
-            const int s = i & 1;
+            const int s = L::SLOTS == 2 ? i & 1 : 0;
             const uint32_t n = s ? n1 : n0, buf = n & 1;
             // Scores go over the weights of two tiles before, once those have been multiplied; in a piece's first
             // two tiles they have been, and its queries are there.
-            if (i < 2) {
+            if (i < L::SLOTS) {
               ok = sy.wait1(&bars[B_Q + s], (s ? nq1 : nq0) & 1);
               if (s) ++nq1; else ++nq0;
-            } else if (i >= 4) {
+            } else if (i >= 2 * L::SLOTS) {
               ok = sy.wait1(&bars[B_O + 2 * s + buf], (n >> 1) - 1 & 1);
             }
             ok = ok && ((two && s) || sy.wait1(&bars[B_KFULL + stage], turn));
@@ -562,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (ok && walk.next(p, x)) {
           const int nt = x.j1 - x.j0;
-          const bool two = x.rows > 128;
+          const bool two = L::SLOTS == 2 && x.rows > 128;
           const int steps = two ? 2 * nt : nt;
 #pragma unroll 1
           for (int i = 0; i < steps; ++i) {
-            const int s = i & 1;
+            const int s = L::SLOTS == 2 ? i & 1 : 0;
             const uint32_t n = s ? n1 : n0;
             ok = sy.wait1(&bars[B_P + 2 * s + (n & 1)], n >> 1 & 1) &&
                  ((two && s) || sy.wait1(&bars[B_VFULL + stage], turn));
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < kKeys / 16; ++e)
               mma_bf16_ts(tmem + T_O + 128 * s, tmem + T_S + 128 * s + 64 * (n & 1) + 8 * e, v + e * (2048 >> 4),
-                          id_o, i > 1 || e > 0);
+                          id_o, i >= L::SLOTS || e > 0);
             mma_commit(&bars[B_O + 2 * s + (n & 1)]);
             if (s) ++n1; else ++n0;
             if (!two || s) {
@@ -646,6 +649,7 @@ cudaError_t go(const TcArgs& a, const CUtensorMap* m) {
 }
 template <typename T>
 cudaError_t go(const TcArgs& a, const CUtensorMap* m, bool tma) {
+  if (a.p.D > 128 || a.p.DV > 128) return tma ? go<T, 256, true>(a, m) : go<T, 256, false>(a, m);
   if (a.p.D > 64 || a.p.DV > 64) return tma ? go<T, 128, true>(a, m) : go<T, 128, false>(a, m);
   return tma ? go<T, 64, true>(a, m) : go<T, 64, false>(a, m);
 }
@@ -653,7 +657,7 @@ cudaError_t go(const TcArgs& a, const CUtensorMap* m, bool tma) {
 }  // namespace
 
 bool tc_shape(int D, int DV, gdp_dtype dt) {
-  return (dt == GDP_BF16 || dt == GDP_F16) && D <= 128 && DV <= 128 && D % 8 == 0 && DV % 8 == 0;
+  return (dt == GDP_BF16 || dt == GDP_F16) && D <= 256 && DV <= 256 && D % 8 == 0 && DV % 8 == 0;
 }
 
 bool tc_ok(const Problem& p) {
@@ -667,7 +671,10 @@ bool tc_ok(const Problem& p) {
   return true;
 }
 
-size_t tc_workspace(int64_t rows, int DV) { return layout(sm_count(), rows, kRows, DV).total; }
+static Layout tc_layout(int64_t rows, int D, int DV) {
+  return layout(sm_count(), rows, D > 128 || DV > 128 ? Lay<256>::ROWS : Lay<128>::ROWS, DV);
+}
+size_t tc_workspace(int64_t rows, int D, int DV) { return tc_layout(rows, D, DV).total; }
 
 void wait_fault(int arm, unsigned long long budget_ns) {
   g_fault.store(arm);
@@ -677,8 +684,8 @@ void wait_fault(int arm, unsigned long long budget_ns) {
 cudaError_t launch_tc(const Problem& p, uint8_t* ws) {
   TcArgs a{};
   a.p = p;
-  set_layout(a, layout(sm_count(), (int64_t)p.T * p.G, kRows, p.DV), ws, sm_count());
-  a.cost = kCost;
+  set_layout(a, tc_layout((int64_t)p.T * p.G, p.D, p.DV), ws, sm_count());
+  a.cost = p.D > 128 || p.DV > 128 ? kCostWide : kCost;
   a.budget = (int)(g_budget_ns.load() >> 10);
   a.fault = g_fault.exchange(0);
   CUtensorMap m[2] = {};

@@ -413,3 +413,30 @@ def test_block_sizes(gdp, block, dtype, D, DV):
     for c in (dead["k_cache"], dead["v_cache"]):
         c[last, 502 % block + 1:] = torch.nan
     assert torch.equal(gdp.gdp_attention_paged(**dead), gdp.gdp_attention_paged(**d))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,DV", [(256, 256), (136, 64), (64, 192), (192, 128)])
+@pytest.mark.parametrize("block,tree", [(64, False), (8, True), (5, True)])
+def test_heads_above_128(gdp, dtype, D, DV, block, tree):
+    """One slot of 128 rows: more rows than that, one token, holes, rows behind the last token."""
+    d = problem([50, 1, 3, 64], [900, 2000, 31, 0], 8, 2, D, DV, block, dtype, tree=tree, holes=[(0, 1), (1, 3)])
+    check(gdp, d)
+    for c in (d["k_cache"], d["v_cache"]):
+        c[int(d["block_tables"][1, 2000 // block]), 2000 % block + 1:] = torch.nan
+    check(gdp, d)
+
+
+def test_heads_above_128_many_times(gdp):
+    d = problem([40, 1, 64, 7] * 8, [2000, 900, 64, 3000] * 8, 8, 2, 256, 256, 64, BF)
+    want = gdp.gdp_attention_paged(**d)
+    flush = torch.empty(400 << 20, dtype=torch.uint8, device=DEV)
+    got = []
+    for i in range(30):
+        if i % 3 == 1:
+            flush.zero_()
+        if i % 5 == 1:
+            torch.cuda.synchronize()
+        got.append(gdp.gdp_attention_paged(**d))
+    assert all(torch.equal(x, want) for x in got)
+    check(gdp, d)
