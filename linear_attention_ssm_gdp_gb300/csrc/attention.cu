@@ -46,14 +46,18 @@ template <typename T> struct alignas(4 * sizeof(T)) Quad { T e[4]; };
 
 struct SimpleArgs : Args {
   SimpleSmem L;
-  int k_chunks, v_chunks;     // of a row, where rows are whole chunks on the 16-byte grid; else 0
-  Div by_k, by_v;
+  int k_wide, v_wide;         // bytes of a copy: 16, 8 or 4, as the rows and their grid allow; 0: by elements
+  Div by_k, by_v;             // copies of a row (rounded up to 16 bytes)
 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
+// N bytes; of what is not there, zeros.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? N : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(there ? N : 0)
+                 : "memory");
 }
 
 // The tiles [j0, j1) of one piece for R rows (x.rows of them in use), outputs of NQ quads a thread.
@@ -95,29 +99,30 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
     if (j < x.j1) {
       uint8_t* st = sm + (j % NST) * L.stage;
       const longlong2* off = s_off + (j & 1) * kKeys;
-      if (a.k_chunks) {
-        for (int i = tid; i < kKeys * a.k_chunks; i += kThreads) {
-          const int key = (int)quot(i, a.by_k), c = i - key * a.k_chunks;
-          const int64_t o = off[key].x;
-          cp_async16(st + key * L.ks + 16 * c, k0 + (o < 0 ? 0 : o + c * VN), o >= 0);
-        }
-      } else {
-        for (int key = warp; key < kKeys; key += kWarps)
-          for (int d = lane; d < qs; d += 32)
-            reinterpret_cast<T*>(st + key * L.ks)[d] = off[key].x >= 0 && d < p.D ? k0[off[key].x + d] : from_f<T>(0.f);
-      }
-      st += kKeys * L.ks;
-      if (a.v_chunks) {
-        for (int i = tid; i < kKeys * a.v_chunks; i += kThreads) {
-          const int key = (int)quot(i, a.by_v), c = i - key * a.v_chunks;
-          const int64_t o = off[key].y;
-          cp_async16(st + key * L.vs + 16 * c, v0 + (o < 0 ? 0 : o + c * VN), o >= 0);
-        }
-      } else {
-        for (int key = warp; key < kKeys; key += kWarps)
-          for (int d = lane; d < L.vs / (int)sizeof(T); d += 32)
-            reinterpret_cast<T*>(st + key * L.vs)[d] = off[key].y >= 0 && d < p.DV ? v0[off[key].y + d] : from_f<T>(0.f);
-      }
+      auto rows = [&](uint8_t* dst, int stride, const T* src, int D, int wide, const Div& by, bool k) {
+        auto copy = [&](auto n) {
+          constexpr int N = decltype(n)::value, E = N / (int)sizeof(T);
+          const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+          const int count = kKeys * by.d;
+          for (int i = tid; i < count; i += kThreads) {
+            const int key = (int)quot(i, by), c = i - key * by.d;
+            const int64_t o = k ? off[key].x : off[key].y;
+            const bool there = o >= 0 && c * E < D;
+            cp_async<N>(to + key * stride + N * c, src + (there ? o + c * E : 0), there);
+          }
+        };
+        if (wide == 16) copy(std::integral_constant<int, 16>());
+        else if (wide == 8) copy(std::integral_constant<int, 8>());
+        else if (wide == 4) copy(std::integral_constant<int, 4>());
+        else
+          for (int key = warp; key < kKeys; key += kWarps) {
+            const int64_t o = k ? off[key].x : off[key].y;
+            for (int d = lane; d < stride / (int)sizeof(T); d += 32)
+              reinterpret_cast<T*>(dst + key * stride)[d] = o >= 0 && d < D ? src[o + d] : from_f<T>(0.f);
+          }
+      };
+      rows(st, L.ks, k0, p.D, a.k_wide, a.by_k, true);
+      rows(st + kKeys * L.ks, L.vs, v0, p.DV, a.v_wide, a.by_v, false);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");           // (one for each tile, empty ones too)
   };
@@ -413,12 +418,15 @@ cudaError_t go(const SimpleArgs& a) {
 
 constexpr int kResident = 2;  // CTAs of an SM at most
 
-// Whether the rows of a cache are whole 16-byte chunks on their grid.
-bool chunks(const Problem& p, const void* base, const int64_t* s, int D, int esz) {
+// The widest asynchronous copy that the rows of a cache are whole multiples of, on its grid; 0: none.
+int widest(const Problem& p, const void* base, const int64_t* s, int D, int esz) {
   const int n[3] = {p.n_pages, p.block, p.HKV};
-  for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && s[i] * esz % 16) return false;
-  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && D * esz % 16 == 0;
+  for (int w = 16; w >= 4; w /= 2) {
+    bool all = reinterpret_cast<uintptr_t>(base) % w == 0 && D * esz % w == 0;
+    for (int i = 0; i < 3; ++i) all = all && (n[i] <= 1 || s[i] * esz % w == 0);
+    if (all) return w;
+  }
+  return 0;
 }
 
 }  // namespace
@@ -451,10 +459,10 @@ cudaError_t launch_simple(const Problem& p, uint8_t* ws) {
   const int ctas = sm_count() * std::max(1, std::min(kResident, (228 * 1024) / (a.L.bytes + 1280)));
   set_layout(a, layout(ctas, (int64_t)p.T * p.G, kRows, p.DV), ws, ctas);
   a.cost = kCost;
-  a.k_chunks = chunks(p, p.k, p.ks, p.D, esz) ? p.D * esz / 16 : 0;
-  a.v_chunks = chunks(p, p.v, p.vs, p.DV, esz) ? p.DV * esz / 16 : 0;
-  a.by_k = div_by(std::max(1, a.k_chunks));
-  a.by_v = div_by(std::max(1, a.v_chunks));
+  a.k_wide = widest(p, p.k, p.ks, p.D, esz);
+  a.v_wide = widest(p, p.v, p.vs, p.DV, esz);
+  a.by_k = div_by(a.L.ks / std::max(4, a.k_wide));
+  a.by_v = div_by(a.L.vs / std::max(4, a.v_wide));
   cudaError_t e;
   switch (p.dt) {
     case GDP_BF16: e = go<__nv_bfloat16>(a); break;
