@@ -47,7 +47,7 @@ template <typename T> struct alignas(4 * sizeof(T)) Quad { T e[4]; };
 struct SimpleArgs : Args {
   SimpleSmem L;
   int k_wide, v_wide;         // bytes of a copy: 16, 8 or 4, as the rows and their grid allow; 0: by elements
-  Div by_k, by_v;             // copies of a row (rounded up to 16 bytes)
+  int by_k, by_v;             // logarithm of the threads of a row
 };
 
 // N bytes; of what is not there, zeros.
@@ -99,16 +99,18 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
     if (j < x.j1) {
       uint8_t* st = sm + (j % NST) * L.stage;
       const longlong2* off = s_off + (j & 1) * kKeys;
-      auto rows = [&](uint8_t* dst, int stride, const T* src, int D, int wide, const Div& by, bool k) {
+      auto rows = [&](uint8_t* dst, int stride, const T* src, int D, int wide, int by, bool k) {
         auto copy = [&](auto n) {
           constexpr int N = decltype(n)::value, E = N / (int)sizeof(T);
           const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-          const int count = kKeys * by.d;
-          for (int i = tid; i < count; i += kThreads) {
-            const int key = (int)quot(i, by), c = i - key * by.d;
+          const int c0 = tid & ((1 << by) - 1);
+#pragma unroll 4
+          for (int key = tid >> by; key < kKeys; key += kThreads >> by) {
             const int64_t o = k ? off[key].x : off[key].y;
-            const bool there = o >= 0 && c * E < D;
-            cp_async<N>(to + key * stride + N * c, src + (there ? o + c * E : 0), there);
+            for (int c = c0; c < stride / N; c += 1 << by) {
+              const bool there = o >= 0 && c * E < D;
+              cp_async<N>(to + key * stride + N * c, src + (there ? o + c * E : 0), there);
+            }
           }
         };
         if (wide == 16) copy(std::integral_constant<int, 16>());
@@ -177,23 +179,25 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
           }
         }
       }
+      // the eight parts' sums: each exchange halves the rows that a lane goes on with, to row part % R
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
-        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
-        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 4);
-      }
-      const int back = j * kKeys + key - x.x.ctx;
-      const bool there = s_ok[j % NST] >> key & 1;
+      for (int h = R / 2; h > 0; h >>= 1)
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (i != part) continue;
-        bool sees = there && i < x.rows;
+        for (int i = 0; i < h; ++i) {
+          const bool up = part & h;
+          const float give = up ? s[i] : s[i + h], keep = up ? s[i + h] : s[i];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+        }
+#pragma unroll
+      for (int h = R; h < 8; h <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], h);
+      if (part < R) {
+        const int back = j * kKeys + key - x.x.ctx;
+        bool sees = (s_ok[j % NST] >> key & 1) && part < x.rows;
         if (sees && back >= 0) {
-          const int t = (int)quot(x.row0 + i, p.by_G);
+          const int t = (int)quot(x.row0 + part, p.by_G);
           sees = p.tree ? (p.tree[x.first + t] >> back) & 1 : back <= t;
         }
-        ss[i * kKeys + key] = sees ? s[i] * p.c : -INFINITY;
+        ss[part * kKeys + key] = sees ? s[0] * p.c : -INFINITY;
       }
     }
     __syncthreads();
@@ -461,8 +465,13 @@ cudaError_t launch_simple(const Problem& p, uint8_t* ws) {
   a.cost = kCost;
   a.k_wide = widest(p, p.k, p.ks, p.D, esz);
   a.v_wide = widest(p, p.v, p.vs, p.DV, esz);
-  a.by_k = div_by(a.L.ks / std::max(4, a.k_wide));
-  a.by_v = div_by(a.L.vs / std::max(4, a.v_wide));
+  auto threads_of = [](int copies) {
+    int l = 0;
+    while (l < 5 && 1 << l < copies) ++l;
+    return l;
+  };
+  a.by_k = threads_of(a.L.ks / std::max(4, a.k_wide));
+  a.by_v = threads_of(a.L.vs / std::max(4, a.v_wide));
   cudaError_t e;
   switch (p.dt) {
     case GDP_BF16: e = go<__nv_bfloat16>(a); break;
