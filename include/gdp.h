@@ -345,7 +345,7 @@ gdp_status gdp_chunk_fwd_noalloc(const void* q, const void* k, const void* v, co
  *            tensor-core kernel (bf16, K <= 128) waits in the first CTA of its
  *            first launch for one commit more than are made; likewise one-shot. arm = 3:
  *            the same in every CTA of the next gdp_attention_paged on the tensor cores
- *            (16-bit types, D and DV <= 128).
+ *            (16-bit types, D and DV <= 256).
  *            arm = 0: disarm.
  *   budget_seconds: new wait budget (0 < budget <= 10), or <= 0 for the
  *            default 2 s. The budget applies to every later launch until

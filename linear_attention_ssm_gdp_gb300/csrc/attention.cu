@@ -13,12 +13,16 @@ namespace attn {
 namespace {
 
 // ------------------------------------------------------------------ any type and size
-// A CTA of eight warps takes up to 8 rows of an item against tiles of 32 keys, which arrive in their own type by
-// cp.async, up to three tiles ahead (rows that are not whole 16-byte chunks are copied by elements). Products are
-// fp32 multiply-adds: for the scores a thread has a key and every eighth chunk of the head, for the outputs four
-// columns (eight above 128) and every eighth key, whose sums meet at the item's end. Bound by issue slots (half
-// used) and three barriers a tile: 64 requests of up to 4000 keys, 16 heads over 4, 128 columns, fp32: 137 us,
-// where HBM needs 65; 16 requests of 9000 keys, 256 columns, bf16: 240 us, HBM 50.
+// fp32, and 16-bit heads that are not steps of 8 or not on a grid of 16 bytes. A CTA of eight warps takes up to 8 rows
+// of an item against tiles of 32 keys, which arrive in their own type by cp.async of the widest size that the rows
+// allow (16, 8 or 4 bytes; odd 16-bit rows by elements), up to three tiles ahead. Products are fp32 multiply-adds: for
+// the scores a thread has a key and every eighth chunk of the head, for the outputs four columns (eight above 128) and
+// every eighth key, whose sums meet at the item's end. Bound by the latency of its steps between three barriers a tile
+// (half of the issue slots used): 64 requests of up to 4000 keys, 16 heads over 4, 128 columns, fp32: 129 us, where HBM
+// needs 65; 32 drafted tokens on up to 4000 keys, 8 requests, 64 columns: 327 us; 16 requests of up to 9000 keys, 100
+// columns, bf16, 8 bytes a copy: 120 us, HBM 20 (by elements 738). Not kept: keys and maxima of its own for each warp
+// with no barrier in a tile (185 us: its sums of a score over lanes and its rescaling are every warp's), three CTAs of
+// 80 registers an SM (123 us, but the small calls 22 for 20 and trees 334), loops unrolled further (129).
 constexpr int kRows = 8, kKeys = 32, kThreads = 256, kWarps = kThreads / 32;
 constexpr Cost kCost = {8, 3, 8, 3};
 
