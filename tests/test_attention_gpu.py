@@ -6,7 +6,6 @@ Tolerances, per element of o, with A = sum p |v| / sum p and n the keys of the l
   a score's error e changes its weight by a factor 1 + e, top and bottom: 2 max_j e_j A, with
     e_j = (D + 4) 2^-24 scale sum_d |q_d k_jd| (a sum of D products in any order, each addition
     rounded or, on the tensor cores, cut off at 2^-23 once per 16 products, and the scale's product)
-  fp32 operands enter products in two parts of 11 bits: 2^-21 more of sum |q k| and of A
   2^x by the hardware               2^-22 each, top and bottom: 2^-20 A with the factors of joins
   sums of n weights                 (80 + n / 16) 2^-23 A
 """
@@ -101,10 +100,9 @@ def reference(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, tree_
             p = torch.softmax(x, -1).nan_to_num(0.0)
             size = abs(scale) * (q[a:b, h].double().abs() @ k.abs().T).masked_fill(~sees, 0.0).amax(-1, keepdim=True)
             A = p @ v.abs()
-            parts = 2.0 ** -21 if dt == FP else 0.0
-            e = ((D + 4) * 2.0 ** -24 + parts) * size
+            e = (D + 4) * 2.0 ** -24 * size
             o[a:b, h] = p @ v
-            tol[a:b, h] = u * o[a:b, h].abs() + A * ((u if dt != FP else parts) + 2 * e + 2.0 ** -20
+            tol[a:b, h] = u * o[a:b, h].abs() + A * ((u if dt != FP else 0.0) + 2 * e + 2.0 ** -20
                                                      + (80 + at.numel() / 16) * 2.0 ** -23)
     return o, tol
 
@@ -142,6 +140,20 @@ SIZES = [
 @pytest.mark.parametrize("tree", [False, True])
 def test_attention(gdp, lens, ctx, H, HKV, D, DV, block, layout, dtype, tree):
     check(gdp, problem(lens, ctx, H, HKV, D, DV, block, dtype, layout, tree))
+
+
+@pytest.mark.parametrize("D,DV", [(100, 36), (50, 250), (33, 64), (64, 33), (4, 2), (1, 1), (255, 256)])
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("layout", ["plain", "pair", "odd"])
+def test_rows_of_any_width(gdp, D, DV, dtype, layout):
+    """Rows that are whole copies of 16, 8 or 4 bytes, or none, on grids of as many; NaN in the slots not in use."""
+    d = problem([1, 6, 2], [130, 31, 0], 6, 2, D, DV, 12, dtype, layout, tree=True)
+    used = d["block_tables"][d["block_tables"] >= 0].long()
+    for name in ("k_cache", "v_cache"):
+        free = torch.ones(d[name].shape[0], dtype=torch.bool, device=DEV)
+        free[used] = False
+        d[name][free] = float("nan")
+    check(gdp, d)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
