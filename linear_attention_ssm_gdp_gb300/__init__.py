@@ -170,6 +170,14 @@ def _status_ok(t):
         raise ValueError("status must be an int32 device tensor")
 
 
+def _one_device(*ts):
+    """The kernels run on the current device, and read every tensor there."""
+    current = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != current:
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
 def gdp_version() -> int:
     return int(load().gdp_version())
 
@@ -861,7 +869,8 @@ def gdp_rotary(x, positions, frequencies, offset: int = 0, interleaved: bool = F
     positions [T] or [B, T] int32, frequencies [R / 2] fp64 (gdp_rotary_frequencies). Pair i
     of the elements [offset, offset + R), (i, i + R / 2) or neighbours (2 i, 2 i + 1) where
     ``interleaved``, turns by position * frequency; ``backward`` turns back (the gradient's
-    pass, or undoing). ``out``: contiguous, or x itself. Returns y in x's dtype."""
+    pass, or undoing). ``out``: contiguous, or x itself. All on the current device. Returns y
+    in x's dtype."""
     if x.dtype not in _DTYPE or frequencies is None:
         raise ValueError("x must be bf16, fp16 or fp32, with frequencies")
     shape, B, T, H, D, xs = _heads("x", x, x.dtype)
@@ -870,6 +879,7 @@ def gdp_rotary(x, positions, frequencies, offset: int = 0, interleaved: bool = F
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out is not x:
         _out_ok(out, shape, x.dtype)
+    _one_device(x, positions, frequencies, out)
     ys = xs if out is x else (T * H * D, H * D, D)
     st = load().gdp_rotary(x.data_ptr(), _pack3(*xs), pos, freq, R, offset, interleaved, amplitude,
                            backward, B, T, H, D, _DTYPE[x.dtype], out.data_ptr(), _pack3(*ys),
@@ -904,7 +914,8 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
     block_size, HKV, DV] with any strides of the first three dimensions, slot_map [T] int64
     and positions [T] int32 as gdp_block_plan gives them (-1: not kept). ``status`` (optional
     int32 device tensor) is set to 1 by a slot outside the cache, which is not kept either.
-    Slots must differ. Returns the rotated q (None without one)."""
+    Slots must differ; all tensors are on the current device. Returns the rotated q (None
+    without one)."""
     dt = k.dtype
     if dt not in _DTYPE:
         raise ValueError("k, v and q must be bf16, fp16 or fp32")
@@ -930,6 +941,9 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
             _out_ok(q_out, qshape, dt)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    _one_device(k, v, q, k_cache, v_cache, slot_map, q_out, status)
+    if R:
+        _one_device(positions, frequencies)
     st = load().gdp_cache_append(
         _a(q), k.data_ptr(), v.data_ptr(), _pack_strides(*qs, *ks, *vs), pos, freq, R, offset,
         interleaved, amplitude, B, T, H, HKV, D, DV, _DTYPE[dt], slot_map.data_ptr(),
@@ -960,7 +974,8 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
     token j (at most 64 tokens a request); without it each sees the new ones up to itself.
     ``scale`` defaults to D**-0.5. ``status`` (optional int32 device tensor) is set to 1 by
     bad pages, contexts or offsets and to 2 where a wait on the device ran out; it is not
-    cleared. Returns o [B, T, H, DV] in q's dtype; rows that see nothing are 0."""
+    cleared. All tensors are on the current device. Returns o [B, T, H, DV] in q's dtype;
+    rows that see nothing are 0."""
     dt = q.dtype
     if dt not in _DTYPE or q.dim() != 4:
         raise ValueError("q must be [B, T, H, D] in bf16, fp16 or fp32")
@@ -992,6 +1007,7 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     else:
         _need_cuda(workspace)
+    _one_device(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, tree_mask, out, workspace, status)
     st = load().gdp_attention_paged(
         q.data_ptr(), _pack3(*qs), k_cache.data_ptr(), kst, v_cache.data_ptr(), vst, pages, block,
         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), _a(cu_seqlens), n, _a(tree_mask), B, T, H,

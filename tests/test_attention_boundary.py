@@ -159,3 +159,23 @@ def test_frequencies(lib):
     assert lib.gdp_rotary_frequencies(0, device="cpu")[0].numel() == 0
     # base 1, one pair: no angle formula divides by ln(base) there
     assert lib.gdp_rotary_frequencies(2, 1.0, device="cpu")[0].tolist() == [1.0]
+
+
+class _On:
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+
+@pytest.mark.parametrize("current,devices,ok", [(0, (0, None, 0), True), (1, (1, 1), True), (0, (1, 1), False),
+                                                (0, (0, 1), False), (1, (1, None, 0), False)])
+def test_tensors_elsewhere_are_refused(lib, monkeypatch, current, devices, ok):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    ts = [None if d is None else _On(d) for d in devices]
+    if ok:
+        lib._one_device(*ts)
+    else:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            lib._one_device(*ts)

@@ -452,3 +452,16 @@ def test_heads_above_128_many_times(gdp):
         got.append(gdp.gdp_attention_paged(**d))
     assert all(torch.equal(x, want) for x in got)
     check(gdp, d)
+
+
+def test_another_current_device_is_refused(gdp, monkeypatch):
+    d = problem([2, 3], [40, 7], 4, 2, 64, 64, 16, BF)
+    k, v = d["q"][0, :, :2].contiguous(), d["q"][0, :, 2:4].contiguous()
+    slot = torch.full((5,), -1, dtype=torch.int64, device=DEV)
+    pos = torch.zeros(5, dtype=torch.int32, device=DEV)
+    f = torch.ones(32, dtype=torch.float64, device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: gdp.gdp_attention_paged(**d), lambda: gdp.gdp_rotary(k, pos, f),
+                 lambda: gdp.gdp_cache_append(k, v, d["k_cache"], d["v_cache"], slot)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
