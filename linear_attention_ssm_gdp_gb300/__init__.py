@@ -170,9 +170,12 @@ def _status_ok(t):
         raise ValueError("status must be an int32 device tensor")
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _one_device(*ts):
     """The kernels run on the current device, and read every tensor there."""
-    current = torch.cuda.current_device()
+    current = _current_device()
     for t in ts:
         if t is not None and t.get_device() != current:
             raise ValueError("every tensor must be on the current CUDA device")

@@ -172,7 +172,7 @@ class _On:
 @pytest.mark.parametrize("current,devices,ok", [(0, (0, None, 0), True), (1, (1, 1), True), (0, (1, 1), False),
                                                 (0, (0, 1), False), (1, (1, None, 0), False)])
 def test_tensors_elsewhere_are_refused(lib, monkeypatch, current, devices, ok):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(lib, "_current_device", lambda: current)
     ts = [None if d is None else _On(d) for d in devices]
     if ok:
         lib._one_device(*ts)

@@ -460,7 +460,7 @@ def test_another_current_device_is_refused(gdp, monkeypatch):
     slot = torch.full((5,), -1, dtype=torch.int64, device=DEV)
     pos = torch.zeros(5, dtype=torch.int32, device=DEV)
     f = torch.ones(32, dtype=torch.float64, device=DEV)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(gdp, "_current_device", lambda: 1)
     for call in (lambda: gdp.gdp_attention_paged(**d), lambda: gdp.gdp_rotary(k, pos, f),
                  lambda: gdp.gdp_cache_append(k, v, d["k_cache"], d["v_cache"], slot)):
         with pytest.raises(ValueError, match="current CUDA device"):
