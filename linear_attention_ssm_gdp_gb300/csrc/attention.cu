@@ -16,14 +16,16 @@ namespace {
 // fp32, and 16-bit heads that are not steps of 8 or not on a grid of 16 bytes. A CTA of eight warps takes up to 8 rows
 // of an item against tiles of 32 keys, which arrive in their own type by cp.async of the widest size that the rows
 // allow (16, 8 or 4 bytes; odd 16-bit rows by elements), up to three tiles ahead. Products are fp32 multiply-adds: for
-// the scores a thread has a key and every eighth chunk of the head, for the outputs four columns (eight above 128) and
-// every eighth key, whose sums meet at the item's end. Bound by the latency of its steps between three barriers a tile
-// (half of the issue slots used): 64 requests of up to 4000 keys, 16 heads over 4, 128 columns, fp32: 129 us, where HBM
-// needs 65; 32 drafted tokens on up to 4000 keys, 8 requests, 64 columns: 327 us; 16 requests of up to 9000 keys, 100
-// columns, bf16, 8 bytes a copy: 120 us, HBM 20 (by elements 738). Not kept: keys and maxima of its own for each warp
-// with no barrier in a tile (185 us: its sums of a score over lanes and its rescaling are every warp's), three CTAs of
-// 80 registers an SM (123 us, but the small calls 22 for 20 and trees 334), loops unrolled further (129).
+// the scores a thread has two keys and every 16th chunk of the head (a chunk of Q is read for both), for the outputs
+// four columns (eight above 128) and every eighth key, whose sums meet at the item's end. Bound by the latency of its
+// steps between three barriers a tile (half of the issue slots used): 64 requests of up to 4000 keys, 16 heads over 4,
+// 128 columns, fp32: 122 us, where HBM needs 65; 32 drafted tokens on up to 4000 keys, 8 requests, 64 columns: 314 us;
+// 16 requests of up to 9000 keys, 100 columns, bf16, 8 bytes a copy: 112 us, HBM 20 (by elements 738). Not kept: one
+// key a thread (129 and 327 us), four (126 and 376); keys and maxima of its own for each warp with no barrier in a
+// tile (185 us: its sums of a score over lanes and its rescaling are every warp's); three CTAs of 80 registers an SM
+// (with one key a thread 123 us, but small calls 22 for 20 and trees 334).
 constexpr int kRows = 8, kKeys = 32, kThreads = 256, kWarps = kThreads / 32;
+constexpr int kScores = kKeys + 1;  // stride of a row of scores: eight rows in other banks
 constexpr Cost kCost = {8, 3, 8, 3};
 
 struct SimpleSmem {
@@ -39,7 +41,7 @@ inline SimpleSmem simple_smem(int D, int DV, int esz) {
   x.stages = std::max(2, std::min(4, 105 * 1024 / x.stage));  // (two CTAs an SM)
   x.q = std::max(x.stages * x.stage, kWarps * kRows * 512 * (DV > 128 ? 2 : 1));  // (the warps' outputs meet there)
   x.s = x.q + 4 * kRows * (x.ks / esz);                            // Q, fp32
-  x.p = x.s + 4 * kRows * kKeys;                                   // scores [row][key], weights [key][row]
+  x.p = x.s + 4 * kRows * kScores;                                 // scores [row][key], weights [key][row]
   x.off = x.p + 4 * kRows * kKeys + 4 * kRows * 2;                 // factors and sums of the rows
   x.bytes = x.off + 2 * kKeys * 16 + 16 + 4 * 4;                   // offsets of two tiles' rows; seen keys by stage
   return x;
@@ -72,7 +74,7 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
   const SimpleSmem& L = a.L;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NST = L.stages;
   float* sq = reinterpret_cast<float*>(sm + L.q);
-  float* ss = reinterpret_cast<float*>(sm + L.s);                  // [kRows][kKeys]
+  float* ss = reinterpret_cast<float*>(sm + L.s);                  // [kRows][kScores]
   float* sp = reinterpret_cast<float*>(sm + L.p);                  // [kKeys][kRows]
   float* s_alpha = sp + kRows * kKeys;
   float* s_sum = s_alpha + kRows;
@@ -165,49 +167,53 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
     __syncthreads();                                               // tile j is there, tile j - 1 has been read
     load(j + NST - 1);
     const uint8_t* st = sm + (j % NST) * L.stage;
-    {  // scores: key tid / 8, chunks tid % 8, + 8, ..
-      const int key = tid >> 3, part = tid & 7;
-      float s[R];
+    {  // scores of two keys: chunks part, + 16, ..
+      constexpr int NK = 2, PARTS = 8 * NK;
+      float s[NK * R];                                             // [key][row]
 #pragma unroll
-      for (int i = 0; i < R; ++i) s[i] = 0.f;
-      const Chunk<T>* kp = reinterpret_cast<const Chunk<T>*>(st + key * L.ks);
-      for (int c = part; c * VN < p.D; c += 8) {
-        const Chunk<T> kk = kp[c];
+      for (int i = 0; i < NK * R; ++i) s[i] = 0.f;
+      const int part = lane % PARTS, key0 = tid / PARTS;           // keys key0, + kThreads / PARTS
+      const uint8_t* kp = st + key0 * L.ks;
+      for (int c = part; c * VN < p.D; c += PARTS) {
+        Chunk<T> kk[NK];
 #pragma unroll
-        for (int e = 0; e < VN; e += 4) {
-          const float k_0 = to_f(kk.e[e]), k_1 = to_f(kk.e[e + 1]), k_2 = to_f(kk.e[e + 2]), k_3 = to_f(kk.e[e + 3]);
+        for (int k = 0; k < NK; ++k) kk[k] = reinterpret_cast<const Chunk<T>*>(kp + k * (kThreads / PARTS) * L.ks)[c];
+#pragma unroll
+        for (int e = 0; e < VN; e += 4)
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             const float4 q = *reinterpret_cast<const float4*>(sq + i * qs + c * VN + e);
-            s[i] = fmaf(q.x, k_0, fmaf(q.y, k_1, fmaf(q.z, k_2, fmaf(q.w, k_3, s[i]))));
-          }
-        }
-      }
-      // the eight parts' sums: each exchange halves the rows that a lane goes on with, to row part % R
 #pragma unroll
-      for (int h = R / 2; h > 0; h >>= 1)
+            for (int k = 0; k < NK; ++k)
+              s[k * R + i] = fmaf(q.x, to_f(kk[k].e[e]), fmaf(q.y, to_f(kk[k].e[e + 1]),
+                             fmaf(q.z, to_f(kk[k].e[e + 2]), fmaf(q.w, to_f(kk[k].e[e + 3]), s[k * R + i]))));
+          }
+      }
+      // the parts' sums: each exchange halves the scores that a lane goes on with, to number part % (NK R)
+#pragma unroll
+      for (int h = NK * R / 2; h > 0; h >>= 1)
 #pragma unroll
         for (int i = 0; i < h; ++i) {
           const bool up = part & h;
           const float give = up ? s[i] : s[i + h], keep = up ? s[i + h] : s[i];
           s[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
         }
-#pragma unroll
-      for (int h = R; h < 8; h <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], h);
-      if (part < R) {
+      if (R == 4) s[0] += __shfl_xor_sync(0xffffffffu, s[0], PARTS / 2);
+      const int i = part % R, key = key0 + kThreads / PARTS * (part / R);
+      if (part < NK * R) {
         const int back = j * kKeys + key - x.x.ctx;
-        bool sees = (s_ok[j % NST] >> key & 1) && part < x.rows;
+        bool sees = (s_ok[j % NST] >> key & 1) && i < x.rows;
         if (sees && back >= 0) {
-          const int t = (int)quot(x.row0 + part, p.by_G);
+          const int t = (int)quot(x.row0 + i, p.by_G);
           sees = p.tree ? (p.tree[x.first + t] >> back) & 1 : back <= t;
         }
-        ss[part * kKeys + key] = sees ? s[0] * p.c : -INFINITY;
+        ss[i * kScores + key] = sees ? s[0] * p.c : -INFINITY;
       }
     }
     __syncthreads();
     find(j + NST);                                                 // (its offsets' place was tile j + NST - 2's)
     if (warp < R) {                                                // running maximum and sum of row `warp`
-      const float s = ss[warp * kKeys + lane];
+      const float s = ss[warp * kScores + lane];
       float top = s;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -292,7 +298,7 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
 }
 
 template <typename T, int NQ>
-__global__ void __launch_bounds__(kThreads) simple_kernel(const __grid_constant__ SimpleArgs a) {
+__global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) simple_kernel(const __grid_constant__ SimpleArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Start s_start;
   __shared__ long long s_scan[kThreads / 32 + 1];
