@@ -28,6 +28,9 @@ constexpr int kRows = 8, kKeys = 32, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kScores = kKeys + 1;  // stride of a row of scores: eight rows in other banks
 constexpr Cost kCost = {8, 3, 8, 3};
 
+// Of any sizes: two stages of fp32 and 256 columns are the most, smaller ones have more stages within 105 KB.
+constexpr int kMostSmem = 144 * 1024;
+
 struct SimpleSmem {
   int ks, vs;                 // bytes of a row of K and of V
   int stage, stages;
@@ -421,7 +424,7 @@ cudaError_t join(const Args& a) {
 
 template <typename T, int NQ>
 cudaError_t go(const SimpleArgs& a) {
-  const cudaError_t e = allow_smem<simple_kernel<T, NQ>>(simple_smem(256, 256, sizeof(T)).bytes);
+  const cudaError_t e = allow_smem<simple_kernel<T, NQ>>(kMostSmem);
   return e != cudaSuccess ? e
                           : launch_pdl(simple_kernel<T, NQ>, dim3(a.ctas), dim3(kThreads), a.L.bytes, a.p.stream, a);
 }

@@ -454,6 +454,14 @@ def test_heads_above_128_many_times(gdp):
     check(gdp, d)
 
 
+@pytest.mark.parametrize("D,DV,layout", [(197, 197, "plain"), (207, 207, "heads"), (238, 150, "plain"), (256, 143, "pair"),
+                                         (160, 238, "plain"), (256, 136, "odd"), (129, 129, "odd"), (1, 256, "plain")])
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+def test_sizes_with_the_most_shared_memory(gdp, D, DV, layout, dtype):
+    """As many stages as fit: what a size takes does not grow with it."""
+    check(gdp, problem([1, 0, 9], [90, 7, 31], 6, 2, D, DV, 24, dtype, layout))
+
+
 def test_another_current_device_is_refused(gdp, monkeypatch):
     d = problem([2, 3], [40, 7], 4, 2, 64, 64, 16, BF)
     k, v = d["q"][0, :, :2].contiguous(), d["q"][0, :, 2:4].contiguous()
