@@ -618,7 +618,7 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  *           at most 64 tokens. NULL: every token sees the new ones up to itself.
  * Output: o [B, T, H, DV] contiguous, dtype `dt`, apart from q; a row that sees nothing is 0. Sums and the
  * softmax's statistics are fp32; 16-bit types round its weights to the type (relative to a
- * maximum that is at most 2^8 too small) before the product with V.
+ * maximum that is at most 2^8 too small; in fp16 those below 2^-21 of the largest lose precision) before the product with V.
  * Refused on the device: a page number of n_pages or more (the block is not there, as for
  * -1), a negative context, one that its table is too short for, more than 64 tokens with a
  * tree_mask (the request's o rows are 0): these set *status (nullable int32, not cleared) to

@@ -15,7 +15,8 @@
 // memory, forms p = 2^(c s - m) in registers and puts them back as 16-bit pairs over S, and O += P V takes
 // P from there and V as it lies (MN-major). m only follows the row's maximum when that has grown by more
 // than 2^8 (then O is scaled in tensor memory): p stays below 2^8, and a 16-bit p keeps its relative
-// precision, half a step of the type, which is what the output's own rounding costs. Sums are fp32.
+// precision, half a step of the type, which is what the output's own rounding costs (fp16's begins 2^7 higher, see
+// kUp). Sums are fp32.
 //
 // Roles: warps 0 to 7 softmax, 8 and 9 load K and V, 10 and 11 issue the products. Loads are boxes of 64
 // columns and `g` keys, g the largest power of two that divides both the page and the tile, through tensor
@@ -51,6 +52,9 @@ constexpr int kThreads = 384;
 // 566, and 216 and 130 of pieces of prompts; now 610 and 588, 132 and 122.)
 constexpr Cost kCost = {10, 2, 22, 3}, kCostWide = {10, 5, 10, 5};
 constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
+// log2 of a factor of all weights, which their sum has too: fp16's reach from 2^15 down to 2^-14 in full precision, so
+// that only those 2^21 times smaller than the largest lose some.
+template <typename T> constexpr float kUp = std::is_same_v<T, __half> ? 7.f : 0.f;
 
 template <int KD>
 struct Lay {
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float base = m == -INFINITY ? 0.f : m;
+          const float base = (m == -INFINITY ? 0.f : m) - kUp<T>;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t w[32];
 #pragma unroll

@@ -462,6 +462,28 @@ def test_sizes_with_the_most_shared_memory(gdp, D, DV, layout, dtype):
     check(gdp, problem([1, 0, 9], [90, 7, 31], 6, 2, D, DV, 24, dtype, layout))
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("far", [14.3, 18.7, 20.6])
+def test_many_small_weights(gdp, far, dtype):
+    """One key of weight 1 and value 0, thousands of weights near 2^-far, all the same, so that their roundings do not
+    average out: weights this far below the largest keep their type's full precision. (Many requests of the same pages: a
+    CTA has whole ones.)"""
+    n, D = 8192, 64
+    d = problem([1], [n - 1], 1, 1, D, D, 64, dtype)
+    for name in ("q", "k_cache", "v_cache"):
+        d[name].zero_()
+    d["q"][0, 0, 0, 0] = 1.0
+    first = int(d["block_tables"][0, 0])
+    d["k_cache"][first, 0, 0, 0] = far * 0.6931471806
+    d["v_cache"].fill_(1.0)
+    d["v_cache"][first, 0] = 0.0
+    R = 320
+    d.update(q=d["q"].expand(1, R, 1, D), block_tables=d["block_tables"].expand(R, -1).contiguous(),
+             context_lens=d["context_lens"].expand(R).contiguous(),
+             cu_seqlens=torch.arange(R + 1, dtype=torch.int32, device=DEV))
+    check(gdp, d, scale=1.0)
+
+
 def test_another_current_device_is_refused(gdp, monkeypatch):
     d = problem([2, 3], [40, 7], 4, 2, 64, 64, 16, BF)
     k, v = d["q"][0, :, :2].contiguous(), d["q"][0, :, 2:4].contiguous()
