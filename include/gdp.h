@@ -579,8 +579,8 @@ gdp_status gdp_rotary(const void* x, const int64_t* x_strides, const int32_t* po
  *   positions, frequencies, rotary_dim, offset, interleaved, amplitude: as gdp_rotary;
  *           rotary_dim 0: no rotation (both may be NULL).
  *   slot_map [B, T] int64: a token's slot page * block_size + place; -1: not kept. A slot
- *           outside the cache is treated so too and sets *status (nullable int32 on the
- *           device; not cleared) to 1. The slots that are kept must differ: where two tokens
+ *           outside the cache is treated so too and raises *status (nullable int32 on the
+ *           device; never lowered) to 1. The slots that are kept must differ: where two tokens
  *           name one, it holds parts of either.
  *   k_cache [n_pages, block_size, HKV, D], v_cache [n_pages, block_size, HKV, DV]: dtype
  *           `dt`, the last dimension contiguous; k_cache_strides and v_cache_strides: HOST
@@ -621,8 +621,8 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  * maximum that is at most 2^8 too small; in fp16 those below 2^-21 of the largest lose precision) before the product with V.
  * Refused on the device: a page number of n_pages or more (the block is not there, as for
  * -1), a negative context, one that its table is too short for, more than 64 tokens with a
- * tree_mask (the request's o rows are 0): these set *status (nullable int32, not cleared) to
- * 1. So does a list of offsets that decreases, starts above 0 or ends past T; o is left as it
+ * tree_mask (the request's o rows are 0): these raise *status (nullable int32, never lowered,
+ * so that a word which calls share keeps the worst of them) to 1. So does a list of offsets that decreases, starts above 0 or ends past T; o is left as it
  * was then. 2: a bounded wait on the device ran out. Rows of o past cu_seqlens[N_seq] are
  * left as they were.
  * Keys and values that are not finite at positions which a request does not have are not

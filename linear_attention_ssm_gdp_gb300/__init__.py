@@ -916,7 +916,7 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
     rows may be strided), k_cache [n_pages, block_size, HKV, D] and v_cache [n_pages,
     block_size, HKV, DV] with any strides of the first three dimensions, slot_map [T] int64
     and positions [T] int32 as gdp_block_plan gives them (-1: not kept). ``status`` (optional
-    int32 device tensor) is set to 1 by a slot outside the cache, which is not kept either.
+    int32 device tensor) is raised to 1 by a slot outside the cache, which is not kept either.
     Slots must differ; all tensors are on the current device. Returns the rotated q (None
     without one)."""
     dt = k.dtype
@@ -975,9 +975,9 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
     block_tables [n, max_blocks] int32 (-1: not there), context_lens [n] int32: tokens before
     the new ones. tree_mask [B, T] int64: bit j of a token set where it sees its request's new
     token j (at most 64 tokens a request); without it each sees the new ones up to itself.
-    ``scale`` defaults to D**-0.5. ``status`` (optional int32 device tensor) is set to 1 by
-    bad pages, contexts or offsets and to 2 where a wait on the device ran out; it is not
-    cleared. All tensors are on the current device. Returns o [B, T, H, DV] in q's dtype;
+    ``scale`` defaults to D**-0.5. ``status`` (optional int32 device tensor) is raised to 1 by
+    bad pages, contexts or offsets and to 2 where a wait on the device ran out; it is never
+    lowered, so calls may share one. All tensors are on the current device. Returns o [B, T, H, DV] in q's dtype;
     rows that see nothing are 0."""
     dt = q.dtype
     if dt not in _DTYPE or q.dim() != 4:

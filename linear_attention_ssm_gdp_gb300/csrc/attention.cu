@@ -95,7 +95,7 @@ __device__ __forceinline__ void simple_piece(const SimpleArgs& a, uint8_t* sm, c
   auto find = [&](int j) {
     if (warp != kWarps - 1) return;
     const int key = j * kKeys + lane, in = key - (int)quot(key, p.by_block) * p.block;
-    if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
+    if (page >= p.n_pages) report(p.status, GDP_ERR_INVALID_ARG);
     const bool there = (uint32_t)page < (uint32_t)p.n_pages;
     s_off[(j & 1) * kKeys + lane] =
         there ? make_longlong2(page * p.ks[0] + in * p.ks[1], page * p.vs[0] + in * p.vs[1]) : make_longlong2(-1, -1);

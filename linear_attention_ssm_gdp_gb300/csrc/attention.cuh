@@ -167,7 +167,7 @@ __device__ __forceinline__ void find_start(const Args& a, Start* out, long long*
     mine += head;
   }
   mine *= p.HKV;
-  if (blockIdx.x == 0 && (odd || bad) && p.status) *p.status = GDP_ERR_INVALID_ARG;
+  if (blockIdx.x == 0 && (odd || bad)) report(p.status, GDP_ERR_INVALID_ARG);
   bad = __syncthreads_or(bad);
   long long sum = mine;
 #pragma unroll

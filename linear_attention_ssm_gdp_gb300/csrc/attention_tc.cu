@@ -96,7 +96,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
     if (((t - t0) >> 10) > (uint32_t)budget) {
-      if (status) atomicExch(status, kDevTimeout);
+      report(status, kDevTimeout);
       *dead = 1;
       return false;
     }
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int next = page_of(j + 1), key = j * kKeys + sub * a.g;
           ok = sy.wait(full + empty + stage, turn);
           if (!ok) break;
-          if (page >= p.n_pages && p.status) *p.status = GDP_ERR_INVALID_ARG;
+          if (page >= p.n_pages) report(p.status, GDP_ERR_INVALID_ARG);
           const bool there = (uint32_t)page < (uint32_t)p.n_pages;
           const uint32_t gone = ~__ballot_sync(0xffffffffu, there) & ((1u << subs) - 1u);
           if (lane == 0) {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int next0 = page_of(j + 1, 0), next1 = page_of(j + 1, 1), key0 = j * kKeys + lane, key1 = key0 + 32;
           ok = sy.wait(full + empty + stage, turn);
           if (!ok) break;
-          if ((page0 >= p.n_pages || page1 >= p.n_pages) && p.status) *p.status = GDP_ERR_INVALID_ARG;
+          if (page0 >= p.n_pages || page1 >= p.n_pages) report(p.status, GDP_ERR_INVALID_ARG);
           const bool there0 = (uint32_t)page0 < (uint32_t)p.n_pages, there1 = (uint32_t)page1 < (uint32_t)p.n_pages;
           const uint64_t gone = ~(__ballot_sync(0xffffffffu, there0) | (uint64_t)__ballot_sync(0xffffffffu, there1) << 32);
           if (lane == 0) tell(gone);

@@ -17,6 +17,11 @@ namespace gdp {
 // Device status word codes (first int32 of a chunk_fwd workspace).
 enum DeviceStatus : int { kDevOk = 0, kDevBadSeqlens = 1, kDevTimeout = 2 };
 
+// A word that threads, kernels and calls share keeps the worst of what they report.
+__device__ __forceinline__ void report(int32_t* status, int code) {
+  if (status) atomicMax(status, code);
+}
+
 // Per-sequence descriptor built on the device from cu_seqlens (or from B, T):
 // x = first token in the flattened [B*T] token stream, y = length in tokens,
 // z = index of its first expanded chunk, w = index of its first token chunk.

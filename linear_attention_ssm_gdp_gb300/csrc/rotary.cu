@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __gri
       if (slot >= 0 && slot < a.n_slots) {
         page = slot / a.block;
         place = slot - page * a.block;
-      } else if (slot != -1 && a.status && lane == 0) {
-        *a.status = GDP_ERR_INVALID_ARG;
+      } else if (slot != -1 && lane == 0) {
+        report(a.status, GDP_ERR_INVALID_ARG);
       }
     }
     if (a.half > 0) {
