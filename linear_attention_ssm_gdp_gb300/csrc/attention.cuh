@@ -6,7 +6,7 @@
 // that a long context is spread over many CTAs and a batch of ragged ones ends evenly; contexts are
 // known on the device only, so every CTA adds up the requests' costs by itself and finds the start of
 // its share. A share covers whole items and at most two cut ones (its first and its last piece). Pieces
-// of cut items leave their row maxima, sums and unnormalised outputs in the workspace, and the join
+// of cut items leave their rows' bases, sums and unnormalised outputs in the workspace, and the join
 // kernel joins them in order.
 #pragma once
 
@@ -55,7 +55,7 @@ struct Args {
   Cost cost;
   Rec* recs;                      // [ctas]
   float* part;                    // [ctas][2][dvp / 4][cap][4] outputs
-  float2* ml;                     // [ctas][2][cap] row maximum (log2) and sum
+  float2* ml;                     // [ctas][2][cap] base (log2) that the row's weights are relative to, and their sum
   int ctas, cap, dvp;             // cap: rows of a piece that are kept
 };
 

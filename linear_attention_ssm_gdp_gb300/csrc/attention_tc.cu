@@ -4,7 +4,7 @@
 // A CTA walks the pieces of its share (attention.cuh) with two slots, each with four warps of its own,
 // two buffers of 64 columns of scores and KD of outputs in tensor memory:
 //   more than 128 rows: the slots are two tiles of 128 rows that read the same keys;
-//   fewer: both slots have the same rows and take the tiles of 64 keys in turn, and their two maxima, sums
+//   fewer: both slots have the same rows and take the tiles of 64 keys in turn, and their two bases, sums
 //   and outputs are joined at the piece's end (they lie in the same lanes of tensor memory).
 // Heads above 128 have one slot, whose outputs take the second one's columns.
 // So one slot's softmax runs beside the other's products either way, and a decode step's few rows cost
@@ -12,8 +12,8 @@
 // third of the time that HBM needs for its keys.
 //
 // A tile: S = Q K^T (tcgen05, K-major operands), then a thread per row takes its 64 scores from tensor
-// memory, forms p = 2^(c s - m) in registers and puts them back as 16-bit pairs over S, and O += P V takes
-// P from there and V as it lies (MN-major). m only follows the row's maximum when that has grown by more
+// memory, forms p = 2^(c s - b) in registers and puts them back as 16-bit pairs over S, and O += P V takes
+// P from there and V as it lies (MN-major). The base b only follows the row's maximum when that has grown by more
 // than 2^8 (then O is scaled in tensor memory): p stays below 2^8, and a 16-bit p keeps its relative
 // precision, half a step of the type, which is what the output's own rounding costs (fp16's begins 2^7 higher, see
 // kUp). Sums are fp32.
@@ -51,10 +51,16 @@ constexpr int kThreads = 384;
 // 0.6 a tile, more rows 6.5 and 0.95; heads above 128, with twice the bytes, 3 and 1.5. (With tiles alone the slowest CTA of a decode batch took 870 us, the median
 // 566, and 216 and 130 of pieces of prompts; now 610 and 588, 132 and 122.)
 constexpr Cost kCost = {10, 2, 22, 3}, kCostWide = {10, 5, 10, 5};
-constexpr float kGrow = 8.f;        // log2 of how far the maximum may lie above m
 // log2 of a factor of all weights, which their sum has too: fp16's reach from 2^15 down to 2^-14 in full precision, so
-// that only those 2^21 times smaller than the largest lose some.
+// that only those 2^21 times smaller than the largest lose some. The base is the row's maximum less this.
 template <typename T> constexpr float kUp = std::is_same_v<T, __half> ? 7.f : 0.f;
+template <typename T> constexpr float kGrow = kUp<T> + 8.f;  // log2 of how far the maximum may lie above the base
+// From here on (powers of two) a score's steps are a half and more. One multiply-add of a score and its base would then
+// give the largest weight anything from 2^-half a step to 2^half a step, in 16 bits as far as 0 and infinity. So such a
+// row's scores are rounded as their maximum was before the base, that maximum itself, is taken off: by a second pass over
+// the tile's scores in tensor memory, so that other tiles pay a vote (pieces of prompts 137 us, 136 without; 138 to 151
+// with the rounding in the first pass, in a function, or in more columns a step).
+constexpr float kFar = 4194304.f;
 
 template <int KD>
 struct Lay {
@@ -67,14 +73,14 @@ struct Lay {
   static constexpr int QT = KD / 64 * 16384;     // 128 rows of queries
   static constexpr int Q = 0, K = SLOTS * QT, V = K + NK * TILE;
   static constexpr int BAR = V + NV * TILE;
-  static constexpr int ML = BAR + 704;           // maxima and sums [2][128]
+  static constexpr int ML = BAR + 704;           // bases and sums [2][128]
   static constexpr int START = ML + 2048;        // the share, and the sums that lead to it
   static constexpr int BYTES = START + 192;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 // by buffer: K full, empty, V full, empty, absent keys known; by slot and buffer of its scores: scores, weights,
 // outputs (a waiter may be two tiles behind, which one barrier's parity cannot tell from none); by slot: queries;
-// a piece's two slots have left their maxima, have read each other's outputs
+// a piece's two slots have left their bases, have read each other's outputs
 enum {
   B_KFULL = 0, B_KEMPTY = 8, B_VFULL = 16, B_VEMPTY = 28, B_META = 40, B_S = 52, B_P = 56, B_O = 60, B_Q = 64,
   B_JOIN = 66, B_DONE, B_END, B_N = B_END + 2
@@ -228,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = quarter * 32 < d.rows;
       const int t = (int)quot(d.row0 + min(row, d.rows - 1), p.by_G);
       const uint64_t bits = p.tree && x.x.live ? (uint64_t)p.tree[x.first + t] : 0ull;
-      float m = -INFINITY, l = 0.f;
+      float b = -INFINITY, off = 0.f, l = 0.f;  // off: what is taken off a score: b, or 0 while nothing is seen
+      bool far = false;                         // b lies beyond kFar
 #pragma unroll 1
       for (int k = 0; ok && k < d.n; ++k, ++n) {
         const int j = d.two || L::SLOTS == 1 ? k : 2 * k + slot, key0 = (x.j0 + j) * kKeys;
@@ -243,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           GDP_TMEM_LD32(tb, s);
           GDP_TMEM_LD32(tb + 32, (s + 32));
           tmem_wait_ld();
+          uint64_t see = ~0ull;
           if (key0 + kKeys > x.x.ctx || absent) {  // some of the keys are not seen by some row
-            uint64_t see;
             if (p.tree) {
               const int back = key0 - x.x.ctx;
               see = low_bits(-back);
@@ -263,12 +270,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
           const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-          const bool grow = mt > m + kGrow;  // (from -inf: as soon as anything is seen)
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mt : m, f = grow ? ex2(m - mn) : 1.f;
-            m = mn;
+          const bool grow = mt - b > kGrow<T>;  // (from -inf: as soon as anything is seen)
+          if (__any_sync(0xffffffffu, grow || far)) {
+            const float bn = grow ? mt - (fabsf(mt) < kFar ? kUp<T> : 0.f) : b, f = grow ? ex2(b - bn) : 1.f;
+            b = bn;
             l *= f;
-            if (k > 0) {  // the last product into O is done, then O is scaled
+            far = row < d.rows && fabsf(b) >= kFar && b != -INFINITY;
+            off = b == -INFINITY ? 0.f : b;
+            if (k > 0 && __any_sync(0xffffffffu, grow)) {  // the last product into O is done, then O is scaled
               ok = sy.wait(&bars[B_O + 2 * slot + (buf ^ 1)], (n - 1) >> 1 & 1);
               if (!ok) break;
               tc_fence_after();
@@ -283,19 +292,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float base = (m == -INFINITY ? 0.f : m) - kUp<T>;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), c, -base));
-            const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), c, -base));
+            const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), c, -off));
+            const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), c, -off));
             sum[2 * (e & 1)] += p0;
             sum[2 * (e & 1) + 1] += p1;
             w[e] = pack<T>(p0, p1);
           }
-          GDP_TMEM_ST32(tb, w);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (__any_sync(0xffffffffu, far)) {  // again, from rounded scores, in place: word e is formed of columns 2 e, 2 e + 1
+            float all = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e) {
+              uint32_t u[2];
+              tmem_ld2(tb + 2 * e, u);
+              tmem_wait_ld();
+              const float s0 = see >> (2 * e) & 1 ? __uint_as_float(u[0]) : -INFINITY;
+              const float s1 = see >> (2 * e + 1) & 1 ? __uint_as_float(u[1]) : -INFINITY;
+              const float p0 = ex2(far ? __fmul_rn(s0, c) - off : fmaf(s0, c, -off));
+              const float p1 = ex2(far ? __fmul_rn(s1, c) - off : fmaf(s1, c, -off));
+              all += p0 + p1;
+              tmem_st1(tb + e, pack<T>(p0, p1));
+              tmem_wait_st();
+            }
+            l += all;
+          } else {
+            GDP_TMEM_ST32(tb, w);
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
           tmem_wait_st();
         }
         const int z0 = x.keys - key0;
@@ -325,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile0 += nt;
       other += d.two ? nt : nt - d.n;
       if (!ok) break;
-      // Two slots on the same rows: each leaves its maxima and sums, then joins half of the columns. (Both
+      // Two slots on the same rows: each leaves its bases and sums, then joins half of the columns. (Both
       // slots' outputs lie in the same lanes of tensor memory.)
       const bool join = L::SLOTS == 2 && !d.two && nt > 1;
       float f0 = 1.f, f1 = 0.f;  // of this slot's and of the other's outputs
       if (d.n > 0) ok = sy.wait(&bars[B_O + 2 * slot + ((n - 1) & 1)], (n - 1) >> 1 & 1);
       if (join) {
-        s_ml[slot * 128 + row] = make_float2(m, l);
+        s_ml[slot * 128 + row] = make_float2(b, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_JOIN]);
         ok = ok && sy.wait(&bars[B_JOIN], joins & 1) && 
@@ -340,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++joins;
         owe = true;
         const float2 u = s_ml[(slot ^ 1) * 128 + row];
-        const float mn = fmaxf(m, u.x), base = mn == -INFINITY ? 0.f : mn;
-        f0 = ex2(m - base);
+        const float bn = fmaxf(b, u.x), base = bn == -INFINITY ? 0.f : bn;
+        f0 = ex2(b - base);
         f1 = ex2(u.x - base);
-        m = mn;
+        b = bn;
         l = f0 * l + f1 * u.y;
       }
       if (!ok) break;
@@ -354,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = d.row0 - x.row0 + row;  // of the item's rows
         const int64_t cut = (int64_t)blockIdx.x * 2 + x.slot;
         const bool whole = x.slot < 0;
-        if (!whole && on && (slot == 0 || d.two)) a.ml[cut * a.cap + at] = make_float2(m, l);
+        if (!whole && on && (slot == 0 || d.two)) a.ml[cut * a.cap + at] = make_float2(b, l);
         float4* part = reinterpret_cast<float4*>(a.part + (whole ? 0 : cut * a.cap * a.dvp)) + at;
         T* dst = static_cast<T*>(p.o) + out_at(p, x.first, x.head, d.row0 + min(row, d.rows - 1));
         if (whole) { f0 *= inv; f1 *= inv; }
