@@ -181,6 +181,14 @@ def _one_device(*ts):
             raise ValueError("every tensor must be on the current CUDA device")
 
 
+def _here():
+    """The current device; None without one (sizes can be asked for there too)."""
+    try:
+        return _current_device()
+    except (RuntimeError, AssertionError):
+        return None
+
+
 def gdp_version() -> int:
     return int(load().gdp_version())
 
@@ -958,9 +966,13 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
 
 
 @functools.lru_cache(maxsize=256)
+def _attention_bytes(device, *args):
+    return int(load().gdp_attention_paged_workspace_size(*args))
+
+
 def gdp_attention_paged_workspace_size(B, T, N_seq, H, HKV, D, DV, dtype) -> int:
-    return int(load().gdp_attention_paged_workspace_size(B, T, N_seq, H, HKV, D, DV,
-                                                         _DTYPE[dtype]))
+    """Bytes of gdp_attention_paged's workspace on the current device."""
+    return _attention_bytes(_here(), B, T, N_seq, H, HKV, D, DV, _DTYPE[dtype])
 
 
 def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens=None,
