@@ -761,8 +761,13 @@ _ACTIVATION = {"none": 0, "silu": 1}
 
 
 @functools.lru_cache(maxsize=256)
+def _norm_bytes(device, *args):
+    return int(load().gdp_group_norm_workspace_size(*args))
+
+
 def gdp_group_norm_workspace_size(N, L, C, num_groups, dtype) -> int:
-    return int(load().gdp_group_norm_workspace_size(N, L, C, num_groups, _DTYPE[dtype]))
+    """Bytes of gdp_group_norm's workspace on the current device."""
+    return _norm_bytes(_here(), N, L, C, num_groups, _DTYPE[dtype])
 
 
 def gdp_group_norm(x, num_groups: int, weight=None, bias=None, gate=None, eps: float = 1e-5,

@@ -15,6 +15,9 @@ class Fake:
     def gdp_attention_paged_workspace_size(self, *a):
         return 1000 + self.device
 
+    def gdp_group_norm_workspace_size(self, *a):
+        return 2000 + self.device
+
 
 @pytest.fixture
 def fake(monkeypatch):
@@ -31,6 +34,12 @@ def test_attention(fake):
         assert gdp.gdp_attention_paged_workspace_size(*args) == 1000 + device
 
 
+def test_group_norm(fake):
+    for device in (0, 1, 0, 3):
+        fake.device = device
+        assert gdp.gdp_group_norm_workspace_size(3, 77, 96, 2, torch.float32) == 2000 + device
+
+
 def test_without_a_device(monkeypatch):
     """Where there is none, sizes can be asked for all the same."""
     def none():
@@ -38,3 +47,4 @@ def test_without_a_device(monkeypatch):
     monkeypatch.setattr(gdp, "load", lambda: Fake())
     monkeypatch.setattr(gdp, "_current_device", none)
     assert gdp.gdp_attention_paged_workspace_size(5, 1, 5, 4, 2, 72, 72, torch.bfloat16) == 1000
+    assert gdp.gdp_group_norm_workspace_size(3, 78, 96, 2, torch.float32) == 2000
