@@ -628,6 +628,7 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  * Keys and values that are not finite at positions which a request does not have are not
  * read; one of a new token's values may also reach tokens of the request that do not see
  * it (0 times infinity is not 0).
+ * scale: finite, its product with log2 e too.
  * workspace: at least gdp_attention_paged_workspace_size() bytes, 256-byte aligned; calls
  * that share one must not overlap on the GPU.
  * D, DV <= 256, max_blocks * block_size below 2^31 - 65536.

@@ -538,7 +538,8 @@ gdp_status gdp_attention_paged(const void* q, const int64_t* q_strides, const vo
     return GDP_ERR_INVALID_ARG;
   if (!sizes_built(B, T, H, HKV, D, DV, dt)) return GDP_ERR_UNSUPPORTED;
   if ((int64_t)max_blocks * block_size > INT32_MAX - 65536) return GDP_ERR_UNSUPPORTED;
-  if (!std::isfinite(scale) || (cu_seqlens ? B != 1 : N_seq != B)) return GDP_ERR_INVALID_ARG;
+  const float c = scale * 1.44269504088896341f;  // scores in powers of two
+  if (!std::isfinite(c) || (cu_seqlens ? B != 1 : N_seq != B)) return GDP_ERR_INVALID_ARG;
   if ((int64_t)B * T == 0 || N_seq == 0) return GDP_OK;
   if (!q || !o || !q_strides || !k_cache_strides || !v_cache_strides || !context_lens) return GDP_ERR_INVALID_ARG;
   if ((max_blocks > 0 && !block_tables) || (n_pages > 0 && (!k_cache || !v_cache))) return GDP_ERR_INVALID_ARG;
@@ -557,7 +558,7 @@ gdp_status gdp_attention_paged(const void* q, const int64_t* q_strides, const vo
   p.n_pages = n_pages; p.block = block_size; p.tables = block_tables; p.width = max_blocks; p.ctx = context_lens;
   p.cu = cu_seqlens; p.n = N_seq; p.B = B; p.T = T; p.H = H; p.HKV = HKV; p.G = H / HKV; p.D = D; p.DV = DV;
   p.by_G = div_by(p.G); p.by_block = div_by(block_size);
-  p.tree = tree_mask; p.c = scale * 1.44269504088896341f; p.dt = dt; p.o = o; p.status = status; p.stream = stream;
+  p.tree = tree_mask; p.c = c; p.dt = dt; p.o = o; p.status = status; p.stream = stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaError_t e = attn::tc_ok(p) ? attn::launch_tc(p, ws) : attn::launch_simple(p, ws);
   return e == cudaSuccess ? GDP_OK : GDP_ERR_CUDA;
