@@ -7,8 +7,8 @@ have written, and appends the accepted tokens' keys and values again at their pl
 
     python examples/serve_attention.py [--requests 8] [--prompt 300] [--steps 16]
 
-The weights are random. At the end the keys in the pages are compared with those of one dense pass
-over each request's tokens.
+The weights are random. At the end the first layer's keys in the pages, which depend on their own token
+only, are compared with those of one dense pass over each request's tokens.
 """
 import argparse
 import os
@@ -137,7 +137,7 @@ def serve(requests=8, prompt=300, steps=16, seed=0, device="cuda"):
         s.keep(kept, paths)
     if int(s.status):
         raise RuntimeError(f"a step reported {int(s.status)}")
-    # keys of the first layer, which depend on their own token only
+    # keys of the first layer
     off = 0.0
     for r, x in enumerate(streams):
         _, k, _ = layers[0].project(embed[torch.tensor(x, device=device)])
@@ -157,7 +157,7 @@ def main():
     streams, lens, off = serve(a.requests, a.prompt, a.steps)
     new = sum(map(len, streams)) - sum(lens)
     print(f"{len(streams)} requests, {new} tokens in {a.steps} steps, {new / a.steps / len(streams):.2f} a step each")
-    print(f"keys in pages against a dense pass: {off:.1e} apart")
+    print(f"keys of the first layer in pages against a dense pass: {off:.1e} apart")
 
 
 if __name__ == "__main__":
