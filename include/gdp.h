@@ -560,8 +560,8 @@ gdp_status gdp_rotary_frequencies(int rotary_dim, double base, gdp_rotary_scalin
  *           y is x with the same strides (in place), or does not overlap it; its own elements
  *           lie apart (strides of 0 are refused).
  *   positions [B, T] int32, any value; frequencies [rotary_dim / 2] fp64, finite, on the
- *           device. Angles are exact to 2^-52 of a frequency times the position.
- * D <= 1024. Sums are fp32, rounded once.
+ *           device. Angles are off by |position| (2^-52 frequency + 2 pi 2^-65) at most.
+ * D <= 1024. Cosines, sines and sums are fp32, the result rounded to `dt`.
  * Errors: GDP_ERR_INVALID_ARG (sizes, an odd rotary_dim, a part outside the head, an
  * amplitude that is not finite), GDP_ERR_UNSUPPORTED (dtype, D), GDP_ERR_CUDA.
  */
@@ -588,6 +588,8 @@ gdp_status gdp_rotary(const void* x, const int64_t* x_strides, const int32_t* po
  *           head-major pages go in as they are (strides of 0 are refused). Other slots are
  *           left as they are.
  *   q_out   [B, T, H, D] contiguous; q itself where that is contiguous.
+ * Tokens are written in no order: k, v and q lie apart from the slots that are written (keys that
+ * move within a cache are copied out first), and q_out, unless it is q, from q, k, v and the caches.
  * D, DV <= 1024. Errors: GDP_ERR_INVALID_ARG, GDP_ERR_UNSUPPORTED (dtype, sizes),
  * GDP_ERR_CUDA.
  */
@@ -619,6 +621,7 @@ gdp_status gdp_cache_append(const void* q, const void* k, const void* v, const i
  * Output: o [B, T, H, DV] contiguous, dtype `dt`, apart from q; a row that sees nothing is 0. Sums and the
  * softmax's statistics are fp32; 16-bit types round its weights to the type (relative to a
  * maximum that is at most 2^8 too small; in fp16 those below 2^-21 of the largest lose precision) before the product with V.
+ * Sums of weights and values are divided at the end: in bf16 they overflow where values of about 2^120 / keys are met.
  * Refused on the device: a page number of n_pages or more (the block is not there, as for
  * -1), a negative context, one that its table is too short for, more than 64 tokens with a
  * tree_mask (the request's o rows are 0): these raise *status (nullable int32, never lowered,

@@ -938,8 +938,8 @@ def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequenci
     block_size, HKV, DV] with any strides of the first three dimensions, slot_map [T] int64
     and positions [T] int32 as gdp_block_plan gives them (-1: not kept). ``status`` (optional
     int32 device tensor) is raised to 1 by a slot outside the cache, which is not kept either.
-    Slots must differ; all tensors are on the current device. Returns the rotated q (None
-    without one)."""
+    Slots must differ, and k, v and q lie apart from them (tokens are written in no order);
+    all tensors are on the current device. Returns the rotated q (None without one)."""
     dt = k.dtype
     if dt not in _DTYPE:
         raise ValueError("k, v and q must be bf16, fp16 or fp32")
@@ -1003,7 +1003,8 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
     ``scale`` defaults to D**-0.5. ``status`` (optional int32 device tensor) is raised to 1 by
     bad pages, contexts or offsets and to 2 where a wait on the device ran out; it is never
     lowered, so calls may share one. All tensors are on the current device. Returns o [B, T, H, DV] in q's dtype;
-    rows that see nothing are 0."""
+    rows that see nothing are 0. Rows past cu_seqlens[n], and all of them where the offsets
+    are refused, are not written: they hold what ``out`` held, or without it anything."""
     dt = q.dtype
     if dt not in _DTYPE or q.dim() != 4:
         raise ValueError("q must be [B, T, H, D] in bf16, fp16 or fp32")

@@ -19,8 +19,9 @@ namespace {
 // the scores a thread has two keys and every 16th chunk of the head (a chunk of Q is read for both), for the outputs
 // four columns (eight above 128) and every eighth key, whose sums meet at the item's end. Bound by the latency of its
 // steps between three barriers a tile (half of the issue slots used): 64 requests of up to 4000 keys, 16 heads over 4,
-// 128 columns, fp32: 122 us, where HBM needs 65; 32 drafted tokens on up to 4000 keys, 8 requests, 64 columns: 314 us;
-// 16 requests of up to 9000 keys, 100 columns, bf16, 8 bytes a copy: 112 us, HBM 20 (by elements 738). Not kept: one
+// 128 columns, fp32: 122 us, where HBM needs 65; 32 drafted tokens on up to 4000 keys, 8 requests, 64 columns: 309 us;
+// pieces of prompts, 8 of up to 256 tokens on up to 1024, 128 columns: 747 us; 16 requests of up to 9000 keys, 100
+// columns, bf16, 8 bytes a copy: 115 us, HBM 20 (by elements 738; 54 bytes a thread spill in 16 bits). Not kept: one
 // key a thread (129 and 327 us), four (126 and 376); keys and maxima of its own for each warp with no barrier in a
 // tile (185 us: its sums of a score over lanes and its rescaling are every warp's); three CTAs of 80 registers an SM
 // (with one key a thread 123 us, but small calls 22 for 20 and trees 334).

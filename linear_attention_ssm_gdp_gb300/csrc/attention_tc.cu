@@ -26,11 +26,12 @@
 // are not 0). Pages whose size is not a multiple of 8 come by 16-byte cp.async.
 //
 // Measured: 256 requests of up to 8192 keys, 32 heads over 8, 128 columns: 610 us, 98 % of the measured copy
-// rate, bound by HBM. Pieces of prompts, 8 of up to 1024 tokens on up to 4096: 136 us, 0.92 PFLOP/s, 47 % of
+// rate, bound by HBM. Pieces of prompts, 8 of up to 1024 tokens on up to 4096: 137 us, 0.91 PFLOP/s, 47 % of
 // the measured bf16 rate: a tile of 2 x 128 rows takes 1830 cycles, where its products fill 1024 and its
 // exponentials 1024 (16 a cycle and SM); the rest is the chain scores, softmax, weights, outputs, scores, which
 // two buffers a slot overlap but once. One slot: 16 requests of up to 9000 keys, 16 heads over 4, 256 columns: 68 us,
-// where HBM needs 50. Beginning a share 4 us, queries in and outputs out 6 us a piece.
+// where HBM needs 50; pieces of prompts of 16 heads over 4, 256 columns: 311 us, 0.81 PFLOP/s. Pages by cp.async (of
+// 100): the decode batch 1450 us, the prompts 262. Beginning a share 4 us, queries in and outputs out 6 us a piece.
 #include <algorithm>
 #include <atomic>
 #include <mutex>

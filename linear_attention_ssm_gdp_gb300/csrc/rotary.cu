@@ -7,8 +7,8 @@
 //
 // Angles. A position times a frequency in 32 bits is off by pos 2^-24 of a turn's radians (0.06 at a
 // position of 10^6), so angles are counted in turns as 64-bit integers: F_i = frac(f_i / 2 pi) 2^64
-// once per CTA from the fp64 frequency, and the phase of a position is the integer product pos F_i
-// mod 2^64, exact for every int32 position. Its nearest quarter turn picks the quadrant, the rest (at
+// once per CTA from the fp64 frequency (off by 2^-52 of a frequency and 2^-65 of a turn), and the phase of a
+// position is the integer product pos F_i mod 2^64, itself exact for every int32 position. Its nearest quarter turn picks the quadrant, the rest (at
 // most an eighth of a turn) goes to sincospif as a float.
 //
 // Bound by HBM: every element is read and written once. A warp takes a token (or a share of its heads, where
