@@ -850,10 +850,10 @@ def gdp_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str 
             amplitude.value)
 
 
-def _sizes_ok(sizes):
-    """The library's sizes are 32-bit: a larger one would arrive as its low half."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"sizes of more than 31 bits: {list(sizes)}")
+# The library's sizes are 32-bit: a larger one would arrive as its low half. (`or` of the sizes: a tenth of a
+# microsecond, of the 10 to 20 that a small call takes.)
+def _too_large(*shapes):
+    return ValueError(f"sizes of more than 31 bits: {[list(s) for s in shapes]}")
 
 
 def _heads(name, t, dtype):
@@ -864,10 +864,15 @@ def _heads(name, t, dtype):
     if t.dtype != dtype or len(shape) not in (3, 4) or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be [T, H, D] or [B, T, H, D] in one dtype of "
                          "{bf16, fp16, fp32} with a contiguous last dimension")
-    _sizes_ok(shape)
     if len(shape) == 3:
-        return shape, 1, shape[0], shape[1], shape[2], (0, stride[0], stride[1])
-    return shape, shape[0], shape[1], shape[2], shape[3], stride[:3]
+        T, H, D = shape
+        if (T | H | D) >> 31:
+            raise _too_large(shape)
+        return shape, 1, T, H, D, (0, stride[0], stride[1])
+    B, T, H, D = shape
+    if (B | T | H | D) >> 31:
+        raise _too_large(shape)
+    return shape, B, T, H, D, stride[:3]
 
 
 def _rotation(lead, positions, frequencies, D, offset):
@@ -923,8 +928,11 @@ def _cache_ok(k_cache, v_cache, dtype):
                          "a contiguous last dimension")
     if ks[:3] != vs[:3]:
         raise ValueError("the caches must have the same pages, block size and heads")
-    _sizes_ok((*ks, vs[3]))
-    return (*ks, vs[3], _pack3(kt[0], kt[1], kt[2]), _pack3(vt[0], vt[1], vt[2]))
+    pages, block, H, D = ks
+    DV = vs[3]
+    if (pages | block | H | D | DV) >> 31:
+        raise _too_large(ks, vs)
+    return (pages, block, H, D, DV, _pack3(kt[0], kt[1], kt[2]), _pack3(vt[0], vt[1], vt[2]))
 
 
 def gdp_cache_append(k, v, k_cache, v_cache, slot_map, positions=None, frequencies=None,
@@ -1019,7 +1027,8 @@ def gdp_attention_paged(q, k_cache, v_cache, block_tables, context_lens, cu_seql
             or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
             or not block_tables.is_contiguous() or not context_lens.is_contiguous()):
         raise ValueError("block_tables must be int32 [n, max_blocks] and context_lens int32 [n]")
-    _sizes_ok(block_tables.shape)
+    if block_tables.shape[1] >> 31:
+        raise _too_large(block_tables.shape)
     if tree_mask is not None:
         if tree_mask.dtype != torch.int64 or tree_mask.shape != (B, T) \
                 or not tree_mask.is_contiguous() or not tree_mask.is_cuda:
